@@ -20,7 +20,10 @@ import torch
 __all__ = ["MOE_F32", "MOE_BF16", "MOE_FP8_BLOCK", "MoeError", "Layout", "library_path", "load_library",
            "moe_route", "moe_dispatch", "moe_expert_mlp", "moe_combine", "moe_dispatch_fp8", "moe_expert_mlp_fp8",
            "moe_combine_send", "moe_combine_recv", "moe_expert_mlp_combine", "moe_dispatch_noalloc",
-           "MOE_DISPATCH_NOALLOC_MAX_WORKSPACE",
+           "MOE_DISPATCH_NOALLOC_MAX_WORKSPACE", "MOE_W4_GROUP", "MOE_DECODE_MAX_TOKENS", "moe_w4_shapes",
+           "moe_w4_codes_bytes", "moe_w4_scales_bytes", "moe_quantize_w4", "moe_dequantize_w4", "moe_expert_mlp_w4",
+           "moe_expert_mlp_w4_workspace_bytes", "moe_layer_decode", "moe_layer_decode_w4",
+           "moe_layer_decode_workspace_bytes",
            "moe_expert_mlp_combine_workspace_bytes", "moe_rows_max", "moe_route_workspace_bytes", "moe_dispatch_workspace_bytes",
            "moe_expert_mlp_workspace_bytes", "moe_status_string", "EXPORTED_SYMBOLS"]
 
@@ -28,6 +31,8 @@ MOE_F32 = 0
 MOE_BF16 = 1
 MOE_FP8_BLOCK = 128  # hidden elements per fp8 block scale
 MOE_DISPATCH_NOALLOC_MAX_WORKSPACE = 4 << 20  # bytes of moe_dispatch_noalloc's static scratch
+MOE_W4_GROUP = 32  # consecutive k of a 4-bit weight row that share a scale
+MOE_DECODE_MAX_TOKENS = 32  # tokens of moe_layer_decode / moe_layer_decode_w4
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
 _LIB_NAME = "libmoe_gfx950.so"
@@ -36,7 +41,9 @@ EXPORTED_SYMBOLS = ("moe_status_string", "moe_rows_max", "moe_route_workspace_by
                     "moe_dispatch_workspace_bytes", "moe_dispatch", "moe_expert_mlp_workspace_bytes",
                     "moe_expert_mlp", "moe_combine", "moe_dispatch_fp8", "moe_expert_mlp_fp8", "moe_combine_send",
                     "moe_combine_recv", "moe_expert_mlp_combine", "moe_expert_mlp_combine_workspace_bytes",
-                    "moe_dispatch_noalloc")
+                    "moe_dispatch_noalloc", "moe_w4_codes_bytes", "moe_w4_scales_bytes", "moe_quantize_w4",
+                    "moe_dequantize_w4", "moe_expert_mlp_w4_workspace_bytes", "moe_expert_mlp_w4",
+                    "moe_layer_decode_workspace_bytes", "moe_layer_decode", "moe_layer_decode_w4")
 
 
 class MoeError(RuntimeError):
@@ -100,6 +107,24 @@ def load_library():
     lib.moe_combine_send.restype = i32
     lib.moe_combine_recv.argtypes = [vp, i32, ctypes.POINTER(_CLayout), vp, vp]
     lib.moe_combine_recv.restype = i32
+    lib.moe_w4_codes_bytes.argtypes = [i64, i32]
+    lib.moe_w4_codes_bytes.restype = sz
+    lib.moe_w4_scales_bytes.argtypes = [i64, i32]
+    lib.moe_w4_scales_bytes.restype = sz
+    lib.moe_quantize_w4.argtypes = [vp, i32, i64, i32, vp, vp, vp]
+    lib.moe_quantize_w4.restype = i32
+    lib.moe_dequantize_w4.argtypes = [vp, vp, i64, i32, vp, i32, vp]
+    lib.moe_dequantize_w4.restype = i32
+    lib.moe_expert_mlp_w4_workspace_bytes.argtypes = [i32, i32, i32, i32, i32, i32]
+    lib.moe_expert_mlp_w4_workspace_bytes.restype = sz
+    lib.moe_expert_mlp_w4.argtypes = [vp, ctypes.POINTER(_CLayout), vp, vp, vp, vp, i32, vp, vp, sz, vp]
+    lib.moe_expert_mlp_w4.restype = i32
+    lib.moe_layer_decode_workspace_bytes.argtypes = [i32, i32, i32, i32, i32, i32]
+    lib.moe_layer_decode_workspace_bytes.restype = sz
+    lib.moe_layer_decode.argtypes = [vp, i32, vp, vp, i64] + [i32] * 7 + [vp] * 7 + [sz, vp]
+    lib.moe_layer_decode.restype = i32
+    lib.moe_layer_decode_w4.argtypes = [vp, vp, vp, i64] + [i32] * 7 + [vp] * 9 + [sz, vp]
+    lib.moe_layer_decode_w4.restype = i32
     _lib = lib
     return lib
 
@@ -177,6 +202,30 @@ def moe_expert_mlp_workspace_bytes(T: int, k: int, E: int, R: int, C: int, F: in
 
 def moe_expert_mlp_combine_workspace_bytes(T: int, k: int, E: int, R: int, C: int, H: int, F: int, xdt: int) -> int:
     return int(load_library().moe_expert_mlp_combine_workspace_bytes(T, k, E, R, C, H, F, xdt))
+
+
+def moe_w4_codes_bytes(rows: int, K: int) -> int:
+    return int(load_library().moe_w4_codes_bytes(rows, K))
+
+
+def moe_w4_scales_bytes(rows: int, K: int) -> int:
+    return int(load_library().moe_w4_scales_bytes(rows, K))
+
+
+def moe_w4_shapes(*shape: int) -> tuple:
+    """Shapes of the packed codes and scales (uint8) of weights [.., N, K]."""
+    *lead, N, K = shape
+    if N % 16 or K % MOE_W4_GROUP:
+        raise MoeError(f"4-bit weights need N % 16 == 0 and K % {MOE_W4_GROUP} == 0, got [{N}, {K}]")
+    return (*lead, N // 16, -(-K // 128), 1024), (*lead, N // 16, -(-K // 512), 256)
+
+
+def moe_expert_mlp_w4_workspace_bytes(T: int, k: int, E: int, R: int, C: int, F: int) -> int:
+    return int(load_library().moe_expert_mlp_w4_workspace_bytes(T, k, E, R, C, F))
+
+
+def moe_layer_decode_workspace_bytes(T: int, H: int, E: int, k: int, F: int, xdt: int) -> int:
+    return int(load_library().moe_layer_decode_workspace_bytes(T, H, E, k, F, xdt))
 
 
 # ------------------------------------------------------------------------------------------------
@@ -415,3 +464,115 @@ def moe_expert_mlp_fp8(send_q: torch.Tensor, send_scale: torch.Tensor, layout: L
         _ptr(w_down, "w_down"), F, _ptr(out_buf, "out_buf"), _ptr(ws, "workspace"), _nbytes(ws),
         _stream(stream))
     _check(st, "moe_expert_mlp_fp8")
+
+
+# ------------------------------------------------------------------------------------------------
+# 4-bit expert weights
+# ------------------------------------------------------------------------------------------------
+
+def _w4_ptrs(codes: torch.Tensor, scales: torch.Tensor, shape, name: str, device):
+    cs, ss = moe_w4_shapes(*shape)
+    return (_ptr(codes, f"{name} codes", torch.uint8, cs, device),
+            _ptr(scales, f"{name} scales", torch.uint8, ss, device))
+
+
+def moe_quantize_w4(w: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor, stream=None) -> None:
+    """Weights [.., N, K] (f32 or bf16) to packed 4-bit codes and scales of the shapes moe_w4_shapes(*w.shape)."""
+    dev = w.device
+    pc, ps = _w4_ptrs(codes, scales, w.shape, "w", dev)
+    K = w.shape[-1]
+    st = load_library().moe_quantize_w4(_ptr(w, "w", device=dev), _dtype_code(w), w.numel() // K if K else 0, K, pc, ps,
+                                        _stream(stream))
+    _check(st, "moe_quantize_w4")
+
+
+def moe_dequantize_w4(codes: torch.Tensor, scales: torch.Tensor, w: torch.Tensor, stream=None) -> None:
+    """The values packed codes and scales stand for, into w [.., N, K] (f32 or bf16, both exact)."""
+    dev = w.device
+    pc, ps = _w4_ptrs(codes, scales, w.shape, "w", dev)
+    K = w.shape[-1]
+    st = load_library().moe_dequantize_w4(pc, ps, w.numel() // K if K else 0, K, _ptr(w, "w", device=dev),
+                                          _dtype_code(w), _stream(stream))
+    _check(st, "moe_dequantize_w4")
+
+
+def moe_expert_mlp_w4(send_buf: torch.Tensor, layout: Layout, gu_codes: torch.Tensor, gu_scales: torch.Tensor,
+                      dn_codes: torch.Tensor, dn_scales: torch.Tensor, out_buf: torch.Tensor,
+                      workspace: Optional[torch.Tensor] = None, stream=None) -> None:
+    """Expert SwiGLU MLP on dispatched bf16 rows with packed 4-bit weights ([El, 2F, H] and [El, H, F])."""
+    dev = send_buf.device
+    L = layout
+    El = L.E // L.R
+    F = gu_codes.shape[1] * 8
+    _ptr(send_buf, "send_buf", torch.bfloat16, (L.rows_max, L.H), dev)
+    gc, gs = _w4_ptrs(gu_codes, gu_scales, (El, 2 * F, L.H), "gate/up", dev)
+    dc, ds = _w4_ptrs(dn_codes, dn_scales, (El, L.H, F), "down", dev)
+    _ptr(out_buf, "out_buf", torch.bfloat16, (L.rows_max, L.H), dev)
+    ws = _workspace(moe_expert_mlp_w4_workspace_bytes(L.T, L.k, L.E, L.R, L.C, F), workspace, dev, stream)
+    cl = L.c_struct()
+    st = load_library().moe_expert_mlp_w4(
+        _ptr(send_buf, "send_buf"), ctypes.byref(cl), gc, gs, dc, ds, F, _ptr(out_buf, "out_buf"),
+        _ptr(ws, "workspace"), _nbytes(ws), _stream(stream))
+    _check(st, "moe_expert_mlp_w4")
+
+
+# ------------------------------------------------------------------------------------------------
+# the whole layer for a few tokens
+# ------------------------------------------------------------------------------------------------
+
+def _decode_outputs(x, w_router, logit_bias, k, logits, topk_ids, topk_w, y):
+    """Checks shared by the two calls; returns (T, H, E, bias row stride)."""
+    T, H = x.shape
+    E = w_router.shape[0]
+    dev = x.device
+    stride = 0
+    if logit_bias is not None:
+        stride = 0 if logit_bias.dim() == 1 else E
+        _ptr(logit_bias, "logit_bias", torch.float32, (T, E) if stride else (E,), dev)
+    _ptr(x, "x", device=dev)
+    _ptr(w_router, "w_router", torch.float32, (E, H), dev)
+    _ptr(logits, "logits", torch.float32, (T, E), dev)
+    _ptr(topk_ids, "topk_ids", torch.int32, (T, k), dev)
+    _ptr(topk_w, "topk_w", torch.float32, (T, k), dev)
+    _ptr(y, "y", x.dtype, (T, H), dev)
+    return T, H, E, stride
+
+
+def moe_layer_decode(x: torch.Tensor, w_router: torch.Tensor, logit_bias: Optional[torch.Tensor], k: int, R: int,
+                     C: int, w_gate_up: torch.Tensor, w_down: torch.Tensor, logits: torch.Tensor,
+                     topk_ids: torch.Tensor, topk_w: torch.Tensor, y: torch.Tensor,
+                     workspace: Optional[torch.Tensor] = None, stream=None) -> None:
+    """The whole layer (route, dispatch with capacity C, expert MLP, combine) for at most MOE_DECODE_MAX_TOKENS
+    tokens: writes logits, topk_ids, topk_w and y."""
+    T, H, E, stride = _decode_outputs(x, w_router, logit_bias, k, logits, topk_ids, topk_w, y)
+    dev, dt = x.device, _dtype_code(x)
+    F = w_gate_up.shape[1] // 2
+    El = E // R if R > 0 else 0
+    _ptr(w_gate_up, "w_gate_up", x.dtype, (El, 2 * F, H), dev)
+    _ptr(w_down, "w_down", x.dtype, (El, H, F), dev)
+    ws = _workspace(moe_layer_decode_workspace_bytes(T, H, E, k, F, dt), workspace, dev, stream)
+    st = load_library().moe_layer_decode(
+        _ptr(x, "x"), dt, _ptr(w_router, "w_router"), _ptr(logit_bias, "logit_bias"), stride, T, H, E, R, k, C, F,
+        _ptr(w_gate_up, "w_gate_up"), _ptr(w_down, "w_down"), _ptr(logits, "logits"), _ptr(topk_ids, "topk_ids"),
+        _ptr(topk_w, "topk_w"), _ptr(y, "y"), _ptr(ws, "workspace"), _nbytes(ws), _stream(stream))
+    _check(st, "moe_layer_decode")
+
+
+def moe_layer_decode_w4(x: torch.Tensor, w_router: torch.Tensor, logit_bias: Optional[torch.Tensor], k: int, R: int,
+                        C: int, gu_codes: torch.Tensor, gu_scales: torch.Tensor, dn_codes: torch.Tensor,
+                        dn_scales: torch.Tensor, logits: torch.Tensor, topk_ids: torch.Tensor, topk_w: torch.Tensor,
+                        y: torch.Tensor, workspace: Optional[torch.Tensor] = None, stream=None) -> None:
+    """moe_layer_decode with packed 4-bit expert weights ([El, 2F, H] and [El, H, F]) and bf16 activations."""
+    T, H, E, stride = _decode_outputs(x, w_router, logit_bias, k, logits, topk_ids, topk_w, y)
+    dev = x.device
+    _ptr(x, "x", torch.bfloat16)
+    F = gu_codes.shape[1] * 8
+    El = E // R if R > 0 else 0
+    gc, gs = _w4_ptrs(gu_codes, gu_scales, (El, 2 * F, H), "gate/up", dev)
+    dc, ds = _w4_ptrs(dn_codes, dn_scales, (El, H, F), "down", dev)
+    ws = _workspace(moe_layer_decode_workspace_bytes(T, H, E, k, F, MOE_BF16), workspace, dev, stream)
+    st = load_library().moe_layer_decode_w4(
+        _ptr(x, "x"), _ptr(w_router, "w_router"), _ptr(logit_bias, "logit_bias"), stride, T, H, E, R, k, C, F,
+        gc, gs, dc, ds, _ptr(logits, "logits"), _ptr(topk_ids, "topk_ids"), _ptr(topk_w, "topk_w"), _ptr(y, "y"),
+        _ptr(ws, "workspace"), _nbytes(ws), _stream(stream))
+    _check(st, "moe_layer_decode_w4")

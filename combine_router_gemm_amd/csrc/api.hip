@@ -328,4 +328,119 @@ int moe_combine_recv(const void* partial, moe_dtype_t xdt, const moe_layout_t* l
   return hip_status(moe::launch_combine_recv(partial, xdt == MOE_BF16, L, y, stream));
 }
 
+size_t moe_w4_codes_bytes(int64_t rows, int K) {
+  if (rows <= 0 || K <= 0 || rows % 16 != 0 || K % MOE_W4_GROUP != 0) return 0;
+  return (size_t)(rows / 16) * (size_t)moe::ceil_div_host(K, 128) * 1024;
+}
+
+size_t moe_w4_scales_bytes(int64_t rows, int K) {
+  if (rows <= 0 || K <= 0 || rows % 16 != 0 || K % MOE_W4_GROUP != 0) return 0;
+  return (size_t)(rows / 16) * (size_t)moe::ceil_div_host(K, 512) * 256;
+}
+
+namespace {
+// Shared by moe_quantize_w4 and moe_dequantize_w4
+int check_w4(const void* w, moe_dtype_t wdt, int64_t rows, int K, const void* codes, const void* scales) {
+  if (!valid_dtype(wdt)) return MOE_ERR_UNSUPPORTED;
+  if (rows < 0 || K < 1) return MOE_ERR_INVALID;
+  if (rows % 16 != 0 || K % MOE_W4_GROUP != 0 || K > INT32_MAX - 512) return MOE_ERR_UNSUPPORTED;
+  if (rows > INT64_MAX / 4 / K) return MOE_ERR_UNSUPPORTED;
+  if (rows > 0 && (!w || !codes || !scales)) return MOE_ERR_INVALID;
+  if (!al16(w) || !al16(codes) || !al16(scales)) return MOE_ERR_INVALID;
+  return MOE_OK;
+}
+}  // namespace
+
+int moe_quantize_w4(const void* w, moe_dtype_t wdt, int64_t rows, int K, uint8_t* codes, uint8_t* scales,
+                    hipStream_t stream) {
+  const int st = check_w4(w, wdt, rows, K, codes, scales);
+  if (st != MOE_OK || rows == 0) return st;
+  return hip_status(moe::launch_quantize_w4(w, wdt == MOE_BF16, rows, K, codes, scales, stream));
+}
+
+int moe_dequantize_w4(const uint8_t* codes, const uint8_t* scales, int64_t rows, int K, void* w, moe_dtype_t wdt,
+                      hipStream_t stream) {
+  const int st = check_w4(w, wdt, rows, K, codes, scales);
+  if (st != MOE_OK || rows == 0) return st;
+  return hip_status(moe::launch_dequantize_w4(codes, scales, rows, K, w, wdt == MOE_BF16, stream));
+}
+
+size_t moe_expert_mlp_w4_workspace_bytes(int T, int k, int E, int R, int C, int F) {
+  if (E <= 0 || R <= 0 || E % R != 0 || F <= 0) return 0;
+  return moe::mlp_w4_workspace_bytes(moe_rows_max(T, k, E, C), E / R, F);
+}
+
+int moe_expert_mlp_w4(const void* send_buf, const moe_layout_t* layout, const uint8_t* gu_codes,
+                      const uint8_t* gu_scales, const uint8_t* dn_codes, const uint8_t* dn_scales, int F,
+                      void* out_buf, void* workspace, size_t workspace_bytes, hipStream_t stream) {
+  const int st = check_layout(layout);
+  if (st != MOE_OK) return st;
+  const moe_layout_t& L = *layout;
+  if (F < 1) return MOE_ERR_INVALID;
+  if (L.H % MOE_W4_GROUP != 0 || F % MOE_W4_GROUP != 0) return MOE_ERR_UNSUPPORTED;
+  if ((int64_t)2 * F > (int64_t)INT32_MAX / 2 || L.H > INT32_MAX / 4) return MOE_ERR_UNSUPPORTED;
+  const int64_t rows = moe_rows_max(L.T, L.k, L.E, L.C);
+  if (!gu_codes || !gu_scales || !dn_codes || !dn_scales) return MOE_ERR_INVALID;
+  if (rows > 0 && (!send_buf || !out_buf)) return MOE_ERR_INVALID;
+  if (!al16(send_buf) || !al16(gu_codes) || !al16(gu_scales) || !al16(dn_codes) || !al16(dn_scales) ||
+      !al16(out_buf) || !al16(workspace))
+    return MOE_ERR_INVALID;
+  if (!workspace || workspace_bytes < moe_expert_mlp_w4_workspace_bytes(L.T, L.k, L.E, L.R, L.C, F))
+    return MOE_ERR_INVALID;
+  return hip_status(moe::launch_expert_mlp_w4(send_buf, L, gu_codes, gu_scales, dn_codes, dn_scales, F, out_buf,
+                                              workspace, device_cus(), stream));
+}
+
+size_t moe_layer_decode_workspace_bytes(int T, int H, int E, int k, int F, moe_dtype_t xdt) {
+  if (T <= 0 || T > MOE_DECODE_MAX_TOKENS || H <= 0 || E <= 0 || k <= 0 || k > MOE_MAX_TOPK || F <= 0 ||
+      !valid_dtype(xdt))
+    return 0;
+  return moe::decode_workspace_bytes(T, k, F);
+}
+
+namespace {
+// Shared by moe_layer_decode and moe_layer_decode_w4 (packed): validation and launch. `unit` divides H and F.
+int layer_decode(moe::DecodeCall& d, moe_dtype_t xdt, bool packed, size_t workspace_bytes, hipStream_t stream) {
+  if (!valid_dtype(xdt)) return MOE_ERR_UNSUPPORTED;
+  if (d.T < 0 || d.H < 1 || d.E < 1 || d.E > MOE_MAX_EXPERTS || d.R < 1 || d.E % d.R != 0 || d.k < 1 ||
+      d.k > MOE_MAX_TOPK || d.k > d.E || d.C < 0 || d.F < 1)
+    return MOE_ERR_INVALID;
+  const int unit = packed ? MOE_W4_GROUP : 8;
+  if (d.T > MOE_DECODE_MAX_TOKENS || d.H % unit != 0 || d.F % unit != 0) return MOE_ERR_UNSUPPORTED;
+  if (d.H > INT32_MAX / 4 || d.F > INT32_MAX / 4) return MOE_ERR_UNSUPPORTED;
+  if (d.bias && d.bias_stride < 0) return MOE_ERR_INVALID;
+  if (d.T == 0) return MOE_OK;
+  if (!d.x || !d.w_router || !d.w_gu || !d.w_dn || (packed && (!d.s_gu || !d.s_dn)) || !d.logits || !d.ids || !d.wts ||
+      !d.y)
+    return MOE_ERR_INVALID;
+  if (!al16(d.x) || !al16(d.w_router) || !al16(d.w_gu) || !al16(d.w_dn) || !al16(d.s_gu) || !al16(d.s_dn) ||
+      !al16(d.y) || !al16(d.workspace) || !al4(d.bias) || !al4(d.logits) || !al4(d.ids) || !al4(d.wts))
+    return MOE_ERR_INVALID;
+  if (!d.workspace || workspace_bytes < moe_layer_decode_workspace_bytes(d.T, d.H, d.E, d.k, d.F, xdt))
+    return MOE_ERR_INVALID;
+  d.bf16 = xdt == MOE_BF16;
+  if (!d.bias) d.bias_stride = 0;
+  return hip_status(moe::launch_layer_decode(d, device_cus(), stream));
+}
+}  // namespace
+
+int moe_layer_decode(const void* x, moe_dtype_t xdt, const float* w_router, const float* logit_bias,
+                     int64_t bias_row_stride, int T, int H, int E, int R, int k, int C, int F,
+                     const void* w_gate_up, const void* w_down, float* logits, int32_t* topk_ids, float* topk_w,
+                     void* y, void* workspace, size_t workspace_bytes, hipStream_t stream) {
+  moe::DecodeCall d{x,      0, w_router, logit_bias, bias_row_stride, T,        H,      E, R,        k, C, F, w_gate_up,
+                    w_down, nullptr, nullptr, logits, topk_ids, topk_w, y, workspace};
+  return layer_decode(d, xdt, false, workspace_bytes, stream);
+}
+
+int moe_layer_decode_w4(const void* x, const float* w_router, const float* logit_bias, int64_t bias_row_stride,
+                        int T, int H, int E, int R, int k, int C, int F, const uint8_t* gu_codes,
+                        const uint8_t* gu_scales, const uint8_t* dn_codes, const uint8_t* dn_scales, float* logits,
+                        int32_t* topk_ids, float* topk_w, void* y, void* workspace, size_t workspace_bytes,
+                        hipStream_t stream) {
+  moe::DecodeCall d{x,        0,         w_router,  logit_bias, bias_row_stride, T,        H,      E, R, k, C, F, gu_codes,
+                    dn_codes, gu_scales, dn_scales, logits,     topk_ids,        topk_w, y, workspace};
+  return layer_decode(d, MOE_BF16, true, workspace_bytes, stream);
+}
+
 }  // extern "C"

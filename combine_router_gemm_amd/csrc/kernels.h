@@ -58,6 +58,9 @@ int mlp_down_cols(const MlpTiles& tiles);
 // whether the variant's GEMM kernels read the plan kernel's output (then it is always launched)
 bool mlp_reads_plan(const MlpTiles& tiles);
 
+// builds the plan (rows and M tiles of BM rows per local expert) and the row map, see mlp_plan_kernel
+void launch_mlp_plan(const moe_layout_t& L, int BM, int* plan, int* perm, hipStream_t stream);
+
 // ---- combine ----
 hipError_t launch_combine(const void* out_buf, int xdt_bf16, const moe_layout_t& L, const float* topk_w, void* y,
                           hipStream_t stream);
@@ -65,5 +68,37 @@ hipError_t launch_combine(const void* out_buf, int xdt_bf16, const moe_layout_t&
 hipError_t launch_combine_send(const void* out_buf, int xdt_bf16, const moe_layout_t& L, const float* topk_w,
                                void* partial, hipStream_t stream);
 hipError_t launch_combine_recv(const void* partial, int xdt_bf16, const moe_layout_t& L, void* y, hipStream_t stream);
+
+// ---- 4-bit weights ----
+hipError_t launch_quantize_w4(const void* w, int bf16, int64_t rows, int K, uint8_t* codes, uint8_t* scales,
+                              hipStream_t stream);
+hipError_t launch_dequantize_w4(const uint8_t* codes, const uint8_t* scales, int64_t rows, int K, void* w, int bf16,
+                                hipStream_t stream);
+
+size_t mlp_w4_workspace_bytes(int64_t rows, int El, int F);
+hipError_t launch_expert_mlp_w4(const void* send_buf, const moe_layout_t& L, const uint8_t* gu_codes,
+                                const uint8_t* gu_scales, const uint8_t* dn_codes, const uint8_t* dn_scales, int F,
+                                void* out_buf, void* workspace, int num_cus, hipStream_t stream);
+
+// ---- the whole layer for a few tokens ----
+struct DecodeCall {
+  const void* x;
+  int bf16;
+  const float* w_router;
+  const float* bias;
+  int64_t bias_stride;
+  int T, H, E, R, k, C, F;
+  const void* w_gu;  // expert weights, or packed codes with their scales
+  const void* w_dn;
+  const uint8_t* s_gu;
+  const uint8_t* s_dn;
+  float* logits;
+  int* ids;
+  float* wts;
+  void* y;
+  void* workspace;
+};
+size_t decode_workspace_bytes(int T, int k, int F);
+hipError_t launch_layer_decode(const DecodeCall& d, int num_cus, hipStream_t stream);
 
 }  // namespace moe

@@ -1932,6 +1932,13 @@ void launch_gemms(const GemmArgs& gu, const GemmArgs& dn, const MlpTiles& tiles,
 }
 }  // namespace
 
+void launch_mlp_plan(const moe_layout_t& L, int BM, int* plan, int* perm, hipStream_t stream) {
+  const int64_t rows_max = moe_rows_max(L.T, L.k, L.E, L.C);
+  const int plan_blocks = (int)(rows_max > 0 ? ceil_div_host64(rows_max, PLAN_ROWS_PER_WG) : 1);
+  mlp_plan_kernel<<<plan_blocks, PLAN_THREADS, 0, stream>>>(L.expert_kept, L.expert_offset, L.E, L.E / L.R, BM, plan,
+                                                            perm);
+}
+
 hipError_t launch_expert_mlp(const void* send_buf, int xdt_bf16, const moe_layout_t& L, const void* w_gate_up,
                              const void* w_down, int F, void* out_buf, int* plan, int* perm, void* hbuf,
                              const MlpTiles& tiles, int num_cus, hipStream_t stream, const float* a_scale,
@@ -1954,11 +1961,7 @@ hipError_t launch_expert_mlp(const void* send_buf, int xdt_bf16, const moe_layou
   // plan's starts from the expert offsets themselves and read rows in send order, with no plan launch
   // (the direct-to-LDS kernels always read the plan kernel's output)
   const bool own_plan = L.R > 1 || mlp_reads_plan(tiles);
-  if (own_plan) {
-    const int plan_blocks = (int)(rows_max > 0 ? ceil_div_host64(rows_max, PLAN_ROWS_PER_WG) : 1);
-    mlp_plan_kernel<<<plan_blocks, PLAN_THREADS, 0, stream>>>(L.expert_kept, L.expert_offset, L.E, El, tiles.BM,
-                                                              plan, perm);
-  }
+  if (own_plan) launch_mlp_plan(L, tiles.BM, plan, perm, stream);
 
   const int64_t max_mtiles = ceil_div_host64(rows_max, tiles.BM) + El;
 

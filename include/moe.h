@@ -8,7 +8,9 @@
  *   moe_expert_mlp -> per-expert SwiGLU MLP over the dispatched rows (grouped bf16 MFMA GEMM)
  *   moe_combine    -> router-weighted sum of each token's expert outputs, back in token order
  *
- * plus an fp8 variant of the dispatch and of the expert MLP (moe_dispatch_fp8, moe_expert_mlp_fp8).
+ * plus an fp8 variant of the dispatch and of the expert MLP (moe_dispatch_fp8, moe_expert_mlp_fp8), an
+ * expert MLP on 4-bit weights (moe_quantize_w4, moe_dequantize_w4, moe_expert_mlp_w4), and the whole layer
+ * for a few tokens in one call (moe_layer_decode, moe_layer_decode_w4).
  *
  * Sources (cited by page title and section):
  *   [EPM] "Efficient and portable mixture-of-experts communication" (Perplexity, 2025)
@@ -310,6 +312,111 @@ int moe_dispatch_fp8(const void* x, moe_dtype_t xdt, const int32_t* topk_ids, co
 int moe_expert_mlp_fp8(const uint8_t* send_q, const float* send_scale, const moe_layout_t* layout,
                        const void* w_gate_up, const void* w_down, int F, void* out_buf, void* workspace,
                        size_t workspace_bytes, hipStream_t stream);
+
+/*
+ * 4-bit expert weights.
+ *   - a row of a weight matrix [N, K] is cut into groups of MOE_W4_GROUP consecutive k; a group has one
+ *     scale byte s standing for 2^(s - 127) (E8M0), each weight one E2M1 code (bit 3 the sign, bits 0..2
+ *     the magnitudes 0, 0.5, 1, 1.5, 2, 3, 4, 6); a code's value is magnitude * 2^(s - 127), exactly a
+ *     bfloat16 and a float32 value for 7 <= s <= 252, the range moe_quantize_w4 writes. What codes stand
+ *     for under other scale bytes is unspecified.
+ *   - quantisation: 2^E with E the smallest integer such that max|w| <= 6 * 2^E over the group, clamped to
+ *     [-120, 125] (E = 0 for an all-zero group); code = w / 2^E rounded to the nearest of the magnitudes,
+ *     ties to the even code, magnitudes above 6 to 6, sign kept for values rounding to zero.
+ *   - packed layout, N % 16 == 0 and K % 32 == 0 (batches of matrices follow one another, [.., N, K]):
+ *     codes  [N/16, ceil(K/128), 1024] bytes. In the tile of row block n/16 and k block k/128, lane
+ *            n%16 + 16 * ((k%128) / 32) owns the 16 bytes from lane * 16 on: its group's 32 codes in k
+ *            order, the even k in a byte's low half. That is what one lane of a wave feeds the matrix unit,
+ *            so a wave reads a tile as one contiguous kilobyte. Codes past K are 0.
+ *     scales [N/16, ceil(K/512), 256] bytes: the same lane owns the 4 bytes from lane * 4 on, one per k
+ *            block of 128 (byte (k%512) / 128). Scale bytes past K are 127.
+ *     Codes and scales are 16-byte aligned.
+ */
+#define MOE_W4_GROUP 32
+
+/* Bytes of the packed codes / scales of `rows` rows of length K (0 unless rows % 16 == 0, K % 32 == 0 and
+ * both are positive). `rows` counts the rows of every matrix of a batch: El * 2F for w_gate_up. */
+size_t moe_w4_codes_bytes(int64_t rows, int K);
+size_t moe_w4_scales_bytes(int64_t rows, int K);
+
+/*
+ * moe_quantize_w4 -- weights to 4-bit codes and scales, packed.
+ *   w       [rows, K] (wdt: MOE_F32 or MOE_BF16), finite (the codes of a group holding an infinity or NaN are
+ *           unspecified)
+ *   codes   moe_w4_codes_bytes(rows, K) bytes (output)
+ *   scales  moe_w4_scales_bytes(rows, K) bytes (output)
+ * Requires rows % 16 == 0 and K % 32 == 0 (else MOE_ERR_UNSUPPORTED); rows == 0 is a no-op.
+ */
+int moe_quantize_w4(const void* w, moe_dtype_t wdt, int64_t rows, int K, uint8_t* codes, uint8_t* scales,
+                    hipStream_t stream);
+
+/*
+ * moe_dequantize_w4 -- the values packed codes and scales stand for, exact.
+ *   codes, scales  as above
+ *   w              [rows, K] (wdt) output
+ */
+int moe_dequantize_w4(const uint8_t* codes, const uint8_t* scales, int64_t rows, int K, void* w, moe_dtype_t wdt,
+                      hipStream_t stream);
+
+/* Bytes of scratch `workspace` moe_expert_mlp_w4 needs for this layout and FFN width. */
+size_t moe_expert_mlp_w4_workspace_bytes(int T, int k, int E, int R, int C, int F);
+
+/*
+ * moe_expert_mlp_w4 -- moe_expert_mlp with 4-bit weights: every weight enters the GEMMs as the bf16 value its
+ * code stands for (exact); everything else is moe_expert_mlp in bf16.
+ *   send_buf   [rows_max, H] bf16 rows written by moe_dispatch
+ *   layout     the layout moe_dispatch filled (expert_kept / expert_offset are read on the device)
+ *   gu_codes, gu_scales  packed [El, 2F, H]: rows 0..F-1 of an expert are Wg, rows F..2F-1 are Wu
+ *   dn_codes, dn_scales  packed [El, H, F]
+ *   out_buf    [rows_max, H] bf16 output, row-aligned with send_buf; rows >= total are left as they were
+ *   workspace  device scratch of at least moe_expert_mlp_w4_workspace_bytes(...) bytes; no contents need
+ *              clearing between calls, and calls that overlap must use separate workspaces
+ * Requires H % 32 == 0 and F % 32 == 0 (else MOE_ERR_UNSUPPORTED).
+ */
+int moe_expert_mlp_w4(const void* send_buf, const moe_layout_t* layout, const uint8_t* gu_codes,
+                      const uint8_t* gu_scales, const uint8_t* dn_codes, const uint8_t* dn_scales, int F,
+                      void* out_buf, void* workspace, size_t workspace_bytes, hipStream_t stream);
+
+/*
+ * moe_layer_decode -- the whole layer (route, dispatch, expert MLP, combine) for at most
+ * MOE_DECODE_MAX_TOKENS tokens in two kernels, with no send buffer and no layout.
+ *   logits, topk_ids, topk_w  as moe_route defines them
+ *   y[t] = sum over kept slots j of topk_w[t,j] * (silu(x Wg[l]^T) * (x Wu[l]^T)) Wd[l]^T with l = e mod El
+ *          for expert e = topk_ids[t,j] (El = E / R); pair (t, j) is kept iff fewer than C earlier tokens
+ *          chose e; a token with every pair dropped gets y[t] = 0
+ *   Sums are fp32 and y is rounded once to xdt. Unlike moe_expert_mlp, which stores h and the expert outputs
+ *   as xdt, bf16 layers keep 16 significant bits of h (two bf16 parts) and fp32 expert outputs, so y is
+ *   nearer the formula than the four calls'. A token's y depends on its own kept experts only: an infinity
+ *   or NaN in an expert's weights or in another token's x does not reach it.
+ *   x            [T, H] activations (xdt)
+ *   w_router     [E, H] fp32; logit_bias, bias_row_stride as for moe_route
+ *   C            per-expert capacity, >= 0 (T: no drop)
+ *   w_gate_up    [El, 2F, H] (xdt), w_down [El, H, F] (xdt), as for moe_expert_mlp
+ *   logits       [T, E] fp32, topk_ids [T, k] int32, topk_w [T, k] fp32, y [T, H] (xdt): outputs
+ *   workspace    device scratch of at least moe_layer_decode_workspace_bytes(T, H, E, k, F, xdt) bytes; no
+ *                contents need clearing between calls, and calls that overlap must use separate workspaces
+ * Requires 0 <= T <= MOE_DECODE_MAX_TOKENS (more is MOE_ERR_UNSUPPORTED: the four calls take it), H % 8 == 0
+ * and F % 8 == 0; T == 0 is a no-op.
+ */
+#define MOE_DECODE_MAX_TOKENS 32
+size_t moe_layer_decode_workspace_bytes(int T, int H, int E, int k, int F, moe_dtype_t xdt);
+int moe_layer_decode(const void* x, moe_dtype_t xdt, const float* w_router, const float* logit_bias,
+                     int64_t bias_row_stride, int T, int H, int E, int R, int k, int C, int F,
+                     const void* w_gate_up, const void* w_down, float* logits, int32_t* topk_ids, float* topk_w,
+                     void* y, void* workspace, size_t workspace_bytes, hipStream_t stream);
+
+/*
+ * moe_layer_decode_w4 -- moe_layer_decode with 4-bit expert weights and bf16 activations: every weight is the
+ * bf16 value its code stands for.
+ *   gu_codes, gu_scales  packed [El, 2F, H], dn_codes, dn_scales packed [El, H, F]
+ *   workspace            moe_layer_decode_workspace_bytes(T, H, E, k, F, MOE_BF16) bytes
+ * Requires H % 32 == 0 and F % 32 == 0 (else MOE_ERR_UNSUPPORTED).
+ */
+int moe_layer_decode_w4(const void* x, const float* w_router, const float* logit_bias, int64_t bias_row_stride,
+                        int T, int H, int E, int R, int k, int C, int F, const uint8_t* gu_codes,
+                        const uint8_t* gu_scales, const uint8_t* dn_codes, const uint8_t* dn_scales, float* logits,
+                        int32_t* topk_ids, float* topk_w, void* y, void* workspace, size_t workspace_bytes,
+                        hipStream_t stream);
 
 #ifdef __cplusplus
 }
