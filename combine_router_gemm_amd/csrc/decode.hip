@@ -6,10 +6,8 @@
 //   y = sum_j w_j h_j Wd^T         decode_down_kernel
 //
 // What bounds it: the bytes of the chosen experts' weights, each read once. The weights are the M operand of the
-// matrix unit (16 output columns per tile) and the tokens its N operand (NB blocks of 16): token t is always column
-// t, so an expert's products of tokens that did not choose it are computed along (the matrix unit has the time) and
-// dropped by a select, never by a multiplication with zero. No row is gathered or scattered and no partial
-// result is added atomically: the down kernel adds a token's experts in expert order in registers.
+// matrix unit (16 output columns per tile) and an expert's tokens its N operand, gathered by the loads. No partial
+// result is added atomically: the down kernel adds a token's experts in expert order.
 #include <algorithm>
 #include <climits>
 #include <type_traits>
@@ -41,7 +39,7 @@ struct DecodeArgs {
   int* ids;             // [T, k]
   float* wts;           // [T, k]
   void* y;              // [T, H]
-  void* h;              // [T * k, F]: fp32, or for bf16 layers the bf16 nearest to h and then [T * k, F] its remainder
+  void* h;              // [T * k, F] by row of Choice: fp32, or for bf16 layers the bf16 nearest to h and then [T * k, F] its remainder
 };
 
 // ------------------------------------------------------------------------------------------------
@@ -99,15 +97,21 @@ __global__ __launch_bounds__(256) void decode_route_kernel(const T* __restrict__
 // ------------------------------------------------------------------------------------------------
 // choice of experts
 // ------------------------------------------------------------------------------------------------
+// The kept pairs by local expert. Two experts of different ranks that share a weight set (e mod El) are one entry,
+// and a token that chose both is one row with the sum of its weights: h and the expert's output are the same.
 struct Choice {
-  int n;                      // experts with a kept pair, ascending
-  int wcnt[DEC_NW];
+  int n;                           // local experts with a row, ascending
   int expert[DEC_PAIRS];
-  uint32_t mask[DEC_PAIRS];   // bit t: token t is kept there
-  uint8_t slot[DEC_PAIRS][MOE_DECODE_MAX_TOKENS];  // its slot
+  uint32_t mask[DEC_PAIRS];        // bit t: token t has a row
+  int row0[DEC_PAIRS + 1];         // its rows (tokens ascending): row0[i] .. row0[i + 1]
+  float w[DEC_PAIRS];              // routing weight of a row
+  uint8_t token[DEC_PAIRS];        // token of a row
+  // scratch
+  int wcnt[DEC_NW], wrow[DEC_NW];
   int ids[DEC_PAIRS];
-  float w[DEC_PAIRS];
-  uint32_t chosen[MOE_MAX_EXPERTS];
+  float pw[DEC_PAIRS];
+  uint32_t chosen[MOE_MAX_EXPERTS];  // tokens of a (global) expert, then those within its capacity
+  uint32_t local[MOE_MAX_EXPERTS];
   uint16_t place[MOE_MAX_EXPERTS];
 };
 
@@ -120,6 +124,8 @@ __device__ __forceinline__ void choose(const DecodeArgs& a, Choice& c, bool writ
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int V = (a.E + 63) / 64;
   c.chosen[tid] = 0;
+  c.local[tid] = 0;
+  if (tid < DEC_PAIRS) c.w[tid] = 0.f;
   __syncthreads();
   for (int t = wave; t < a.T; t += DEC_NW) {
     int key[VMAX];
@@ -165,7 +171,7 @@ __device__ __forceinline__ void choose(const DecodeArgs& a, Choice& c, bool writ
       }
     if (lane < a.k) {
       c.ids[t * a.k + lane] = mine;
-      c.w[t * a.k + lane] = z_mine / sum;
+      c.pw[t * a.k + lane] = z_mine / sum;
       atomicOr(&c.chosen[mine], 1u << t);
       if (write) {
         a.ids[t * a.k + lane] = mine;
@@ -174,27 +180,55 @@ __device__ __forceinline__ void choose(const DecodeArgs& a, Choice& c, bool writ
     }
   }
   __syncthreads();
-  // the first C tokens of every expert; experts with any, in ascending order
-  uint32_t m = tid < a.E ? c.chosen[tid] : 0u;
-  for (int over = __popc(m) - a.C; over > 0; --over) m &= ~(0x80000000u >> __clz(m));
-  const uint64_t b = __ballot(m != 0);
-  if (lane == 0) c.wcnt[wave] = __popcll(b);
+  // the first C tokens of every expert
+  if (tid < a.E) {
+    uint32_t m = c.chosen[tid];
+    for (int over = __popc(m) - a.C; over > 0; --over) m &= ~(0x80000000u >> __clz(m));
+    c.chosen[tid] = m;
+    if (m != 0) atomicOr(&c.local[tid % a.El], m);
+  }
   __syncthreads();
-  int base = 0;
+  // local experts with any, and their rows: exclusive scans over the threads
+  const uint32_t m = tid < a.El ? c.local[tid] : 0u;
+  const uint64_t b = __ballot(m != 0);
+  int rows = __popc(m);
 #pragma unroll
-  for (int w = 0; w < DEC_NW; ++w) base += w < wave ? c.wcnt[w] : 0;
-  if (tid < a.E) c.chosen[tid] = m;
+  for (int off = 1; off < 64; off <<= 1) {
+    const int v = __shfl_up(rows, off, 64);
+    if (lane >= off) rows += v;
+  }
+  if (lane == 63) {
+    c.wcnt[wave] = __popcll(b);
+    c.wrow[wave] = rows;
+  }
+  __syncthreads();
+  int i = __popcll(b & lanemask_lt()), row = rows - __popc(m);
+#pragma unroll
+  for (int w = 0; w < DEC_NW; ++w) {
+    i += w < wave ? c.wcnt[w] : 0;
+    row += w < wave ? c.wrow[w] : 0;
+  }
   if (m != 0) {
-    const int i = base + __popcll(b & lanemask_lt());
     c.expert[i] = tid;
     c.mask[i] = m;
+    c.row0[i] = row;
     c.place[tid] = (uint16_t)i;
   }
-  if (tid == DEC_NTH - 1) c.n = base + __popcll(b);
+  if (tid == DEC_NTH - 1) {  // past the last expert: the totals
+    c.n = i + (m != 0);
+    c.row0[i + (m != 0)] = row + __popc(m);
+  }
   __syncthreads();
-  for (int p = tid; p < a.T * a.k; p += DEC_NTH) {
-    const int e = c.ids[p], t = p / a.k;
-    if ((c.chosen[e] >> t) & 1u) c.slot[c.place[e]][t] = (uint8_t)(p - t * a.k);
+  if (tid < a.T) {
+    for (int j = 0; j < a.k; ++j) {
+      const int e = c.ids[tid * a.k + j];
+      if ((c.chosen[e] >> tid) & 1u) {
+        const int at = c.place[e % a.El];
+        const int r = c.row0[at] + __popc(c.mask[at] & ((1u << tid) - 1u));
+        c.token[r] = (uint8_t)tid;
+        c.w[r] += c.pw[tid * a.k + j];  // a row is one token's: this thread's alone
+      }
+    }
   }
   __syncthreads();
 }
@@ -212,6 +246,13 @@ template <>
 struct DecOp<float> {
   using Op = OpF32;
 };
+
+// Columns (rows of x or h) are read with buffer loads: a lane without one, or past K, reads at an offset beyond the
+// buffer, which the hardware answers with zeros and without a memory request.
+constexpr int DEC_NONE = 0x7fffff00;
+__device__ __forceinline__ u32x4 ld_col(__amdgpu_buffer_rsrc_t r, int off) {
+  return __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(r, off, 0, 0));
+}
 
 constexpr int DEC_PITCH = 128 + 16;  // bytes of a staged weight row: 128 and one vector of padding
 
@@ -249,17 +290,15 @@ struct RowStep {
 #pragma unroll
     for (int q = 0; q < VPF; ++q) f[q] = ld16(p + q * 16);
   }
-  // this lane's fragments of a column (a row of x or h): k = kk * 32 + (lane / 16) * 8 of the step
-  __device__ __forceinline__ static void load_col(u32x4 (&x)[XV], const T* col, int step, int K, int lane) {
-    const u32x4 zero = {0u, 0u, 0u, 0u};
+  // this lane's fragments of a column (a row of x or h, at byte `row` of the buffer): k = kk * 32 + (lane / 16) * 8
+  __device__ __forceinline__ static void load_col(u32x4 (&x)[XV], __amdgpu_buffer_rsrc_t r, int row, int step, int K,
+                                                  int lane) {
 #pragma unroll
     for (int kk = 0; kk < KST; ++kk) {
       const int k = step * STEP + kk * 32 + (lane >> 4) * 8;
+      const int off = row >= 0 && k < K ? row + k * (int)sizeof(T) : DEC_NONE;
 #pragma unroll
-      for (int q = 0; q < VPF; ++q) {
-        const u32x4 v = ld16(col + min(k, K - 8) + q * VN);
-        x[kk * VPF + q] = k < K ? v : zero;
-      }
+      for (int q = 0; q < VPF; ++q) x[kk * VPF + q] = ld_col(r, off + q * 16);
     }
   }
 };
@@ -278,14 +317,12 @@ struct W4Step {
     r.w = ld16_nt(codes + (int64_t)step * W4_CODE_TILE + lane * 16);
     r.s = scales[(step >> 2) * W4_SCALE_TILE + lane * 4 + (step & 3)];
   }
-  __device__ __forceinline__ static void load_col(u32x4 (&x)[XV], const bf16_t* col, int step, int K, int lane) {
-    const u32x4 zero = {0u, 0u, 0u, 0u};
+  __device__ __forceinline__ static void load_col(u32x4 (&x)[XV], __amdgpu_buffer_rsrc_t r, int row, int step, int K,
+                                                  int lane) {
     const int k = step * STEP + (lane >> 4) * 32;
+    const int off = row >= 0 && k < K ? row + k * 2 : DEC_NONE;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const u32x4 v = ld16(col + min(k, K - 32) + 8 * j);
-      x[j] = k < K ? v : zero;
-    }
+    for (int j = 0; j < 4; ++j) x[j] = ld_col(r, off + j * 16);
   }
 };
 
@@ -299,23 +336,25 @@ __device__ __forceinline__ float silu(float g) { return g / (1.0f + expf(-g)); }
 template <typename T, bool W4, int NB>
 struct GateUp {
   using RS = RowStep<T, 2>;
-  static constexpr int PF = W4 ? 3 : 3;  // steps of loads in flight per wave
-  static constexpr int WAVE_LDS = W4 ? 2 * NB * 4 * 64 * 4 : RS::LDS_BYTES;
+  static constexpr int PF = W4 ? (NB == 1 ? 3 : 2) : (NB == 1 ? 3 : 2);  // steps of loads in flight per wave
+  static constexpr int WAVE_LDS = W4 ? 2 * 2 * 4 * 64 * 4 : RS::LDS_BYTES;
   static_assert(WAVE_LDS >= 2 * NB * 4 * 64 * 4, "a wave's sums fit its LDS");
   static constexpr int XV = W4 ? W4Step::XV : RS::XV;
 
   __device__ __forceinline__ static void tile(const DecodeArgs& a, const Choice& c, int i, int ft, unsigned char* smem) {
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int K = a.H, F = a.F, f0 = ft * 16;
-    const int64_t l = c.expert[i] % a.El;
-    const uint32_t mask = c.mask[i];
+    const int64_t l = __builtin_amdgcn_readfirstlane(c.expert[i]);
+    const int row0 = __builtin_amdgcn_readfirstlane(c.row0[i]);
+    const int cnt = __builtin_amdgcn_readfirstlane(c.row0[i + 1]) - row0;
     unsigned char* lds = smem + wave * WAVE_LDS;
-    // columns of tokens elsewhere read a token of this expert (the same cache lines) and are dropped at the end
-    const T* cols[NB];
+    const __amdgpu_buffer_rsrc_t xr =
+        __builtin_amdgcn_make_buffer_rsrc((void*)a.x, (short)0, a.T * K * (int)sizeof(T), 0x00020000);
+    int cols[NB];
 #pragma unroll
     for (int nb = 0; nb < NB; ++nb) {
-      const int t = nb * 16 + (lane & 15);
-      cols[nb] = static_cast<const T*>(a.x) + (int64_t)(((mask >> t) & 1u) ? t : __builtin_ctz(mask)) * K;
+      const int r = nb * 16 + (lane & 15);
+      cols[nb] = r < cnt ? c.token[row0 + r] * K * (int)sizeof(T) : -1;
     }
     f32x4 acc[2][NB];
 #pragma unroll
@@ -337,7 +376,7 @@ struct GateUp {
         W4Step::load(rg[u], gc, gs, s, lane);
         W4Step::load(ru[u], uc, us, s, lane);
 #pragma unroll
-        for (int nb = 0; nb < NB; ++nb) W4Step::load_col(rx[u][nb], reinterpret_cast<const bf16_t*>(cols[nb]), s, K, lane);
+        for (int nb = 0; nb < NB; ++nb) W4Step::load_col(rx[u][nb], xr, cols[nb], s, K, lane);
       };
 #pragma unroll
       for (int u = 0; u < PF; ++u) load(wave + u * DEC_NW, u);
@@ -377,7 +416,7 @@ struct GateUp {
         const int s = min(st, last);
         RS::load(rw[u], rows, s, K, lane);
 #pragma unroll
-        for (int nb = 0; nb < NB; ++nb) RS::load_col(rx[u][nb], cols[nb], s, K, lane);
+        for (int nb = 0; nb < NB; ++nb) RS::load_col(rx[u][nb], xr, cols[nb], s, K, lane);
       };
 #pragma unroll
       for (int u = 0; u < PF; ++u) load(wave + u * DEC_NW, u);
@@ -416,17 +455,17 @@ struct GateUp {
     __syncthreads();
     for (int o = tid; o < NB * 256; o += DEC_NTH) {
       const int ln = o & 63, q = (o >> 6) & 3, nb = o >> 8;
-      const int t = nb * 16 + (ln & 15), f = f0 + (ln >> 4) * 4 + q;
-      if (((mask >> t) & 1u) && f < F) {
+      const int r = nb * 16 + (ln & 15), f = f0 + (ln >> 4) * 4 + q;
+      if (r < cnt && f < F) {
         float g = 0.f, u = 0.f;
 #pragma unroll
         for (int w = 0; w < DEC_NW; ++w) {
-          const float* r = reinterpret_cast<const float*>(smem + w * WAVE_LDS);
-          g += r[(nb * 4 + q) * 64 + ln];
-          u += r[((NB + nb) * 4 + q) * 64 + ln];
+          const float* red_w = reinterpret_cast<const float*>(smem + w * WAVE_LDS);
+          g += red_w[(nb * 4 + q) * 64 + ln];
+          u += red_w[((NB + nb) * 4 + q) * 64 + ln];
         }
         const float h = silu(g) * u;
-        const int64_t at = (int64_t)(t * a.k + c.slot[i][t]) * F + f;
+        const int64_t at = (int64_t)(row0 + r) * F + f;
         if constexpr (sizeof(T) == 2) {
           const bf16_t hi = (bf16_t)h;
           static_cast<bf16_t*>(a.h)[at] = hi;
@@ -440,170 +479,180 @@ struct GateUp {
   }
 };
 
-template <typename T, bool W4, int NB>
-__global__ __launch_bounds__(DEC_NTH) void decode_gate_up_kernel(DecodeArgs a) {
-  using G = GateUp<T, W4, NB>;
+template <typename T, bool W4>
+__global__ __launch_bounds__(DEC_NTH, 4) void decode_gate_up_kernel(DecodeArgs a) {
   __shared__ Choice c;
-  __shared__ __attribute__((aligned(16))) unsigned char smem[DEC_NW * G::WAVE_LDS];
+  __shared__ __attribute__((aligned(16))) unsigned char smem[DEC_NW * GateUp<T, W4, 2>::WAVE_LDS];
   choose(a, c, blockIdx.x == 0);
   const int nft = (a.F + 15) / 16, total = c.n * nft;
-  for (int tile = blockIdx.x; tile < total; tile += gridDim.x) G::tile(a, c, tile / nft, tile % nft, smem);
+  for (int tile = blockIdx.x; tile < total; tile += gridDim.x) {
+    const int i = tile / nft;
+    if (c.row0[i + 1] - c.row0[i] <= 16) GateUp<T, W4, 1>::tile(a, c, i, tile - i * nft, smem);
+    else GateUp<T, W4, 2>::tile(a, c, i, tile - i * nft, smem);
+  }
 }
 
 // ------------------------------------------------------------------------------------------------
 // down and combine
 // ------------------------------------------------------------------------------------------------
 // A tile is 16 columns of y for every token, over all chosen experts. The units (expert, K step), expert by expert,
-// are cut into eight runs, one per wave; where a run passes from an expert to the next the wave multiplies its sums by
-// the tokens' routing weights and adds them up, and the waves' results are added through LDS in wave order.
-// For bf16 layers h has two bf16 parts, hi and lo: h keeps 16 significant bits at the price of a second matrix
-// step, which costs nothing next to the weights' bytes.
-template <typename T, bool W4, int NB>
+// are cut into eight runs, one per wave. Where a run passes from an expert to the next, the wave multiplies its sums
+// by the rows' routing weights and adds them to its tokens' sums in LDS; the waves' sums are added in wave order.
+// For bf16 layers h has two bf16 parts, hi and lo, so it keeps 16 significant bits: a matrix step's 16 columns are
+// the hi parts of eight rows and their lo parts, which are added at the end. f32 layers have 16 rows per step.
+template <typename T, bool W4>
 struct Down {
   using RS = RowStep<T, 1>;
-  static constexpr int PF = W4 ? (NB == 1 ? 3 : 2) : (NB == 1 ? 4 : 3);
-  static constexpr int HP = sizeof(T) == 2 ? 2 : 1;  // parts of h
-  static constexpr int WAVE_LDS = W4 ? NB * 4 * 64 * 4 : RS::LDS_BYTES;
-  static_assert(WAVE_LDS >= NB * 4 * 64 * 4, "a wave's sums fit its LDS");
+  static constexpr int RPB = sizeof(T) == 2 ? 8 : 16;  // rows per block of 16 columns
+  static constexpr int STEP = W4 ? W4Step::STEP : RS::STEP;
   static constexpr int XV = W4 ? W4Step::XV : RS::XV;
+  static constexpr int STAGE = W4 ? 0 : RS::LDS_BYTES;
+  static constexpr int SUMS = MOE_DECODE_MAX_TOKENS * 16 * 4;
+  static constexpr int WAVE_LDS = STAGE + SUMS;
 
-  __device__ __forceinline__ static void tile(const DecodeArgs& a, const Choice& c, int n0, unsigned char* smem) {
-    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  // K steps [s_begin, s_end) of one expert for NB blocks of its rows from row r0 on
+  template <int NB>
+  __device__ __forceinline__ static void run(const DecodeArgs& a, const Choice& c, int i, int r0, int s_begin, int s_end,
+                                             int n0, unsigned char* lds, float* sums) {
+    constexpr int PF = W4 ? (NB > 1 ? 2 : 4) : (NB > 1 ? 3 : 4);  // steps of loads in flight
+    const int lane = threadIdx.x & 63;
     const int K = a.F, H = a.H;
-    constexpr int STEP = W4 ? W4Step::STEP : RS::STEP;
-    const int ns = (K + STEP - 1) / STEP, units = c.n * ns;
-    const int per = (units + DEC_NW - 1) / DEC_NW;
-    const int u_begin = min(units, wave * per), u_end = min(units, u_begin + per);
-    unsigned char* lds = smem + wave * WAVE_LDS;
-    const int64_t lo_off = (int64_t)a.T * a.k * K;
-
-    f32x4 acc[NB], y[NB];
+    const int64_t l = __builtin_amdgcn_readfirstlane(c.expert[i]);
+    const int row0 = __builtin_amdgcn_readfirstlane(c.row0[i]) + r0;
+    const int cnt = __builtin_amdgcn_readfirstlane(c.row0[i + 1]) - row0;
+    const int64_t part = (int64_t)a.T * a.k * K;  // elements of one part of h
+    const __amdgpu_buffer_rsrc_t hr = __builtin_amdgcn_make_buffer_rsrc(
+        (char*)a.h + (int64_t)row0 * K * (int)sizeof(T), (short)0,
+        (int)((sizeof(T) == 2 ? part : 0) + (int64_t)cnt * K) * (int)sizeof(T), 0x00020000);
+    int cols[NB];
 #pragma unroll
-    for (int nb = 0; nb < NB; ++nb) acc[nb] = y[nb] = f32x4{0.f, 0.f, 0.f, 0.f};
-
-    struct Slot {
-      typename RS::Regs row;
-      W4Step::Regs w4;
-      u32x4 x[NB][HP][XV];
-    };
-    Slot buf[PF];
-    int li = ns > 0 ? u_begin / ns : 0, ls = u_begin - li * ns;  // the next unit to load
-    auto load = [&](int u) {
-      const int64_t l = c.expert[li] % a.El;
-      const uint32_t mask = c.mask[li];
+    for (int nb = 0; nb < NB; ++nb) {
+      const int col = lane & 15, r = nb * RPB + col % RPB;
+      cols[nb] = r < cnt ? (r * K + (col >= RPB ? (int)part : 0)) * (int)sizeof(T) : -1;
+    }
+    f32x4 acc[NB];
 #pragma unroll
-      for (int nb = 0; nb < NB; ++nb) {
-        const int tt = nb * 16 + (lane & 15);
-        const int t = ((mask >> tt) & 1u) ? tt : __builtin_ctz(mask);
-        const T* col = static_cast<const T*>(a.h) + (int64_t)(t * a.k + c.slot[li][t]) * K;
+    for (int nb = 0; nb < NB; ++nb) acc[nb] = f32x4{0.f, 0.f, 0.f, 0.f};
+    u32x4 rx[PF][NB][XV];
+    if constexpr (W4) {
+      const int kc = (K + W4_TILE_K - 1) / W4_TILE_K, ks = (K + W4_STILE_K - 1) / W4_STILE_K;
+      const int64_t rb = (l * H + n0) / 16;
+      const uint8_t* wc = static_cast<const uint8_t*>(a.w_dn) + rb * kc * W4_CODE_TILE;
+      const uint8_t* ws = a.s_dn + rb * ks * W4_SCALE_TILE;
+      W4Step::Regs rw[PF];
+      auto load = [&](int st, int u) {
+        const int s = min(st, s_end - 1);
+        W4Step::load(rw[u], wc, ws, s, lane);
 #pragma unroll
-        for (int p = 0; p < HP; ++p) {
-          if constexpr (W4) W4Step::load_col(buf[u].x[nb][p], reinterpret_cast<const bf16_t*>(col + p * lo_off), ls, K, lane);
-          else RS::load_col(buf[u].x[nb][p], col + p * lo_off, ls, K, lane);
-        }
-      }
-      if constexpr (W4) {
-        const int kc = ns, ks = (K + W4_STILE_K - 1) / W4_STILE_K;
-        const int64_t rb = (l * H + n0) / 16;
-        W4Step::load(buf[u].w4, static_cast<const uint8_t*>(a.w_dn) + rb * kc * W4_CODE_TILE,
-                     a.s_dn + rb * ks * W4_SCALE_TILE, ls, lane);
-      } else {
-        const T* rows[2];
+        for (int nb = 0; nb < NB; ++nb) W4Step::load_col(rx[u][nb], hr, cols[nb], s, K, lane);
+      };
 #pragma unroll
-        for (int q = 0; q < 2; ++q)
-          rows[q] = static_cast<const T*>(a.w_dn) + (l * H + min(n0 + q * 8 + (lane >> 3), H - 1)) * K;
-        RS::load(buf[u].row, rows, ls, K, lane);
-      }
-      if (li * ns + ls + 1 < u_end) {  // past the last unit: the same one again
-        if (++ls == ns) {
-          ls = 0;
-          ++li;
-        }
-      }
-    };
-    if (u_begin < u_end) {
-#pragma unroll
-      for (int u = 0; u < PF; ++u) load(u);
-      int ci = u_begin / ns, cs = u_begin - ci * ns;
-      for (int n = u_begin; n < u_end; n += PF) {
+      for (int u = 0; u < PF; ++u) load(s_begin + u, u);
+      for (int s0 = s_begin; s0 < s_end; s0 += PF) {
 #pragma unroll
         for (int u = 0; u < PF; ++u) {
-          if (n + u < u_end) {
-            if constexpr (W4) {
-              const float sc = w4_scale(buf[u].w4.s);
+          if (s0 + u < s_end) {
+            const float sc = w4_scale(rw[u].s);
 #pragma unroll
-              for (int j = 0; j < 4; ++j) {
-                const u32x4 f[1] = {w4_to_bf16(buf[u].w4.w[j], sc)};
-#pragma unroll
-                for (int nb = 0; nb < NB; ++nb)
-#pragma unroll
-                  for (int p = 0; p < HP; ++p) {
-                    const u32x4 b[1] = {buf[u].x[nb][p][j]};
-                    Op16::step(acc[nb], f, b);
-                  }
-              }
-            } else {
-              RS::stage(buf[u].row, lds, cs, K, lane);
-#pragma unroll
-              for (int kk = 0; kk < RS::KST; ++kk) {
-                u32x4 f[RS::VPF];
-                RS::frag(lds, 0, kk, lane, f);
-#pragma unroll
-                for (int nb = 0; nb < NB; ++nb)
-#pragma unroll
-                  for (int p = 0; p < HP; ++p) {
-                    u32x4 b[RS::VPF];
-#pragma unroll
-                    for (int q = 0; q < RS::VPF; ++q) b[q] = buf[u].x[nb][p][kk * RS::VPF + q];
-                    DecOp<T>::Op::step(acc[nb], f, b);
-                  }
-              }
-            }
-            load(u);
-            if (++cs == ns || n + u + 1 == u_end) {
-              const uint32_t mask = c.mask[ci];
+            for (int j = 0; j < 4; ++j) {
+              const u32x4 f[1] = {w4_to_bf16(rw[u].w[j], sc)};
 #pragma unroll
               for (int nb = 0; nb < NB; ++nb) {
-                const int t = nb * 16 + (lane & 15);
-                const bool on = (mask >> t) & 1u;
-                const float w = on ? c.w[t * a.k + c.slot[ci][t]] : 0.f;
-#pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                  y[nb][q] = on ? fmaf(w, acc[nb][q], y[nb][q]) : y[nb][q];
-                  acc[nb][q] = 0.f;
-                }
+                const u32x4 b[1] = {rx[u][nb][j]};
+                Op16::step(acc[nb], f, b);
               }
-              cs = 0;
-              ++ci;
             }
+            load(s0 + u + PF, u);
+          }
+        }
+      }
+    } else {
+      const T* rows[2];
+#pragma unroll
+      for (int q = 0; q < 2; ++q)
+        rows[q] = static_cast<const T*>(a.w_dn) + (l * H + min(n0 + q * 8 + (lane >> 3), H - 1)) * K;
+      typename RS::Regs rw[PF];
+      auto load = [&](int st, int u) {
+        const int s = min(st, s_end - 1);
+        RS::load(rw[u], rows, s, K, lane);
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb) RS::load_col(rx[u][nb], hr, cols[nb], s, K, lane);
+      };
+#pragma unroll
+      for (int u = 0; u < PF; ++u) load(s_begin + u, u);
+      for (int s0 = s_begin; s0 < s_end; s0 += PF) {
+#pragma unroll
+        for (int u = 0; u < PF; ++u) {
+          if (s0 + u < s_end) {
+            RS::stage(rw[u], lds, s0 + u, K, lane);
+#pragma unroll
+            for (int kk = 0; kk < RS::KST; ++kk) {
+              u32x4 f[RS::VPF];
+              RS::frag(lds, 0, kk, lane, f);
+#pragma unroll
+              for (int nb = 0; nb < NB; ++nb) {
+                u32x4 b[RS::VPF];
+#pragma unroll
+                for (int q = 0; q < RS::VPF; ++q) b[q] = rx[u][nb][kk * RS::VPF + q];
+                DecOp<T>::Op::step(acc[nb], f, b);
+              }
+            }
+            load(s0 + u + PF, u);
           }
         }
       }
     }
-    float* red = reinterpret_cast<float*>(lds);
 #pragma unroll
-    for (int nb = 0; nb < NB; ++nb)
+    for (int nb = 0; nb < NB; ++nb) {
+      if constexpr (sizeof(T) == 2) {
 #pragma unroll
-      for (int q = 0; q < 4; ++q) red[(nb * 4 + q) * 64 + lane] = y[nb][q];
+        for (int q = 0; q < 4; ++q) acc[nb][q] += dpp_f32<0x128>(acc[nb][q]);  // row_ror 8: the other part
+      }
+      const int col = lane & 15, r = nb * RPB + col;
+      if (col < RPB && r < cnt) {
+        const float w = c.w[row0 + r];
+        float* y = sums + c.token[row0 + r] * 16 + (lane >> 4) * 4;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) y[q] = fmaf(w, acc[nb][q], y[q]);
+      }
+    }
+  }
+
+  __device__ __forceinline__ static void tile(const DecodeArgs& a, const Choice& c, int n0, unsigned char* smem) {
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int ns = (a.F + STEP - 1) / STEP, units = c.n * ns;
+    const int per = (units + DEC_NW - 1) / DEC_NW;
+    const int u_end = min(units, (wave + 1) * per);
+    unsigned char* lds = smem + wave * WAVE_LDS;
+    float* sums = reinterpret_cast<float*>(lds + STAGE);
+    for (int o = lane; o < a.T * 16; o += 64) sums[o] = 0.f;
+    for (int u = min(units, wave * per); u < u_end;) {
+      const int i = __builtin_amdgcn_readfirstlane(u / ns), s = u - i * ns;
+      const int n = min(ns - s, u_end - u);
+      const int nb = (c.row0[i + 1] - c.row0[i] + RPB - 1) / RPB;
+      // more than two blocks: two at a time, the weights again from L2 (one expert's run is a few KB)
+      if (nb <= 1) run<1>(a, c, i, 0, s, s + n, n0, lds, sums);
+      else
+        for (int r0 = 0; r0 < nb * RPB; r0 += 2 * RPB) run<2>(a, c, i, r0, s, s + n, n0, lds, sums);
+      u += n;
+    }
     __syncthreads();
-    for (int o = tid; o < NB * 256; o += DEC_NTH) {
-      const int r = o & 15, t = o >> 4;  // 16 threads write 16 columns of one token
-      const int nb = t >> 4, q = r & 3, ln = (r >> 2) * 16 + (t & 15);
-      if (t < a.T && n0 + r < H) {
+    for (int o = tid; o < a.T * 16; o += DEC_NTH) {
+      const int r = o & 15, t = o >> 4;
+      if (n0 + r < a.H) {
         float v = 0.f;
 #pragma unroll
-        for (int w = 0; w < DEC_NW; ++w)
-          v += reinterpret_cast<const float*>(smem + w * WAVE_LDS)[(nb * 4 + q) * 64 + ln];
-        static_cast<T*>(a.y)[(int64_t)t * H + n0 + r] = from_f32<T>(v);
+        for (int w = 0; w < DEC_NW; ++w) v += reinterpret_cast<const float*>(smem + w * WAVE_LDS + STAGE)[o];
+        static_cast<T*>(a.y)[(int64_t)t * a.H + n0 + r] = from_f32<T>(v);
       }
     }
     __syncthreads();
   }
 };
 
-template <typename T, bool W4, int NB>
-__global__ __launch_bounds__(DEC_NTH) void decode_down_kernel(DecodeArgs a) {
-  using D = Down<T, W4, NB>;
+template <typename T, bool W4>
+__global__ __launch_bounds__(DEC_NTH, 4) void decode_down_kernel(DecodeArgs a) {
+  using D = Down<T, W4>;
   __shared__ Choice c;
   __shared__ __attribute__((aligned(16))) unsigned char smem[DEC_NW * D::WAVE_LDS];
   choose(a, c, false);
@@ -625,12 +674,11 @@ void launch_route_rows(const T* x, const float* w, const float* bias, int64_t bi
   else go(std::integral_constant<int, 8>{});
 }
 
-template <typename T, bool W4, int NB>
+template <typename T, bool W4>
 void launch_experts(const DecodeArgs& a, int num_cus, hipStream_t stream) {
-  const int pairs = std::min(a.T * a.k, a.E);
-  const int64_t gu = (int64_t)pairs * ((a.F + 15) / 16);
-  decode_gate_up_kernel<T, W4, NB><<<(int)std::min<int64_t>(gu, 2 * num_cus), DEC_NTH, 0, stream>>>(a);
-  decode_down_kernel<T, W4, NB><<<std::min((a.H + 15) / 16, 2 * num_cus), DEC_NTH, 0, stream>>>(a);
+  const int64_t gu = (int64_t)std::min(a.T * a.k, a.El) * ((a.F + 15) / 16);
+  decode_gate_up_kernel<T, W4><<<(int)std::min<int64_t>(gu, 2 * num_cus), DEC_NTH, 0, stream>>>(a);
+  decode_down_kernel<T, W4><<<std::min((a.H + 15) / 16, 2 * num_cus), DEC_NTH, 0, stream>>>(a);
 }
 
 }  // namespace
@@ -660,10 +708,9 @@ hipError_t launch_layer_decode(const DecodeCall& d, int num_cus, hipStream_t str
   a.wts = d.wts;
   a.y = d.y;
   a.h = d.workspace;
-  const bool two = d.T > 16;
-  if (!d.bf16) two ? launch_experts<float, false, 2>(a, num_cus, stream) : launch_experts<float, false, 1>(a, num_cus, stream);
-  else if (d.s_gu) two ? launch_experts<bf16_t, true, 2>(a, num_cus, stream) : launch_experts<bf16_t, true, 1>(a, num_cus, stream);
-  else two ? launch_experts<bf16_t, false, 2>(a, num_cus, stream) : launch_experts<bf16_t, false, 1>(a, num_cus, stream);
+  if (!d.bf16) launch_experts<float, false>(a, num_cus, stream);
+  else if (d.s_gu) launch_experts<bf16_t, true>(a, num_cus, stream);
+  else launch_experts<bf16_t, false>(a, num_cus, stream);
   return hipGetLastError();
 }
 
