@@ -8,7 +8,11 @@
 //   w4_stream_kernel  few rows per expert, bound by the bytes of the codes: every wave streams its own blocks'
 //                     codes through registers, several K steps in flight; the rows' 128-k slices are shared through
 //                     LDS (two buffers, one barrier per step).
+//   w4_tile_kernel    many rows per expert, bound by the matrix units: 256 (or 128) rows x 256 weight rows per tile on
+//                     v_mfma_f32_32x32x16_bf16. Rows go to LDS directly; the codes go from L2 to the registers of
+//                     the wave that multiplies them and never pass LDS, which halves the LDS traffic per product.
 #include <algorithm>
+#include <type_traits>
 
 #include "common.h"
 #include "kernels.h"
@@ -202,6 +206,187 @@ __global__ __launch_bounds__(512) void w4_stream_kernel(W4Args a) {
   }
 }
 
+// ------------------------------------------------------------------------------------------------
+// many rows per expert
+// ------------------------------------------------------------------------------------------------
+template <int N>
+__device__ __forceinline__ void wait_loads() {
+  asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
+}
+
+// BM rows x 256 weight rows per tile; eight waves, 2 (rows) x 4 (weights), each BM / 2 rows x 64 weight rows: the gate
+// and the up rows of 32 columns of h, or 64 down rows. K goes in stages of 64:
+//  - rows: 128 bytes each, straight to LDS, NS slots, three stages ahead. 16-byte chunk c of row r sits at
+//    c ^ ((r >> 1) & 7), so that a fragment read touches every bank once.
+//  - codes: one 16-byte load per lane and 32 weight rows holds a stage (lane % 32 the row, lane / 32 one of its two
+//    scale groups), two stages ahead. Its word j is the fragment of matrix step j, whose k are 8 j on of both
+//    groups; the row fragments follow that order.
+//  - one barrier per stage: it publishes stage s and frees the slot that stage s + NS - 1 is loaded into. Loads past
+//    the last stage are issued too, at offsets that read nothing, so the number in flight is the same at every wait.
+template <int BM, bool GATED>
+__global__ __launch_bounds__(512) void w4_tile_kernel(W4Args a, int a_bytes) {
+  constexpr int NW = 8, WN = 4, S = 32, NS = 4;
+  constexpr int WTM = BM / 2, TM = WTM / S;
+  constexpr int STAGE = BM * 128, XI = BM / 8 / NW;  // bytes of a stage; 1 KB row loads per wave
+  constexpr int OUTC = GATED ? 128 : 256;
+  constexpr int BODY = NS * STAGE > BM * OUTC * 2 ? NS * STAGE : BM * OUTC * 2;
+  constexpr int LOADS = XI + 4;                      // loads per wave and stage: rows, two codes, two scales
+  constexpr int OOB = 0x7ffffff0;
+  // the only LDS object (a second one makes the compiler wait for every load in flight before LDS reads): the
+  // stages, which the output tile reuses, then its destination rows
+  __shared__ __attribute__((aligned(1024))) unsigned char smem[BODY + BM * 4];
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wm = wave / WN, wn = wave % WN;
+  const int fr = lane & 31, fq = lane >> 5;
+  const int K = a.K, nk = (K + 63) / 64;
+  const int kc = (K + W4_TILE_K - 1) / W4_TILE_K, ks = (K + W4_STILE_K - 1) / W4_STILE_K;
+  const int* row_start = a.plan + 2;
+  const int* tile_start = a.plan + 3 + a.El;
+  const int n_tiles = (a.N + OUTC - 1) / OUTC;
+  const Tiles mine = my_tiles(a.plan[0] * n_tiles);
+  const __amdgpu_buffer_rsrc_t a_rsrc = __builtin_amdgcn_make_buffer_rsrc((void*)a.A, (short)0, a_bytes, 0x00020000);
+  for (int tile = mine.begin; tile < mine.end; tile += mine.step) {
+    const int l = find_expert(tile_start, a.El, n_tiles, tile);
+    const int mt_l = tile_start[l + 1] - tile_start[l];
+    const int local = tile - tile_start[l] * n_tiles;
+    const int nt = local / mt_l, mt = local % mt_l;
+    const int p0 = row_start[l] + mt * BM, m_rows = min(BM, row_start[l + 1] - p0);
+    // the two 32-row weight blocks (N % 32 == 0: a block is whole or past N, then it repeats the first rows)
+    const int c0 = nt * OUTC + wn * (GATED ? 32 : 64);
+    const bool on[2] = {c0 < a.N, GATED ? c0 < a.N : c0 + 32 < a.N};
+    const uint8_t* wc[2];
+    const uint8_t* ws[2];
+#pragma unroll
+    for (int b = 0; b < 2; ++b) {
+      const int64_t row = (int64_t)l * a.w_rows + (on[b] ? c0 + b * (GATED ? a.up : 32) : 0) + fr;
+      wc[b] = a.codes + (row >> 4) * kc * W4_CODE_TILE + (fr & 15) * 16 + fq * 256;
+      ws[b] = a.scales + (row >> 4) * ks * W4_SCALE_TILE + ((fr & 15) + 16 * fq) * 4;
+    }
+    int voff[XI];
+#pragma unroll
+    for (int q = 0; q < XI; ++q) {
+      const int r = (wave * XI + q) * 8 + (lane >> 3);
+      const int p = p0 + min(r, m_rows - 1);
+      voff[q] = a.a_perm ? a.a_perm[p] : p;
+    }
+#pragma unroll
+    for (int q = 0; q < XI; ++q) {
+      const int r = (wave * XI + q) * 8 + (lane >> 3);
+      voff[q] = r < m_rows ? voff[q] * K * 2 + (((lane & 7) ^ ((r >> 1) & 7)) << 4) : OOB;
+    }
+    auto load_rows = [&](int st) {
+      unsigned char* base = smem + (st % NS) * STAGE + wave * XI * 1024;
+#pragma unroll
+      for (int q = 0; q < XI; ++q) {
+        const int r = (wave * XI + q) * 8 + (lane >> 3);
+        const bool in = st * 64 + (((lane & 7) ^ ((r >> 1) & 7)) << 3) < K;
+        const int vo = in && voff[q] != OOB ? voff[q] + st * 128 : OOB;
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(a_rsrc, (__attribute__((address_space(3))) void*)(base + q * 1024), 16,
+                                                 vo, 0, 0, 0);
+      }
+    };
+    u32x4 cw[2][2];
+    uint32_t cs[2][2];
+    auto load_codes = [&](int st, int u) {
+      const int s = min(st, nk - 1);
+#pragma unroll
+      for (int b = 0; b < 2; ++b) {
+        cw[u][b] = ld16(wc[b] + (int64_t)(s >> 1) * W4_CODE_TILE + (s & 1) * 512);
+        cs[u][b] = ws[b][(s >> 3) * W4_SCALE_TILE + (s & 1) * 128 + ((s >> 1) & 3)];
+      }
+    };
+    f32x16 acc[TM][2];
+#pragma unroll
+    for (int i = 0; i < TM; ++i)
+#pragma unroll
+      for (int b = 0; b < 2; ++b)
+#pragma unroll
+        for (int q = 0; q < 16; ++q) acc[i][b][q] = 0.f;
+    const int mb = min(TM, max(0, (m_rows - wm * WTM + S - 1) / S));  // blocks with rows (wave-uniform)
+
+    wait_loads<0>();
+    lds_barrier();  // the previous tile's output has left LDS
+    // the waits count loads: these groups must be issued in this order
+    auto fence = [] { asm volatile("" ::: "memory"); };
+    load_rows(0);
+    fence();
+    load_rows(1);
+    fence();
+    load_codes(0, 0);
+    fence();
+    load_rows(2);
+    fence();
+    load_codes(1, 1);
+    auto stage = [&](int s, auto U) {
+      constexpr int u = decltype(U)::value;
+      wait_loads<2 * LOADS>();  // stage s has landed: at most its two successors are in flight
+      lds_barrier();
+      load_rows(s + NS - 1);
+      const unsigned char* base = smem + (s % NS) * STAGE + (wm * WTM + fr) * 128;
+      const int sw = (fr >> 1) & 7;
+      u32x4 wf[2][4];
+#pragma unroll
+      for (int b = 0; b < 2; ++b) {
+        const float sc = w4_scale(cs[u][b]);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) wf[b][j] = w4_to_bf16(cw[u][b][j], sc);
+      }
+      load_codes(s + 2, u);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        u32x4 xf[TM];
+#pragma unroll
+        for (int i = 0; i < TM; ++i) xf[i] = ld16(base + i * S * 128 + (((fq * 4 + j) ^ sw) << 4));
+#pragma unroll
+        for (int i = 0; i < TM; ++i)
+          if (i < mb) {
+            const u32x4 b[1] = {xf[i]};
+            const u32x4 w0[1] = {wf[0][j]}, w1[1] = {wf[1][j]};
+            Op32::step(acc[i][0], w0, b);
+            Op32::step(acc[i][1], w1, b);
+          }
+      }
+    };
+    for (int s = 0; s < nk; s += 2) {
+      stage(s, std::integral_constant<int, 0>{});
+      if (s + 1 < nk) stage(s + 1, std::integral_constant<int, 1>{});
+    }
+    // epilogue through LDS: lane l holds row l % 32 of a block and four consecutive columns per group of registers
+    // (Op32::out_row); 16-byte chunk c of output row r sits at c ^ (r & 15)
+    wait_loads<0>();
+    lds_barrier();
+    int* s_orow = reinterpret_cast<int*>(smem + BODY);
+    if (tid < BM) {
+      const int p = p0 + min(tid, m_rows - 1);
+      s_orow[tid] = a.out_perm ? a.out_perm[p] : p;
+    }
+#pragma unroll
+    for (int i = 0; i < TM; ++i) {
+      const int r = wm * WTM + i * S + fr;
+#pragma unroll
+      for (int b = 0; b < (GATED ? 1 : 2); ++b)
+#pragma unroll
+        for (int q4 = 0; q4 < 4; ++q4) {
+          float v[4];
+#pragma unroll
+          for (int q = 0; q < 4; ++q)
+            v[q] = GATED ? silu(acc[i][0][4 * q4 + q]) * acc[i][1][4 * q4 + q] : acc[i][b][4 * q4 + q];
+          const int chunk = (wn * (GATED ? 32 : 64) + b * 32) / 8 + q4;
+          *reinterpret_cast<u32x2*>(smem + r * OUTC * 2 + ((chunk ^ (r & 15)) << 4) + fq * 8) =
+              u32x2{pack2_bf16(v[0], v[1]), pack2_bf16(v[2], v[3])};
+        }
+    }
+    lds_barrier();
+    constexpr int CPO = OUTC / 8;
+    for (int o = tid; o < BM * CPO; o += 512) {
+      const int r = o / CPO, chunk = o % CPO;
+      if (r < m_rows && nt * OUTC + chunk * 8 < a.N)
+        st16(a.Out + (int64_t)s_orow[r] * a.N + nt * OUTC + chunk * 8,
+             ld16(smem + r * OUTC * 2 + ((chunk ^ (r & 15)) << 4)));
+    }
+  }
+}
+
 int w4_grid(int64_t tiles, int64_t most) {
   int64_t g = std::min(tiles, most);
   if (g >= 8) g &= ~7ll;
@@ -214,10 +399,22 @@ void launch_stream(const W4Args& gu, const W4Args& dn, int64_t mtiles, int num_c
   w4_stream_kernel<NB, false, 2><<<w4_grid(mtiles * ceil_div_host(dn.N, 256), 2 * num_cus), 512, 0, stream>>>(dn);
 }
 
-// rows per M tile: the capacity per local expert bounds its rows
-int w4_rows(int64_t rows_max, int El) {
+template <int BM>
+void launch_tiles(const W4Args& gu, const W4Args& dn, int64_t rows, int64_t mtiles, int num_cus, hipStream_t stream) {
+  w4_tile_kernel<BM, true><<<w4_grid(mtiles * ceil_div_host(gu.N, 128), num_cus), 512, 0, stream>>>(
+      gu, (int)(rows * gu.K * 2));
+  w4_tile_kernel<BM, false><<<w4_grid(mtiles * ceil_div_host(dn.N, 256), num_cus), 512, 0, stream>>>(
+      dn, (int)(rows * dn.K * 2));
+}
+
+// rows per M tile: the capacity per local expert bounds its rows. 128 and 256 are the matrix-bound kernel's, which
+// addresses its rows with 31-bit byte offsets.
+int w4_rows(int64_t rows_max, int El, int H, int F) {
   const int64_t per = El > 0 ? ceil_div_host64(rows_max, El) : rows_max;
-  return per <= 16 ? 16 : per <= 32 ? 32 : 64;
+  if (per <= 16) return 16;
+  if (per <= 32) return 32;
+  if (per <= 64 || rows_max * std::max(H, F) * 2 >= 0x7fffff00ll) return 64;
+  return per <= 192 ? 128 : 256;
 }
 
 }  // namespace
@@ -240,7 +437,7 @@ hipError_t launch_expert_mlp_w4(const void* send_buf, const moe_layout_t& L, con
   ws += align256((size_t)rows * sizeof(int));
   bf16_t* h = reinterpret_cast<bf16_t*>(ws);
   const int64_t h_part = (int64_t)(align256((size_t)rows * (size_t)F * 2) / 2);
-  const int bm = w4_rows(rows, El);
+  const int bm = w4_rows(rows, El, L.H, F);
   launch_mlp_plan(L, bm, plan, perm, stream);
   W4Args gu{};
   gu.A = static_cast<const bf16_t*>(send_buf);
@@ -270,7 +467,9 @@ hipError_t launch_expert_mlp_w4(const void* send_buf, const moe_layout_t& L, con
   const int64_t mtiles = ceil_div_host64(rows, bm) + El;
   if (bm == 16) launch_stream<1>(gu, dn, mtiles, num_cus, stream);
   else if (bm == 32) launch_stream<2>(gu, dn, mtiles, num_cus, stream);
-  else launch_stream<4>(gu, dn, mtiles, num_cus, stream);
+  else if (bm == 64) launch_stream<4>(gu, dn, mtiles, num_cus, stream);
+  else if (bm == 128) launch_tiles<128>(gu, dn, rows, mtiles, num_cus, stream);
+  else launch_tiles<256>(gu, dn, rows, mtiles, num_cus, stream);
   return hipGetLastError();
 }
 
