@@ -380,6 +380,7 @@ int moe_expert_mlp_w4(const void* send_buf, const moe_layout_t* layout, const ui
   if (L.H % MOE_W4_GROUP != 0 || F % MOE_W4_GROUP != 0) return MOE_ERR_UNSUPPORTED;
   if ((int64_t)2 * F > (int64_t)INT32_MAX / 2 || L.H > INT32_MAX / 4) return MOE_ERR_UNSUPPORTED;
   const int64_t rows = moe_rows_max(L.T, L.k, L.E, L.C);
+  if (!moe::mlp_w4_fits(rows, L.H, F)) return MOE_ERR_UNSUPPORTED;
   if (!gu_codes || !gu_scales || !dn_codes || !dn_scales) return MOE_ERR_INVALID;
   if (rows > 0 && (!send_buf || !out_buf)) return MOE_ERR_INVALID;
   if (!al16(send_buf) || !al16(gu_codes) || !al16(gu_scales) || !al16(dn_codes) || !al16(dn_scales) ||

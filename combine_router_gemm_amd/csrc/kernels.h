@@ -75,6 +75,8 @@ hipError_t launch_quantize_w4(const void* w, int bf16, int64_t rows, int K, uint
 hipError_t launch_dequantize_w4(const uint8_t* codes, const uint8_t* scales, int64_t rows, int K, void* w, int bf16,
                                 hipStream_t stream);
 
+// rows and both parts of h are read at 31-bit byte offsets
+bool mlp_w4_fits(int64_t rows, int H, int F);
 size_t mlp_w4_workspace_bytes(int64_t rows, int El, int F);
 hipError_t launch_expert_mlp_w4(const void* send_buf, const moe_layout_t& L, const uint8_t* gu_codes,
                                 const uint8_t* gu_scales, const uint8_t* dn_codes, const uint8_t* dn_scales, int F,

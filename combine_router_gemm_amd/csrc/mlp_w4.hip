@@ -5,12 +5,10 @@
 // rows its N operand, so a packed code tile, one contiguous kilobyte, is decoded in registers right into the
 // operand it is (w4.h), and a lane ends up with four consecutive output columns of one row.
 //
-//   w4_stream_kernel  few rows per expert, bound by the bytes of the codes: every wave streams its own blocks'
-//                     codes through registers, several K steps in flight; the rows' 128-k slices are shared through
-//                     LDS (two buffers, one barrier per step).
-//   w4_tile_kernel    many rows per expert, bound by the matrix units: 256 (or 128) rows x 256 weight rows per tile on
-//                     v_mfma_f32_32x32x16_bf16. Rows go to LDS directly; the codes go from L2 to the registers of
-//                     the wave that multiplies them and never pass LDS, which halves the LDS traffic per product.
+//   w4_gemm_kernel  BM rows x 64 WN weight rows per tile on v_mfma_f32_32x32x16_bf16. Rows go to LDS directly; the
+//                   codes go from memory to the registers of the wave that multiplies them and never pass LDS. BM = 32
+//                   and 64 (four waves, several workgroups per CU) stream the codes of experts with few rows and are
+//                   bound by their bytes; BM = 128 and 256 (eight waves) are bound by the matrix units.
 #include <algorithm>
 #include <type_traits>
 
@@ -33,7 +31,7 @@ struct W4Args {
   int w_rows;            // weight rows per expert (2F or H)
   int up;                // weight row of the up half (gate/up only)
   bf16_t* Out;           // [., N]
-  int64_t out_part;      // elements from Out to the second part of h, 0: one rounding
+  int64_t out_part;      // elements from Out to the second part of h
   const int* out_perm;   // destination row of a plan row, or nullptr
   const int* plan;
   int El;
@@ -70,168 +68,36 @@ __device__ __forceinline__ Tiles my_tiles(int total) {
 }
 
 // ------------------------------------------------------------------------------------------------
-// few rows per expert
-// ------------------------------------------------------------------------------------------------
-// NB blocks of 16 rows; 8 waves, each two 16-row weight blocks: the gate and the up rows of the same 16 columns of h
-// (a tile is 128 columns), or two neighbouring blocks of down rows (a tile is 256 columns). HP parts of the rows.
-template <int NB, bool GATED, int HP>
-__global__ __launch_bounds__(512) void w4_stream_kernel(W4Args a) {
-  constexpr int NW = 8, BM = NB * 16, PF = 3;
-  constexpr int COLS = GATED ? NW * 16 : NW * 32;
-  constexpr int PITCH = 256 + 16;               // bytes of a staged row: 128 k and a vector of padding
-  constexpr int XL = (BM * 16 + 511) / 512;     // 16-byte loads per thread, part and step
-  __shared__ __attribute__((aligned(16))) unsigned char s_x[2][HP][BM * PITCH];
-  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int K = a.K, ns = (K + W4_TILE_K - 1) / W4_TILE_K, ks = (K + W4_STILE_K - 1) / W4_STILE_K;
-  const int* row_start = a.plan + 2;
-  const int* tile_start = a.plan + 3 + a.El;
-  const int n_tiles = (a.N + COLS - 1) / COLS;
-  const Tiles mine = my_tiles(a.plan[0] * n_tiles);
-  for (int tile = mine.begin; tile < mine.end; tile += mine.step) {
-    const int l = find_expert(tile_start, a.El, n_tiles, tile);
-    const int mt_l = tile_start[l + 1] - tile_start[l];
-    const int local = tile - tile_start[l] * n_tiles;
-    const int nt = local / mt_l, mt = local % mt_l;
-    const int p0 = row_start[l] + mt * BM, m_rows = min(BM, row_start[l + 1] - p0);
-    // this wave's two weight blocks; blocks past N repeat the first one and are not stored
-    const int c0 = nt * COLS + wave * (GATED ? 16 : 32);
-    const bool on0 = c0 < a.N, on1 = GATED ? on0 : c0 + 16 < a.N;
-    const int64_t base = (int64_t)l * a.w_rows;
-    const int64_t b0 = (base + (on0 ? c0 : 0)) / 16;
-    const int64_t b1 = GATED ? (base + a.up + (on0 ? c0 : 0)) / 16 : (base + (on1 ? c0 + 16 : 0)) / 16;
-    const uint8_t* wc[2] = {a.codes + b0 * ns * W4_CODE_TILE + lane * 16, a.codes + b1 * ns * W4_CODE_TILE + lane * 16};
-    const uint8_t* wsc[2] = {a.scales + b0 * ks * W4_SCALE_TILE + lane * 4, a.scales + b1 * ks * W4_SCALE_TILE + lane * 4};
-    // this thread's rows of the shared slices: vector tid + i * 512 of BM x 16
-    const bf16_t* src[XL];
-#pragma unroll
-    for (int i = 0; i < XL; ++i) {
-      const int r = min((tid + i * 512) >> 4, m_rows - 1);
-      src[i] = a.A + (int64_t)(a.a_perm ? a.a_perm[p0 + r] : p0 + r) * K;
-    }
-    u32x4 rw[PF][2];
-    uint32_t rs[PF][2];
-    u32x4 rx[HP][XL];
-    auto load_w = [&](int st, int u) {
-      const int s = min(st, ns - 1);
-#pragma unroll
-      for (int b = 0; b < 2; ++b) {
-        rw[u][b] = ld16_nt(wc[b] + (int64_t)s * W4_CODE_TILE);
-        rs[u][b] = wsc[b][(s >> 2) * W4_SCALE_TILE + (s & 3)];
-      }
-    };
-    auto load_x = [&](int st) {
-      const int k = min(st, ns - 1) * W4_TILE_K + (tid & 15) * 8;
-#pragma unroll
-      for (int p = 0; p < HP; ++p)
-#pragma unroll
-        for (int i = 0; i < XL; ++i) rx[p][i] = ld16(src[i] + p * a.part + min(k, K - 8));
-    };
-    auto store_x = [&](int st) {
-      const u32x4 zero = {0u, 0u, 0u, 0u};
-      const bool in = st * W4_TILE_K + (tid & 15) * 8 < K;
-#pragma unroll
-      for (int p = 0; p < HP; ++p)
-#pragma unroll
-        for (int i = 0; i < XL; ++i) {
-          const int r = (tid + i * 512) >> 4;
-          if (BM * 16 % 512 == 0 || r < BM) st16(s_x[st & 1][p] + r * PITCH + (tid & 15) * 16, in ? rx[p][i] : zero);
-        }
-    };
-    f32x4 acc[2][NB];
-#pragma unroll
-    for (int b = 0; b < 2; ++b)
-#pragma unroll
-      for (int nb = 0; nb < NB; ++nb) acc[b][nb] = f32x4{0.f, 0.f, 0.f, 0.f};
-    load_x(0);
-#pragma unroll
-    for (int u = 0; u < PF; ++u) load_w(u, u);
-    store_x(0);
-    load_x(1);
-    lds_barrier();
-    for (int s0 = 0; s0 < ns; s0 += PF) {
-#pragma unroll
-      for (int u = 0; u < PF; ++u) {
-        const int st = s0 + u;
-        if (st < ns) {
-          const float sc0 = w4_scale(rs[u][0]), sc1 = w4_scale(rs[u][1]);
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const u32x4 f0[1] = {w4_to_bf16(rw[u][0][j], sc0)}, f1[1] = {w4_to_bf16(rw[u][1][j], sc1)};
-#pragma unroll
-            for (int p = 0; p < HP; ++p)
-#pragma unroll
-              for (int nb = 0; nb < NB; ++nb) {
-                const u32x4 b[1] = {ld16(s_x[st & 1][p] + (nb * 16 + (lane & 15)) * PITCH + (lane >> 4) * 64 + j * 16)};
-                Op16::step(acc[0][nb], f0, b);
-                Op16::step(acc[1][nb], f1, b);
-              }
-          }
-          load_w(st + PF, u);
-          if (st + 1 < ns) {
-            store_x(st + 1);
-            load_x(st + 2);
-          }
-          lds_barrier();
-        }
-      }
-    }
-#pragma unroll
-    for (int nb = 0; nb < NB; ++nb) {
-      const int r = nb * 16 + (lane & 15);
-      if (r < m_rows) {
-        const int64_t orow = a.out_perm ? a.out_perm[p0 + r] : p0 + r;
-        const int q0 = (lane >> 4) * 4;
-        if constexpr (GATED) {
-          if (on0) {
-            float h[4], rest[4];
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-              h[q] = silu(acc[0][nb][q]) * acc[1][nb][q];
-              rest[q] = h[q] - (float)(bf16_t)h[q];
-            }
-            bf16_t* o = a.Out + orow * a.N + c0 + q0;
-            *reinterpret_cast<u32x2*>(o) = u32x2{pack2_bf16(h[0], h[1]), pack2_bf16(h[2], h[3])};
-            if (a.out_part != 0)
-              *reinterpret_cast<u32x2*>(o + a.out_part) = u32x2{pack2_bf16(rest[0], rest[1]), pack2_bf16(rest[2], rest[3])};
-          }
-        } else {
-#pragma unroll
-          for (int b = 0; b < 2; ++b)
-            if (b ? on1 : on0)
-              *reinterpret_cast<u32x2*>(a.Out + orow * a.N + c0 + b * 16 + q0) =
-                  u32x2{pack2_bf16(acc[b][nb][0], acc[b][nb][1]), pack2_bf16(acc[b][nb][2], acc[b][nb][3])};
-        }
-      }
-    }
-  }
-}
-
-// ------------------------------------------------------------------------------------------------
-// many rows per expert
+// the GEMM
 // ------------------------------------------------------------------------------------------------
 template <int N>
 __device__ __forceinline__ void wait_loads() {
   asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
 }
 
-// BM rows x 256 weight rows per tile; eight waves, 2 (rows) x 4 (weights), each BM / 2 rows x 64 weight rows: the gate
-// and the up rows of 32 columns of h, or 64 down rows. K goes in stages of 64:
-//  - rows: 128 bytes each, straight to LDS, NS slots, three stages ahead. 16-byte chunk c of row r sits at
+// BM rows x 64 WN weight rows per tile; WM x WN waves, each BM / WM rows x 64 weight rows: the gate and the up rows of 32
+// columns of h, or 64 down rows. K goes in stages of 64:
+//  - rows: 128 bytes each, straight to LDS, NS slots, NS - 1 stages ahead. 16-byte chunk c of row r sits at
 //    c ^ ((r >> 1) & 7), so that a fragment read touches every bank once.
 //  - codes: one 16-byte load per lane and 32 weight rows holds a stage (lane % 32 the row, lane / 32 one of its two
 //    scale groups), two stages ahead. Its word j is the fragment of matrix step j, whose k are 8 j on of both
 //    groups; the row fragments follow that order.
 //  - one barrier per stage: it publishes stage s and frees the slot that stage s + NS - 1 is loaded into. Loads past
 //    the last stage are issued too, at offsets that read nothing, so the number in flight is the same at every wait.
-template <int BM, bool GATED>
-__global__ __launch_bounds__(512) void w4_tile_kernel(W4Args a, int a_bytes) {
-  constexpr int NW = 8, WN = 4, S = 32, NS = 4;
-  constexpr int WTM = BM / 2, TM = WTM / S;
-  constexpr int STAGE = BM * 128, XI = BM / 8 / NW;  // bytes of a stage; 1 KB row loads per wave
-  constexpr int OUTC = GATED ? 128 : 256;
-  constexpr int BODY = NS * STAGE > BM * OUTC * 2 ? NS * STAGE : BM * OUTC * 2;
-  constexpr int LOADS = XI + 4;                      // loads per wave and stage: rows, two codes, two scales
+// PARTS: h has two bf16 parts (16 significant bits) where few rows make the weights' bytes the bound, so that the
+// down pass's doubled matrix work is free, and one where the matrix units are the bound.
+template <int BM, int WM, int WN, bool GATED, int PARTS>
+__global__ __launch_bounds__(WM * WN * 64) void w4_gemm_kernel(W4Args a, int a_bytes) {
+  constexpr int NW = WM * WN, NTH = NW * 64, S = 32, NS = 4;
+  constexpr int WTM = BM / WM, TM = WTM / S;
+  constexpr int XP = GATED ? 1 : PARTS, OP = GATED ? PARTS : 1;  // parts of the rows read and written
+  constexpr int STAGE = XP * BM * 128, XI = XP * BM / 8 / NW;    // bytes of a stage; 1 KB row loads per wave
+  constexpr int OUTC = WN * (GATED ? 32 : 64);
+  constexpr int OUT_BYTES = BM * OUTC * 2;
+  constexpr int BODY = NS * STAGE > OP * OUT_BYTES ? NS * STAGE : OP * OUT_BYTES;
+  constexpr int LOADS = XI + 4;  // loads per wave and stage: rows, two codes, two scales
   constexpr int OOB = 0x7ffffff0;
+  static_assert(TM >= 1 && XP * BM / 8 % NW == 0 && OUTC >= 128, "tile");
   // the only LDS object (a second one makes the compiler wait for every load in flight before LDS reads): the
   // stages, which the output tile reuses, then its destination rows
   __shared__ __attribute__((aligned(1024))) unsigned char smem[BODY + BM * 4];
@@ -262,23 +128,24 @@ __global__ __launch_bounds__(512) void w4_tile_kernel(W4Args a, int a_bytes) {
       wc[b] = a.codes + (row >> 4) * kc * W4_CODE_TILE + (fr & 15) * 16 + fq * 256;
       ws[b] = a.scales + (row >> 4) * ks * W4_SCALE_TILE + ((fr & 15) + 16 * fq) * 4;
     }
+    // this lane's row and 16-byte chunk in each of the wave's row loads
     int voff[XI];
 #pragma unroll
     for (int q = 0; q < XI; ++q) {
-      const int r = (wave * XI + q) * 8 + (lane >> 3);
+      const int r = ((wave * XI + q) * 8 + (lane >> 3)) % BM;
       const int p = p0 + min(r, m_rows - 1);
       voff[q] = a.a_perm ? a.a_perm[p] : p;
     }
 #pragma unroll
     for (int q = 0; q < XI; ++q) {
-      const int r = (wave * XI + q) * 8 + (lane >> 3);
-      voff[q] = r < m_rows ? voff[q] * K * 2 + (((lane & 7) ^ ((r >> 1) & 7)) << 4) : OOB;
+      const int v = (wave * XI + q) * 8 + (lane >> 3), r = v % BM;
+      voff[q] = r < m_rows ? (voff[q] * K + (v >= BM ? (int)a.part : 0)) * 2 + (((lane & 7) ^ ((r >> 1) & 7)) << 4) : OOB;
     }
     auto load_rows = [&](int st) {
       unsigned char* base = smem + (st % NS) * STAGE + wave * XI * 1024;
 #pragma unroll
       for (int q = 0; q < XI; ++q) {
-        const int r = (wave * XI + q) * 8 + (lane >> 3);
+        const int r = ((wave * XI + q) * 8 + (lane >> 3)) % BM;
         const bool in = st * 64 + (((lane & 7) ^ ((r >> 1) & 7)) << 3) < K;
         const int vo = in && voff[q] != OOB ? voff[q] + st * 128 : OOB;
         __builtin_amdgcn_raw_ptr_buffer_load_lds(a_rsrc, (__attribute__((address_space(3))) void*)(base + q * 1024), 16,
@@ -333,19 +200,21 @@ __global__ __launch_bounds__(512) void w4_tile_kernel(W4Args a, int a_bytes) {
       }
       load_codes(s + 2, u);
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        u32x4 xf[TM];
+      for (int j = 0; j < 4; ++j)
 #pragma unroll
-        for (int i = 0; i < TM; ++i) xf[i] = ld16(base + i * S * 128 + (((fq * 4 + j) ^ sw) << 4));
+        for (int p = 0; p < XP; ++p) {
+          u32x4 xf[TM];
 #pragma unroll
-        for (int i = 0; i < TM; ++i)
-          if (i < mb) {
-            const u32x4 b[1] = {xf[i]};
-            const u32x4 w0[1] = {wf[0][j]}, w1[1] = {wf[1][j]};
-            Op32::step(acc[i][0], w0, b);
-            Op32::step(acc[i][1], w1, b);
-          }
-      }
+          for (int i = 0; i < TM; ++i) xf[i] = ld16(base + (p * BM + i * S) * 128 + (((fq * 4 + j) ^ sw) << 4));
+#pragma unroll
+          for (int i = 0; i < TM; ++i)
+            if (i < mb) {
+              const u32x4 b[1] = {xf[i]};
+              const u32x4 w0[1] = {wf[0][j]}, w1[1] = {wf[1][j]};
+              Op32::step(acc[i][0], w0, b);
+              Op32::step(acc[i][1], w1, b);
+            }
+        }
     };
     for (int s = 0; s < nk; s += 2) {
       stage(s, std::integral_constant<int, 0>{});
@@ -356,9 +225,9 @@ __global__ __launch_bounds__(512) void w4_tile_kernel(W4Args a, int a_bytes) {
     wait_loads<0>();
     lds_barrier();
     int* s_orow = reinterpret_cast<int*>(smem + BODY);
-    if (tid < BM) {
-      const int p = p0 + min(tid, m_rows - 1);
-      s_orow[tid] = a.out_perm ? a.out_perm[p] : p;
+    for (int r = tid; r < BM; r += NTH) {
+      const int p = p0 + min(r, m_rows - 1);
+      s_orow[r] = a.out_perm ? a.out_perm[p] : p;
     }
 #pragma unroll
     for (int i = 0; i < TM; ++i) {
@@ -372,17 +241,22 @@ __global__ __launch_bounds__(512) void w4_tile_kernel(W4Args a, int a_bytes) {
           for (int q = 0; q < 4; ++q)
             v[q] = GATED ? silu(acc[i][0][4 * q4 + q]) * acc[i][1][4 * q4 + q] : acc[i][b][4 * q4 + q];
           const int chunk = (wn * (GATED ? 32 : 64) + b * 32) / 8 + q4;
-          *reinterpret_cast<u32x2*>(smem + r * OUTC * 2 + ((chunk ^ (r & 15)) << 4) + fq * 8) =
-              u32x2{pack2_bf16(v[0], v[1]), pack2_bf16(v[2], v[3])};
+          unsigned char* o = smem + r * OUTC * 2 + ((chunk ^ (r & 15)) << 4) + fq * 8;
+          *reinterpret_cast<u32x2*>(o) = u32x2{pack2_bf16(v[0], v[1]), pack2_bf16(v[2], v[3])};
+          if constexpr (OP == 2) {
+#pragma unroll
+            for (int q = 0; q < 4; ++q) v[q] -= (float)(bf16_t)v[q];
+            *reinterpret_cast<u32x2*>(o + OUT_BYTES) = u32x2{pack2_bf16(v[0], v[1]), pack2_bf16(v[2], v[3])};
+          }
         }
     }
     lds_barrier();
     constexpr int CPO = OUTC / 8;
-    for (int o = tid; o < BM * CPO; o += 512) {
-      const int r = o / CPO, chunk = o % CPO;
+    for (int o = tid; o < OP * BM * CPO; o += NTH) {
+      const int v = o / CPO, chunk = o % CPO, r = v % BM, part = v / BM;
       if (r < m_rows && nt * OUTC + chunk * 8 < a.N)
-        st16(a.Out + (int64_t)s_orow[r] * a.N + nt * OUTC + chunk * 8,
-             ld16(smem + r * OUTC * 2 + ((chunk ^ (r & 15)) << 4)));
+        st16(a.Out + (part ? a.out_part : 0) + (int64_t)s_orow[r] * a.N + nt * OUTC + chunk * 8,
+             ld16(smem + part * OUT_BYTES + r * OUTC * 2 + ((chunk ^ (r & 15)) << 4)));
     }
   }
 }
@@ -393,31 +267,26 @@ int w4_grid(int64_t tiles, int64_t most) {
   return (int)std::max<int64_t>(g, 1);
 }
 
-template <int NB>
-void launch_stream(const W4Args& gu, const W4Args& dn, int64_t mtiles, int num_cus, hipStream_t stream) {
-  w4_stream_kernel<NB, true, 1><<<w4_grid(mtiles * ceil_div_host(gu.N, 128), 2 * num_cus), 512, 0, stream>>>(gu);
-  w4_stream_kernel<NB, false, 2><<<w4_grid(mtiles * ceil_div_host(dn.N, 256), 2 * num_cus), 512, 0, stream>>>(dn);
+// workgroups per CU: the LDS of BM = 32 and 64 lets several stay resident
+template <int BM, int WM, int WN, int PARTS>
+void launch_gemms(const W4Args& gu, const W4Args& dn, int64_t rows, int64_t mtiles, int num_cus, hipStream_t stream) {
+  constexpr int PER_CU = WM * WN == 4 ? 4 : 1, NTH = WM * WN * 64;
+  w4_gemm_kernel<BM, WM, WN, true, PARTS>
+      <<<w4_grid(mtiles * ceil_div_host(gu.N, WN * 32), PER_CU * num_cus), NTH, 0, stream>>>(gu, (int)(rows * gu.K * 2));
+  w4_gemm_kernel<BM, WM, WN, false, PARTS>
+      <<<w4_grid(mtiles * ceil_div_host(dn.N, WN * 64), PER_CU * num_cus), NTH, 0, stream>>>(
+          dn, (int)((PARTS == 2 ? dn.part * 2 : 0) + rows * dn.K * 2));
 }
 
-template <int BM>
-void launch_tiles(const W4Args& gu, const W4Args& dn, int64_t rows, int64_t mtiles, int num_cus, hipStream_t stream) {
-  w4_tile_kernel<BM, true><<<w4_grid(mtiles * ceil_div_host(gu.N, 128), num_cus), 512, 0, stream>>>(
-      gu, (int)(rows * gu.K * 2));
-  w4_tile_kernel<BM, false><<<w4_grid(mtiles * ceil_div_host(dn.N, 256), num_cus), 512, 0, stream>>>(
-      dn, (int)(rows * dn.K * 2));
-}
-
-// rows per M tile: the capacity per local expert bounds its rows. 128 and 256 are the matrix-bound kernel's, which
-// addresses its rows with 31-bit byte offsets.
-int w4_rows(int64_t rows_max, int El, int H, int F) {
-  const int64_t per = El > 0 ? ceil_div_host64(rows_max, El) : rows_max;
-  if (per <= 16) return 16;
-  if (per <= 32) return 32;
-  if (per <= 64 || rows_max * std::max(H, F) * 2 >= 0x7fffff00ll) return 64;
-  return per <= 192 ? 128 : 256;
+// rows per M tile: the capacity per local expert bounds its rows
+int w4_rows(int64_t rows_max, int El) {
+  const int64_t per = ceil_div_host64(rows_max, El);
+  return per <= 32 ? 32 : per <= 64 ? 64 : per <= 192 ? 128 : 256;
 }
 
 }  // namespace
+
+bool mlp_w4_fits(int64_t rows, int H, int F) { return rows * std::max<int64_t>(H, 2 * (int64_t)F) * 2 < 0x7ffffe00ll; }
 
 size_t mlp_w4_workspace_bytes(int64_t rows, int El, int F) {
   return align256(mlp_plan_ints(El) * sizeof(int)) + align256((size_t)rows * sizeof(int)) +
@@ -437,7 +306,7 @@ hipError_t launch_expert_mlp_w4(const void* send_buf, const moe_layout_t& L, con
   ws += align256((size_t)rows * sizeof(int));
   bf16_t* h = reinterpret_cast<bf16_t*>(ws);
   const int64_t h_part = (int64_t)(align256((size_t)rows * (size_t)F * 2) / 2);
-  const int bm = w4_rows(rows, El, L.H, F);
+  const int bm = w4_rows(rows, El);
   launch_mlp_plan(L, bm, plan, perm, stream);
   W4Args gu{};
   gu.A = static_cast<const bf16_t*>(send_buf);
@@ -465,11 +334,10 @@ hipError_t launch_expert_mlp_w4(const void* send_buf, const moe_layout_t& L, con
   dn.plan = plan;
   dn.El = El;
   const int64_t mtiles = ceil_div_host64(rows, bm) + El;
-  if (bm == 16) launch_stream<1>(gu, dn, mtiles, num_cus, stream);
-  else if (bm == 32) launch_stream<2>(gu, dn, mtiles, num_cus, stream);
-  else if (bm == 64) launch_stream<4>(gu, dn, mtiles, num_cus, stream);
-  else if (bm == 128) launch_tiles<128>(gu, dn, rows, mtiles, num_cus, stream);
-  else launch_tiles<256>(gu, dn, rows, mtiles, num_cus, stream);
+  if (bm == 32) launch_gemms<32, 1, 4, 2>(gu, dn, rows, mtiles, num_cus, stream);
+  else if (bm == 64) launch_gemms<64, 1, 4, 2>(gu, dn, rows, mtiles, num_cus, stream);
+  else if (bm == 128) launch_gemms<128, 2, 4, 1>(gu, dn, rows, mtiles, num_cus, stream);
+  else launch_gemms<256, 2, 4, 1>(gu, dn, rows, mtiles, num_cus, stream);
   return hipGetLastError();
 }
 
