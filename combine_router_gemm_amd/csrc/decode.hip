@@ -23,10 +23,8 @@ namespace moe {
 
 namespace {
 
-constexpr int DEC_NW = 8;                // waves per workgroup: they split K
-constexpr int DEC_NTH = DEC_NW * 64;
+constexpr int DEC_MAX_NW = 16;  // waves per workgroup, 8 or 16: they split K
 constexpr int DEC_PAIRS = MOE_DECODE_MAX_TOKENS * MOE_MAX_TOPK;
-static_assert(DEC_NTH >= MOE_MAX_EXPERTS, "choose() has a thread per expert");
 
 struct DecodeArgs {
   const void* x;        // [T, H]
@@ -107,7 +105,7 @@ struct Choice {
   float w[DEC_PAIRS];              // routing weight of a row
   uint8_t token[DEC_PAIRS];        // token of a row
   // scratch
-  int wcnt[DEC_NW], wrow[DEC_NW];
+  int wcnt[DEC_MAX_NW], wrow[DEC_MAX_NW];
   int ids[DEC_PAIRS];
   float pw[DEC_PAIRS];
   uint32_t chosen[MOE_MAX_EXPERTS];  // tokens of a (global) expert, then those within its capacity
@@ -119,15 +117,19 @@ struct Choice {
 // lane * V + i in the lane's i-th value; each of the k rounds takes the wave's largest key, the lowest expert among
 // equals (moe_route's rule: -0 == +0, a NaN ranks as -inf). Repeated by every workgroup: it takes about as long as
 // one more dependent launch would, and nothing has to be passed on.
+template <int NW>
 __device__ __forceinline__ void choose(const DecodeArgs& a, Choice& c, bool write) {
   constexpr int VMAX = MOE_MAX_EXPERTS / 64;
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int V = (a.E + 63) / 64;
-  c.chosen[tid] = 0;
-  c.local[tid] = 0;
+  static_assert(NW * 64 >= MOE_MAX_EXPERTS, "a thread per expert");
+  if (tid < MOE_MAX_EXPERTS) {
+    c.chosen[tid] = 0;
+    c.local[tid] = 0;
+  }
   if (tid < DEC_PAIRS) c.w[tid] = 0.f;
   __syncthreads();
-  for (int t = wave; t < a.T; t += DEC_NW) {
+  for (int t = wave; t < a.T; t += NW) {
     int key[VMAX];
 #pragma unroll
     for (int i = 0; i < VMAX; ++i) {
@@ -204,7 +206,7 @@ __device__ __forceinline__ void choose(const DecodeArgs& a, Choice& c, bool writ
   __syncthreads();
   int i = __popcll(b & lanemask_lt()), row = rows - __popc(m);
 #pragma unroll
-  for (int w = 0; w < DEC_NW; ++w) {
+  for (int w = 0; w < NW; ++w) {
     i += w < wave ? c.wcnt[w] : 0;
     row += w < wave ? c.wrow[w] : 0;
   }
@@ -214,7 +216,7 @@ __device__ __forceinline__ void choose(const DecodeArgs& a, Choice& c, bool writ
     c.row0[i] = row;
     c.place[tid] = (uint16_t)i;
   }
-  if (tid == DEC_NTH - 1) {  // past the last expert: the totals
+  if (tid == (NW * 64) - 1) {  // past the last expert: the totals
     c.n = i + (m != 0);
     c.row0[i + (m != 0)] = row + __popc(m);
   }
@@ -303,19 +305,40 @@ struct RowStep {
   }
 };
 
-// Packed 4-bit weights of one 16-row block, 128 k per step: one load is a code tile, and a lane's 16 bytes are the
-// 32 k of one row that share a scale. The word j of them is its fragment of matrix step j, whose k are
-// (lane / 16) * 32 + 8 j on: the columns' fragments follow that order.
+// Packed 4-bit weights of BL 16-row blocks, 128 k per step. One load is a code tile, and a lane's 16 bytes are the 32 k
+// of one row that share a scale. The word j of them is its fragment of matrix step j, whose k are
+// (lane / 16) * 32 + 8 j on: the columns' fragments follow that order. The load path is what these kernels run out of
+// first (it takes as long over a byte per lane as over sixteen), so scales come sixteen bytes per lane, four tiles at
+// a time, through LDS of the wave's own, and several blocks share a column's fragments.
+template <int BL>
 struct W4Step {
   static constexpr int STEP = W4_TILE_K;
   static constexpr int XV = 4;
-  struct Regs {
-    u32x4 w;
-    uint32_t s;
-  };
-  __device__ __forceinline__ static void load(Regs& r, const uint8_t* codes, const uint8_t* scales, int step, int lane) {
-    r.w = ld16_nt(codes + (int64_t)step * W4_CODE_TILE + lane * 16);
-    r.s = scales[(step >> 2) * W4_SCALE_TILE + lane * 4 + (step & 3)];
+  static constexpr int CHUNK = 4;  // scale tiles in LDS: 2048 k
+  static constexpr int LDS_BYTES = BL * CHUNK * W4_SCALE_TILE;
+  // the blocks' tiles: wave-uniform, so that they stay in scalar registers
+  const uint8_t* codes[BL];
+  const uint8_t* scales[BL];
+  __device__ __forceinline__ void block(int b, const void* c, const uint8_t* s, int64_t rb, int K) {
+    codes[b] = static_cast<const uint8_t*>(c) + rb * ((K + W4_TILE_K - 1) / W4_TILE_K) * W4_CODE_TILE;
+    scales[b] = s + rb * ((K + W4_STILE_K - 1) / W4_STILE_K) * W4_SCALE_TILE;
+  }
+  __device__ __forceinline__ void load(u32x4 (&w)[BL], int step, int lane) const {
+#pragma unroll
+    for (int b = 0; b < BL; ++b) w[b] = ld16_nt(codes[b] + (int64_t)step * W4_CODE_TILE + (uint32_t)(lane * 16));
+  }
+  // scale tiles t0 .. t0 + CHUNK - 1 (of ks) to LDS, through registers
+  __device__ __forceinline__ void load_scales(u32x4 (&v)[BL], int t0, int ks, int lane) const {
+#pragma unroll
+    for (int b = 0; b < BL; ++b)
+      v[b] = ld16(scales[b] + (uint32_t)(min(t0 + (lane >> 4), ks - 1) * W4_SCALE_TILE + (lane & 15) * 16));
+  }
+  __device__ __forceinline__ static void store_scales(const u32x4 (&v)[BL], unsigned char* lds, int lane) {
+#pragma unroll
+    for (int b = 0; b < BL; ++b) st16(lds + b * CHUNK * W4_SCALE_TILE + lane * 16, v[b]);
+  }
+  __device__ __forceinline__ static float scale(const unsigned char* lds, int b, int t0, int step, int lane) {
+    return w4_scale(lds[(b * CHUNK + (step >> 2) - t0) * W4_SCALE_TILE + lane * 4 + (step & 3)]);
   }
   __device__ __forceinline__ static void load_col(u32x4 (&x)[XV], __amdgpu_buffer_rsrc_t r, int row, int step, int K,
                                                   int lane) {
@@ -331,19 +354,24 @@ __device__ __forceinline__ float silu(float g) { return g / (1.0f + expf(-g)); }
 // ------------------------------------------------------------------------------------------------
 // gate / up
 // ------------------------------------------------------------------------------------------------
-// A tile is one expert's 16 columns of h. The eight waves take its K steps in turn and add their sums through LDS
-// in wave order.
+// A tile is one expert's 16 columns of h (32 with 4-bit weights). The eight waves split its K and add their sums
+// through LDS in wave order.
 template <typename T, bool W4, int NB>
 struct GateUp {
+  static constexpr int NW = 8, NTH = NW * 64;
+  static constexpr int CB = W4 ? 2 : 1;      // blocks of 16 columns
+  static constexpr int COLS = CB * 16;
   using RS = RowStep<T, 2>;
-  static constexpr int PF = W4 ? (NB == 1 ? 3 : 2) : (NB == 1 ? 3 : 2);  // steps of loads in flight per wave
-  static constexpr int WAVE_LDS = W4 ? 2 * 2 * 4 * 64 * 4 : RS::LDS_BYTES;
-  static_assert(WAVE_LDS >= 2 * NB * 4 * 64 * 4, "a wave's sums fit its LDS");
-  static constexpr int XV = W4 ? W4Step::XV : RS::XV;
+  using WS = W4Step<2 * CB>;
+  static constexpr int PF = W4 ? (NB == 1 ? 2 : 1) : (NB == 1 ? 3 : 2);  // steps of loads in flight per wave
+  static constexpr int RED = 2 * CB * NB * 4 * 64 * 4;
+  static constexpr int STAGE = W4 ? WS::LDS_BYTES : RS::LDS_BYTES;
+  static constexpr int WAVE_LDS = RED > STAGE ? RED : STAGE;
+  static constexpr int XV = W4 ? WS::XV : RS::XV;
 
   __device__ __forceinline__ static void tile(const DecodeArgs& a, const Choice& c, int i, int ft, unsigned char* smem) {
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int K = a.H, F = a.F, f0 = ft * 16;
+    const int K = a.H, F = a.F, f0 = ft * COLS;
     const int64_t l = __builtin_amdgcn_readfirstlane(c.expert[i]);
     const int row0 = __builtin_amdgcn_readfirstlane(c.row0[i]);
     const int cnt = __builtin_amdgcn_readfirstlane(c.row0[i + 1]) - row0;
@@ -356,49 +384,60 @@ struct GateUp {
       const int r = nb * 16 + (lane & 15);
       cols[nb] = r < cnt ? c.token[row0 + r] * K * (int)sizeof(T) : -1;
     }
-    f32x4 acc[2][NB];
+    f32x4 acc[2][CB][NB];  // gate, up
 #pragma unroll
     for (int s = 0; s < 2; ++s)
 #pragma unroll
-      for (int nb = 0; nb < NB; ++nb) acc[s][nb] = f32x4{0.f, 0.f, 0.f, 0.f};
+      for (int cb = 0; cb < CB; ++cb)
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb) acc[s][cb][nb] = f32x4{0.f, 0.f, 0.f, 0.f};
 
     if constexpr (W4) {
       const int kc = (K + W4_TILE_K - 1) / W4_TILE_K, ks = (K + W4_STILE_K - 1) / W4_STILE_K;
-      const int64_t rb = (l * 2 * F + f0) / 16, ub = (l * 2 * F + F + f0) / 16;
-      const uint8_t* wc = static_cast<const uint8_t*>(a.w_gu);
-      const uint8_t *gc = wc + rb * kc * W4_CODE_TILE, *uc = wc + ub * kc * W4_CODE_TILE;
-      const uint8_t *gs = a.s_gu + rb * ks * W4_SCALE_TILE, *us = a.s_gu + ub * ks * W4_SCALE_TILE;
-      W4Step::Regs rg[PF], ru[PF];
-      u32x4 rx[PF][NB][XV];
-      const int last = kc - 1;
+      const int per = (kc + NW - 1) / NW, end = min(kc, (wave + 1) * per);
+      WS ws;
+#pragma unroll
+      for (int b = 0; b < 2 * CB; ++b)
+        ws.block(b, a.w_gu, a.s_gu, (l * 2 * F + (b >= CB ? F : 0) + f0) / 16 + b % CB, K);
+      u32x4 rw[PF][2 * CB], rx[PF][NB][XV];
       auto load = [&](int st, int u) {
-        const int s = min(st, last);
-        W4Step::load(rg[u], gc, gs, s, lane);
-        W4Step::load(ru[u], uc, us, s, lane);
+        const int s = min(st, end - 1);
+        ws.load(rw[u], s, lane);
 #pragma unroll
-        for (int nb = 0; nb < NB; ++nb) W4Step::load_col(rx[u][nb], xr, cols[nb], s, K, lane);
+        for (int nb = 0; nb < NB; ++nb) WS::load_col(rx[u][nb], xr, cols[nb], s, K, lane);
       };
+      for (int s0 = wave * per; s0 < end;) {
+        const int t0 = s0 >> 2, stop = min(end, (t0 + WS::CHUNK) * 4);
+        u32x4 sv[2 * CB];
+        ws.load_scales(sv, t0, ks, lane);
 #pragma unroll
-      for (int u = 0; u < PF; ++u) load(wave + u * DEC_NW, u);
-      for (int s0 = wave; s0 < kc; s0 += PF * DEC_NW) {
+        for (int u = 0; u < PF; ++u) load(s0 + u, u);
+        WS::store_scales(sv, lds, lane);
+        for (; s0 < stop; s0 += PF) {
 #pragma unroll
-        for (int u = 0; u < PF; ++u) {
-          const int st = s0 + u * DEC_NW;
-          if (st < kc) {
-            const float sg = w4_scale(rg[u].s), su = w4_scale(ru[u].s);
+          for (int u = 0; u < PF; ++u) {
+            const int st = s0 + u;
+            if (st < stop) {
+              float sc[2 * CB];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              const u32x4 ag[1] = {w4_to_bf16(rg[u].w[j], sg)}, au[1] = {w4_to_bf16(ru[u].w[j], su)};
+              for (int b = 0; b < 2 * CB; ++b) sc[b] = WS::scale(lds, b, t0, st, lane);
 #pragma unroll
-              for (int nb = 0; nb < NB; ++nb) {
-                const u32x4 b[1] = {rx[u][nb][j]};
-                Op16::step(acc[0][nb], ag, b);
-                Op16::step(acc[1][nb], au, b);
+              for (int j = 0; j < 4; ++j) {
+#pragma unroll
+                for (int b = 0; b < 2 * CB; ++b) {
+                  const u32x4 f[1] = {w4_to_bf16(rw[u][b][j], sc[b])};
+#pragma unroll
+                  for (int nb = 0; nb < NB; ++nb) {
+                    const u32x4 x[1] = {rx[u][nb][j]};
+                    Op16::step(acc[b / CB][b % CB][nb], f, x);
+                  }
+                }
               }
+              load(st + PF, u);
             }
-            load(st + PF * DEC_NW, u);
           }
         }
+        s0 = stop;
       }
     } else {
       using Op = typename DecOp<T>::Op;
@@ -419,11 +458,11 @@ struct GateUp {
         for (int nb = 0; nb < NB; ++nb) RS::load_col(rx[u][nb], xr, cols[nb], s, K, lane);
       };
 #pragma unroll
-      for (int u = 0; u < PF; ++u) load(wave + u * DEC_NW, u);
-      for (int s0 = wave; s0 < ns; s0 += PF * DEC_NW) {
+      for (int u = 0; u < PF; ++u) load(wave + u * NW, u);
+      for (int s0 = wave; s0 < ns; s0 += PF * NW) {
 #pragma unroll
         for (int u = 0; u < PF; ++u) {
-          const int st = s0 + u * DEC_NW;
+          const int st = s0 + u * NW;
           if (st < ns) {
             RS::stage(rw[u], lds, st, K, lane);
 #pragma unroll
@@ -436,11 +475,11 @@ struct GateUp {
                 u32x4 b[RS::VPF];
 #pragma unroll
                 for (int q = 0; q < RS::VPF; ++q) b[q] = rx[u][nb][kk * RS::VPF + q];
-                Op::step(acc[0][nb], fg, b);
-                Op::step(acc[1][nb], fu, b);
+                Op::step(acc[0][0][nb], fg, b);
+                Op::step(acc[1][0][nb], fu, b);
               }
             }
-            load(st + PF * DEC_NW, u);
+            load(st + PF * NW, u);
           }
         }
       }
@@ -449,20 +488,22 @@ struct GateUp {
 #pragma unroll
     for (int s = 0; s < 2; ++s)
 #pragma unroll
-      for (int nb = 0; nb < NB; ++nb)
+      for (int cb = 0; cb < CB; ++cb)
 #pragma unroll
-        for (int q = 0; q < 4; ++q) red[((s * NB + nb) * 4 + q) * 64 + lane] = acc[s][nb][q];
+        for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+          for (int q = 0; q < 4; ++q) red[(((s * CB + cb) * NB + nb) * 4 + q) * 64 + lane] = acc[s][cb][nb][q];
     __syncthreads();
-    for (int o = tid; o < NB * 256; o += DEC_NTH) {
-      const int ln = o & 63, q = (o >> 6) & 3, nb = o >> 8;
-      const int r = nb * 16 + (ln & 15), f = f0 + (ln >> 4) * 4 + q;
+    for (int o = tid; o < CB * NB * 256; o += NTH) {
+      const int ln = o & 63, q = (o >> 6) & 3, nb = (o >> 8) % NB, cb = (o >> 8) / NB;
+      const int r = nb * 16 + (ln & 15), f = f0 + cb * 16 + (ln >> 4) * 4 + q;
       if (r < cnt && f < F) {
         float g = 0.f, u = 0.f;
 #pragma unroll
-        for (int w = 0; w < DEC_NW; ++w) {
+        for (int w = 0; w < NW; ++w) {
           const float* red_w = reinterpret_cast<const float*>(smem + w * WAVE_LDS);
-          g += red_w[(nb * 4 + q) * 64 + ln];
-          u += red_w[((NB + nb) * 4 + q) * 64 + ln];
+          g += red_w[((cb * NB + nb) * 4 + q) * 64 + ln];
+          u += red_w[(((CB + cb) * NB + nb) * 4 + q) * 64 + ln];
         }
         const float h = silu(g) * u;
         const int64_t at = (int64_t)(row0 + r) * F + f;
@@ -480,41 +521,47 @@ struct GateUp {
 };
 
 template <typename T, bool W4>
-__global__ __launch_bounds__(DEC_NTH, 4) void decode_gate_up_kernel(DecodeArgs a) {
+__global__ __launch_bounds__(512, 4) void decode_gate_up_kernel(DecodeArgs a) {
+  using G = GateUp<T, W4, 2>;
   __shared__ Choice c;
-  __shared__ __attribute__((aligned(16))) unsigned char smem[DEC_NW * GateUp<T, W4, 2>::WAVE_LDS];
-  choose(a, c, blockIdx.x == 0);
-  const int nft = (a.F + 15) / 16, total = c.n * nft;
+  __shared__ __attribute__((aligned(16))) unsigned char smem[G::NW * G::WAVE_LDS];
+  choose<G::NW>(a, c, blockIdx.x == 0);
+  const int nft = (a.F + G::COLS - 1) / G::COLS, total = c.n * nft;
   for (int tile = blockIdx.x; tile < total; tile += gridDim.x) {
     const int i = tile / nft;
     if (c.row0[i + 1] - c.row0[i] <= 16) GateUp<T, W4, 1>::tile(a, c, i, tile - i * nft, smem);
-    else GateUp<T, W4, 2>::tile(a, c, i, tile - i * nft, smem);
+    else G::tile(a, c, i, tile - i * nft, smem);
   }
 }
 
 // ------------------------------------------------------------------------------------------------
 // down and combine
 // ------------------------------------------------------------------------------------------------
-// A tile is 16 columns of y for every token, over all chosen experts. The units (expert, K step), expert by expert,
-// are cut into eight runs, one per wave. Where a run passes from an expert to the next, the wave multiplies its sums
-// by the rows' routing weights and adds them to its tokens' sums in LDS; the waves' sums are added in wave order.
-// For bf16 layers h has two bf16 parts, hi and lo, so it keeps 16 significant bits: a matrix step's 16 columns are
-// the hi parts of eight rows and their lo parts, which are added at the end. f32 layers have 16 rows per step.
+// A tile is 16 columns of y (32 with 4-bit weights) for every token, over all chosen experts. The units (expert, K
+// step), expert by expert, are cut into runs, one per wave. Where a run passes from an expert to the next, the wave
+// multiplies its sums by the rows' routing weights and adds them to its tokens' sums in LDS; the waves' sums are added
+// in wave order. For bf16 layers h has two bf16 parts, hi and lo, so it keeps 16 significant bits: a matrix step's 16
+// columns are the hi parts of eight rows and their lo parts, which are added at the end. f32 layers have 16 rows per
+// step. The wider 4-bit tiles are half as many, so they take sixteen waves instead of eight.
 template <typename T, bool W4>
 struct Down {
+  static constexpr int NW = W4 ? 16 : 8, NTH = NW * 64;
+  static constexpr int CB = W4 ? 2 : 1;                // blocks of 16 columns
+  static constexpr int COLS = CB * 16;
   using RS = RowStep<T, 1>;
-  static constexpr int RPB = sizeof(T) == 2 ? 8 : 16;  // rows per block of 16 columns
-  static constexpr int STEP = W4 ? W4Step::STEP : RS::STEP;
-  static constexpr int XV = W4 ? W4Step::XV : RS::XV;
-  static constexpr int STAGE = W4 ? 0 : RS::LDS_BYTES;
-  static constexpr int SUMS = MOE_DECODE_MAX_TOKENS * 16 * 4;
+  using WS = W4Step<CB>;
+  static constexpr int RPB = sizeof(T) == 2 ? 8 : 16;  // rows per block of 16 columns of the matrix step
+  static constexpr int STEP = W4 ? WS::STEP : RS::STEP;
+  static constexpr int XV = W4 ? WS::XV : RS::XV;
+  static constexpr int STAGE = W4 ? WS::LDS_BYTES : RS::LDS_BYTES;
+  static constexpr int SUMS = MOE_DECODE_MAX_TOKENS * COLS * 4;
   static constexpr int WAVE_LDS = STAGE + SUMS;
 
   // K steps [s_begin, s_end) of one expert for NB blocks of its rows from row r0 on
   template <int NB>
   __device__ __forceinline__ static void run(const DecodeArgs& a, const Choice& c, int i, int r0, int s_begin, int s_end,
                                              int n0, unsigned char* lds, float* sums) {
-    constexpr int PF = W4 ? (NB > 1 ? 2 : 4) : (NB > 1 ? 3 : 4);  // steps of loads in flight
+    constexpr int PF = W4 ? (NB > 1 ? 1 : 3) : (NB > 1 ? 3 : 4);  // steps of loads in flight
     const int lane = threadIdx.x & 63;
     const int K = a.F, H = a.H;
     const int64_t l = __builtin_amdgcn_readfirstlane(c.expert[i]);
@@ -530,41 +577,55 @@ struct Down {
       const int col = lane & 15, r = nb * RPB + col % RPB;
       cols[nb] = r < cnt ? (r * K + (col >= RPB ? (int)part : 0)) * (int)sizeof(T) : -1;
     }
-    f32x4 acc[NB];
+    f32x4 acc[CB][NB];
 #pragma unroll
-    for (int nb = 0; nb < NB; ++nb) acc[nb] = f32x4{0.f, 0.f, 0.f, 0.f};
+    for (int cb = 0; cb < CB; ++cb)
+#pragma unroll
+      for (int nb = 0; nb < NB; ++nb) acc[cb][nb] = f32x4{0.f, 0.f, 0.f, 0.f};
     u32x4 rx[PF][NB][XV];
     if constexpr (W4) {
-      const int kc = (K + W4_TILE_K - 1) / W4_TILE_K, ks = (K + W4_STILE_K - 1) / W4_STILE_K;
-      const int64_t rb = (l * H + n0) / 16;
-      const uint8_t* wc = static_cast<const uint8_t*>(a.w_dn) + rb * kc * W4_CODE_TILE;
-      const uint8_t* ws = a.s_dn + rb * ks * W4_SCALE_TILE;
-      W4Step::Regs rw[PF];
+      const int ks = (K + W4_STILE_K - 1) / W4_STILE_K;
+      WS ws;
+#pragma unroll
+      for (int b = 0; b < CB; ++b) ws.block(b, a.w_dn, a.s_dn, (l * H + n0) / 16 + b, K);
+      u32x4 rw[PF][CB];
       auto load = [&](int st, int u) {
         const int s = min(st, s_end - 1);
-        W4Step::load(rw[u], wc, ws, s, lane);
+        ws.load(rw[u], s, lane);
 #pragma unroll
-        for (int nb = 0; nb < NB; ++nb) W4Step::load_col(rx[u][nb], hr, cols[nb], s, K, lane);
+        for (int nb = 0; nb < NB; ++nb) WS::load_col(rx[u][nb], hr, cols[nb], s, K, lane);
       };
+      for (int s0 = s_begin; s0 < s_end;) {
+        const int t0 = s0 >> 2, stop = min(s_end, (t0 + WS::CHUNK) * 4);
+        u32x4 sv[CB];
+        ws.load_scales(sv, t0, ks, lane);
 #pragma unroll
-      for (int u = 0; u < PF; ++u) load(s_begin + u, u);
-      for (int s0 = s_begin; s0 < s_end; s0 += PF) {
+        for (int u = 0; u < PF; ++u) load(s0 + u, u);
+        WS::store_scales(sv, lds, lane);
+        for (; s0 < stop; s0 += PF) {
 #pragma unroll
-        for (int u = 0; u < PF; ++u) {
-          if (s0 + u < s_end) {
-            const float sc = w4_scale(rw[u].s);
+          for (int u = 0; u < PF; ++u) {
+            if (s0 + u < stop) {
+              float sc[CB];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              const u32x4 f[1] = {w4_to_bf16(rw[u].w[j], sc)};
+              for (int b = 0; b < CB; ++b) sc[b] = WS::scale(lds, b, t0, s0 + u, lane);
 #pragma unroll
-              for (int nb = 0; nb < NB; ++nb) {
-                const u32x4 b[1] = {rx[u][nb][j]};
-                Op16::step(acc[nb], f, b);
+              for (int j = 0; j < 4; ++j) {
+#pragma unroll
+                for (int cb = 0; cb < CB; ++cb) {
+                  const u32x4 f[1] = {w4_to_bf16(rw[u][cb][j], sc[cb])};
+#pragma unroll
+                  for (int nb = 0; nb < NB; ++nb) {
+                    const u32x4 b[1] = {rx[u][nb][j]};
+                    Op16::step(acc[cb][nb], f, b);
+                  }
+                }
               }
+              load(s0 + u + PF, u);
             }
-            load(s0 + u + PF, u);
           }
         }
+        s0 = stop;
       }
     } else {
       const T* rows[2];
@@ -594,7 +655,7 @@ struct Down {
                 u32x4 b[RS::VPF];
 #pragma unroll
                 for (int q = 0; q < RS::VPF; ++q) b[q] = rx[u][nb][kk * RS::VPF + q];
-                DecOp<T>::Op::step(acc[nb], f, b);
+                DecOp<T>::Op::step(acc[0][nb], f, b);
               }
             }
             load(s0 + u + PF, u);
@@ -606,14 +667,18 @@ struct Down {
     for (int nb = 0; nb < NB; ++nb) {
       if constexpr (sizeof(T) == 2) {
 #pragma unroll
-        for (int q = 0; q < 4; ++q) acc[nb][q] += dpp_f32<0x128>(acc[nb][q]);  // row_ror 8: the other part
+        for (int cb = 0; cb < CB; ++cb)
+#pragma unroll
+          for (int q = 0; q < 4; ++q) acc[cb][nb][q] += dpp_f32<0x128>(acc[cb][nb][q]);  // row_ror 8: the other part
       }
       const int col = lane & 15, r = nb * RPB + col;
       if (col < RPB && r < cnt) {
         const float w = c.w[row0 + r];
-        float* y = sums + c.token[row0 + r] * 16 + (lane >> 4) * 4;
+        float* y = sums + c.token[row0 + r] * COLS + (lane >> 4) * 4;
 #pragma unroll
-        for (int q = 0; q < 4; ++q) y[q] = fmaf(w, acc[nb][q], y[q]);
+        for (int cb = 0; cb < CB; ++cb)
+#pragma unroll
+          for (int q = 0; q < 4; ++q) y[cb * 16 + q] = fmaf(w, acc[cb][nb][q], y[cb * 16 + q]);
       }
     }
   }
@@ -621,11 +686,11 @@ struct Down {
   __device__ __forceinline__ static void tile(const DecodeArgs& a, const Choice& c, int n0, unsigned char* smem) {
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int ns = (a.F + STEP - 1) / STEP, units = c.n * ns;
-    const int per = (units + DEC_NW - 1) / DEC_NW;
+    const int per = (units + NW - 1) / NW;
     const int u_end = min(units, (wave + 1) * per);
     unsigned char* lds = smem + wave * WAVE_LDS;
     float* sums = reinterpret_cast<float*>(lds + STAGE);
-    for (int o = lane; o < a.T * 16; o += 64) sums[o] = 0.f;
+    for (int o = lane; o < a.T * COLS; o += 64) sums[o] = 0.f;
     for (int u = min(units, wave * per); u < u_end;) {
       const int i = __builtin_amdgcn_readfirstlane(u / ns), s = u - i * ns;
       const int n = min(ns - s, u_end - u);
@@ -637,12 +702,12 @@ struct Down {
       u += n;
     }
     __syncthreads();
-    for (int o = tid; o < a.T * 16; o += DEC_NTH) {
-      const int r = o & 15, t = o >> 4;
+    for (int o = tid; o < a.T * COLS; o += NTH) {
+      const int r = o % COLS, t = o / COLS;
       if (n0 + r < a.H) {
         float v = 0.f;
 #pragma unroll
-        for (int w = 0; w < DEC_NW; ++w) v += reinterpret_cast<const float*>(smem + w * WAVE_LDS + STAGE)[o];
+        for (int w = 0; w < NW; ++w) v += reinterpret_cast<const float*>(smem + w * WAVE_LDS + STAGE)[o];
         static_cast<T*>(a.y)[(int64_t)t * a.H + n0 + r] = from_f32<T>(v);
       }
     }
@@ -651,13 +716,13 @@ struct Down {
 };
 
 template <typename T, bool W4>
-__global__ __launch_bounds__(DEC_NTH, 4) void decode_down_kernel(DecodeArgs a) {
+__global__ __launch_bounds__((Down<T, W4>::NTH), 4) void decode_down_kernel(DecodeArgs a) {
   using D = Down<T, W4>;
   __shared__ Choice c;
-  __shared__ __attribute__((aligned(16))) unsigned char smem[DEC_NW * D::WAVE_LDS];
-  choose(a, c, false);
-  const int total = (a.H + 15) / 16;
-  for (int tile = blockIdx.x; tile < total; tile += gridDim.x) D::tile(a, c, tile * 16, smem);
+  __shared__ __attribute__((aligned(16))) unsigned char smem[D::NW * D::WAVE_LDS];
+  choose<D::NW>(a, c, false);
+  const int total = (a.H + D::COLS - 1) / D::COLS;
+  for (int tile = blockIdx.x; tile < total; tile += gridDim.x) D::tile(a, c, tile * D::COLS, smem);
 }
 
 template <typename T>
@@ -676,9 +741,11 @@ void launch_route_rows(const T* x, const float* w, const float* bias, int64_t bi
 
 template <typename T, bool W4>
 void launch_experts(const DecodeArgs& a, int num_cus, hipStream_t stream) {
-  const int64_t gu = (int64_t)std::min(a.T * a.k, a.El) * ((a.F + 15) / 16);
-  decode_gate_up_kernel<T, W4><<<(int)std::min<int64_t>(gu, 2 * num_cus), DEC_NTH, 0, stream>>>(a);
-  decode_down_kernel<T, W4><<<std::min((a.H + 15) / 16, 2 * num_cus), DEC_NTH, 0, stream>>>(a);
+  using G = GateUp<T, W4, 2>;
+  using D = Down<T, W4>;
+  const int64_t gu = (int64_t)std::min(a.T * a.k, a.El) * ceil_div_host(a.F, G::COLS);
+  decode_gate_up_kernel<T, W4><<<(int)std::min<int64_t>(gu, 2 * num_cus), G::NTH, 0, stream>>>(a);
+  decode_down_kernel<T, W4><<<std::min(ceil_div_host(a.H, D::COLS), 16 / D::NW * num_cus), D::NTH, 0, stream>>>(a);
 }
 
 }  // namespace
