@@ -1,7 +1,7 @@
 // The whole MoE layer for a few tokens (T <= 32): moe_layer_decode and moe_layer_decode_w4.
 //
 //   logits = x Wr^T + b            decode_route_kernel
-//   top-k, softmax, capacity       choose(), by every workgroup of the next kernels for itself
+//   top-k, softmax, capacity       choose(), by every workgroup of the next kernel for itself
 //   h = silu(x Wg^T) * (x Wu^T)    decode_gate_up_kernel, per chosen expert
 //   y = sum_j w_j h_j Wd^T         decode_down_kernel
 //
@@ -23,8 +23,10 @@ namespace moe {
 
 namespace {
 
-constexpr int DEC_MAX_NW = 16;  // waves per workgroup, 8 or 16: they split K
+constexpr int DEC_GU_NW = 8;  // waves of a gate/up workgroup: they split K
 constexpr int DEC_PAIRS = MOE_DECODE_MAX_TOKENS * MOE_MAX_TOPK;
+
+struct Choice;
 
 struct DecodeArgs {
   const void* x;        // [T, H]
@@ -37,6 +39,7 @@ struct DecodeArgs {
   int* ids;             // [T, k]
   float* wts;           // [T, k]
   void* y;              // [T, H]
+  Choice* choice;       // written by the gate/up kernel, read by the down kernel
   void* h;              // [T * k, F] by row of Choice: fp32, or for bf16 layers the bf16 nearest to h and then [T * k, F] its remainder
 };
 
@@ -100,86 +103,109 @@ __global__ __launch_bounds__(256) void decode_route_kernel(const T* __restrict__
 struct Choice {
   int n;                           // local experts with a row, ascending
   int expert[DEC_PAIRS];
-  uint32_t mask[DEC_PAIRS];        // bit t: token t has a row
   int row0[DEC_PAIRS + 1];         // its rows (tokens ascending): row0[i] .. row0[i + 1]
   float w[DEC_PAIRS];              // routing weight of a row
-  uint8_t token[DEC_PAIRS];        // token of a row
-  // scratch
-  int wcnt[DEC_MAX_NW], wrow[DEC_MAX_NW];
-  int ids[DEC_PAIRS];
+  int token[DEC_PAIRS];            // token of a row
+};
+struct ChoiceScratch {
+  int wcnt[DEC_GU_NW], wrow[DEC_GU_NW];
+  int ids[DEC_PAIRS], local_id[DEC_PAIRS];
   float pw[DEC_PAIRS];
   uint32_t chosen[MOE_MAX_EXPERTS];  // tokens of a (global) expert, then those within its capacity
-  uint32_t local[MOE_MAX_EXPERTS];
+  uint32_t local[MOE_MAX_EXPERTS];   // tokens of a local expert
   uint16_t place[MOE_MAX_EXPERTS];
 };
 
-// Top-k, softmax and capacity of every token from the logits, by a whole workgroup: a wave per token, expert
-// lane * V + i in the lane's i-th value; each of the k rounds takes the wave's largest key, the lowest expert among
-// equals (moe_route's rule: -0 == +0, a NaN ranks as -inf). Repeated by every workgroup: it takes about as long as
-// one more dependent launch would, and nothing has to be passed on.
-template <int NW>
-__device__ __forceinline__ void choose(const DecodeArgs& a, Choice& c, bool write) {
+// Top-k, softmax and capacity of every token from the logits, by a whole workgroup: a wave per token (TW of them
+// interleaved: a round is one long chain of dependent operations), expert lane * V + i in the lane's i-th value; each
+// of the k rounds takes the wave's largest key, the lowest expert among equals (moe_route's rule: -0 == +0, a NaN ranks
+// as -inf). Every gate/up workgroup does it for itself (one token 4-6 us of which 1.2 are the logits' latency): one
+// that did it for all would have to be waited for. Workgroup 0 publishes the result for the down kernel.
+template <int TW>
+__device__ __forceinline__ void choose_topk(const DecodeArgs& a, ChoiceScratch& c, int t0, bool write) {
   constexpr int VMAX = MOE_MAX_EXPERTS / 64;
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int lane = threadIdx.x & 63;
   const int V = (a.E + 63) / 64;
-  static_assert(NW * 64 >= MOE_MAX_EXPERTS, "a thread per expert");
-  if (tid < MOE_MAX_EXPERTS) {
-    c.chosen[tid] = 0;
-    c.local[tid] = 0;
-  }
-  if (tid < DEC_PAIRS) c.w[tid] = 0.f;
-  __syncthreads();
-  for (int t = wave; t < a.T; t += NW) {
-    int key[VMAX];
+  // every logit requested at once; a lane without an i-th expert, and a token past T, read the last one
+  float v[TW][VMAX];
+#pragma unroll
+  for (int x = 0; x < TW; ++x)
+#pragma unroll
+    for (int i = 0; i < VMAX; ++i)
+      v[x][i] = i < V ? a.logits[(int64_t)min(t0 + x * DEC_GU_NW, a.T - 1) * a.E + min(lane * V + i, a.E - 1)] : 0.f;
+  int key[TW][VMAX];
+#pragma unroll
+  for (int x = 0; x < TW; ++x)
 #pragma unroll
     for (int i = 0; i < VMAX; ++i) {
-      const int e = lane * V + i;
-      key[i] = INT_MIN;
-      if (i < V && e < a.E) {
-        const float s = a.logits[(int64_t)t * a.E + e] + 0.0f;  // -0 -> +0
-        key[i] = float_key(s == s ? s : -INFINITY);
-      }
+      const float s = v[x][i] + 0.0f;  // -0 -> +0
+      key[x][i] = i < V && lane * V + i < a.E ? float_key(s == s ? s : -INFINITY) : INT_MIN;
     }
-    float sel_v[MOE_MAX_TOPK];
-    int mine = 0;
+  float sel_v[TW][MOE_MAX_TOPK];
+  int mine[TW];
 #pragma unroll
-    for (int j = 0; j < MOE_MAX_TOPK; ++j) {
-      sel_v[j] = 0.f;
-      if (j < a.k) {
-        int head = INT_MIN, at = 0;
+  for (int j = 0; j < MOE_MAX_TOPK; ++j) {
 #pragma unroll
-        for (int i = 0; i < VMAX; ++i)
-          if (key[i] > head) {
-            head = key[i];
-            at = i;
-          }
+    for (int x = 0; x < TW; ++x) {
+      sel_v[x][j] = 0.f;
+      if (j == 0) mine[x] = 0;
+    }
+    if (j < a.k) {
+#pragma unroll
+      for (int x = 0; x < TW; ++x) {
+        int head = key[x][0], at = 0;
+#pragma unroll
+        for (int i = 1; i < VMAX; ++i) {
+          at = key[x][i] > head ? i : at;
+          head = max(head, key[x][i]);
+        }
         const int m = wave_max_i32(head);
         const int wl = __builtin_ctzll(__ballot(head == m));  // k <= E: m is a present value's key
         const int e = __builtin_amdgcn_readlane(lane * V + at, wl);
-        sel_v[j] = key_float(m);
-        if (lane == j) mine = e;
+        sel_v[x][j] = key_float(m);
+        mine[x] = lane == j ? e : mine[x];
+        const int gone = lane == wl ? at : VMAX;
 #pragma unroll
-        for (int i = 0; i < VMAX; ++i)
-          if (lane == wl && i == at) key[i] = INT_MIN;
+        for (int i = 0; i < VMAX; ++i) key[x][i] = i == gone ? INT_MIN : key[x][i];
       }
     }
+  }
+#pragma unroll
+  for (int x = 0; x < TW; ++x) {
+    const int t = t0 + x * DEC_GU_NW;
     float sum = 0.f, z_mine = 0.f;
 #pragma unroll
     for (int j = 0; j < MOE_MAX_TOPK; ++j)
       if (j < a.k) {
-        const float z = expf(sel_v[j] - sel_v[0]);
+        const float z = expf(sel_v[x][j] - sel_v[x][0]);
         sum += z;
-        if (j == lane) z_mine = z;
+        z_mine = j == lane ? z : z_mine;
       }
-    if (lane < a.k) {
-      c.ids[t * a.k + lane] = mine;
-      c.pw[t * a.k + lane] = z_mine / sum;
-      atomicOr(&c.chosen[mine], 1u << t);
+    if (lane < a.k && t < a.T) {
+      const int p = t * a.k + lane;
+      c.ids[p] = mine[x];
+      c.local_id[p] = mine[x] % a.El;
+      c.pw[p] = z_mine / sum;
+      atomicOr(&c.chosen[mine[x]], 1u << t);
       if (write) {
-        a.ids[t * a.k + lane] = mine;
-        a.wts[t * a.k + lane] = z_mine / sum;
+        a.ids[p] = mine[x];
+        a.wts[p] = z_mine / sum;
       }
     }
+  }
+}
+
+__device__ __forceinline__ void choose(const DecodeArgs& a, Choice& o, ChoiceScratch& c, bool write) {
+  constexpr int NW = DEC_GU_NW, NTH = NW * 64;
+  static_assert(NTH >= MOE_MAX_EXPERTS && NTH >= DEC_PAIRS, "a thread per expert and per pair");
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  c.chosen[tid] = 0;
+  c.local[tid] = 0;
+  __syncthreads();
+  if (a.T <= NW) {
+    if (wave < a.T) choose_topk<1>(a, c, wave, write);
+  } else {
+    for (int t0 = wave; t0 < a.T; t0 += 2 * NW) choose_topk<2>(a, c, t0, write);
   }
   __syncthreads();
   // the first C tokens of every expert
@@ -211,28 +237,38 @@ __device__ __forceinline__ void choose(const DecodeArgs& a, Choice& c, bool writ
     row += w < wave ? c.wrow[w] : 0;
   }
   if (m != 0) {
-    c.expert[i] = tid;
-    c.mask[i] = m;
-    c.row0[i] = row;
+    o.expert[i] = tid;
+    o.row0[i] = row;
     c.place[tid] = (uint16_t)i;
   }
-  if (tid == (NW * 64) - 1) {  // past the last expert: the totals
-    c.n = i + (m != 0);
-    c.row0[i + (m != 0)] = row + __popc(m);
+  if (tid == NTH - 1) {  // past the last expert: the totals
+    o.n = i + (m != 0);
+    o.row0[i + (m != 0)] = row + __popc(m);
   }
   __syncthreads();
-  if (tid < a.T) {
-    for (int j = 0; j < a.k; ++j) {
-      const int e = c.ids[tid * a.k + j];
-      if ((c.chosen[e] >> tid) & 1u) {
-        const int at = c.place[e % a.El];
-        const int r = c.row0[at] + __popc(c.mask[at] & ((1u << tid) - 1u));
-        c.token[r] = (uint8_t)tid;
-        c.w[r] += c.pw[tid * a.k + j];  // a row is one token's: this thread's alone
+  // the first slot of a token that reaches a local expert writes its row, with the weights of the later ones added
+  if (tid < a.T * a.k) {
+    const int t = tid / a.k, p0 = t * a.k, le = c.local_id[tid];
+    float w = 0.f;
+    bool first = true, mine = false;
+#pragma unroll
+    for (int j = 0; j < MOE_MAX_TOPK; ++j)
+      if (j < a.k) {
+        const bool on = c.local_id[p0 + j] == le && ((c.chosen[c.ids[p0 + j]] >> t) & 1u);
+        w += on && p0 + j >= tid ? c.pw[p0 + j] : 0.f;
+        first = first && !(on && p0 + j < tid);
+        mine = mine || (on && p0 + j == tid);
       }
+    if (first && mine) {
+      const int r = o.row0[c.place[le]] + __popc(c.local[le] & ((1u << t) - 1u));
+      o.token[r] = t;
+      o.w[r] = w;
     }
   }
   __syncthreads();
+  if (write)
+    for (int x = tid; x < (int)(sizeof(Choice) / 4); x += NTH)
+      reinterpret_cast<int*>(a.choice)[x] = reinterpret_cast<const int*>(&o)[x];
 }
 
 // ------------------------------------------------------------------------------------------------
@@ -358,7 +394,7 @@ __device__ __forceinline__ float silu(float g) { return g / (1.0f + expf(-g)); }
 // through LDS in wave order.
 template <typename T, bool W4, int NB>
 struct GateUp {
-  static constexpr int NW = 8, NTH = NW * 64;
+  static constexpr int NW = DEC_GU_NW, NTH = NW * 64;
   static constexpr int CB = W4 ? 2 : 1;      // blocks of 16 columns
   static constexpr int COLS = CB * 16;
   using RS = RowStep<T, 2>;
@@ -525,7 +561,9 @@ __global__ __launch_bounds__(512, 4) void decode_gate_up_kernel(DecodeArgs a) {
   using G = GateUp<T, W4, 2>;
   __shared__ Choice c;
   __shared__ __attribute__((aligned(16))) unsigned char smem[G::NW * G::WAVE_LDS];
-  choose<G::NW>(a, c, blockIdx.x == 0);
+  static_assert(sizeof(ChoiceScratch) <= sizeof(smem), "the scratch is done with before the first tile");
+  choose(a, c, *reinterpret_cast<ChoiceScratch*>(smem), blockIdx.x == 0);
+  __syncthreads();
   const int nft = (a.F + G::COLS - 1) / G::COLS, total = c.n * nft;
   for (int tile = blockIdx.x; tile < total; tile += gridDim.x) {
     const int i = tile / nft;
@@ -720,7 +758,9 @@ __global__ __launch_bounds__((Down<T, W4>::NTH), 4) void decode_down_kernel(Deco
   using D = Down<T, W4>;
   __shared__ Choice c;
   __shared__ __attribute__((aligned(16))) unsigned char smem[D::NW * D::WAVE_LDS];
-  choose<D::NW>(a, c, false);
+  for (int x = threadIdx.x; x < (int)(sizeof(Choice) / 4); x += D::NTH)
+    reinterpret_cast<int*>(&c)[x] = reinterpret_cast<const int*>(a.choice)[x];
+  __syncthreads();
   const int total = (a.H + D::COLS - 1) / D::COLS;
   for (int tile = blockIdx.x; tile < total; tile += gridDim.x) D::tile(a, c, tile * D::COLS, smem);
 }
@@ -750,7 +790,9 @@ void launch_experts(const DecodeArgs& a, int num_cus, hipStream_t stream) {
 
 }  // namespace
 
-size_t decode_workspace_bytes(int T, int k, int F) { return align256((size_t)T * k * (size_t)F * 4); }
+size_t decode_workspace_bytes(int T, int k, int F) {
+  return align256(sizeof(Choice)) + align256((size_t)T * k * (size_t)F * 4);
+}
 
 hipError_t launch_layer_decode(const DecodeCall& d, int num_cus, hipStream_t stream) {
   if (d.bf16)
@@ -774,7 +816,8 @@ hipError_t launch_layer_decode(const DecodeCall& d, int num_cus, hipStream_t str
   a.ids = d.ids;
   a.wts = d.wts;
   a.y = d.y;
-  a.h = d.workspace;
+  a.choice = static_cast<Choice*>(d.workspace);
+  a.h = static_cast<char*>(d.workspace) + align256(sizeof(Choice));
   if (!d.bf16) launch_experts<float, false>(a, num_cus, stream);
   else if (d.s_gu) launch_experts<bf16_t, true>(a, num_cus, stream);
   else launch_experts<bf16_t, false>(a, num_cus, stream);
