@@ -396,7 +396,7 @@ size_t moe_layer_decode_workspace_bytes(int T, int H, int E, int k, int F, moe_d
   if (T <= 0 || T > MOE_DECODE_MAX_TOKENS || H <= 0 || E <= 0 || k <= 0 || k > MOE_MAX_TOPK || F <= 0 ||
       !valid_dtype(xdt))
     return 0;
-  return moe::decode_workspace_bytes(T, k, F);
+  return moe::decode_workspace_bytes(T, H, k, F);
 }
 
 namespace {

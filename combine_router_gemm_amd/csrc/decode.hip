@@ -29,7 +29,7 @@ constexpr int DEC_PAIRS = MOE_DECODE_MAX_TOKENS * MOE_MAX_TOPK;
 struct Choice;
 
 struct DecodeArgs {
-  const void* x;        // [T, H]
+  const void* x;        // [T, H]; with 4-bit weights rows of w4_pitch(H), each 128 k in w4_place order
   const float* logits;  // [T, E]
   int T, H, E, El, k, C, F;
   const void* w_gu;     // [El, 2F, H], or its packed codes
@@ -40,8 +40,17 @@ struct DecodeArgs {
   float* wts;           // [T, k]
   void* y;              // [T, H]
   Choice* choice;       // written by the gate/up kernel, read by the down kernel
-  void* h;              // [T * k, F] by row of Choice: fp32, or for bf16 layers the bf16 nearest to h and then [T * k, F] its remainder
+  void* h;              // [T * k, F] by row of Choice: fp32, or for bf16 layers the bf16 nearest to h and then
+                        // [T * k, F] its remainder; with 4-bit weights in rows like x's
 };
+
+// With 4-bit weights the matrix step j of 128 k takes k = 32 g + 8 j .. + 7 from lane group g (W4Step). Rows of x and h
+// are kept with those four pieces of a step side by side, so that a row's fragment load is one 64-byte segment rather
+// than four pieces of 16 bytes 64 apart: element k of a row is at w4_place(k). The router writes x so, gate/up h.
+__host__ __device__ __forceinline__ int w4_pitch(int K) { return (K + W4_TILE_K - 1) / W4_TILE_K * W4_TILE_K; }
+__device__ __forceinline__ int w4_place(int k) {
+  return (k & ~(W4_TILE_K - 1)) + ((k >> 3) & 3) * 32 + ((k >> 5) & 3) * 8 + (k & 7);
+}
 
 // ------------------------------------------------------------------------------------------------
 // router
@@ -64,7 +73,8 @@ __device__ __forceinline__ void load8<float>(const float* p, float (&v)[8]) {
 template <typename T, int TB>
 __global__ __launch_bounds__(256) void decode_route_kernel(const T* __restrict__ x, const float* __restrict__ w,
                                                            const float* __restrict__ bias, int64_t bias_stride, int T_,
-                                                           int H, int E, float* __restrict__ logits) {
+                                                           int H, int E, float* __restrict__ logits,
+                                                           bf16_t* __restrict__ placed) {
   __shared__ float s_sum[4][TB];
   const int e = blockIdx.x, t0 = blockIdx.y * TB;
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
@@ -88,6 +98,15 @@ __global__ __launch_bounds__(256) void decode_route_kernel(const T* __restrict__
     if (lane == 0) s_sum[wave][j] = s;
   }
   __syncthreads();
+  if constexpr (sizeof(T) == 2) {
+    if (placed) {  // x in w4_place order, by all workgroups together
+      const int n = min(TB, T_ - t0) * (H / 8);
+      for (int c = e * 256 + tid; c < n; c += E * 256) {
+        const int t = t0 + c / (H / 8), k = c % (H / 8) * 8;
+        st16(placed + (int64_t)t * w4_pitch(H) + w4_place(k), ld16(x + (int64_t)t * H + k));
+      }
+    }
+  }
   if (tid < TB && t0 + tid < T_) {
     float v = (s_sum[0][tid] + s_sum[1][tid]) + (s_sum[2][tid] + s_sum[3][tid]);
     if (bias) v += bias[(int64_t)(t0 + tid) * bias_stride + e];
@@ -378,10 +397,10 @@ struct W4Step {
   }
   __device__ __forceinline__ static void load_col(u32x4 (&x)[XV], __amdgpu_buffer_rsrc_t r, int row, int step, int K,
                                                   int lane) {
-    const int k = step * STEP + (lane >> 4) * 32;
-    const int off = row >= 0 && k < K ? row + k * 2 : DEC_NONE;
+    const bool in = row >= 0 && step * STEP + (lane >> 4) * 32 < K;
+    const int off = in ? row + step * (STEP * 2) + (lane >> 4) * 16 : DEC_NONE;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) x[j] = ld_col(r, off + j * 16);
+    for (int j = 0; j < 4; ++j) x[j] = ld_col(r, off + j * 64);
   }
 };
 
@@ -412,13 +431,14 @@ struct GateUp {
     const int row0 = __builtin_amdgcn_readfirstlane(c.row0[i]);
     const int cnt = __builtin_amdgcn_readfirstlane(c.row0[i + 1]) - row0;
     unsigned char* lds = smem + wave * WAVE_LDS;
+    const int pitch = W4 ? w4_pitch(K) : K;
     const __amdgpu_buffer_rsrc_t xr =
-        __builtin_amdgcn_make_buffer_rsrc((void*)a.x, (short)0, a.T * K * (int)sizeof(T), 0x00020000);
+        __builtin_amdgcn_make_buffer_rsrc((void*)a.x, (short)0, a.T * pitch * (int)sizeof(T), 0x00020000);
     int cols[NB];
 #pragma unroll
     for (int nb = 0; nb < NB; ++nb) {
       const int r = nb * 16 + (lane & 15);
-      cols[nb] = r < cnt ? c.token[row0 + r] * K * (int)sizeof(T) : -1;
+      cols[nb] = r < cnt ? c.token[row0 + r] * pitch * (int)sizeof(T) : -1;
     }
     f32x4 acc[2][CB][NB];  // gate, up
 #pragma unroll
@@ -542,11 +562,12 @@ struct GateUp {
           u += red_w[(((CB + cb) * NB + nb) * 4 + q) * 64 + ln];
         }
         const float h = silu(g) * u;
-        const int64_t at = (int64_t)(row0 + r) * F + f;
+        const int hp = W4 ? w4_pitch(F) : F;
+        const int64_t at = (int64_t)(row0 + r) * hp + (W4 ? w4_place(f) : f);
         if constexpr (sizeof(T) == 2) {
           const bf16_t hi = (bf16_t)h;
           static_cast<bf16_t*>(a.h)[at] = hi;
-          static_cast<bf16_t*>(a.h)[(int64_t)a.T * a.k * F + at] = (bf16_t)(h - (float)hi);
+          static_cast<bf16_t*>(a.h)[(int64_t)a.T * a.k * hp + at] = (bf16_t)(h - (float)hi);
         } else {
           static_cast<float*>(a.h)[at] = h;
         }
@@ -605,15 +626,16 @@ struct Down {
     const int64_t l = __builtin_amdgcn_readfirstlane(c.expert[i]);
     const int row0 = __builtin_amdgcn_readfirstlane(c.row0[i]) + r0;
     const int cnt = __builtin_amdgcn_readfirstlane(c.row0[i + 1]) - row0;
-    const int64_t part = (int64_t)a.T * a.k * K;  // elements of one part of h
+    const int pitch = W4 ? w4_pitch(K) : K;
+    const int64_t part = (int64_t)a.T * a.k * pitch;  // elements of one part of h
     const __amdgpu_buffer_rsrc_t hr = __builtin_amdgcn_make_buffer_rsrc(
-        (char*)a.h + (int64_t)row0 * K * (int)sizeof(T), (short)0,
-        (int)((sizeof(T) == 2 ? part : 0) + (int64_t)cnt * K) * (int)sizeof(T), 0x00020000);
+        (char*)a.h + (int64_t)row0 * pitch * (int)sizeof(T), (short)0,
+        (int)((sizeof(T) == 2 ? part : 0) + (int64_t)cnt * pitch) * (int)sizeof(T), 0x00020000);
     int cols[NB];
 #pragma unroll
     for (int nb = 0; nb < NB; ++nb) {
       const int col = lane & 15, r = nb * RPB + col % RPB;
-      cols[nb] = r < cnt ? (r * K + (col >= RPB ? (int)part : 0)) * (int)sizeof(T) : -1;
+      cols[nb] = r < cnt ? (r * pitch + (col >= RPB ? (int)part : 0)) * (int)sizeof(T) : -1;
     }
     f32x4 acc[CB][NB];
 #pragma unroll
@@ -767,11 +789,11 @@ __global__ __launch_bounds__((Down<T, W4>::NTH), 4) void decode_down_kernel(Deco
 
 template <typename T>
 void launch_route_rows(const T* x, const float* w, const float* bias, int64_t bias_stride, int T_, int H, int E,
-                       float* logits, hipStream_t stream) {
+                       float* logits, bf16_t* placed, hipStream_t stream) {
   auto go = [&](auto tb) {
     constexpr int TB = decltype(tb)::value;
     decode_route_kernel<T, TB><<<dim3(E, ceil_div_host(T_, TB)), 256, 0, stream>>>(x, w, bias, bias_stride, T_, H, E,
-                                                                                   logits);
+                                                                                   logits, placed);
   };
   if (T_ == 1) go(std::integral_constant<int, 1>{});
   else if (T_ <= 2) go(std::integral_constant<int, 2>{});
@@ -790,17 +812,26 @@ void launch_experts(const DecodeArgs& a, int num_cus, hipStream_t stream) {
 
 }  // namespace
 
-size_t decode_workspace_bytes(int T, int k, int F) {
-  return align256(sizeof(Choice)) + align256((size_t)T * k * (size_t)F * 4);
+size_t decode_workspace_bytes(int T, int H, int k, int F) {
+  return align256(sizeof(Choice)) + align256((size_t)T * k * (size_t)w4_pitch(F) * 4) +
+         align256((size_t)T * (size_t)w4_pitch(H) * 2);
 }
 
 hipError_t launch_layer_decode(const DecodeCall& d, int num_cus, hipStream_t stream) {
-  if (d.bf16)
-    launch_route_rows(static_cast<const bf16_t*>(d.x), d.w_router, d.bias, d.bias_stride, d.T, d.H, d.E, d.logits, stream);
-  else
-    launch_route_rows(static_cast<const float*>(d.x), d.w_router, d.bias, d.bias_stride, d.T, d.H, d.E, d.logits, stream);
+  char* ws = static_cast<char*>(d.workspace);
   DecodeArgs a{};
-  a.x = d.x;
+  a.choice = reinterpret_cast<Choice*>(ws);
+  ws += align256(sizeof(Choice));
+  a.h = ws;
+  ws += align256((size_t)d.T * d.k * (size_t)w4_pitch(d.F) * 4);
+  bf16_t* placed = d.s_gu ? reinterpret_cast<bf16_t*>(ws) : nullptr;
+  if (d.bf16)
+    launch_route_rows(static_cast<const bf16_t*>(d.x), d.w_router, d.bias, d.bias_stride, d.T, d.H, d.E, d.logits,
+                      placed, stream);
+  else
+    launch_route_rows(static_cast<const float*>(d.x), d.w_router, d.bias, d.bias_stride, d.T, d.H, d.E, d.logits,
+                      nullptr, stream);
+  a.x = placed ? placed : d.x;
   a.logits = d.logits;
   a.T = d.T;
   a.H = d.H;
@@ -816,8 +847,6 @@ hipError_t launch_layer_decode(const DecodeCall& d, int num_cus, hipStream_t str
   a.ids = d.ids;
   a.wts = d.wts;
   a.y = d.y;
-  a.choice = static_cast<Choice*>(d.workspace);
-  a.h = static_cast<char*>(d.workspace) + align256(sizeof(Choice));
   if (!d.bf16) launch_experts<float, false>(a, num_cus, stream);
   else if (d.s_gu) launch_experts<bf16_t, true>(a, num_cus, stream);
   else launch_experts<bf16_t, false>(a, num_cus, stream);

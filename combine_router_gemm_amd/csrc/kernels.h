@@ -100,7 +100,7 @@ struct DecodeCall {
   void* y;
   void* workspace;
 };
-size_t decode_workspace_bytes(int T, int k, int F);
+size_t decode_workspace_bytes(int T, int H, int k, int F);
 hipError_t launch_layer_decode(const DecodeCall& d, int num_cus, hipStream_t stream);
 
 }  // namespace moe
