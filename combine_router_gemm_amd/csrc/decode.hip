@@ -418,17 +418,20 @@ struct GateUp {
   static constexpr int COLS = CB * 16;
   using RS = RowStep<T, 2>;
   using WS = W4Step<2 * CB>;
-  static constexpr int PF = W4 ? (NB == 1 ? 2 : 1) : (NB == 1 ? 3 : 2);  // steps of loads in flight per wave
+  static constexpr int PF = W4 ? 2 : NB == 1 ? 3 : 2;  // steps of loads in flight per wave
   static constexpr int RED = 2 * CB * NB * 4 * 64 * 4;
   static constexpr int STAGE = W4 ? WS::LDS_BYTES : RS::LDS_BYTES;
-  static constexpr int WAVE_LDS = RED > STAGE ? RED : STAGE;
+  static constexpr int WAVE_LDS = W4 ? (RED > STAGE ? RED : STAGE) : STAGE;
+  static_assert(WAVE_LDS >= RED, "a wave's sums fit its LDS");
   static constexpr int XV = W4 ? WS::XV : RS::XV;
 
-  __device__ __forceinline__ static void tile(const DecodeArgs& a, const Choice& c, int i, int ft, unsigned char* smem) {
+  // NB blocks of 16 of the expert's rows, from row r0 on
+  __device__ __forceinline__ static void tile(const DecodeArgs& a, const Choice& c, int i, int r0, int ft,
+                                              unsigned char* smem) {
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int K = a.H, F = a.F, f0 = ft * COLS;
     const int64_t l = __builtin_amdgcn_readfirstlane(c.expert[i]);
-    const int row0 = __builtin_amdgcn_readfirstlane(c.row0[i]);
+    const int row0 = __builtin_amdgcn_readfirstlane(c.row0[i]) + r0;
     const int cnt = __builtin_amdgcn_readfirstlane(c.row0[i + 1]) - row0;
     unsigned char* lds = smem + wave * WAVE_LDS;
     const int pitch = W4 ? w4_pitch(K) : K;
@@ -579,7 +582,7 @@ struct GateUp {
 
 template <typename T, bool W4>
 __global__ __launch_bounds__(512, 4) void decode_gate_up_kernel(DecodeArgs a) {
-  using G = GateUp<T, W4, 2>;
+  using G = GateUp<T, W4, W4 ? 1 : 2>;
   __shared__ Choice c;
   __shared__ __attribute__((aligned(16))) unsigned char smem[G::NW * G::WAVE_LDS];
   static_assert(sizeof(ChoiceScratch) <= sizeof(smem), "the scratch is done with before the first tile");
@@ -587,9 +590,18 @@ __global__ __launch_bounds__(512, 4) void decode_gate_up_kernel(DecodeArgs a) {
   __syncthreads();
   const int nft = (a.F + G::COLS - 1) / G::COLS, total = c.n * nft;
   for (int tile = blockIdx.x; tile < total; tile += gridDim.x) {
-    const int i = tile / nft;
-    if (c.row0[i + 1] - c.row0[i] <= 16) GateUp<T, W4, 1>::tile(a, c, i, tile - i * nft, smem);
-    else G::tile(a, c, i, tile - i * nft, smem);
+    const int i = tile / nft, cnt = c.row0[i + 1] - c.row0[i];
+    if constexpr (W4) {
+      // more than 16 rows (only with more than 16 tokens): the codes once more, for the rest. Both blocks at once need
+      // 19 registers more than two workgroups per CU leave, and a spilled register is reloaded behind every load in
+      // flight: with that path compiled in, 25.6 -> 33.7 us for one token and 155 -> 173 us for 32 (DeepSeek-V3 and
+      // Kimi-K2 shares).
+      for (int r0 = 0; r0 < cnt; r0 += 16) G::tile(a, c, i, r0, tile - i * nft, smem);
+    } else if (cnt <= 16) {
+      GateUp<T, W4, 1>::tile(a, c, i, 0, tile - i * nft, smem);
+    } else {
+      G::tile(a, c, i, 0, tile - i * nft, smem);
+    }
   }
 }
 
@@ -620,7 +632,7 @@ struct Down {
   template <int NB>
   __device__ __forceinline__ static void run(const DecodeArgs& a, const Choice& c, int i, int r0, int s_begin, int s_end,
                                              int n0, unsigned char* lds, float* sums) {
-    constexpr int PF = W4 ? (NB > 1 ? 1 : 3) : (NB > 1 ? 3 : 4);  // steps of loads in flight
+    constexpr int PF = W4 ? (NB > 1 ? 1 : 3) : (NB > 1 ? 2 : 4);  // steps of loads in flight
     const int lane = threadIdx.x & 63;
     const int K = a.F, H = a.H;
     const int64_t l = __builtin_amdgcn_readfirstlane(c.expert[i]);
@@ -803,7 +815,7 @@ void launch_route_rows(const T* x, const float* w, const float* bias, int64_t bi
 
 template <typename T, bool W4>
 void launch_experts(const DecodeArgs& a, int num_cus, hipStream_t stream) {
-  using G = GateUp<T, W4, 2>;
+  using G = GateUp<T, W4, 1>;
   using D = Down<T, W4>;
   const int64_t gu = (int64_t)std::min(a.T * a.k, a.El) * ceil_div_host(a.F, G::COLS);
   decode_gate_up_kernel<T, W4><<<(int)std::min<int64_t>(gu, 2 * num_cus), G::NTH, 0, stream>>>(a);
