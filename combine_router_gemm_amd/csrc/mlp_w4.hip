@@ -77,13 +77,17 @@ __device__ __forceinline__ void wait_loads() {
 
 // BM rows x 64 WN weight rows per tile; WM x WN waves, each BM / WM rows x 64 weight rows: the gate and the up rows of 32
 // columns of h, or 64 down rows. K goes in stages of 64:
-//  - rows: 128 bytes each, straight to LDS, NS slots, NS - 1 stages ahead. 16-byte chunk c of row r sits at
-//    c ^ ((r >> 1) & 7), so that a fragment read touches every bank once.
+//  - rows: 128 bytes each, straight to LDS, NS slots. 16-byte chunk c of row r sits at c ^ ((r >> 1) & 7), so that a
+//    fragment read touches every bank once.
 //  - codes: one 16-byte load per lane and 32 weight rows holds a stage (lane % 32 the row, lane / 32 one of its two
-//    scale groups), two stages ahead. Its word j is the fragment of matrix step j, whose k are 8 j on of both
-//    groups; the row fragments follow that order.
-//  - one barrier per stage: it publishes stage s and frees the slot that stage s + NS - 1 is loaded into. Loads past
-//    the last stage are issued too, at offsets that read nothing, so the number in flight is the same at every wait.
+//    scale groups). Its word j is the fragment of matrix step j, whose k are 8 j on of both groups; the row fragments
+//    follow that order.
+//  - scales: the tiles of eight stages go to LDS of the wave's own in one load, eight stages ahead (a load of a byte per
+//    stage and row keeps the load path as long as one of sixteen).
+//  - schedule: the weights of step j + 1 are decoded and its rows read while step j is multiplied. The barrier that
+//    publishes stage s + 1 sits before the last step of stage s, whose fragments are in registers: after it the
+//    slot of stage s is free and takes the rows of stage s + NS. Loads past the last stage are issued too, at offsets
+//    that read nothing, so at least as many are in flight at every wait as it counts on.
 // PARTS: h has two bf16 parts (16 significant bits) where few rows make the weights' bytes the bound, so that the
 // down pass's doubled matrix work is free, and one where the matrix units are the bound.
 template <int BM, int WM, int WN, bool GATED, int PARTS>
@@ -95,15 +99,16 @@ __global__ __launch_bounds__(WM * WN * 64) void w4_gemm_kernel(W4Args a, int a_b
   constexpr int OUTC = WN * (GATED ? 32 : 64);
   constexpr int OUT_BYTES = BM * OUTC * 2;
   constexpr int BODY = NS * STAGE > OP * OUT_BYTES ? NS * STAGE : OP * OUT_BYTES;
-  constexpr int LOADS = XI + 4;  // loads per wave and stage: rows, two codes, two scales
+  constexpr int LOADS = XI + 2;  // loads per wave and stage: rows and codes
   constexpr int OOB = 0x7ffffff0;
   static_assert(TM >= 1 && XP * BM / 8 % NW == 0 && OUTC >= 128, "tile");
   // the only LDS object (a second one makes the compiler wait for every load in flight before LDS reads): the
-  // stages, which the output tile reuses, then its destination rows
-  __shared__ __attribute__((aligned(1024))) unsigned char smem[BODY + BM * 4];
-  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  // stages, which the output tile reuses, then its destination rows, then the waves' scales
+  __shared__ __attribute__((aligned(1024))) unsigned char smem[BODY + BM * 4 + NW * 2048];
+  int tid = threadIdx.x, lane = tid & 63;  // made opaque at each tile start (below)
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wm = wave / WN, wn = wave % WN;
-  const int fr = lane & 31, fq = lane >> 5;
+  int fr = lane & 31, fq = lane >> 5;
   const int K = a.K, nk = (K + 63) / 64;
   const int kc = (K + W4_TILE_K - 1) / W4_TILE_K, ks = (K + W4_STILE_K - 1) / W4_STILE_K;
   const int* row_start = a.plan + 2;
@@ -112,22 +117,27 @@ __global__ __launch_bounds__(WM * WN * 64) void w4_gemm_kernel(W4Args a, int a_b
   const Tiles mine = my_tiles(a.plan[0] * n_tiles);
   const __amdgpu_buffer_rsrc_t a_rsrc = __builtin_amdgcn_make_buffer_rsrc((void*)a.A, (short)0, a_bytes, 0x00020000);
   for (int tile = mine.begin; tile < mine.end; tile += mine.step) {
-    const int l = find_expert(tile_start, a.El, n_tiles, tile);
-    const int mt_l = tile_start[l + 1] - tile_start[l];
-    const int local = tile - tile_start[l] * n_tiles;
+    // per-lane values are computed again in each tile: kept across the tile loop they do not fit the registers next
+    // to the accumulators
+    asm volatile("" : "+v"(tid), "+v"(lane), "+v"(fr), "+v"(fq));
+    const int l = __builtin_amdgcn_readfirstlane(find_expert(tile_start, a.El, n_tiles, tile));
+    const int ts = __builtin_amdgcn_readfirstlane(tile_start[l]);
+    const int mt_l = __builtin_amdgcn_readfirstlane(tile_start[l + 1]) - ts;
+    const int local = tile - ts * n_tiles;
     const int nt = local / mt_l, mt = local % mt_l;
-    const int p0 = row_start[l] + mt * BM, m_rows = min(BM, row_start[l + 1] - p0);
-    // the two 32-row weight blocks (N % 32 == 0: a block is whole or past N, then it repeats the first rows)
+    const int p0 = __builtin_amdgcn_readfirstlane(row_start[l]) + mt * BM;
+    const int m_rows = min(BM, __builtin_amdgcn_readfirstlane(row_start[l + 1]) - p0);
+    // the two 32-row weight blocks (N % 32 == 0: a block is whole or past N, then it repeats the first rows): a
+    // wave-uniform start, and the lane's offset from there
     const int c0 = nt * OUTC + wn * (GATED ? 32 : 64);
     const bool on[2] = {c0 < a.N, GATED ? c0 < a.N : c0 + 32 < a.N};
     const uint8_t* wc[2];
-    const uint8_t* ws[2];
 #pragma unroll
     for (int b = 0; b < 2; ++b) {
-      const int64_t row = (int64_t)l * a.w_rows + (on[b] ? c0 + b * (GATED ? a.up : 32) : 0) + fr;
-      wc[b] = a.codes + (row >> 4) * kc * W4_CODE_TILE + (fr & 15) * 16 + fq * 256;
-      ws[b] = a.scales + (row >> 4) * ks * W4_SCALE_TILE + ((fr & 15) + 16 * fq) * 4;
+      const int64_t rb = ((int64_t)l * a.w_rows + (on[b] ? c0 + b * (GATED ? a.up : 32) : 0)) >> 4;
+      wc[b] = a.codes + rb * kc * W4_CODE_TILE;
     }
+    const uint32_t c_off = (uint32_t)((fr >> 4) * kc * W4_CODE_TILE + (fr & 15) * 16 + fq * 256);
     // this lane's row and 16-byte chunk in each of the wave's row loads
     int voff[XI];
 #pragma unroll
@@ -141,26 +151,45 @@ __global__ __launch_bounds__(WM * WN * 64) void w4_gemm_kernel(W4Args a, int a_b
       const int v = (wave * XI + q) * 8 + (lane >> 3), r = v % BM;
       voff[q] = r < m_rows ? (voff[q] * K + (v >= BM ? (int)a.part : 0)) * 2 + (((lane & 7) ^ ((r >> 1) & 7)) << 4) : OOB;
     }
+    // bit q: this lane's chunk of load q lies within K in the last stage
+    int tail = 0;
+#pragma unroll
+    for (int q = 0; q < XI; ++q) {
+      const int r = ((wave * XI + q) * 8 + (lane >> 3)) % BM;
+      tail |= ((nk - 1) * 64 + (((lane & 7) ^ ((r >> 1) & 7)) << 3) < K ? 1 : 0) << q;
+    }
     auto load_rows = [&](int st) {
       unsigned char* base = smem + (st % NS) * STAGE + wave * XI * 1024;
 #pragma unroll
       for (int q = 0; q < XI; ++q) {
-        const int r = ((wave * XI + q) * 8 + (lane >> 3)) % BM;
-        const bool in = st * 64 + (((lane & 7) ^ ((r >> 1) & 7)) << 3) < K;
+        const bool in = st < nk - 1 || (st < nk && ((tail >> q) & 1));
         const int vo = in && voff[q] != OOB ? voff[q] + st * 128 : OOB;
         __builtin_amdgcn_raw_ptr_buffer_load_lds(a_rsrc, (__attribute__((address_space(3))) void*)(base + q * 1024), 16,
                                                  vo, 0, 0, 0);
       }
     };
-    u32x4 cw[2][2];
-    uint32_t cs[2][2];
+    u32x4 cw[3][2];
     auto load_codes = [&](int st, int u) {
       const int s = min(st, nk - 1);
 #pragma unroll
-      for (int b = 0; b < 2; ++b) {
-        cw[u][b] = ld16(wc[b] + (int64_t)(s >> 1) * W4_CODE_TILE + (s & 1) * 512);
-        cs[u][b] = ws[b][(s >> 3) * W4_SCALE_TILE + (s & 1) * 128 + ((s >> 1) & 3)];
-      }
+      for (int b = 0; b < 2; ++b) cw[u][b] = ld16(wc[b] + ((s >> 1) * W4_CODE_TILE + (s & 1) * 512) + c_off);
+    };
+    // scale tiles q of the wave's four 16-row blocks (1 KB) to its LDS, slot q & 1
+    unsigned char* s_sc = smem + BODY + BM * 4 + wave * 2048;
+    const __amdgpu_buffer_rsrc_t s_rsrc = __builtin_amdgcn_make_buffer_rsrc(
+        (void*)(a.scales + (int64_t)l * (a.w_rows >> 4) * ks * W4_SCALE_TILE), (short)0,
+        (a.w_rows >> 4) * ks * W4_SCALE_TILE, 0x00020000);
+    const int s_off = (((on[fq] ? c0 + fq * (GATED ? a.up : 32) : 0) >> 4) + (fr >> 4)) * ks * W4_SCALE_TILE + (fr & 15) * 16;
+    auto load_scales = [&](int q) {
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(s_rsrc, (__attribute__((address_space(3))) void*)(s_sc + (q & 1) * 1024), 16,
+                                               s_off + min(q, ks - 1) * W4_SCALE_TILE, 0, 0, 0);
+    };
+    float sc[2];
+    auto stage_scales = [&](int st) {
+      const unsigned char* p = s_sc + ((st >> 3) & 1) * 1024 + (fr >> 4) * 256 + ((fr & 15) + 16 * fq) * 4 +
+                               (st & 1) * 128 + ((st >> 1) & 3);
+#pragma unroll
+      for (int b = 0; b < 2; ++b) sc[b] = w4_scale(p[b * 512]);
     };
     f32x16 acc[TM][2];
 #pragma unroll
@@ -173,52 +202,72 @@ __global__ __launch_bounds__(WM * WN * 64) void w4_gemm_kernel(W4Args a, int a_b
 
     wait_loads<0>();
     lds_barrier();  // the previous tile's output has left LDS
+    const unsigned char* frag_base = smem + (wm * WTM + fr) * 128;
+    const int sw = (fr >> 1) & 7;
+    u32x4 xf[XP][TM], wf[2][2];
+    auto read_row = [&](int st, int j, int x, int i) {
+      xf[x][i] = ld16(frag_base + (st % NS) * STAGE + (x * BM + i * S) * 128 + (((fq * 4 + j) ^ sw) << 4));
+    };
     // the waits count loads: these groups must be issued in this order
     auto fence = [] { asm volatile("" ::: "memory"); };
+    load_scales(0);
+    load_scales(1);
+    fence();
     load_rows(0);
     fence();
+    load_codes(0, 0);
     load_rows(1);
     fence();
-    load_codes(0, 0);
-    fence();
+    load_codes(1, 1);
     load_rows(2);
     fence();
-    load_codes(1, 1);
+    load_codes(2, 2);
+    load_rows(3);
+    wait_loads<2 * LOADS>();
+    lds_barrier();
+    stage_scales(0);
+#pragma unroll
+    for (int x = 0; x < XP; ++x)
+#pragma unroll
+      for (int i = 0; i < TM; ++i) read_row(0, 0, x, i);
+#pragma unroll
+    for (int b = 0; b < 2; ++b) wf[0][b] = w4_to_bf16(cw[0][b][0], sc[b]);
     auto stage = [&](int s, auto U) {
-      constexpr int u = decltype(U)::value;
-      wait_loads<2 * LOADS>();  // stage s has landed: at most its two successors are in flight
-      lds_barrier();
-      load_rows(s + NS - 1);
-      const unsigned char* base = smem + (s % NS) * STAGE + (wm * WTM + fr) * 128;
-      const int sw = (fr >> 1) & 7;
-      u32x4 wf[2][4];
+      constexpr int u = decltype(U)::value, un = (u + 1) % 3;
 #pragma unroll
-      for (int b = 0; b < 2; ++b) {
-        const float sc = w4_scale(cs[u][b]);
+      for (int j = 0; j < 4; ++j) {
+        if (j < 3) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) wf[b][j] = w4_to_bf16(cw[u][b][j], sc);
-      }
-      load_codes(s + 2, u);
+          for (int b = 0; b < 2; ++b) wf[(j + 1) & 1][b] = w4_to_bf16(cw[u][b][j + 1], sc[b]);
+        } else {
+          wait_loads<2 * LOADS>();  // stage s + 1 has landed: at most its two successors are in flight
+          lds_barrier();
+          load_codes(s + 3, u);
+          load_rows(s + NS);
+          if (((s + 1) & 7) == 0) load_scales(((s + 1) >> 3) + 1);
+          stage_scales(s + 1);
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
+          for (int b = 0; b < 2; ++b) wf[0][b] = w4_to_bf16(cw[un][b][0], sc[b]);
+        }
+        // a row fragment is read again, for the next step, as soon as this step has used it
 #pragma unroll
-        for (int p = 0; p < XP; ++p) {
-          u32x4 xf[TM];
+        for (int x = 0; x < XP; ++x)
 #pragma unroll
-          for (int i = 0; i < TM; ++i) xf[i] = ld16(base + (p * BM + i * S) * 128 + (((fq * 4 + j) ^ sw) << 4));
-#pragma unroll
-          for (int i = 0; i < TM; ++i)
+          for (int i = 0; i < TM; ++i) {
             if (i < mb) {
-              const u32x4 b[1] = {xf[i]};
-              const u32x4 w0[1] = {wf[0][j]}, w1[1] = {wf[1][j]};
+              const u32x4 b[1] = {xf[x][i]};
+              const u32x4 w0[1] = {wf[j & 1][0]}, w1[1] = {wf[j & 1][1]};
               Op32::step(acc[i][0], w0, b);
               Op32::step(acc[i][1], w1, b);
             }
-        }
+            read_row(j < 3 ? s : s + 1, (j + 1) & 3, x, i);
+          }
+      }
     };
-    for (int s = 0; s < nk; s += 2) {
+    for (int s = 0; s < nk; s += 3) {
       stage(s, std::integral_constant<int, 0>{});
       if (s + 1 < nk) stage(s + 1, std::integral_constant<int, 1>{});
+      if (s + 2 < nk) stage(s + 2, std::integral_constant<int, 2>{});
     }
     // epilogue through LDS: lane l holds row l % 32 of a block and four consecutive columns per group of registers
     // (Op32::out_row); 16-byte chunk c of output row r sits at c ^ (r & 15)
