@@ -39,17 +39,6 @@ struct W4Args {
 
 __device__ __forceinline__ float silu(float g) { return g / (1.0f + expf(-g)); }
 
-// the last index i in [0, n) with first[i] * scale <= v (first ascending, first[0] = 0)
-__device__ __forceinline__ int find_expert(const int* first, int n, int scale, int v) {
-  int lo = 0, hi = n;
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (first[mid] * scale <= v) lo = mid;
-    else hi = mid;
-  }
-  return lo;
-}
-
 // This workgroup's tiles out of `total`: the list is cut into eight contiguous ranges, one per XCD (workgroup b runs
 // on XCD b % 8), so tiles that share weights or rows meet in one L2.
 struct Tiles {
@@ -101,26 +90,36 @@ __global__ __launch_bounds__(WM * WN * 64) void w4_gemm_kernel(W4Args a, int a_b
   constexpr int BODY = NS * STAGE > OP * OUT_BYTES ? NS * STAGE : OP * OUT_BYTES;
   constexpr int LOADS = XI + 2;  // loads per wave and stage: rows and codes
   constexpr int OOB = 0x7ffffff0;
+  static_assert(PARTS == 1 || WM == 1, "parts share a matrix step within one wave row");
   static_assert(TM >= 1 && XP * BM / 8 % NW == 0 && OUTC >= 128, "tile");
   // the only LDS object (a second one makes the compiler wait for every load in flight before LDS reads): the
-  // stages, which the output tile reuses, then its destination rows, then the waves' scales
-  __shared__ __attribute__((aligned(1024))) unsigned char smem[BODY + BM * 4 + NW * 2048];
+  // stages, which the output tile reuses, then its destination rows, the waves' scales, the
+  // plan's starts
+  __shared__ __attribute__((aligned(1024))) unsigned char smem[BODY + BM * 4 + NW * 2048 + 2 * (MOE_MAX_EXPERTS + 1) * 4];
   int tid = threadIdx.x, lane = tid & 63;  // made opaque at each tile start (below)
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wm = wave / WN, wn = wave % WN;
   int fr = lane & 31, fq = lane >> 5;
   const int K = a.K, nk = (K + 63) / 64;
   const int kc = (K + W4_TILE_K - 1) / W4_TILE_K, ks = (K + W4_STILE_K - 1) / W4_STILE_K;
-  const int* row_start = a.plan + 2;
-  const int* tile_start = a.plan + 3 + a.El;
+  // the plan's row and tile starts in LDS: a search through memory costs a microsecond per step at each tile
+  int* row_start = reinterpret_cast<int*>(smem + BODY + BM * 4 + NW * 2048);
+  int* tile_start = row_start + MOE_MAX_EXPERTS + 1;
+  for (int i = tid; i <= a.El; i += NTH) {
+    row_start[i] = a.plan[2 + i];
+    tile_start[i] = a.plan[3 + a.El + i];
+  }
   const int n_tiles = (a.N + OUTC - 1) / OUTC;
   const Tiles mine = my_tiles(a.plan[0] * n_tiles);
   const __amdgpu_buffer_rsrc_t a_rsrc = __builtin_amdgcn_make_buffer_rsrc((void*)a.A, (short)0, a_bytes, 0x00020000);
+  lds_barrier();
+  int l = 0;
   for (int tile = mine.begin; tile < mine.end; tile += mine.step) {
     // per-lane values are computed again in each tile: kept across the tile loop they do not fit the registers next
     // to the accumulators
     asm volatile("" : "+v"(tid), "+v"(lane), "+v"(fr), "+v"(fq));
-    const int l = __builtin_amdgcn_readfirstlane(find_expert(tile_start, a.El, n_tiles, tile));
+    // tiles list (expert, N tile, M tile) in expert order and a workgroup's tiles increase: scan on
+    while (__builtin_amdgcn_readfirstlane(tile_start[l + 1]) * n_tiles <= tile) ++l;
     const int ts = __builtin_amdgcn_readfirstlane(tile_start[l]);
     const int mt_l = __builtin_amdgcn_readfirstlane(tile_start[l + 1]) - ts;
     const int local = tile - ts * n_tiles;
@@ -202,7 +201,10 @@ __global__ __launch_bounds__(WM * WN * 64) void w4_gemm_kernel(W4Args a, int a_b
 
     wait_loads<0>();
     lds_barrier();  // the previous tile's output has left LDS
-    const unsigned char* frag_base = smem + (wm * WTM + fr) * 128;
+    // With two parts and at most 16 rows, both parts share a matrix step: its columns 0 .. 15 are the rows' first
+    // parts and 16 .. 31 their second ones, which the epilogue adds up.
+    const bool packed = XP == 2 && m_rows <= 16;
+    const unsigned char* frag_base = smem + (packed ? (fr >> 4) * BM + (fr & 15) : wm * WTM + fr) * 128;
     const int sw = (fr >> 1) & 7;
     u32x4 xf[XP][TM], wf[2][2];
     auto read_row = [&](int st, int j, int x, int i) {
@@ -254,6 +256,7 @@ __global__ __launch_bounds__(WM * WN * 64) void w4_gemm_kernel(W4Args a, int a_b
         for (int x = 0; x < XP; ++x)
 #pragma unroll
           for (int i = 0; i < TM; ++i) {
+            if (x == 1 && packed) continue;
             if (i < mb) {
               const u32x4 b[1] = {xf[x][i]};
               const u32x4 w0[1] = {wf[j & 1][0]}, w1[1] = {wf[j & 1][1]};
@@ -273,6 +276,12 @@ __global__ __launch_bounds__(WM * WN * 64) void w4_gemm_kernel(W4Args a, int a_b
     // (Op32::out_row); 16-byte chunk c of output row r sits at c ^ (r & 15)
     wait_loads<0>();
     lds_barrier();
+    if (packed) {
+#pragma unroll
+      for (int b = 0; b < 2; ++b)
+#pragma unroll
+        for (int q = 0; q < 16; ++q) acc[0][b][q] += __shfl_xor(acc[0][b][q], 16, 64);
+    }
     int* s_orow = reinterpret_cast<int*>(smem + BODY);
     for (int r = tid; r < BM; r += NTH) {
       const int p = p0 + min(r, m_rows - 1);
