@@ -89,6 +89,9 @@ __global__ __launch_bounds__(WM * WN * 64) void w4_gemm_kernel(W4Args a, int a_b
   constexpr int OUT_BYTES = BM * OUTC * 2;
   constexpr int BODY = NS * STAGE > OP * OUT_BYTES ? NS * STAGE : OP * OUT_BYTES;
   constexpr int LOADS = XI + 2;  // loads per wave and stage: rows and codes
+  // stages of codes in flight: three are what the registers leave next to 128 accumulators, and enough where several
+  // workgroups share a CU; the 128-row tiles run alone on theirs, often with few tiles to hide a miss behind
+  constexpr int CS = BM == 128 ? 6 : 3;
   constexpr int OOB = 0x7ffffff0;
   static_assert(PARTS == 1 || WM == 1, "parts share a matrix step within one wave row");
   static_assert(TM >= 1 && XP * BM / 8 % NW == 0 && OUTC >= 128, "tile");
@@ -145,6 +148,18 @@ __global__ __launch_bounds__(WM * WN * 64) void w4_gemm_kernel(W4Args a, int a_b
       const int p = p0 + min(r, m_rows - 1);
       voff[q] = a.a_perm ? a.a_perm[p] : p;
     }
+    u32x4 cw[CS][2];
+    auto load_codes = [&](int st, int u) {
+      const int s = min(st, nk - 1);
+#pragma unroll
+      for (int b = 0; b < 2; ++b) cw[u][b] = ld16(wc[b] + ((s >> 1) * W4_CODE_TILE + (s & 1) * 512) + c_off);
+    };
+    // the first codes are requested while the row lookups are on their way
+    auto fence = [] { asm volatile("" ::: "memory"); };
+    fence();
+#pragma unroll
+    for (int u = 0; u < CS - 3; ++u) load_codes(u, u);
+    fence();
 #pragma unroll
     for (int q = 0; q < XI; ++q) {
       const int v = (wave * XI + q) * 8 + (lane >> 3), r = v % BM;
@@ -166,12 +181,6 @@ __global__ __launch_bounds__(WM * WN * 64) void w4_gemm_kernel(W4Args a, int a_b
         __builtin_amdgcn_raw_ptr_buffer_load_lds(a_rsrc, (__attribute__((address_space(3))) void*)(base + q * 1024), 16,
                                                  vo, 0, 0, 0);
       }
-    };
-    u32x4 cw[3][2];
-    auto load_codes = [&](int st, int u) {
-      const int s = min(st, nk - 1);
-#pragma unroll
-      for (int b = 0; b < 2; ++b) cw[u][b] = ld16(wc[b] + ((s >> 1) * W4_CODE_TILE + (s & 1) * 512) + c_off);
     };
     // scale tiles q of the wave's four 16-row blocks (1 KB) to its LDS, slot q & 1
     unsigned char* s_sc = smem + BODY + BM * 4 + wave * 2048;
@@ -211,19 +220,18 @@ __global__ __launch_bounds__(WM * WN * 64) void w4_gemm_kernel(W4Args a, int a_b
       xf[x][i] = ld16(frag_base + (st % NS) * STAGE + (x * BM + i * S) * 128 + (((fq * 4 + j) ^ sw) << 4));
     };
     // the waits count loads: these groups must be issued in this order
-    auto fence = [] { asm volatile("" ::: "memory"); };
     load_scales(0);
     load_scales(1);
     fence();
     load_rows(0);
     fence();
-    load_codes(0, 0);
+    load_codes(CS - 3, CS - 3);
     load_rows(1);
     fence();
-    load_codes(1, 1);
+    load_codes(CS - 2, CS - 2);
     load_rows(2);
     fence();
-    load_codes(2, 2);
+    load_codes(CS - 1, CS - 1);
     load_rows(3);
     wait_loads<2 * LOADS>();
     lds_barrier();
@@ -235,7 +243,7 @@ __global__ __launch_bounds__(WM * WN * 64) void w4_gemm_kernel(W4Args a, int a_b
 #pragma unroll
     for (int b = 0; b < 2; ++b) wf[0][b] = w4_to_bf16(cw[0][b][0], sc[b]);
     auto stage = [&](int s, auto U) {
-      constexpr int u = decltype(U)::value, un = (u + 1) % 3;
+      constexpr int u = decltype(U)::value, un = (u + 1) % CS;
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         if (j < 3) {
@@ -244,7 +252,7 @@ __global__ __launch_bounds__(WM * WN * 64) void w4_gemm_kernel(W4Args a, int a_b
         } else {
           wait_loads<2 * LOADS>();  // stage s + 1 has landed: at most its two successors are in flight
           lds_barrier();
-          load_codes(s + 3, u);
+          load_codes(s + CS, u);
           load_rows(s + NS);
           if (((s + 1) & 7) == 0) load_scales(((s + 1) >> 3) + 1);
           stage_scales(s + 1);
@@ -267,10 +275,15 @@ __global__ __launch_bounds__(WM * WN * 64) void w4_gemm_kernel(W4Args a, int a_b
           }
       }
     };
-    for (int s = 0; s < nk; s += 3) {
+    for (int s = 0; s < nk; s += CS) {
       stage(s, std::integral_constant<int, 0>{});
       if (s + 1 < nk) stage(s + 1, std::integral_constant<int, 1>{});
       if (s + 2 < nk) stage(s + 2, std::integral_constant<int, 2>{});
+      if constexpr (CS > 3) {
+        if (s + 3 < nk) stage(s + 3, std::integral_constant<int, 3>{});
+        if (s + 4 < nk) stage(s + 4, std::integral_constant<int, 4>{});
+        if (s + 5 < nk) stage(s + 5, std::integral_constant<int, 5>{});
+      }
     }
     // epilogue through LDS: lane l holds row l % 32 of a block and four consecutive columns per group of registers
     // (Op32::out_row); 16-byte chunk c of output row r sits at c ^ (r & 15)
