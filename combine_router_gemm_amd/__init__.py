@@ -12,6 +12,7 @@ unless `stream` is given.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 from typing import Optional
 
@@ -212,6 +213,7 @@ def moe_w4_scales_bytes(rows: int, K: int) -> int:
     return int(load_library().moe_w4_scales_bytes(rows, K))
 
 
+@functools.lru_cache(maxsize=1024)
 def moe_w4_shapes(*shape: int) -> tuple:
     """Shapes of the packed codes and scales (uint8) of weights [.., N, K]."""
     *lead, N, K = shape
@@ -469,73 +471,123 @@ def moe_expert_mlp_fp8(send_q: torch.Tensor, send_scale: torch.Tensor, layout: L
 # ------------------------------------------------------------------------------------------------
 # 4-bit expert weights
 # ------------------------------------------------------------------------------------------------
+# The calls from here on take a few microseconds on the device, as long as a handful of attribute lookups take on the
+# host: their checks are one pass over the arguments, and the sizes they ask the library for are remembered by shape.
 
-def _w4_ptrs(codes: torch.Tensor, scales: torch.Tensor, shape, name: str, device):
-    cs, ss = moe_w4_shapes(*shape)
-    return (_ptr(codes, f"{name} codes", torch.uint8, cs, device),
-            _ptr(scales, f"{name} scales", torch.uint8, ss, device))
+def _device(t: torch.Tensor, name: str) -> int:
+    """Index of the device of a call's first tensor, which has to be the current one."""
+    dev = t.get_device()
+    if dev < 0:
+        raise MoeError(f"{name} must be a device tensor")
+    if dev != torch.cuda.current_device():
+        raise MoeError(f"{name} is on device {dev}, the current one is {torch.cuda.current_device()}")
+    return dev
+
+
+def _arg(t: torch.Tensor, name: str, dtype, shape, dev: int) -> Optional[int]:
+    """Device pointer of a contiguous tensor of this type and shape on device `dev` (None without elements)."""
+    if t.dtype is not dtype:
+        raise MoeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.shape != shape:
+        raise MoeError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if t.get_device() != dev:
+        raise MoeError(f"{name} is on {t.device}, expected device {dev}")
+    if not t.is_contiguous():
+        raise MoeError(f"{name} must be contiguous")
+    return t.data_ptr() or None
+
+
+def _raw_stream(stream, dev: int) -> int:
+    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream)
+
+
+_size = functools.lru_cache(maxsize=1024)(lambda name, *args: int(getattr(load_library(), name)(*args)))
+
+
+def _scratch(nbytes: int, workspace: Optional[torch.Tensor], dev: int, stream):
+    """(pointer, bytes) of the caller's workspace or of a temporary one, and the tensor that holds it."""
+    ws = _workspace(nbytes, workspace, dev, stream)
+    if ws is None:
+        return None, 0, None
+    if ws.get_device() != dev or not ws.is_contiguous():
+        raise MoeError(f"workspace must be a contiguous tensor on device {dev}")
+    return ws.data_ptr() or None, _nbytes(ws), ws
 
 
 def moe_quantize_w4(w: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor, stream=None) -> None:
     """Weights [.., N, K] (f32 or bf16) to packed 4-bit codes and scales of the shapes moe_w4_shapes(*w.shape)."""
-    dev = w.device
-    pc, ps = _w4_ptrs(codes, scales, w.shape, "w", dev)
-    K = w.shape[-1]
-    st = load_library().moe_quantize_w4(_ptr(w, "w", device=dev), _dtype_code(w), w.numel() // K if K else 0, K, pc, ps,
-                                        _stream(stream))
-    _check(st, "moe_quantize_w4")
+    cs, ss = moe_w4_shapes(*w.shape)
+    dev, K = _device(w, "w"), w.shape[-1]
+    st = load_library().moe_quantize_w4(
+        _arg(w, "w", w.dtype, w.shape, dev), _dtype_code(w), w.numel() // K if K else 0, K,
+        _arg(codes, "codes", torch.uint8, cs, dev), _arg(scales, "scales", torch.uint8, ss, dev),
+        _raw_stream(stream, dev))
+    if st:
+        _check(st, "moe_quantize_w4")
 
 
 def moe_dequantize_w4(codes: torch.Tensor, scales: torch.Tensor, w: torch.Tensor, stream=None) -> None:
     """The values packed codes and scales stand for, into w [.., N, K] (f32 or bf16, both exact)."""
-    dev = w.device
-    pc, ps = _w4_ptrs(codes, scales, w.shape, "w", dev)
-    K = w.shape[-1]
-    st = load_library().moe_dequantize_w4(pc, ps, w.numel() // K if K else 0, K, _ptr(w, "w", device=dev),
-                                          _dtype_code(w), _stream(stream))
-    _check(st, "moe_dequantize_w4")
+    cs, ss = moe_w4_shapes(*w.shape)
+    dev, K = _device(w, "w"), w.shape[-1]
+    st = load_library().moe_dequantize_w4(
+        _arg(codes, "codes", torch.uint8, cs, dev), _arg(scales, "scales", torch.uint8, ss, dev),
+        w.numel() // K if K else 0, K, _arg(w, "w", w.dtype, w.shape, dev), _dtype_code(w), _raw_stream(stream, dev))
+    if st:
+        _check(st, "moe_dequantize_w4")
+
+
+def _expert_shapes(El: int, F: int, H: int):
+    """Packed shapes of the experts' gate/up and down weights: (codes, scales) of each."""
+    return moe_w4_shapes(El, 2 * F, H) + moe_w4_shapes(El, H, F)
 
 
 def moe_expert_mlp_w4(send_buf: torch.Tensor, layout: Layout, gu_codes: torch.Tensor, gu_scales: torch.Tensor,
                       dn_codes: torch.Tensor, dn_scales: torch.Tensor, out_buf: torch.Tensor,
                       workspace: Optional[torch.Tensor] = None, stream=None) -> None:
     """Expert SwiGLU MLP on dispatched bf16 rows with packed 4-bit weights ([El, 2F, H] and [El, H, F])."""
-    dev = send_buf.device
+    dev = _device(send_buf, "send_buf")
     L = layout
-    El = L.E // L.R
     F = gu_codes.shape[1] * 8
-    _ptr(send_buf, "send_buf", torch.bfloat16, (L.rows_max, L.H), dev)
-    gc, gs = _w4_ptrs(gu_codes, gu_scales, (El, 2 * F, L.H), "gate/up", dev)
-    dc, ds = _w4_ptrs(dn_codes, dn_scales, (El, L.H, F), "down", dev)
-    _ptr(out_buf, "out_buf", torch.bfloat16, (L.rows_max, L.H), dev)
-    ws = _workspace(moe_expert_mlp_w4_workspace_bytes(L.T, L.k, L.E, L.R, L.C, F), workspace, dev, stream)
+    gc, gs, dc, ds = _expert_shapes(L.E // L.R, F, L.H)
+    u8, rows = torch.uint8, (L.rows_max, L.H)
+    need = _size("moe_expert_mlp_w4_workspace_bytes", L.T, L.k, L.E, L.R, L.C, F)
+    p_ws, n_ws, ws = _scratch(need, workspace, dev, stream)
     cl = L.c_struct()
     st = load_library().moe_expert_mlp_w4(
-        _ptr(send_buf, "send_buf"), ctypes.byref(cl), gc, gs, dc, ds, F, _ptr(out_buf, "out_buf"),
-        _ptr(ws, "workspace"), _nbytes(ws), _stream(stream))
-    _check(st, "moe_expert_mlp_w4")
+        _arg(send_buf, "send_buf", torch.bfloat16, rows, dev), ctypes.byref(cl),
+        _arg(gu_codes, "gu_codes", u8, gc, dev), _arg(gu_scales, "gu_scales", u8, gs, dev),
+        _arg(dn_codes, "dn_codes", u8, dc, dev), _arg(dn_scales, "dn_scales", u8, ds, dev), F,
+        _arg(out_buf, "out_buf", torch.bfloat16, rows, dev), p_ws, n_ws, _raw_stream(stream, dev))
+    if st:
+        _check(st, "moe_expert_mlp_w4")
 
 
 # ------------------------------------------------------------------------------------------------
 # the whole layer for a few tokens
 # ------------------------------------------------------------------------------------------------
 
-def _decode_outputs(x, w_router, logit_bias, k, logits, topk_ids, topk_w, y):
-    """Checks shared by the two calls; returns (T, H, E, bias row stride)."""
+def _layer(name, x, w_router, logit_bias, k, R, C, F, weights, logits, topk_ids, topk_w, y, workspace, stream):
+    """The call shared by moe_layer_decode and moe_layer_decode_w4: `weights` are (tensor, name, type, shape)."""
+    dev, dt = _device(x, "x"), x.dtype
     T, H = x.shape
     E = w_router.shape[0]
-    dev = x.device
-    stride = 0
+    f32 = torch.float32
+    bias, stride = None, 0
     if logit_bias is not None:
         stride = 0 if logit_bias.dim() == 1 else E
-        _ptr(logit_bias, "logit_bias", torch.float32, (T, E) if stride else (E,), dev)
-    _ptr(x, "x", device=dev)
-    _ptr(w_router, "w_router", torch.float32, (E, H), dev)
-    _ptr(logits, "logits", torch.float32, (T, E), dev)
-    _ptr(topk_ids, "topk_ids", torch.int32, (T, k), dev)
-    _ptr(topk_w, "topk_w", torch.float32, (T, k), dev)
-    _ptr(y, "y", x.dtype, (T, H), dev)
-    return T, H, E, stride
+        bias = _arg(logit_bias, "logit_bias", f32, (T, E) if stride else (E,), dev)
+    code = _dtype_code(x)
+    p_ws, n_ws, ws = _scratch(_size("moe_layer_decode_workspace_bytes", T, H, E, k, F, code), workspace, dev, stream)
+    fn = getattr(load_library(), name)
+    head = (_arg(x, "x", dt, (T, H), dev),) + (() if name.endswith("w4") else (code,))
+    st = fn(*head, _arg(w_router, "w_router", f32, (E, H), dev), bias, stride, T, H, E, R, k, C, F,
+            *[_arg(t, n, d, s, dev) for t, n, d, s in weights],
+            _arg(logits, "logits", f32, (T, E), dev), _arg(topk_ids, "topk_ids", torch.int32, (T, k), dev),
+            _arg(topk_w, "topk_w", f32, (T, k), dev), _arg(y, "y", dt, (T, H), dev), p_ws, n_ws,
+            _raw_stream(stream, dev))
+    if st:
+        _check(st, name)
 
 
 def moe_layer_decode(x: torch.Tensor, w_router: torch.Tensor, logit_bias: Optional[torch.Tensor], k: int, R: int,
@@ -544,18 +596,11 @@ def moe_layer_decode(x: torch.Tensor, w_router: torch.Tensor, logit_bias: Option
                      workspace: Optional[torch.Tensor] = None, stream=None) -> None:
     """The whole layer (route, dispatch with capacity C, expert MLP, combine) for at most MOE_DECODE_MAX_TOKENS
     tokens: writes logits, topk_ids, topk_w and y."""
-    T, H, E, stride = _decode_outputs(x, w_router, logit_bias, k, logits, topk_ids, topk_w, y)
-    dev, dt = x.device, _dtype_code(x)
-    F = w_gate_up.shape[1] // 2
-    El = E // R if R > 0 else 0
-    _ptr(w_gate_up, "w_gate_up", x.dtype, (El, 2 * F, H), dev)
-    _ptr(w_down, "w_down", x.dtype, (El, H, F), dev)
-    ws = _workspace(moe_layer_decode_workspace_bytes(T, H, E, k, F, dt), workspace, dev, stream)
-    st = load_library().moe_layer_decode(
-        _ptr(x, "x"), dt, _ptr(w_router, "w_router"), _ptr(logit_bias, "logit_bias"), stride, T, H, E, R, k, C, F,
-        _ptr(w_gate_up, "w_gate_up"), _ptr(w_down, "w_down"), _ptr(logits, "logits"), _ptr(topk_ids, "topk_ids"),
-        _ptr(topk_w, "topk_w"), _ptr(y, "y"), _ptr(ws, "workspace"), _nbytes(ws), _stream(stream))
-    _check(st, "moe_layer_decode")
+    H, F = x.shape[1], w_gate_up.shape[1] // 2
+    El = w_router.shape[0] // R if R > 0 else 0
+    weights = ((w_gate_up, "w_gate_up", x.dtype, (El, 2 * F, H)), (w_down, "w_down", x.dtype, (El, H, F)))
+    _layer("moe_layer_decode", x, w_router, logit_bias, k, R, C, F, weights, logits, topk_ids, topk_w, y, workspace,
+           stream)
 
 
 def moe_layer_decode_w4(x: torch.Tensor, w_router: torch.Tensor, logit_bias: Optional[torch.Tensor], k: int, R: int,
@@ -563,16 +608,11 @@ def moe_layer_decode_w4(x: torch.Tensor, w_router: torch.Tensor, logit_bias: Opt
                         dn_scales: torch.Tensor, logits: torch.Tensor, topk_ids: torch.Tensor, topk_w: torch.Tensor,
                         y: torch.Tensor, workspace: Optional[torch.Tensor] = None, stream=None) -> None:
     """moe_layer_decode with packed 4-bit expert weights ([El, 2F, H] and [El, H, F]) and bf16 activations."""
-    T, H, E, stride = _decode_outputs(x, w_router, logit_bias, k, logits, topk_ids, topk_w, y)
-    dev = x.device
-    _ptr(x, "x", torch.bfloat16)
-    F = gu_codes.shape[1] * 8
-    El = E // R if R > 0 else 0
-    gc, gs = _w4_ptrs(gu_codes, gu_scales, (El, 2 * F, H), "gate/up", dev)
-    dc, ds = _w4_ptrs(dn_codes, dn_scales, (El, H, F), "down", dev)
-    ws = _workspace(moe_layer_decode_workspace_bytes(T, H, E, k, F, MOE_BF16), workspace, dev, stream)
-    st = load_library().moe_layer_decode_w4(
-        _ptr(x, "x"), _ptr(w_router, "w_router"), _ptr(logit_bias, "logit_bias"), stride, T, H, E, R, k, C, F,
-        gc, gs, dc, ds, _ptr(logits, "logits"), _ptr(topk_ids, "topk_ids"), _ptr(topk_w, "topk_w"), _ptr(y, "y"),
-        _ptr(ws, "workspace"), _nbytes(ws), _stream(stream))
-    _check(st, "moe_layer_decode_w4")
+    if x.dtype is not torch.bfloat16:
+        raise MoeError(f"x must be torch.bfloat16, got {x.dtype}")
+    F, u8 = gu_codes.shape[1] * 8, torch.uint8
+    gc, gs, dc, ds = _expert_shapes(w_router.shape[0] // R if R > 0 else 0, F, x.shape[1])
+    weights = ((gu_codes, "gu_codes", u8, gc), (gu_scales, "gu_scales", u8, gs), (dn_codes, "dn_codes", u8, dc),
+               (dn_scales, "dn_scales", u8, ds))
+    _layer("moe_layer_decode_w4", x, w_router, logit_bias, k, R, C, F, weights, logits, topk_ids, topk_w, y,
+           workspace, stream)

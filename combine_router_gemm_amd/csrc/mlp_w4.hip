@@ -92,6 +92,7 @@ __global__ __launch_bounds__(WM * WN * 64) void w4_gemm_kernel(W4Args a, int a_b
   // stages of codes in flight: three are what the registers leave next to 128 accumulators, and enough where several
   // workgroups share a CU; the 128-row tiles run alone on theirs, often with few tiles to hide a miss behind
   constexpr int CS = BM == 128 ? 6 : 3;
+  constexpr int XB = BM == 256 ? 1 : 2;      // buffers of row fragments
   constexpr int OOB = 0x7ffffff0;
   static_assert(PARTS == 1 || WM == 1, "parts share a matrix step within one wave row");
   static_assert(TM >= 1 && XP * BM / 8 % NW == 0 && OUTC >= 128, "tile");
@@ -215,9 +216,9 @@ __global__ __launch_bounds__(WM * WN * 64) void w4_gemm_kernel(W4Args a, int a_b
     const bool packed = XP == 2 && m_rows <= 16;
     const unsigned char* frag_base = smem + (packed ? (fr >> 4) * BM + (fr & 15) : wm * WTM + fr) * 128;
     const int sw = (fr >> 1) & 7;
-    u32x4 xf[XP][TM], wf[2][2];
+    u32x4 xf[XB][XP][TM], wf[2][2];
     auto read_row = [&](int st, int j, int x, int i) {
-      xf[x][i] = ld16(frag_base + (st % NS) * STAGE + (x * BM + i * S) * 128 + (((fq * 4 + j) ^ sw) << 4));
+      xf[j & (XB - 1)][x][i] = ld16(frag_base + (st % NS) * STAGE + (x * BM + i * S) * 128 + (((fq * 4 + j) ^ sw) << 4));
     };
     // the waits count loads: these groups must be issued in this order
     load_scales(0);
@@ -259,19 +260,25 @@ __global__ __launch_bounds__(WM * WN * 64) void w4_gemm_kernel(W4Args a, int a_b
 #pragma unroll
           for (int b = 0; b < 2; ++b) wf[0][b] = w4_to_bf16(cw[un][b][0], sc[b]);
         }
-        // a row fragment is read again, for the next step, as soon as this step has used it
+        // the next step's row fragments: before this step's products where there are registers for two sets, else
+        // each as soon as this step has used it
+        if constexpr (XB == 2) {
+#pragma unroll
+          for (int x = 0; x < XP; ++x)
+#pragma unroll
+            for (int i = 0; i < TM; ++i) read_row(j < 3 ? s : s + 1, (j + 1) & 3, x, i);
+        }
 #pragma unroll
         for (int x = 0; x < XP; ++x)
 #pragma unroll
           for (int i = 0; i < TM; ++i) {
-            if (x == 1 && packed) continue;
-            if (i < mb) {
-              const u32x4 b[1] = {xf[x][i]};
+            if (i < mb && !(x == 1 && packed)) {
+              const u32x4 b[1] = {xf[j & (XB - 1)][x][i]};
               const u32x4 w0[1] = {wf[j & 1][0]}, w1[1] = {wf[j & 1][1]};
               Op32::step(acc[i][0], w0, b);
               Op32::step(acc[i][1], w1, b);
             }
-            read_row(j < 3 ? s : s + 1, (j + 1) & 3, x, i);
+            if constexpr (XB == 1) read_row(j < 3 ? s : s + 1, (j + 1) & 3, x, i);
           }
       }
     };
