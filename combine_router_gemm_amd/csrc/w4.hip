@@ -46,20 +46,18 @@ __device__ __forceinline__ int group_exponent(float a) {
   return min(125, max(-120, E));
 }
 
-// The E2M1 code of v = w / 2^E (exact: a power of two, and v is far from float32's smallest values wherever a
-// rounding border is near): the number of borders between neighbouring magnitudes below |v|, a border itself
-// going to the even code.
-__device__ __forceinline__ uint32_t e2m1_code(float v) {
-  const float a = fabsf(v);
-  uint32_t c = 0;
-  c += a > 0.25f;
-  c += a >= 0.75f;
-  c += a > 1.25f;
-  c += a >= 1.75f;
-  c += a > 2.5f;
-  c += a >= 3.5f;
-  c += a > 5.0f;
-  return c | ((__float_as_uint(v) >> 28) & 8u);
+// The E2M1 codes of eight values over 2^E, the first in the low four bits: v_cvt_scalef32_pk_fp4_f32 divides by the
+// scale, rounds to nearest with ties to the even code, clamps to +-6 and keeps the sign of zero, two values per
+// instruction. Counting the seven borders below each value by comparisons instead took 136-155 us against 91 for
+// 8 x 4096 x 7168 bf16 weights: 20 operations a weight made the vector units the bound.
+__device__ __forceinline__ uint32_t e2m1_codes(const float (&v)[8], int E) {
+  const float scale = __uint_as_float((uint32_t)(127 + E) << 23);
+  uint32_t w = 0;
+  w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, v[0], v[1], scale, 0);
+  w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, v[2], v[3], scale, 1);
+  w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, v[4], v[5], scale, 2);
+  w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, v[6], v[7], scale, 3);
+  return w;
 }
 
 template <typename T>
@@ -89,10 +87,7 @@ __global__ __launch_bounds__(W4_NTH) void quantize_w4_kernel(const T* __restrict
       for (int q = 0; q < 8; ++q) a = fmaxf(a, fabsf(v[i][q]));
       a = quad_max(in ? a : 0.f);
       const int E = group_exponent(a);
-      const float inv = __uint_as_float((uint32_t)(127 - E) << 23);
-      uint32_t word = 0;
-#pragma unroll
-      for (int q = 0; q < 8; ++q) word |= e2m1_code(v[i][q] * inv) << (4 * q);
+      const uint32_t word = e2m1_codes(v[i], E);
       const int r = wave * W4_RPW + i;
       const int own = r + 16 * (g & 3);  // the tile lane that owns this group
       s_codes[(g >> 2) * (W4_CODE_TILE / 4) + own * 4 + (lane & 3)] = in ? word : 0u;
