@@ -55,62 +55,81 @@ __device__ __forceinline__ int w4_place(int k) {
 // ------------------------------------------------------------------------------------------------
 // router
 // ------------------------------------------------------------------------------------------------
-// One workgroup per expert and TB tokens: its 256 threads share the fp32 weight row, every thread takes eight
+// One workgroup per EB experts and TB tokens: its 256 threads share the fp32 weight rows, every thread takes eight
 // consecutive k at a time (exact products, at most ceil(H / 2048) * 8 fp32 additions in a row), then a fixed
-// tree of additions.
+// tree of additions. Bound by the reads of x and the weights from L2: EB experts share one read of x.
 template <typename T>
-__device__ __forceinline__ void load8(const T* p, float (&v)[8]);
-template <>
-__device__ __forceinline__ void load8<bf16_t>(const bf16_t* p, float (&v)[8]) {
-  unpack(ld16(p), v);
-}
-template <>
-__device__ __forceinline__ void load8<float>(const float* p, float (&v)[8]) {
-  unpack(ld16(p), *reinterpret_cast<float(*)[4]>(&v[0]));
-  unpack(ld16(p + 4), *reinterpret_cast<float(*)[4]>(&v[4]));
+__device__ __forceinline__ void unpack8(const u32x4 (&v)[sizeof(T) / 2], float (&o)[8]) {
+  if constexpr (sizeof(T) == 2) {
+    unpack(v[0], o);
+  } else {
+    unpack(v[0], *reinterpret_cast<float(*)[4]>(&o[0]));
+    unpack(v[1], *reinterpret_cast<float(*)[4]>(&o[4]));
+  }
 }
 
-template <typename T, int TB>
+template <typename T, int TB, int EB>
 __global__ __launch_bounds__(256) void decode_route_kernel(const T* __restrict__ x, const float* __restrict__ w,
                                                            const float* __restrict__ bias, int64_t bias_stride, int T_,
                                                            int H, int E, float* __restrict__ logits,
                                                            bf16_t* __restrict__ placed) {
-  __shared__ float s_sum[4][TB];
-  const int e = blockIdx.x, t0 = blockIdx.y * TB;
+  __shared__ float s_sum[4][EB][TB];
+  const int e0 = blockIdx.x * EB, t0 = blockIdx.y * TB;
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  float acc[TB];
+  float acc[EB][TB];
 #pragma unroll
-  for (int j = 0; j < TB; ++j) acc[j] = 0.f;
+  for (int i = 0; i < EB; ++i)
+#pragma unroll
+    for (int j = 0; j < TB; ++j) acc[i][j] = 0.f;
+  constexpr int XV = (int)sizeof(T) / 2;  // 16-byte vectors of eight elements
   for (int c = tid * 8; c < H; c += 2048) {
-    float wv[8];
-    load8(w + (int64_t)e * H + c, wv);
+    u32x4 wr[EB][2], xr[TB][XV];
+#pragma unroll
+    for (int i = 0; i < EB; ++i)
+#pragma unroll
+      for (int q = 0; q < 2; ++q) wr[i][q] = ld16(w + (int64_t)min(e0 + i, E - 1) * H + c + 4 * q);
+#pragma unroll
+    for (int j = 0; j < TB; ++j)
+#pragma unroll
+      for (int q = 0; q < XV; ++q) xr[j][q] = ld16(x + (int64_t)min(t0 + j, T_ - 1) * H + c + Vec<T>::N * q);
+    __builtin_amdgcn_sched_barrier(0);  // all requested before the first is waited for
+    float wv[EB][8];
+#pragma unroll
+    for (int i = 0; i < EB; ++i) unpack8<float>(wr[i], wv[i]);
 #pragma unroll
     for (int j = 0; j < TB; ++j) {
       float xv[8];
-      load8(x + (int64_t)min(t0 + j, T_ - 1) * H + c, xv);
+      unpack8<T>(xr[j], xv);
 #pragma unroll
-      for (int q = 0; q < 8; ++q) acc[j] = fmaf(xv[q], wv[q], acc[j]);
+      for (int i = 0; i < EB; ++i)
+#pragma unroll
+        for (int q = 0; q < 8; ++q) acc[i][j] = fmaf(xv[q], wv[i][q], acc[i][j]);
     }
   }
 #pragma unroll
-  for (int j = 0; j < TB; ++j) {
-    const float s = wave_sum(acc[j]);
-    if (lane == 0) s_sum[wave][j] = s;
-  }
+  for (int i = 0; i < EB; ++i)
+#pragma unroll
+    for (int j = 0; j < TB; ++j) {
+      const float s = wave_sum(acc[i][j]);
+      if (lane == 0) s_sum[wave][i][j] = s;
+    }
   __syncthreads();
   if constexpr (sizeof(T) == 2) {
     if (placed) {  // x in w4_place order, by all workgroups together
       const int n = min(TB, T_ - t0) * (H / 8);
-      for (int c = e * 256 + tid; c < n; c += E * 256) {
+      for (int c = blockIdx.x * 256 + tid; c < n; c += gridDim.x * 256) {
         const int t = t0 + c / (H / 8), k = c % (H / 8) * 8;
         st16(placed + (int64_t)t * w4_pitch(H) + w4_place(k), ld16(x + (int64_t)t * H + k));
       }
     }
   }
-  if (tid < TB && t0 + tid < T_) {
-    float v = (s_sum[0][tid] + s_sum[1][tid]) + (s_sum[2][tid] + s_sum[3][tid]);
-    if (bias) v += bias[(int64_t)(t0 + tid) * bias_stride + e];
-    logits[(int64_t)(t0 + tid) * E + e] = v;
+  if (tid < EB * TB) {
+    const int i = tid / TB, j = tid % TB, e = e0 + i, t = t0 + j;
+    if (e < E && t < T_) {
+      float v = (s_sum[0][i][j] + s_sum[1][i][j]) + (s_sum[2][i][j] + s_sum[3][i][j]);
+      if (bias) v += bias[(int64_t)t * bias_stride + e];
+      logits[(int64_t)t * E + e] = v;
+    }
   }
 }
 
@@ -802,15 +821,22 @@ __global__ __launch_bounds__((Down<T, W4>::NTH), 4) void decode_down_kernel(Deco
 template <typename T>
 void launch_route_rows(const T* x, const float* w, const float* bias, int64_t bias_stride, int T_, int H, int E,
                        float* logits, bf16_t* placed, hipStream_t stream) {
-  auto go = [&](auto tb) {
-    constexpr int TB = decltype(tb)::value;
-    decode_route_kernel<T, TB><<<dim3(E, ceil_div_host(T_, TB)), 256, 0, stream>>>(x, w, bias, bias_stride, T_, H, E,
-                                                                                   logits, placed);
+  auto go = [&](auto tb, auto eb) {
+    constexpr int TB = decltype(tb)::value, EB = decltype(eb)::value;
+    decode_route_kernel<T, TB, EB><<<dim3(ceil_div_host(E, EB), ceil_div_host(T_, TB)), 256, 0, stream>>>(
+        x, w, bias, bias_stride, T_, H, E, logits, placed);
   };
-  if (T_ == 1) go(std::integral_constant<int, 1>{});
-  else if (T_ <= 2) go(std::integral_constant<int, 2>{});
-  else if (T_ <= 4) go(std::integral_constant<int, 4>{});
-  else go(std::integral_constant<int, 8>{});
+  using C1 = std::integral_constant<int, 1>;
+  using C2 = std::integral_constant<int, 2>;
+  using C4 = std::integral_constant<int, 4>;
+  // Four tokens and as many experts as leave a few workgroups per CU: a workgroup's loads of a step are all in flight
+  // together. 384 experts, H 7168 (us): 32 tokens 4 x 4 9.4, 8 x 2 9.8, 8 x 4 10.6, 8 x 1 11.5; 16 tokens 4 x 2 6.7,
+  // 8 x 1 7.5, 8 x 4 9.0
+  if (T_ == 1) go(C1{}, C1{});
+  else if (T_ == 2) go(C2{}, C1{});
+  else if (T_ <= 4 || E < 128) go(C4{}, C1{});
+  else if (T_ <= 16 || E < 256) go(C4{}, C2{});
+  else go(C4{}, C4{});
 }
 
 template <typename T, bool W4>
