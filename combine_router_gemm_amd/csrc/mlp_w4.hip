@@ -6,10 +6,12 @@
 // operand it is (w4.h), and a lane ends up with four consecutive output columns of one row.
 //
 //   w4_gemm_kernel  BM rows x 64 WN weight rows per tile on v_mfma_f32_32x32x16_bf16. Rows go to LDS directly; the
-//                   codes go from memory to the registers of the wave that multiplies them and never pass LDS. BM = 32
-//                   and 64 (four waves, several workgroups per CU) stream the codes of experts with few rows and are
-//                   bound by their bytes; BM = 128 and 256 (eight waves) are bound by the matrix units.
+//                   codes go from memory to the registers of the wave that multiplies them and never pass LDS.
+//                   BM = 32 (four waves, up to four workgroups per CU) streams the codes of experts with few rows and
+//                   is bound by their bytes; BM = 128 and 256 (eight waves, one workgroup per CU) are bound by the
+//                   matrix units.
 #include <algorithm>
+#include <cmath>
 #include <type_traits>
 
 #include "common.h"
@@ -345,7 +347,7 @@ int w4_grid(int64_t tiles, int64_t most) {
   return (int)std::max<int64_t>(g, 1);
 }
 
-// workgroups per CU: the LDS of BM = 32 and 64 lets several stay resident
+// workgroups per CU: the registers and LDS of BM = 32 let four stay resident
 template <int BM, int WM, int WN, int PARTS>
 void launch_gemms(const W4Args& gu, const W4Args& dn, int64_t rows, int64_t mtiles, int num_cus, hipStream_t stream) {
   constexpr int PER_CU = WM * WN == 4 ? 4 : 1, NTH = WM * WN * 64;
@@ -356,10 +358,27 @@ void launch_gemms(const W4Args& gu, const W4Args& dn, int64_t rows, int64_t mtil
           dn, (int)((PARTS == 2 ? dn.part * 2 : 0) + rows * dn.K * 2));
 }
 
-// rows per M tile: the capacity per local expert bounds its rows
-int w4_rows(int64_t rows_max, int El) {
+// Rows per M tile, by the time the gate/up pass would take with each, from the largest tile counts the capacity allows.
+// A round of 256-row tiles, one per CU, is the unit; a round of 128-row tiles takes 0.57 of it, and 32-row tiles, up to
+// four per CU, 0.2 and 0.27 for each tile a CU holds: they wait on memory, not on the matrix units. Whole passes (us):
+//   experts, H, F, rows each      32     128     256
+//   32, 7168, 2048, 32           198     252     377
+//   32, 7168, 2048, 96           408     353     436
+//   32, 7168, 2048, 192          814     662     584
+//   8, 4096, 14336, 64           334     346     489
+//   8, 4096, 14336, 256         1054     720     798
+//   4, 2048, 1024, 256            39      56      88
+//   4, 2048, 1024, 1024           93      70      99
+//   12, 1184, 736, 64             28      35      50
+// (64-row tiles with two workgroups per CU were never more than 8 % better than the best of these, and often worse.)
+int w4_rows(int64_t rows_max, int El, int F, int num_cus) {
   const int64_t per = ceil_div_host64(rows_max, El);
-  return per <= 32 ? 32 : per <= 64 ? 64 : per <= 192 ? 128 : 256;
+  auto tiles = [&](int bm) { return (double)El * ceil_div_host64(per, bm) * ceil_div_host(F, 128) / num_cus; };
+  const double t32 = tiles(32), full = std::floor(t32 / 4.0), rest = t32 - 4.0 * full;
+  const double c32 = full * 1.28 + (rest > 0 ? 0.2 + 0.27 * rest : 0.0);
+  const double c128 = 0.57 * std::ceil(tiles(128)), c256 = std::ceil(tiles(256));
+  if (c32 <= c128 && c32 <= c256) return 32;
+  return c128 <= c256 ? 128 : 256;
 }
 
 }  // namespace
@@ -384,7 +403,7 @@ hipError_t launch_expert_mlp_w4(const void* send_buf, const moe_layout_t& L, con
   ws += align256((size_t)rows * sizeof(int));
   bf16_t* h = reinterpret_cast<bf16_t*>(ws);
   const int64_t h_part = (int64_t)(align256((size_t)rows * (size_t)F * 2) / 2);
-  const int bm = w4_rows(rows, El);
+  const int bm = w4_rows(rows, El, F, num_cus);
   launch_mlp_plan(L, bm, plan, perm, stream);
   W4Args gu{};
   gu.A = static_cast<const bf16_t*>(send_buf);
@@ -413,7 +432,6 @@ hipError_t launch_expert_mlp_w4(const void* send_buf, const moe_layout_t& L, con
   dn.El = El;
   const int64_t mtiles = ceil_div_host64(rows, bm) + El;
   if (bm == 32) launch_gemms<32, 1, 4, 2>(gu, dn, rows, mtiles, num_cus, stream);
-  else if (bm == 64) launch_gemms<64, 1, 4, 2>(gu, dn, rows, mtiles, num_cus, stream);
   else if (bm == 128) launch_gemms<128, 2, 4, 1>(gu, dn, rows, mtiles, num_cus, stream);
   else launch_gemms<256, 2, 4, 1>(gu, dn, rows, mtiles, num_cus, stream);
   return hipGetLastError();
