@@ -316,11 +316,22 @@ template <typename T>
 struct DecOp;
 template <>
 struct DecOp<bf16_t> {
-  using Op = Op16;
+  static constexpr int VPF = Op16::VPF;
+  static __device__ __forceinline__ void step(f32x4& acc, const u32x4 (&a)[1], const u32x4 (&b)[1]) {
+    Op16::step(acc, a, b);
+  }
 };
+// f32: the eight products of a step are summed apart and then added, so that the roundings of a long K stay those of
+// K / 256 additions per wave rather than of K / 32 (y is off by 3.6e-7 of its norm at H 4096, F 14336)
 template <>
 struct DecOp<float> {
-  using Op = OpF32;
+  static constexpr int VPF = OpF32::VPF;
+  static __device__ __forceinline__ void step(f32x4& acc, const u32x4 (&a)[2], const u32x4 (&b)[2]) {
+    f32x4 part = {0.f, 0.f, 0.f, 0.f};
+    OpF32::step(part, a, b);
+#pragma unroll
+    for (int q = 0; q < 4; ++q) acc[q] += part[q];
+  }
 };
 
 // Columns (rows of x or h) are read with buffer loads: a lane without one, or past K, reads at an offset beyond the
@@ -341,7 +352,7 @@ struct RowStep {
   static constexpr int VN = Vec<T>::N;
   static constexpr int STEP = 128 / (int)sizeof(T);  // k per step
   static constexpr int KST = STEP / 32;              // matrix steps of 32 k
-  static constexpr int VPF = DecOp<T>::Op::VPF;
+  static constexpr int VPF = DecOp<T>::VPF;
   static constexpr int XV = KST * VPF;               // vectors of a column's fragment per step
   static constexpr int LDS_BYTES = SETS * 16 * DEC_PITCH;
   struct Regs {
@@ -518,7 +529,6 @@ struct GateUp {
         s0 = stop;
       }
     } else {
-      using Op = typename DecOp<T>::Op;
       const T* W = static_cast<const T*>(a.w_gu) + l * 2 * F * K;
       const T* rows[4];
 #pragma unroll
@@ -553,8 +563,8 @@ struct GateUp {
                 u32x4 b[RS::VPF];
 #pragma unroll
                 for (int q = 0; q < RS::VPF; ++q) b[q] = rx[u][nb][kk * RS::VPF + q];
-                Op::step(acc[0][0][nb], fg, b);
-                Op::step(acc[1][0][nb], fu, b);
+                DecOp<T>::step(acc[0][0][nb], fg, b);
+                DecOp<T>::step(acc[1][0][nb], fu, b);
               }
             }
             load(st + PF * NW, u);
@@ -746,7 +756,7 @@ struct Down {
                 u32x4 b[RS::VPF];
 #pragma unroll
                 for (int q = 0; q < RS::VPF; ++q) b[q] = rx[u][nb][kk * RS::VPF + q];
-                DecOp<T>::Op::step(acc[0][nb], f, b);
+                DecOp<T>::step(acc[0][nb], f, b);
               }
             }
             load(s0 + u + PF, u);
