@@ -41,7 +41,7 @@ struct DecodeArgs {
   void* y;              // [T, H]
   Choice* choice;       // written by the gate/up kernel, read by the down kernel
   void* h;              // [T * k, F] by row of Choice: fp32, or for bf16 layers the bf16 nearest to h and then
-                        // [T * k, F] its remainder; with 4-bit weights in rows like x's
+                        // [T * k, F] its remainder; with 4-bit weights rows of both parts, at w4_place2
 };
 
 // With 4-bit weights the matrix step j of 128 k takes k = 32 g + 8 j .. + 7 from lane group g (W4Step). Rows of x and h
@@ -51,6 +51,8 @@ __host__ __device__ __forceinline__ int w4_pitch(int K) { return (K + W4_TILE_K 
 __device__ __forceinline__ int w4_place(int k) {
   return (k & ~(W4_TILE_K - 1)) + ((k >> 3) & 3) * 32 + ((k >> 5) & 3) * 8 + (k & 7);
 }
+// the same for the first of h's two parts, each 32 elements of it followed by those of the second
+__device__ __forceinline__ int w4_place2(int k) { return w4_place(k) * 2 - (((k >> 5) & 3) * 8 + (k & 7)); }
 
 // ------------------------------------------------------------------------------------------------
 // router
@@ -425,12 +427,13 @@ struct W4Step {
   __device__ __forceinline__ static float scale(const unsigned char* lds, int b, int t0, int step, int lane) {
     return w4_scale(lds[(b * CHUNK + (step >> 2) - t0) * W4_SCALE_TILE + lane * 4 + (step & 3)]);
   }
+  template <int PARTS>
   __device__ __forceinline__ static void load_col(u32x4 (&x)[XV], __amdgpu_buffer_rsrc_t r, int row, int step, int K,
                                                   int lane) {
     const bool in = row >= 0 && step * STEP + (lane >> 4) * 32 < K;
-    const int off = in ? row + step * (STEP * 2) + (lane >> 4) * 16 : DEC_NONE;
+    const int off = in ? row + step * (STEP * 2 * PARTS) + (lane >> 4) * 16 : DEC_NONE;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) x[j] = ld_col(r, off + j * 64);
+    for (int j = 0; j < 4; ++j) x[j] = ld_col(r, off + j * (64 * PARTS));
   }
 };
 
@@ -493,7 +496,7 @@ struct GateUp {
         const int s = min(st, end - 1);
         ws.load(rw[u], s, lane);
 #pragma unroll
-        for (int nb = 0; nb < NB; ++nb) WS::load_col(rx[u][nb], xr, cols[nb], s, K, lane);
+        for (int nb = 0; nb < NB; ++nb) WS::template load_col<1>(rx[u][nb], xr, cols[nb], s, K, lane);
       };
       for (int s0 = wave * per; s0 < end;) {
         const int t0 = s0 >> 2, stop = min(end, (t0 + WS::CHUNK) * 4);
@@ -594,12 +597,13 @@ struct GateUp {
           u += red_w[(((CB + cb) * NB + nb) * 4 + q) * 64 + ln];
         }
         const float h = silu(g) * u;
-        const int hp = W4 ? w4_pitch(F) : F;
-        const int64_t at = (int64_t)(row0 + r) * hp + (W4 ? w4_place(f) : f);
+        // 4-bit weights: the two parts of 32 elements side by side, a 128-byte line per row and fragment load
+        const int64_t at = W4 ? (int64_t)(row0 + r) * w4_pitch(F) * 2 + w4_place2(f) : (int64_t)(row0 + r) * F + f;
+        const int64_t lo = W4 ? 32 : (int64_t)a.T * a.k * F;
         if constexpr (sizeof(T) == 2) {
           const bf16_t hi = (bf16_t)h;
           static_cast<bf16_t*>(a.h)[at] = hi;
-          static_cast<bf16_t*>(a.h)[(int64_t)a.T * a.k * hp + at] = (bf16_t)(h - (float)hi);
+          static_cast<bf16_t*>(a.h)[at + lo] = (bf16_t)(h - (float)hi);
         } else {
           static_cast<float*>(a.h)[at] = h;
         }
@@ -667,11 +671,12 @@ struct Down {
     const int64_t l = __builtin_amdgcn_readfirstlane(c.expert[i]);
     const int row0 = __builtin_amdgcn_readfirstlane(c.row0[i]) + r0;
     const int cnt = __builtin_amdgcn_readfirstlane(c.row0[i + 1]) - row0;
-    const int pitch = W4 ? w4_pitch(K) : K;
-    const int64_t part = (int64_t)a.T * a.k * pitch;  // elements of one part of h
+    // elements of a row of h, and from its first to its second part
+    const int pitch = W4 ? w4_pitch(K) * 2 : K;
+    const int64_t part = W4 ? 32 : (int64_t)a.T * a.k * K;
     const __amdgpu_buffer_rsrc_t hr = __builtin_amdgcn_make_buffer_rsrc(
         (char*)a.h + (int64_t)row0 * pitch * (int)sizeof(T), (short)0,
-        (int)((sizeof(T) == 2 ? part : 0) + (int64_t)cnt * pitch) * (int)sizeof(T), 0x00020000);
+        (int)((sizeof(T) == 2 && !W4 ? part : 0) + (int64_t)cnt * pitch) * (int)sizeof(T), 0x00020000);
     int cols[NB];
 #pragma unroll
     for (int nb = 0; nb < NB; ++nb) {
@@ -694,7 +699,7 @@ struct Down {
         const int s = min(st, s_end - 1);
         ws.load(rw[u], s, lane);
 #pragma unroll
-        for (int nb = 0; nb < NB; ++nb) WS::load_col(rx[u][nb], hr, cols[nb], s, K, lane);
+        for (int nb = 0; nb < NB; ++nb) WS::template load_col<2>(rx[u][nb], hr, cols[nb], s, K, lane);
       };
       for (int s0 = s_begin; s0 < s_end;) {
         const int t0 = s0 >> 2, stop = min(s_end, (t0 + WS::CHUNK) * 4);
