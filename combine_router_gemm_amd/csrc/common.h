@@ -93,6 +93,13 @@ __device__ __forceinline__ u32x4 pack(const float (&o)[8]) {
   return v;
 }
 
+// What a value's nearest bf16 leaves of it, for a second bf16 part: value - hi, or 0 where hi is infinite or NaN (the
+// difference would turn an infinite value into NaN).
+__device__ __forceinline__ float bf16_rest(float v) {
+  const float d = v - (float)(bf16_t)v;
+  return fabsf(d) <= 3.4e38f ? d : 0.f;
+}
+
 // ------------------------------------------------------------------------------------------------
 // wave helpers
 // ------------------------------------------------------------------------------------------------

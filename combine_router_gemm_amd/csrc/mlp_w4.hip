@@ -325,7 +325,7 @@ __global__ __launch_bounds__(WM * WN * 64) void w4_gemm_kernel(W4Args a, int a_b
           *reinterpret_cast<u32x2*>(o) = u32x2{pack2_bf16(v[0], v[1]), pack2_bf16(v[2], v[3])};
           if constexpr (OP == 2) {
 #pragma unroll
-            for (int q = 0; q < 4; ++q) v[q] -= (float)(bf16_t)v[q];
+            for (int q = 0; q < 4; ++q) v[q] = bf16_rest(v[q]);
             *reinterpret_cast<u32x2*>(o + OUT_BYTES) = u32x2{pack2_bf16(v[0], v[1]), pack2_bf16(v[2], v[3])};
           }
         }

@@ -363,7 +363,8 @@ size_t moe_expert_mlp_w4_workspace_bytes(int T, int k, int E, int R, int C, int 
 
 /*
  * moe_expert_mlp_w4 -- moe_expert_mlp with 4-bit weights: every weight enters the GEMMs as the bf16 value its
- * code stands for (exact); everything else is moe_expert_mlp in bf16.
+ * code stands for (exact); everything else is moe_expert_mlp in bf16, but that h keeps 16 significant bits (two
+ * bf16 parts) where 32-row tiles run (few rows per expert, or few tiles).
  *   send_buf   [rows_max, H] bf16 rows written by moe_dispatch
  *   layout     the layout moe_dispatch filled (expert_kept / expert_offset are read on the device)
  *   gu_codes, gu_scales  packed [El, 2F, H]: rows 0..F-1 of an expert are Wg, rows F..2F-1 are Wu
@@ -380,7 +381,8 @@ int moe_expert_mlp_w4(const void* send_buf, const moe_layout_t* layout, const ui
 
 /*
  * moe_layer_decode -- the whole layer (route, dispatch, expert MLP, combine) for at most
- * MOE_DECODE_MAX_TOKENS tokens in two kernels, with no send buffer and no layout.
+ * MOE_DECODE_MAX_TOKENS tokens in three launches (router; choice of experts and gate/up; down and combine), with
+ * no send buffer and no layout.
  *   logits, topk_ids, topk_w  as moe_route defines them
  *   y[t] = sum over kept slots j of topk_w[t,j] * (silu(x Wg[l]^T) * (x Wu[l]^T)) Wd[l]^T with l = e mod El
  *          for expert e = topk_ids[t,j] (El = E / R); pair (t, j) is kept iff fewer than C earlier tokens

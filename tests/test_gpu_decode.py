@@ -170,6 +170,22 @@ def test_a_bad_token_or_expert_reaches_no_other_token(w4):
     assert not torch.isfinite(got[3][0].float()).all()
 
 
+@pytest.mark.parametrize("w4", [False, True])
+def test_an_infinite_h_stays_infinite(w4):
+    """h beyond bf16's range is an infinity, as it is when stored as bf16; its second part must not make it NaN."""
+    H = F = 32
+    inp = inputs("inf", 1, H, 2, 1, F, 1, torch.bfloat16, "uniform", 8)
+    inp["x"].fill_(1.0)
+    for n in ("w_gate_up", "w_down"):
+        inp[n].zero_()
+    inp["w_gate_up"][:, 3, 0] = 2.0 ** 100
+    inp["w_gate_up"][:, F + 3, 0] = 2.0 ** 100     # h_3 = 2^200
+    inp["w_down"].fill_(1.0)
+    packs = pack4(inp["w_gate_up"])[0] + pack4(inp["w_down"])[0] if w4 else None
+    y = Run(inp, 1, 1, 1, packs)().y
+    assert torch.all(y == float("inf"))
+
+
 def test_zero_tokens_write_nothing():
     inp = inputs("none", 4, 64, 8, 2, 32, 1, torch.bfloat16, "uniform", 6)
     inp["x"] = inp["x"][:0]

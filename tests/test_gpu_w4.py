@@ -162,6 +162,22 @@ def test_expert_mlp_w4_keeps_non_finite_rows_apart():
     assert bad[6] and bad[27] and int(bad.sum()) == 2
 
 
+def test_expert_mlp_w4_infinite_h_stays_infinite():
+    counts, H, F = [2, 20], 32, 32
+    L, send, _, _ = case(counts, 22, 1, 1, 22, H, F, 12)
+    send.fill_(1.0)
+    gu = torch.zeros(2, 2 * F, H, dtype=torch.bfloat16, device=DEV)
+    gu[:, 3, 0] = gu[:, F + 3, 0] = 2.0 ** 100
+    packs = []
+    for w in (gu, torch.ones(2, H, F, dtype=torch.bfloat16, device=DEV)):
+        c, s = packed(w.shape[1], w.shape[2], (2,))
+        moe.moe_quantize_w4(w, c, s)
+        packs += [c, s]
+    out = torch.zeros(L.rows_max, H, dtype=torch.bfloat16, device=DEV)
+    moe.moe_expert_mlp_w4(send.to(DEV), L, *packs, out)
+    assert torch.all(out[:22] == float("inf"))
+
+
 def test_expert_mlp_w4_graph_and_side_stream():
     counts = [20, 7, 0, 33]
     L, send, packs, _ = case(counts, 40, 2, 1, 40, 160, 96, 10)
