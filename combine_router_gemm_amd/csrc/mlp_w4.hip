@@ -37,6 +37,10 @@ struct W4Args {
   const int* out_perm;   // destination row of a plan row, or nullptr
   const int* plan;
   int El;
+  // SPLIT: K in `split` parts of split_stages stages (a multiple of 8) each, their fp32 sums to partial [split, rows, N]
+  int split, split_stages;
+  float* partial;
+  int64_t partial_stride;  // elements of one part
 };
 
 __device__ __forceinline__ float silu(float g) { return g / (1.0f + expf(-g)); }
@@ -81,8 +85,10 @@ __device__ __forceinline__ void wait_loads() {
 //    that read nothing, so at least as many are in flight at every wait as it counts on.
 // PARTS: h has two bf16 parts (16 significant bits) where few rows make the weights' bytes the bound, so that the
 // down pass's doubled matrix work is free, and one where the matrix units are the bound.
-template <int BM, int WM, int WN, bool GATED, int PARTS>
+// SPLIT: the down pass with K cut over workgroups, where its tiles are few and its K long (see w4_split).
+template <int BM, int WM, int WN, bool GATED, int PARTS, bool SPLIT = false>
 __global__ __launch_bounds__(WM * WN * 64) void w4_gemm_kernel(W4Args a, int a_bytes) {
+  static_assert(!SPLIT || !GATED, "the gate/up pass is not split");
   constexpr int NW = WM * WN, NTH = NW * 64, S = 32, NS = 4;
   constexpr int WTM = BM / WM, TM = WTM / S;
   constexpr int XP = GATED ? 1 : PARTS, OP = GATED ? PARTS : 1;  // parts of the rows read and written
@@ -116,11 +122,13 @@ __global__ __launch_bounds__(WM * WN * 64) void w4_gemm_kernel(W4Args a, int a_b
     tile_start[i] = a.plan[3 + a.El + i];
   }
   const int n_tiles = (a.N + OUTC - 1) / OUTC;
-  const Tiles mine = my_tiles(a.plan[0] * n_tiles);
+  const Tiles mine = my_tiles(a.plan[0] * n_tiles * (SPLIT ? a.split : 1));
   const __amdgpu_buffer_rsrc_t a_rsrc = __builtin_amdgcn_make_buffer_rsrc((void*)a.A, (short)0, a_bytes, 0x00020000);
   lds_barrier();
   int l = 0;
-  for (int tile = mine.begin; tile < mine.end; tile += mine.step) {
+  for (int unit = mine.begin; unit < mine.end; unit += mine.step) {
+    const int tile = SPLIT ? unit / a.split : unit, sp = SPLIT ? unit - tile * a.split : 0;
+    const int s_begin = SPLIT ? sp * a.split_stages : 0, s_end = SPLIT ? min(nk, s_begin + a.split_stages) : nk;
     // per-lane values are computed again in each tile: kept across the tile loop they do not fit the registers next
     // to the accumulators
     asm volatile("" : "+v"(tid), "+v"(lane), "+v"(fr), "+v"(fq));
@@ -161,7 +169,7 @@ __global__ __launch_bounds__(WM * WN * 64) void w4_gemm_kernel(W4Args a, int a_b
     auto fence = [] { asm volatile("" ::: "memory"); };
     fence();
 #pragma unroll
-    for (int u = 0; u < CS - 3; ++u) load_codes(u, u);
+    for (int u = 0; u < CS - 3; ++u) load_codes(s_begin + u, u);
     fence();
 #pragma unroll
     for (int q = 0; q < XI; ++q) {
@@ -223,26 +231,26 @@ __global__ __launch_bounds__(WM * WN * 64) void w4_gemm_kernel(W4Args a, int a_b
       xf[j & (XB - 1)][x][i] = ld16(frag_base + (st % NS) * STAGE + (x * BM + i * S) * 128 + (((fq * 4 + j) ^ sw) << 4));
     };
     // the waits count loads: these groups must be issued in this order
-    load_scales(0);
-    load_scales(1);
+    load_scales(s_begin >> 3);
+    load_scales((s_begin >> 3) + 1);
     fence();
-    load_rows(0);
+    load_rows(s_begin);
     fence();
-    load_codes(CS - 3, CS - 3);
-    load_rows(1);
+    load_codes(s_begin + CS - 3, CS - 3);
+    load_rows(s_begin + 1);
     fence();
-    load_codes(CS - 2, CS - 2);
-    load_rows(2);
+    load_codes(s_begin + CS - 2, CS - 2);
+    load_rows(s_begin + 2);
     fence();
-    load_codes(CS - 1, CS - 1);
-    load_rows(3);
+    load_codes(s_begin + CS - 1, CS - 1);
+    load_rows(s_begin + 3);
     wait_loads<2 * LOADS>();
     lds_barrier();
-    stage_scales(0);
+    stage_scales(s_begin);
 #pragma unroll
     for (int x = 0; x < XP; ++x)
 #pragma unroll
-      for (int i = 0; i < TM; ++i) read_row(0, 0, x, i);
+      for (int i = 0; i < TM; ++i) read_row(s_begin, 0, x, i);
 #pragma unroll
     for (int b = 0; b < 2; ++b) wf[0][b] = w4_to_bf16(cw[0][b][0], sc[b]);
     auto stage = [&](int s, auto U) {
@@ -284,14 +292,14 @@ __global__ __launch_bounds__(WM * WN * 64) void w4_gemm_kernel(W4Args a, int a_b
           }
       }
     };
-    for (int s = 0; s < nk; s += CS) {
+    for (int s = s_begin; s < s_end; s += CS) {
       stage(s, std::integral_constant<int, 0>{});
-      if (s + 1 < nk) stage(s + 1, std::integral_constant<int, 1>{});
-      if (s + 2 < nk) stage(s + 2, std::integral_constant<int, 2>{});
+      if (s + 1 < s_end) stage(s + 1, std::integral_constant<int, 1>{});
+      if (s + 2 < s_end) stage(s + 2, std::integral_constant<int, 2>{});
       if constexpr (CS > 3) {
-        if (s + 3 < nk) stage(s + 3, std::integral_constant<int, 3>{});
-        if (s + 4 < nk) stage(s + 4, std::integral_constant<int, 4>{});
-        if (s + 5 < nk) stage(s + 5, std::integral_constant<int, 5>{});
+        if (s + 3 < s_end) stage(s + 3, std::integral_constant<int, 3>{});
+        if (s + 4 < s_end) stage(s + 4, std::integral_constant<int, 4>{});
+        if (s + 5 < s_end) stage(s + 5, std::integral_constant<int, 5>{});
       }
     }
     // epilogue through LDS: lane l holds row l % 32 of a block and four consecutive columns per group of registers
@@ -303,6 +311,25 @@ __global__ __launch_bounds__(WM * WN * 64) void w4_gemm_kernel(W4Args a, int a_b
       for (int b = 0; b < 2; ++b)
 #pragma unroll
         for (int q = 0; q < 16; ++q) acc[0][b][q] += __shfl_xor(acc[0][b][q], 16, 64);
+    }
+    if constexpr (SPLIT) {
+      // lane l holds row l % 32 of a block and four consecutive columns per group of registers
+#pragma unroll
+      for (int i = 0; i < TM; ++i) {
+        const int r = wm * WTM + i * S + fr;
+        if (r < m_rows) {
+          float* o = a.partial + sp * a.partial_stride + (int64_t)(p0 + r) * a.N + c0 + 4 * fq;
+#pragma unroll
+          for (int b = 0; b < 2; ++b)
+#pragma unroll
+            for (int q4 = 0; q4 < 4; ++q4)
+              if (on[b]) {
+                const float v[4] = {acc[i][b][4 * q4], acc[i][b][4 * q4 + 1], acc[i][b][4 * q4 + 2], acc[i][b][4 * q4 + 3]};
+                st16(o + b * 32 + 8 * q4, pack(v));
+              }
+        }
+      }
+      continue;
     }
     int* s_orow = reinterpret_cast<int*>(smem + BODY);
     for (int r = tid; r < BM; r += NTH) {
@@ -341,6 +368,27 @@ __global__ __launch_bounds__(WM * WN * 64) void w4_gemm_kernel(W4Args a, int a_b
   }
 }
 
+// The parts of a split down pass added in order, rounded once and put into their rows: eight columns per thread.
+__global__ __launch_bounds__(256) void w4_sum_kernel(const float* __restrict__ partial, int split, int64_t stride,
+                                                     const int* __restrict__ plan, const int* __restrict__ perm, int N,
+                                                     bf16_t* __restrict__ out) {
+  const int64_t at = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 8;
+  const int64_t p = at / N;
+  if (p >= plan[1]) return;
+  float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+  for (int s = 0; s < split; ++s) {
+    float lo[4], hi[4];
+    unpack(ld16(partial + s * stride + at), lo);
+    unpack(ld16(partial + s * stride + at + 4), hi);
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      v[q] += lo[q];
+      v[4 + q] += hi[q];
+    }
+  }
+  st16(out + (int64_t)perm[p] * N + (at - p * N), pack(v));
+}
+
 int w4_grid(int64_t tiles, int64_t most) {
   int64_t g = std::min(tiles, most);
   if (g >= 8) g &= ~7ll;
@@ -348,35 +396,66 @@ int w4_grid(int64_t tiles, int64_t most) {
 }
 
 // workgroups per CU: the registers and LDS of BM = 32 let four stay resident
+constexpr int kPerCu32 = 4;
 template <int BM, int WM, int WN, int PARTS>
 void launch_gemms(const W4Args& gu, const W4Args& dn, int64_t rows, int64_t mtiles, int num_cus, hipStream_t stream) {
-  constexpr int PER_CU = WM * WN == 4 ? 4 : 1, NTH = WM * WN * 64;
+  constexpr int PER_CU = BM == 32 ? kPerCu32 : 1, NTH = WM * WN * 64;
   w4_gemm_kernel<BM, WM, WN, true, PARTS>
       <<<w4_grid(mtiles * ceil_div_host(gu.N, WN * 32), PER_CU * num_cus), NTH, 0, stream>>>(gu, (int)(rows * gu.K * 2));
-  w4_gemm_kernel<BM, WM, WN, false, PARTS>
-      <<<w4_grid(mtiles * ceil_div_host(dn.N, WN * 64), PER_CU * num_cus), NTH, 0, stream>>>(
-          dn, (int)((PARTS == 2 ? dn.part * 2 : 0) + rows * dn.K * 2));
+  const int a_bytes = (int)((PARTS == 2 ? dn.part * 2 : 0) + rows * dn.K * 2);
+  const int64_t tiles = mtiles * ceil_div_host(dn.N, WN * 64);
+  if constexpr (BM == 32) {
+    if (dn.split > 1) {
+      w4_gemm_kernel<BM, WM, WN, false, PARTS, true>
+          <<<w4_grid(tiles * dn.split, PER_CU * num_cus), NTH, 0, stream>>>(dn, a_bytes);
+      w4_sum_kernel<<<(unsigned)ceil_div_host64(rows * dn.N / 8, 256), 256, 0, stream>>>(
+          dn.partial, dn.split, dn.partial_stride, dn.plan, dn.out_perm, dn.N, dn.Out);
+      return;
+    }
+  }
+  w4_gemm_kernel<BM, WM, WN, false, PARTS><<<w4_grid(tiles, PER_CU * num_cus), NTH, 0, stream>>>(dn, a_bytes);
 }
 
-// Rows per M tile, by the time the gate/up pass would take with each, from the largest tile counts the capacity allows.
-// A round of 256-row tiles, one per CU, is the unit; a round of 128-row tiles takes 0.57 of it, and 32-row tiles, up to
-// four per CU, 0.2 and 0.27 for each tile a CU holds: they wait on memory, not on the matrix units. Whole passes (us):
+// Parts of the down pass's K with 32-row tiles: as many as give every CU its four workgroups, of 16 stages at least, and
+// no more than F / H, so that the parts' sums take no more workspace than h's two parts. 8 experts of 16 rows, H 4096,
+// F 14336 (128 tiles of 224 stages): the whole pass 241 -> 186 us; 4
+// experts of 16 rows, H 512, F 8192: 73 -> 30 us
+constexpr int kSplitMaxRows = 64;  // rows per expert
+int w4_split(int64_t rows_max, int El, int H, int F, int num_cus) {
+  const int64_t per = ceil_div_host64(rows_max, El);
+  if (per > kSplitMaxRows) return 1;
+  const int64_t tiles = El * ceil_div_host64(per, 32) * ceil_div_host(H, 256);
+  const int64_t s = std::min<int64_t>({kPerCu32 * num_cus / tiles, F / H, F / 64 / 16});
+  return s < 2 ? 1 : (int)s;
+}
+
+// Rows per M tile, by the time both passes would take with each, from the largest tile counts the capacity allows. A
+// round of 256-row tiles, one per CU, is the unit for every k; a round of 128-row tiles takes 0.57 of it, and 32-row
+// tiles, up to four per CU, 0.2 and 0.27 for each tile a CU holds: they wait on memory, not on the matrix units.
+// Whole passes (us):
 //   experts, H, F, rows each      32     128     256
 //   32, 7168, 2048, 32           198     252     377
 //   32, 7168, 2048, 96           408     353     436
 //   32, 7168, 2048, 192          814     662     584
-//   8, 4096, 14336, 64           334     346     489
+//   8, 4096, 14336, 128          559     461     563
 //   8, 4096, 14336, 256         1054     720     798
 //   4, 2048, 1024, 256            39      56      88
 //   4, 2048, 1024, 1024           93      70      99
 //   12, 1184, 736, 64             28      35      50
 // (64-row tiles with two workgroups per CU were never more than 8 % better than the best of these, and often worse.)
-int w4_rows(int64_t rows_max, int El, int F, int num_cus) {
+int w4_rows(int64_t rows_max, int El, int H, int F, int num_cus) {
   const int64_t per = ceil_div_host64(rows_max, El);
-  auto tiles = [&](int bm) { return (double)El * ceil_div_host64(per, bm) * ceil_div_host(F, 128) / num_cus; };
-  const double t32 = tiles(32), full = std::floor(t32 / 4.0), rest = t32 - 4.0 * full;
-  const double c32 = full * 1.28 + (rest > 0 ? 0.2 + 0.27 * rest : 0.0);
-  const double c128 = 0.57 * std::ceil(tiles(128)), c256 = std::ceil(tiles(256));
+  auto rounds = [&](int bm, int64_t n_tiles) {
+    const double t = (double)El * ceil_div_host64(per, bm) * n_tiles / num_cus;  // tiles per CU
+    if (bm == 256) return std::ceil(t);
+    if (bm == 128) return 0.57 * std::ceil(t);
+    const double full = std::floor(t / kPerCu32), rest = t - kPerCu32 * full;
+    return full * 1.28 + (rest > 0 ? 0.2 + 0.27 * rest : 0.0);
+  };
+  auto cost = [&](int bm, int split) {
+    return H * rounds(bm, ceil_div_host(F, 128)) + (double)F / split * rounds(bm, (int64_t)ceil_div_host(H, 256) * split);
+  };
+  const double c32 = cost(32, w4_split(rows_max, El, H, F, num_cus)), c128 = cost(128, 1), c256 = cost(256, 1);
   if (c32 <= c128 && c32 <= c256) return 32;
   return c128 <= c256 ? 128 : 256;
 }
@@ -387,7 +466,8 @@ bool mlp_w4_fits(int64_t rows, int H, int F) { return rows * std::max<int64_t>(H
 
 size_t mlp_w4_workspace_bytes(int64_t rows, int El, int F) {
   return align256(mlp_plan_ints(El) * sizeof(int)) + align256((size_t)rows * sizeof(int)) +
-         2 * align256((size_t)rows * (size_t)F * 2);
+         2 * align256((size_t)rows * (size_t)F * 2) +
+         (ceil_div_host64(rows, El) <= kSplitMaxRows ? align256((size_t)rows * (size_t)F * 4) : 0);
 }
 
 hipError_t launch_expert_mlp_w4(const void* send_buf, const moe_layout_t& L, const uint8_t* gu_codes,
@@ -403,7 +483,7 @@ hipError_t launch_expert_mlp_w4(const void* send_buf, const moe_layout_t& L, con
   ws += align256((size_t)rows * sizeof(int));
   bf16_t* h = reinterpret_cast<bf16_t*>(ws);
   const int64_t h_part = (int64_t)(align256((size_t)rows * (size_t)F * 2) / 2);
-  const int bm = w4_rows(rows, El, F, num_cus);
+  const int bm = w4_rows(rows, El, L.H, F, num_cus);
   launch_mlp_plan(L, bm, plan, perm, stream);
   W4Args gu{};
   gu.A = static_cast<const bf16_t*>(send_buf);
@@ -430,6 +510,14 @@ hipError_t launch_expert_mlp_w4(const void* send_buf, const moe_layout_t& L, con
   dn.out_perm = perm;
   dn.plan = plan;
   dn.El = El;
+  if (bm == 32) {
+    const int nk = ceil_div_host(F, 64);
+    dn.split = w4_split(rows, El, L.H, F, num_cus);
+    dn.split_stages = (ceil_div_host(nk, dn.split) + 7) & ~7;
+    dn.split = ceil_div_host(nk, dn.split_stages);  // every part has stages
+    dn.partial = reinterpret_cast<float*>(h + 2 * h_part);
+    dn.partial_stride = rows * L.H;
+  }
   const int64_t mtiles = ceil_div_host64(rows, bm) + El;
   if (bm == 32) launch_gemms<32, 1, 4, 2>(gu, dn, rows, mtiles, num_cus, stream);
   else if (bm == 128) launch_gemms<128, 2, 4, 1>(gu, dn, rows, mtiles, num_cus, stream);

@@ -128,6 +128,9 @@ CASES = [
     ("many_rows", [300, 129, 1, 513], 513, 2, 1, 513, 288, 352),
     ("many_rows_ranks", [257, 255, 256, 1, 400, 0], 700, 2, 3, 500, 640, 256),
     ("tall", [1500, 1025], 1500, 2, 1, 1500, 96, 160),
+    # F much wider than H and few tiles: the down pass splits its K, unevenly; with two ranks
+    ("split", [9, 0, 32, 1], 42, 1, 1, 42, 160, 2304),
+    ("split_ranks", [3, 16, 0, 1, 7, 20], 47, 1, 2, 20, 64, 4160),
     # enough tiles for 256 CUs that the 128- and the 256-row tiles run
     ("tile_128", [640, 129, 0, 1, 257, 500, 64, 33], 2560, 2, 1, 2560, 288, 2016),
     ("tile_256_ranks", [512, 1, 0, 300, 255, 17, 128, 33, 256, 0, 31, 90, 1, 700, 64, 129], 2048, 2, 2, 2048, 160, 2016),
