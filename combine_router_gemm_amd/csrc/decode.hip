@@ -436,10 +436,15 @@ __device__ __forceinline__ float silu(float g) { return g / (1.0f + expf(-g)); }
 // ------------------------------------------------------------------------------------------------
 // gate / up
 // ------------------------------------------------------------------------------------------------
-// A tile is one expert's 16 columns of h (32 with 4-bit weights). The eight waves split its K and add their sums
-// through LDS in wave order.
+// A tile is 16 columns of h (32 with 4-bit weights) for NB blocks of 16 rows of one expert. The eight waves split its K
+// and add their sums through LDS in wave order; the next tile's first loads are requested before that, so the weight
+// stream does not stop at a tile's end. With 4-bit weights NB is 1 and an expert of more than 16 rows is more than one
+// tile, its codes read again: two blocks need 19 registers more than two workgroups per CU leave, and a spilled register
+// is reloaded behind every load in flight (with that path compiled in, 25.6 -> 33.7 us for one token and 155 -> 173 us
+// for 32, DeepSeek-V3 and Kimi-K2 shares).
 template <typename T, bool W4, int NB>
 struct GateUp {
+  static_assert(!W4 || NB == 1, "see above");
   static constexpr int NW = DEC_GU_NW, NTH = NW * 64;
   static constexpr int CB = W4 ? 2 : 1;      // blocks of 16 columns
   static constexpr int COLS = CB * 16;
@@ -448,187 +453,197 @@ struct GateUp {
   static constexpr int PF = W4 ? 2 : NB == 1 ? 3 : 2;  // steps of loads in flight per wave
   static constexpr int RED = 2 * CB * NB * 4 * 64 * 4;
   static constexpr int STAGE = W4 ? WS::LDS_BYTES : RS::LDS_BYTES;
-  static constexpr int WAVE_LDS = W4 ? (RED > STAGE ? RED : STAGE) : STAGE;
-  static_assert(WAVE_LDS >= RED, "a wave's sums fit its LDS");
+  static constexpr int WAVE_LDS = RED > STAGE ? RED : STAGE;
   static constexpr int XV = W4 ? WS::XV : RS::XV;
 
-  // NB blocks of 16 of the expert's rows, from row r0 on
-  __device__ __forceinline__ static void tile(const DecodeArgs& a, const Choice& c, int i, int r0, int ft,
-                                              unsigned char* smem) {
+  __device__ __forceinline__ static void run(const DecodeArgs& a, const Choice& c, unsigned char* smem) {
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int K = a.H, F = a.F, f0 = ft * COLS;
-    const int64_t l = __builtin_amdgcn_readfirstlane(c.expert[i]);
-    const int row0 = __builtin_amdgcn_readfirstlane(c.row0[i]) + r0;
-    const int cnt = __builtin_amdgcn_readfirstlane(c.row0[i + 1]) - row0;
+    const int K = a.H, F = a.F;
+    const int nft = (F + COLS - 1) / COLS, total = c.n * nft;
     unsigned char* lds = smem + wave * WAVE_LDS;
     const int pitch = W4 ? w4_pitch(K) : K;
     const __amdgpu_buffer_rsrc_t xr =
         __builtin_amdgcn_make_buffer_rsrc((void*)a.x, (short)0, a.T * pitch * (int)sizeof(T), 0x00020000);
-    int cols[NB];
-#pragma unroll
-    for (int nb = 0; nb < NB; ++nb) {
-      const int r = nb * 16 + (lane & 15);
-      cols[nb] = r < cnt ? c.token[row0 + r] * pitch * (int)sizeof(T) : -1;
-    }
-    f32x4 acc[2][CB][NB];  // gate, up
-#pragma unroll
-    for (int s = 0; s < 2; ++s)
-#pragma unroll
-      for (int cb = 0; cb < CB; ++cb)
-#pragma unroll
-        for (int nb = 0; nb < NB; ++nb) acc[s][cb][nb] = f32x4{0.f, 0.f, 0.f, 0.f};
+    // K steps of this wave: a run of them with 4-bit weights (scales come by four tiles), every eighth else
+    constexpr int STEP = W4 ? WS::STEP : RS::STEP;
+    const int ns = (K + STEP - 1) / STEP, ks = (K + W4_STILE_K - 1) / W4_STILE_K;
+    const int per = (ns + NW - 1) / NW;
+    const int begin = W4 ? wave * per : wave, end = W4 ? min(ns, begin + per) : ns;
 
-    if constexpr (W4) {
-      const int kc = (K + W4_TILE_K - 1) / W4_TILE_K, ks = (K + W4_STILE_K - 1) / W4_STILE_K;
-      const int per = (kc + NW - 1) / NW, end = min(kc, (wave + 1) * per);
-      WS ws;
-#pragma unroll
-      for (int b = 0; b < 2 * CB; ++b)
-        ws.block(b, a.w_gu, a.s_gu, (l * 2 * F + (b >= CB ? F : 0) + f0) / 16 + b % CB, K);
-      u32x4 rw[PF][2 * CB], rx[PF][NB][XV];
-      auto load = [&](int st, int u) {
+    // the tile whose loads are requested next: tile index, expert, its rows from r0 on, first column
+    int tile = blockIdx.x, r0 = 0, row0 = 0, cnt = 0, f0 = 0;
+    int cols[NB];
+    WS ws;
+    const T* rows[4];
+    typename RS::Regs rr[W4 ? 1 : PF];
+    u32x4 rw[W4 ? PF : 1][2 * CB], rx[PF][NB][XV];
+    auto load = [&](int st, int u) {
+      if constexpr (W4) {
         const int s = min(st, end - 1);
         ws.load(rw[u], s, lane);
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb) WS::template load_col<1>(rx[u][nb], xr, cols[nb], s, K, lane);
-      };
-      for (int s0 = wave * per; s0 < end;) {
-        const int t0 = s0 >> 2, stop = min(end, (t0 + WS::CHUNK) * 4);
-        u32x4 sv[2 * CB];
-        ws.load_scales(sv, t0, ks, lane);
-#pragma unroll
-        for (int u = 0; u < PF; ++u) load(s0 + u, u);
-        WS::store_scales(sv, lds, lane);
-        for (; s0 < stop; s0 += PF) {
-#pragma unroll
-          for (int u = 0; u < PF; ++u) {
-            const int st = s0 + u;
-            if (st < stop) {
-              float sc[2 * CB];
-#pragma unroll
-              for (int b = 0; b < 2 * CB; ++b) sc[b] = WS::scale(lds, b, t0, st, lane);
-#pragma unroll
-              for (int j = 0; j < 4; ++j) {
-#pragma unroll
-                for (int b = 0; b < 2 * CB; ++b) {
-                  const u32x4 f[1] = {w4_to_bf16(rw[u][b][j], sc[b])};
-#pragma unroll
-                  for (int nb = 0; nb < NB; ++nb) {
-                    const u32x4 x[1] = {rx[u][nb][j]};
-                    Op16::step(acc[b / CB][b % CB][nb], f, x);
-                  }
-                }
-              }
-              load(st + PF, u);
-            }
-          }
-        }
-        s0 = stop;
-      }
-    } else {
-      const T* W = static_cast<const T*>(a.w_gu) + l * 2 * F * K;
-      const T* rows[4];
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const int f = min(f0 + (q & 1) * 8 + (lane >> 3), F - 1);
-        rows[q] = W + (int64_t)((q >> 1) * F + f) * K;
-      }
-      typename RS::Regs rw[PF];
-      u32x4 rx[PF][NB][XV];
-      const int ns = (K + RS::STEP - 1) / RS::STEP, last = ns - 1;
-      auto load = [&](int st, int u) {
-        const int s = min(st, last);
-        RS::load(rw[u], rows, s, K, lane);
+      } else {
+        const int s = min(st, ns - 1);
+        RS::load(rr[u], rows, s, K, lane);
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb) RS::load_col(rx[u][nb], xr, cols[nb], s, K, lane);
-      };
+      }
+    };
+    auto start = [&]() {  // the tile's addresses and its first loads
+      const int i = tile / nft;
+      f0 = (tile - i * nft) * COLS;
+      const int64_t l = __builtin_amdgcn_readfirstlane(c.expert[i]);
+      row0 = __builtin_amdgcn_readfirstlane(c.row0[i]) + r0;
+      cnt = __builtin_amdgcn_readfirstlane(c.row0[i + 1]) - row0;
 #pragma unroll
-      for (int u = 0; u < PF; ++u) load(wave + u * NW, u);
-      for (int s0 = wave; s0 < ns; s0 += PF * NW) {
+      for (int nb = 0; nb < NB; ++nb) {
+        const int r = nb * 16 + (lane & 15);
+        cols[nb] = r < cnt ? c.token[row0 + r] * pitch * (int)sizeof(T) : -1;
+      }
+      if constexpr (W4) {
 #pragma unroll
-        for (int u = 0; u < PF; ++u) {
-          const int st = s0 + u * NW;
-          if (st < ns) {
-            RS::stage(rw[u], lds, st, K, lane);
+        for (int b = 0; b < 2 * CB; ++b)
+          ws.block(b, a.w_gu, a.s_gu, (l * 2 * F + (b >= CB ? F : 0) + f0) / 16 + b % CB, K);
+      } else {
+        const T* W = static_cast<const T*>(a.w_gu) + l * 2 * F * K;
 #pragma unroll
-            for (int kk = 0; kk < RS::KST; ++kk) {
-              u32x4 fg[RS::VPF], fu[RS::VPF];
-              RS::frag(lds, 0, kk, lane, fg);
-              RS::frag(lds, 1, kk, lane, fu);
+        for (int q = 0; q < 4; ++q) {
+          const int f = min(f0 + (q & 1) * 8 + (lane >> 3), F - 1);
+          rows[q] = W + (int64_t)((q >> 1) * F + f) * K;
+        }
+      }
 #pragma unroll
-              for (int nb = 0; nb < NB; ++nb) {
-                u32x4 b[RS::VPF];
+      for (int u = 0; u < PF; ++u) load(begin + u * (W4 ? 1 : NW), u);
+    };
+    if (tile < total) start();
+    while (tile < total) {
+      f32x4 acc[2][CB][NB];  // gate, up
 #pragma unroll
-                for (int q = 0; q < RS::VPF; ++q) b[q] = rx[u][nb][kk * RS::VPF + q];
-                DecOp<T>::step(acc[0][0][nb], fg, b);
-                DecOp<T>::step(acc[1][0][nb], fu, b);
+      for (int s = 0; s < 2; ++s)
+#pragma unroll
+        for (int cb = 0; cb < CB; ++cb)
+#pragma unroll
+          for (int nb = 0; nb < NB; ++nb) acc[s][cb][nb] = f32x4{0.f, 0.f, 0.f, 0.f};
+      if constexpr (W4) {
+        for (int s0 = begin; s0 < end;) {
+          const int t0 = s0 >> 2, stop = min(end, (t0 + WS::CHUNK) * 4);
+          u32x4 sv[2 * CB];
+          ws.load_scales(sv, t0, ks, lane);
+          if (s0 != begin) {
+#pragma unroll
+            for (int u = 0; u < PF; ++u) load(s0 + u, u);
+          }
+          WS::store_scales(sv, lds, lane);
+          for (; s0 < stop; s0 += PF) {
+#pragma unroll
+            for (int u = 0; u < PF; ++u) {
+              const int st = s0 + u;
+              if (st < stop) {
+                float sc[2 * CB];
+#pragma unroll
+                for (int b = 0; b < 2 * CB; ++b) sc[b] = WS::scale(lds, b, t0, st, lane);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+#pragma unroll
+                  for (int b = 0; b < 2 * CB; ++b) {
+                    const u32x4 f[1] = {w4_to_bf16(rw[u][b][j], sc[b])};
+#pragma unroll
+                    for (int nb = 0; nb < NB; ++nb) {
+                      const u32x4 x[1] = {rx[u][nb][j]};
+                      Op16::step(acc[b / CB][b % CB][nb], f, x);
+                    }
+                  }
+                }
+                load(st + PF, u);
               }
             }
-            load(st + PF * NW, u);
+          }
+          s0 = stop;
+        }
+      } else {
+        for (int s0 = begin; s0 < end; s0 += PF * NW) {
+#pragma unroll
+          for (int u = 0; u < PF; ++u) {
+            const int st = s0 + u * NW;
+            if (st < end) {
+              RS::stage(rr[u], lds, st, K, lane);
+#pragma unroll
+              for (int kk = 0; kk < RS::KST; ++kk) {
+                u32x4 fg[RS::VPF], fu[RS::VPF];
+                RS::frag(lds, 0, kk, lane, fg);
+                RS::frag(lds, 1, kk, lane, fu);
+#pragma unroll
+                for (int nb = 0; nb < NB; ++nb) {
+                  u32x4 b[RS::VPF];
+#pragma unroll
+                  for (int q = 0; q < RS::VPF; ++q) b[q] = rx[u][nb][kk * RS::VPF + q];
+                  DecOp<T>::step(acc[0][0][nb], fg, b);
+                  DecOp<T>::step(acc[1][0][nb], fu, b);
+                }
+              }
+              load(st + PF * NW, u);
+            }
           }
         }
       }
-    }
-    float* red = reinterpret_cast<float*>(lds);
+      float* red = reinterpret_cast<float*>(lds);
 #pragma unroll
-    for (int s = 0; s < 2; ++s)
+      for (int s = 0; s < 2; ++s)
 #pragma unroll
-      for (int cb = 0; cb < CB; ++cb)
+        for (int cb = 0; cb < CB; ++cb)
 #pragma unroll
-        for (int nb = 0; nb < NB; ++nb)
+          for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-          for (int q = 0; q < 4; ++q) red[(((s * CB + cb) * NB + nb) * 4 + q) * 64 + lane] = acc[s][cb][nb][q];
-    __syncthreads();
-    for (int o = tid; o < CB * NB * 256; o += NTH) {
-      const int ln = o & 63, q = (o >> 6) & 3, nb = (o >> 8) % NB, cb = (o >> 8) / NB;
-      const int r = nb * 16 + (ln & 15), f = f0 + cb * 16 + (ln >> 4) * 4 + q;
-      if (r < cnt && f < F) {
-        float g = 0.f, u = 0.f;
+            for (int q = 0; q < 4; ++q) red[(((s * CB + cb) * NB + nb) * 4 + q) * 64 + lane] = acc[s][cb][nb][q];
+      const int done_row0 = row0, done_cnt = cnt, done_f0 = f0;
+      if (cnt > NB * 16) {
+        r0 += NB * 16;
+      } else {
+        r0 = 0;
+        tile += gridDim.x;
+      }
+      if (tile < total) start();
+      lds_barrier();
+      for (int o = tid; o < CB * NB * 256; o += NTH) {
+        const int ln = o & 63, q = (o >> 6) & 3, nb = (o >> 8) % NB, cb = (o >> 8) / NB;
+        const int r = nb * 16 + (ln & 15), f = done_f0 + cb * 16 + (ln >> 4) * 4 + q;
+        if (r < done_cnt && f < F) {
+          float g = 0.f, u = 0.f;
 #pragma unroll
-        for (int w = 0; w < NW; ++w) {
-          const float* red_w = reinterpret_cast<const float*>(smem + w * WAVE_LDS);
-          g += red_w[((cb * NB + nb) * 4 + q) * 64 + ln];
-          u += red_w[(((CB + cb) * NB + nb) * 4 + q) * 64 + ln];
-        }
-        const float h = silu(g) * u;
-        // 4-bit weights: the two parts of 32 elements side by side, a 128-byte line per row and fragment load
-        const int64_t at = W4 ? (int64_t)(row0 + r) * w4_pitch(F) * 2 + w4_place2(f) : (int64_t)(row0 + r) * F + f;
-        const int64_t lo = W4 ? 32 : (int64_t)a.T * a.k * F;
-        if constexpr (sizeof(T) == 2) {
-          static_cast<bf16_t*>(a.h)[at] = (bf16_t)h;
-          static_cast<bf16_t*>(a.h)[at + lo] = (bf16_t)bf16_rest(h);
-        } else {
-          static_cast<float*>(a.h)[at] = h;
+          for (int w = 0; w < NW; ++w) {
+            const float* red_w = reinterpret_cast<const float*>(smem + w * WAVE_LDS);
+            g += red_w[((cb * NB + nb) * 4 + q) * 64 + ln];
+            u += red_w[(((CB + cb) * NB + nb) * 4 + q) * 64 + ln];
+          }
+          const float h = silu(g) * u;
+          // 4-bit weights: the two parts of 32 elements side by side, a 128-byte line per row and fragment load
+          const int64_t at = W4 ? (int64_t)(done_row0 + r) * w4_pitch(F) * 2 + w4_place2(f) : (int64_t)(done_row0 + r) * F + f;
+          const int64_t lo = W4 ? 32 : (int64_t)a.T * a.k * F;
+          if constexpr (sizeof(T) == 2) {
+            static_cast<bf16_t*>(a.h)[at] = (bf16_t)h;
+            static_cast<bf16_t*>(a.h)[at + lo] = (bf16_t)bf16_rest(h);
+          } else {
+            static_cast<float*>(a.h)[at] = h;
+          }
         }
       }
+      lds_barrier();  // the sums are read before the next tile's stages overwrite them
     }
-    __syncthreads();  // the sums are read before the next tile's stages overwrite them
   }
 };
 
-template <typename T, bool W4>
+// NB: two blocks of rows for more than 16 tokens, but with 4-bit weights
+template <typename T, bool W4, int NB>
 __global__ __launch_bounds__(512, 4) void decode_gate_up_kernel(DecodeArgs a) {
-  using G = GateUp<T, W4, W4 ? 1 : 2>;
+  using G = GateUp<T, W4, NB>;
+  constexpr int BYTES = G::NW * G::WAVE_LDS;
   __shared__ Choice c;
-  __shared__ __attribute__((aligned(16))) unsigned char smem[G::NW * G::WAVE_LDS];
-  static_assert(sizeof(ChoiceScratch) <= sizeof(smem), "the scratch is done with before the first tile");
-  choose(a, c, *reinterpret_cast<ChoiceScratch*>(smem), blockIdx.x == 0);
+  __shared__ __attribute__((aligned(16))) unsigned char
+      smem[BYTES > (int)sizeof(ChoiceScratch) ? BYTES : (int)sizeof(ChoiceScratch)];
+  choose(a, c, *reinterpret_cast<ChoiceScratch*>(smem), blockIdx.x == 0);  // done with its scratch before the first tile
   __syncthreads();
-  const int nft = (a.F + G::COLS - 1) / G::COLS, total = c.n * nft;
-  for (int tile = blockIdx.x; tile < total; tile += gridDim.x) {
-    const int i = tile / nft, cnt = c.row0[i + 1] - c.row0[i];
-    if constexpr (W4) {
-      // more than 16 rows (only with more than 16 tokens): the codes once more, for the rest. Both blocks at once need
-      // 19 registers more than two workgroups per CU leave, and a spilled register is reloaded behind every load in
-      // flight: with that path compiled in, 25.6 -> 33.7 us for one token and 155 -> 173 us for 32 (DeepSeek-V3 and
-      // Kimi-K2 shares).
-      for (int r0 = 0; r0 < cnt; r0 += 16) G::tile(a, c, i, r0, tile - i * nft, smem);
-    } else if (cnt <= 16) {
-      GateUp<T, W4, 1>::tile(a, c, i, 0, tile - i * nft, smem);
-    } else {
-      G::tile(a, c, i, 0, tile - i * nft, smem);
-    }
-  }
+  G::run(a, c, smem);
 }
 
 // ------------------------------------------------------------------------------------------------
@@ -852,7 +867,13 @@ void launch_experts(const DecodeArgs& a, int num_cus, hipStream_t stream) {
   using G = GateUp<T, W4, 1>;
   using D = Down<T, W4>;
   const int64_t gu = (int64_t)std::min(a.T * a.k, a.El) * ceil_div_host(a.F, G::COLS);
-  decode_gate_up_kernel<T, W4><<<(int)std::min<int64_t>(gu, 2 * num_cus), G::NTH, 0, stream>>>(a);
+  const int grid = (int)std::min<int64_t>(gu, 2 * num_cus);
+  if constexpr (!W4) {
+    if (a.T > 16) decode_gate_up_kernel<T, W4, 2><<<grid, G::NTH, 0, stream>>>(a);
+    else decode_gate_up_kernel<T, W4, 1><<<grid, G::NTH, 0, stream>>>(a);
+  } else {
+    decode_gate_up_kernel<T, W4, 1><<<grid, G::NTH, 0, stream>>>(a);
+  }
   decode_down_kernel<T, W4><<<std::min(ceil_div_host(a.H, D::COLS), 16 / D::NW * num_cus), D::NTH, 0, stream>>>(a);
 }
 
