@@ -386,15 +386,23 @@ struct RowStep {
   }
 };
 
+template <int CTRL>
+__device__ __forceinline__ uint32_t dpp_u32(uint32_t v) {
+  return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, 0xF, 0xF, false);
+}
+
 // Packed 4-bit weights of BL 16-row blocks, 128 k per step. One load is a code tile, and a lane's 16 bytes are the 32 k
 // of one row that share a scale. The word j of them is its fragment of matrix step j, whose k are
 // (lane / 16) * 32 + 8 j on: the columns' fragments follow that order. The load path is what these kernels run out of
 // first (it takes as long over a byte per lane as over sixteen), so scales come sixteen bytes per lane, four tiles at
-// a time, through LDS of the wave's own, and several blocks share a column's fragments.
+// a time, through LDS of the wave's own, and several blocks share a column's fragments. Where only four columns are in use (CW 4, not 16) one load takes what four
+// would: lane c of 16 takes column c % 4's fragment of step c / 4, and a rotation within the 16 lanes brings it to its
+// column when that step comes. What then stands in the other columns is never looked at. One token of a DeepSeek-V3
+// share: gate/up 25.4 -> 24.8 us, down 17.0 -> 15.7 us; eight columns in two loads gave nothing (Kimi-K2 share, 32
+// tokens).
 template <int BL>
 struct W4Step {
   static constexpr int STEP = W4_TILE_K;
-  static constexpr int XV = 4;
   static constexpr int CHUNK = 4;  // scale tiles in LDS: 2048 k
   static constexpr int LDS_BYTES = BL * CHUNK * W4_SCALE_TILE;
   // the blocks' tiles: wave-uniform, so that they stay in scalar registers
@@ -421,13 +429,30 @@ struct W4Step {
   __device__ __forceinline__ static float scale(const unsigned char* lds, int b, int t0, int step, int lane) {
     return w4_scale(lds[(b * CHUNK + (step >> 2) - t0) * W4_SCALE_TILE + lane * 4 + (step & 3)]);
   }
-  template <int PARTS>
-  __device__ __forceinline__ static void load_col(u32x4 (&x)[XV], __amdgpu_buffer_rsrc_t r, int row, int step, int K,
+  // row: byte of the buffer where the row of this lane's column starts (lane % 16 % CW), or -1
+  template <int PARTS, int CW>
+  __device__ __forceinline__ static void load_col(u32x4 (&x)[CW / 4], __amdgpu_buffer_rsrc_t r, int row, int step, int K,
                                                   int lane) {
     const bool in = row >= 0 && step * STEP + (lane >> 4) * 32 < K;
-    const int off = in ? row + step * (STEP * 2 * PARTS) + (lane >> 4) * 16 : DEC_NONE;
+    const int off =
+        in ? row + step * (STEP * 2 * PARTS) + (lane >> 4) * 16 + (lane & 15) / CW * (64 * PARTS) : DEC_NONE;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) x[j] = ld_col(r, off + j * (64 * PARTS));
+    for (int q = 0; q < CW / 4; ++q) x[q] = ld_col(r, off + q * (64 * PARTS));
+  }
+  // the fragments of matrix step j
+  template <int CW>
+  __device__ __forceinline__ static u32x4 col(const u32x4 (&x)[CW / 4], int j) {
+    if constexpr (CW == 16) {
+      return x[j];
+    } else {
+      const u32x4 v = x[0];
+      switch (j) {  // lane c from lane c + 4 j: a rotation to the right by 16 less that
+        case 1: return u32x4{dpp_u32<0x12c>(v.x), dpp_u32<0x12c>(v.y), dpp_u32<0x12c>(v.z), dpp_u32<0x12c>(v.w)};
+        case 2: return u32x4{dpp_u32<0x128>(v.x), dpp_u32<0x128>(v.y), dpp_u32<0x128>(v.z), dpp_u32<0x128>(v.w)};
+        case 3: return u32x4{dpp_u32<0x124>(v.x), dpp_u32<0x124>(v.y), dpp_u32<0x124>(v.z), dpp_u32<0x124>(v.w)};
+        default: return v;
+      }
+    }
   }
 };
 
@@ -436,154 +461,87 @@ __device__ __forceinline__ float silu(float g) { return g / (1.0f + expf(-g)); }
 // ------------------------------------------------------------------------------------------------
 // gate / up
 // ------------------------------------------------------------------------------------------------
-// A tile is 16 columns of h (32 with 4-bit weights) for NB blocks of 16 rows of one expert. The eight waves split its K
-// and add their sums through LDS in wave order; the next tile's first loads are requested before that, so the weight
-// stream does not stop at a tile's end. With 4-bit weights NB is 1 and an expert of more than 16 rows is more than one
-// tile, its codes read again: two blocks need 19 registers more than two workgroups per CU leave, and a spilled register
-// is reloaded behind every load in flight (with that path compiled in, 25.6 -> 33.7 us for one token and 155 -> 173 us
-// for 32, DeepSeek-V3 and Kimi-K2 shares).
-template <typename T, bool W4, int NB>
+// Row-major weights: a tile is 16 columns of h for NB blocks of 16 rows of one expert (two for more than 16 tokens).
+// The eight waves split its K and add their sums through LDS in wave order; the next tile's first loads are requested
+// before that, so the weight stream does not stop at a tile's end (Mixtral layer, one token, 79.8 -> 77.9 us).
+template <typename T, int NB>
 struct GateUp {
-  static_assert(!W4 || NB == 1, "see above");
   static constexpr int NW = DEC_GU_NW, NTH = NW * 64;
-  static constexpr int CB = W4 ? 2 : 1;      // blocks of 16 columns
-  static constexpr int COLS = CB * 16;
   using RS = RowStep<T, 2>;
-  using WS = W4Step<2 * CB>;
-  static constexpr int PF = W4 ? 2 : NB == 1 ? 3 : 2;  // steps of loads in flight per wave
-  static constexpr int RED = 2 * CB * NB * 4 * 64 * 4;
-  static constexpr int STAGE = W4 ? WS::LDS_BYTES : RS::LDS_BYTES;
-  static constexpr int WAVE_LDS = RED > STAGE ? RED : STAGE;
-  static constexpr int XV = W4 ? WS::XV : RS::XV;
+  static constexpr int COLS = 16;
+  static constexpr int PF = NB == 1 ? 3 : 2;  // steps of loads in flight per wave
+  static constexpr int RED = 2 * NB * 4 * 64 * 4;
+  static constexpr int WAVE_LDS = RED > RS::LDS_BYTES ? RED : RS::LDS_BYTES;
 
   __device__ __forceinline__ static void run(const DecodeArgs& a, const Choice& c, unsigned char* smem) {
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int K = a.H, F = a.F;
     const int nft = (F + COLS - 1) / COLS, total = c.n * nft;
     unsigned char* lds = smem + wave * WAVE_LDS;
-    const int pitch = W4 ? w4_pitch(K) : K;
     const __amdgpu_buffer_rsrc_t xr =
-        __builtin_amdgcn_make_buffer_rsrc((void*)a.x, (short)0, a.T * pitch * (int)sizeof(T), 0x00020000);
-    // K steps of this wave: a run of them with 4-bit weights (scales come by four tiles), every eighth else
-    constexpr int STEP = W4 ? WS::STEP : RS::STEP;
-    const int ns = (K + STEP - 1) / STEP, ks = (K + W4_STILE_K - 1) / W4_STILE_K;
-    const int per = (ns + NW - 1) / NW;
-    const int begin = W4 ? wave * per : wave, end = W4 ? min(ns, begin + per) : ns;
+        __builtin_amdgcn_make_buffer_rsrc((void*)a.x, (short)0, a.T * K * (int)sizeof(T), 0x00020000);
+    const int ns = (K + RS::STEP - 1) / RS::STEP;
 
-    // the tile whose loads are requested next: tile index, expert, its rows from r0 on, first column
-    int tile = blockIdx.x, r0 = 0, row0 = 0, cnt = 0, f0 = 0;
+    // the tile whose loads are requested next
+    int tile = blockIdx.x, row0 = 0, cnt = 0, f0 = 0;
     int cols[NB];
-    WS ws;
     const T* rows[4];
-    typename RS::Regs rr[W4 ? 1 : PF];
-    u32x4 rw[W4 ? PF : 1][2 * CB], rx[PF][NB][XV];
+    typename RS::Regs rw[PF];
+    u32x4 rx[PF][NB][RS::XV];
     auto load = [&](int st, int u) {
-      if constexpr (W4) {
-        const int s = min(st, end - 1);
-        ws.load(rw[u], s, lane);
+      const int s = min(st, ns - 1);
+      RS::load(rw[u], rows, s, K, lane);
 #pragma unroll
-        for (int nb = 0; nb < NB; ++nb) WS::template load_col<1>(rx[u][nb], xr, cols[nb], s, K, lane);
-      } else {
-        const int s = min(st, ns - 1);
-        RS::load(rr[u], rows, s, K, lane);
-#pragma unroll
-        for (int nb = 0; nb < NB; ++nb) RS::load_col(rx[u][nb], xr, cols[nb], s, K, lane);
-      }
+      for (int nb = 0; nb < NB; ++nb) RS::load_col(rx[u][nb], xr, cols[nb], s, K, lane);
     };
     auto start = [&]() {  // the tile's addresses and its first loads
       const int i = tile / nft;
       f0 = (tile - i * nft) * COLS;
       const int64_t l = __builtin_amdgcn_readfirstlane(c.expert[i]);
-      row0 = __builtin_amdgcn_readfirstlane(c.row0[i]) + r0;
+      row0 = __builtin_amdgcn_readfirstlane(c.row0[i]);
       cnt = __builtin_amdgcn_readfirstlane(c.row0[i + 1]) - row0;
 #pragma unroll
       for (int nb = 0; nb < NB; ++nb) {
         const int r = nb * 16 + (lane & 15);
-        cols[nb] = r < cnt ? c.token[row0 + r] * pitch * (int)sizeof(T) : -1;
+        cols[nb] = r < cnt ? c.token[row0 + r] * K * (int)sizeof(T) : -1;
       }
-      if constexpr (W4) {
+      const T* W = static_cast<const T*>(a.w_gu) + l * 2 * F * K;
 #pragma unroll
-        for (int b = 0; b < 2 * CB; ++b)
-          ws.block(b, a.w_gu, a.s_gu, (l * 2 * F + (b >= CB ? F : 0) + f0) / 16 + b % CB, K);
-      } else {
-        const T* W = static_cast<const T*>(a.w_gu) + l * 2 * F * K;
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const int f = min(f0 + (q & 1) * 8 + (lane >> 3), F - 1);
-          rows[q] = W + (int64_t)((q >> 1) * F + f) * K;
-        }
+      for (int q = 0; q < 4; ++q) {
+        const int f = min(f0 + (q & 1) * 8 + (lane >> 3), F - 1);
+        rows[q] = W + (int64_t)((q >> 1) * F + f) * K;
       }
 #pragma unroll
-      for (int u = 0; u < PF; ++u) load(begin + u * (W4 ? 1 : NW), u);
+      for (int u = 0; u < PF; ++u) load(wave + u * NW, u);
     };
     if (tile < total) start();
     while (tile < total) {
-      f32x4 acc[2][CB][NB];  // gate, up
+      f32x4 acc[2][NB];  // gate, up
 #pragma unroll
       for (int s = 0; s < 2; ++s)
 #pragma unroll
-        for (int cb = 0; cb < CB; ++cb)
+        for (int nb = 0; nb < NB; ++nb) acc[s][nb] = f32x4{0.f, 0.f, 0.f, 0.f};
+      for (int s0 = wave; s0 < ns; s0 += PF * NW) {
 #pragma unroll
-          for (int nb = 0; nb < NB; ++nb) acc[s][cb][nb] = f32x4{0.f, 0.f, 0.f, 0.f};
-      if constexpr (W4) {
-        for (int s0 = begin; s0 < end;) {
-          const int t0 = s0 >> 2, stop = min(end, (t0 + WS::CHUNK) * 4);
-          u32x4 sv[2 * CB];
-          ws.load_scales(sv, t0, ks, lane);
-          if (s0 != begin) {
+        for (int u = 0; u < PF; ++u) {
+          const int st = s0 + u * NW;
+          if (st < ns) {
+            RS::stage(rw[u], lds, st, K, lane);
 #pragma unroll
-            for (int u = 0; u < PF; ++u) load(s0 + u, u);
-          }
-          WS::store_scales(sv, lds, lane);
-          for (; s0 < stop; s0 += PF) {
+            for (int kk = 0; kk < RS::KST; ++kk) {
+              u32x4 fg[RS::VPF], fu[RS::VPF];
+              RS::frag(lds, 0, kk, lane, fg);
+              RS::frag(lds, 1, kk, lane, fu);
 #pragma unroll
-            for (int u = 0; u < PF; ++u) {
-              const int st = s0 + u;
-              if (st < stop) {
-                float sc[2 * CB];
+              for (int nb = 0; nb < NB; ++nb) {
+                u32x4 b[RS::VPF];
 #pragma unroll
-                for (int b = 0; b < 2 * CB; ++b) sc[b] = WS::scale(lds, b, t0, st, lane);
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-#pragma unroll
-                  for (int b = 0; b < 2 * CB; ++b) {
-                    const u32x4 f[1] = {w4_to_bf16(rw[u][b][j], sc[b])};
-#pragma unroll
-                    for (int nb = 0; nb < NB; ++nb) {
-                      const u32x4 x[1] = {rx[u][nb][j]};
-                      Op16::step(acc[b / CB][b % CB][nb], f, x);
-                    }
-                  }
-                }
-                load(st + PF, u);
+                for (int q = 0; q < RS::VPF; ++q) b[q] = rx[u][nb][kk * RS::VPF + q];
+                DecOp<T>::step(acc[0][nb], fg, b);
+                DecOp<T>::step(acc[1][nb], fu, b);
               }
             }
-          }
-          s0 = stop;
-        }
-      } else {
-        for (int s0 = begin; s0 < end; s0 += PF * NW) {
-#pragma unroll
-          for (int u = 0; u < PF; ++u) {
-            const int st = s0 + u * NW;
-            if (st < end) {
-              RS::stage(rr[u], lds, st, K, lane);
-#pragma unroll
-              for (int kk = 0; kk < RS::KST; ++kk) {
-                u32x4 fg[RS::VPF], fu[RS::VPF];
-                RS::frag(lds, 0, kk, lane, fg);
-                RS::frag(lds, 1, kk, lane, fu);
-#pragma unroll
-                for (int nb = 0; nb < NB; ++nb) {
-                  u32x4 b[RS::VPF];
-#pragma unroll
-                  for (int q = 0; q < RS::VPF; ++q) b[q] = rx[u][nb][kk * RS::VPF + q];
-                  DecOp<T>::step(acc[0][0][nb], fg, b);
-                  DecOp<T>::step(acc[1][0][nb], fu, b);
-                }
-              }
-              load(st + PF * NW, u);
-            }
+            load(st + PF * NW, u);
           }
         }
       }
@@ -591,38 +549,29 @@ struct GateUp {
 #pragma unroll
       for (int s = 0; s < 2; ++s)
 #pragma unroll
-        for (int cb = 0; cb < CB; ++cb)
+        for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-          for (int nb = 0; nb < NB; ++nb)
-#pragma unroll
-            for (int q = 0; q < 4; ++q) red[(((s * CB + cb) * NB + nb) * 4 + q) * 64 + lane] = acc[s][cb][nb][q];
+          for (int q = 0; q < 4; ++q) red[((s * NB + nb) * 4 + q) * 64 + lane] = acc[s][nb][q];
       const int done_row0 = row0, done_cnt = cnt, done_f0 = f0;
-      if (cnt > NB * 16) {
-        r0 += NB * 16;
-      } else {
-        r0 = 0;
-        tile += gridDim.x;
-      }
+      tile += gridDim.x;
       if (tile < total) start();
       lds_barrier();
-      for (int o = tid; o < CB * NB * 256; o += NTH) {
-        const int ln = o & 63, q = (o >> 6) & 3, nb = (o >> 8) % NB, cb = (o >> 8) / NB;
-        const int r = nb * 16 + (ln & 15), f = done_f0 + cb * 16 + (ln >> 4) * 4 + q;
+      for (int o = tid; o < NB * 256; o += NTH) {
+        const int ln = o & 63, q = (o >> 6) & 3, nb = o >> 8;
+        const int r = nb * 16 + (ln & 15), f = done_f0 + (ln >> 4) * 4 + q;
         if (r < done_cnt && f < F) {
           float g = 0.f, u = 0.f;
 #pragma unroll
           for (int w = 0; w < NW; ++w) {
             const float* red_w = reinterpret_cast<const float*>(smem + w * WAVE_LDS);
-            g += red_w[((cb * NB + nb) * 4 + q) * 64 + ln];
-            u += red_w[(((CB + cb) * NB + nb) * 4 + q) * 64 + ln];
+            g += red_w[(nb * 4 + q) * 64 + ln];
+            u += red_w[((NB + nb) * 4 + q) * 64 + ln];
           }
           const float h = silu(g) * u;
-          // 4-bit weights: the two parts of 32 elements side by side, a 128-byte line per row and fragment load
-          const int64_t at = W4 ? (int64_t)(done_row0 + r) * w4_pitch(F) * 2 + w4_place2(f) : (int64_t)(done_row0 + r) * F + f;
-          const int64_t lo = W4 ? 32 : (int64_t)a.T * a.k * F;
+          const int64_t at = (int64_t)(done_row0 + r) * F + f;
           if constexpr (sizeof(T) == 2) {
             static_cast<bf16_t*>(a.h)[at] = (bf16_t)h;
-            static_cast<bf16_t*>(a.h)[at + lo] = (bf16_t)bf16_rest(h);
+            static_cast<bf16_t*>(a.h)[at + (int64_t)a.T * a.k * F] = (bf16_t)bf16_rest(h);
           } else {
             static_cast<float*>(a.h)[at] = h;
           }
@@ -633,10 +582,115 @@ struct GateUp {
   }
 };
 
-// NB: two blocks of rows for more than 16 tokens, but with 4-bit weights
-template <typename T, bool W4, int NB>
+// 4-bit weights: a tile is 32 columns of h for up to 16 rows of one expert; an expert of more rows is more than one tile,
+// its codes read again (a second block of columns costs 19 registers more than two workgroups per CU leave, and a
+// spilled register is reloaded behind every load in flight). Each wave takes a run of K, because scales come by four
+// steps.
+struct GateUpW4 {
+  static constexpr int NW = DEC_GU_NW, NTH = NW * 64;
+  static constexpr int COLS = 32;
+  using WS = W4Step<4>;  // gate, gate, up, up
+  static constexpr int RED = 4 * 4 * 64 * 4;
+  static constexpr int WAVE_LDS = RED > WS::LDS_BYTES ? RED : WS::LDS_BYTES;
+
+  template <int CW>
+  __device__ __forceinline__ static void tile(const DecodeArgs& a, const Choice& c, int i, int r0, int f0,
+                                              unsigned char* smem) {
+    constexpr int PF = 2;  // steps of loads in flight per wave; three: 24.8 -> 26.1 us (one token, DeepSeek-V3 share)
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int K = a.H, F = a.F, pitch = w4_pitch(K);
+    const int64_t l = __builtin_amdgcn_readfirstlane(c.expert[i]);
+    const int row0 = __builtin_amdgcn_readfirstlane(c.row0[i]) + r0;
+    const int cnt = __builtin_amdgcn_readfirstlane(c.row0[i + 1]) - row0;
+    unsigned char* lds = smem + wave * WAVE_LDS;
+    const __amdgpu_buffer_rsrc_t xr =
+        __builtin_amdgcn_make_buffer_rsrc((void*)a.x, (short)0, a.T * pitch * 2, 0x00020000);
+    const int col = (lane & 15) % CW < cnt ? c.token[row0 + (lane & 15) % CW] * pitch * 2 : -1;
+    const int ns = pitch / WS::STEP, ks = (K + W4_STILE_K - 1) / W4_STILE_K;
+    const int per = (ns + NW - 1) / NW, begin = wave * per, end = min(ns, begin + per);
+    WS ws;
+#pragma unroll
+    for (int b = 0; b < 4; ++b) ws.block(b, a.w_gu, a.s_gu, (l * 2 * F + (b >> 1) * F + f0) / 16 + (b & 1), K);
+    f32x4 acc[4];
+#pragma unroll
+    for (int b = 0; b < 4; ++b) acc[b] = f32x4{0.f, 0.f, 0.f, 0.f};
+    u32x4 rw[PF][4], rx[PF][CW / 4];
+    auto load = [&](int st, int u) {
+      const int s = min(st, end - 1);
+      ws.load(rw[u], s, lane);
+      WS::template load_col<1, CW>(rx[u], xr, col, s, K, lane);
+    };
+    for (int s0 = begin; s0 < end;) {
+      const int t0 = s0 >> 2, stop = min(end, (t0 + WS::CHUNK) * 4);
+      u32x4 sv[4];
+      ws.load_scales(sv, t0, ks, lane);
+#pragma unroll
+      for (int u = 0; u < PF; ++u) load(s0 + u, u);
+      WS::store_scales(sv, lds, lane);
+      for (; s0 < stop; s0 += PF) {
+#pragma unroll
+        for (int u = 0; u < PF; ++u) {
+          const int st = s0 + u;
+          if (st < stop) {
+            float sc[4];
+#pragma unroll
+            for (int b = 0; b < 4; ++b) sc[b] = WS::scale(lds, b, t0, st, lane);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const u32x4 x[1] = {WS::template col<CW>(rx[u], j)};
+#pragma unroll
+              for (int b = 0; b < 4; ++b) {
+                const u32x4 f[1] = {w4_to_bf16(rw[u][b][j], sc[b])};
+                Op16::step(acc[b], f, x);
+              }
+            }
+            load(st + PF, u);
+          }
+        }
+      }
+      s0 = stop;
+    }
+    float* red = reinterpret_cast<float*>(lds);
+#pragma unroll
+    for (int b = 0; b < 4; ++b)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) red[(b * 4 + q) * 64 + lane] = acc[b][q];
+    __syncthreads();
+    for (int o = tid; o < 512; o += NTH) {
+      const int ln = o & 63, q = (o >> 6) & 3, cb = o >> 8;
+      const int r = ln & 15, f = f0 + cb * 16 + (ln >> 4) * 4 + q;
+      if (r < min(cnt, CW) && f < F) {
+        float g = 0.f, u = 0.f;
+#pragma unroll
+        for (int w = 0; w < NW; ++w) {
+          const float* red_w = reinterpret_cast<const float*>(smem + w * WAVE_LDS);
+          g += red_w[(cb * 4 + q) * 64 + ln];
+          u += red_w[((2 + cb) * 4 + q) * 64 + ln];
+        }
+        const float h = silu(g) * u;
+        // the two parts of 32 elements side by side: a 128-byte line per row and fragment load
+        bf16_t* to = static_cast<bf16_t*>(a.h) + (int64_t)(row0 + r) * w4_pitch(F) * 2 + w4_place2(f);
+        to[0] = (bf16_t)h;
+        to[32] = (bf16_t)bf16_rest(h);
+      }
+    }
+    __syncthreads();
+  }
+
+  __device__ __forceinline__ static void run(const DecodeArgs& a, const Choice& c, unsigned char* smem) {
+    const int nft = (a.F + COLS - 1) / COLS, total = c.n * nft;
+    for (int t = blockIdx.x; t < total; t += gridDim.x) {
+      const int i = t / nft, f0 = (t - i * nft) * COLS;
+      const int n = c.row0[i + 1] - c.row0[i];
+      if (n <= 4) tile<4>(a, c, i, 0, f0, smem);
+      else
+        for (int r0 = 0; r0 < n; r0 += 16) tile<16>(a, c, i, r0, f0, smem);
+    }
+  }
+};
+
+template <typename G>
 __global__ __launch_bounds__(512, 4) void decode_gate_up_kernel(DecodeArgs a) {
-  using G = GateUp<T, W4, NB>;
   constexpr int BYTES = G::NW * G::WAVE_LDS;
   __shared__ Choice c;
   __shared__ __attribute__((aligned(16))) unsigned char
@@ -662,18 +716,19 @@ struct Down {
   static constexpr int COLS = CB * 16;
   using RS = RowStep<T, 1>;
   using WS = W4Step<CB>;
-  static constexpr int RPB = sizeof(T) == 2 ? 8 : 16;  // rows per block of 16 columns of the matrix step
   static constexpr int STEP = W4 ? WS::STEP : RS::STEP;
-  static constexpr int XV = W4 ? WS::XV : RS::XV;
   static constexpr int STAGE = W4 ? WS::LDS_BYTES : RS::LDS_BYTES;
   static constexpr int SUMS = MOE_DECODE_MAX_TOKENS * COLS * 4;
   static constexpr int WAVE_LDS = STAGE + SUMS;
 
-  // K steps [s_begin, s_end) of one expert for NB blocks of its rows from row r0 on
-  template <int NB>
+  static constexpr int rows(int cw) { return sizeof(T) == 2 ? cw / 2 : cw; }  // rows in cw columns of a matrix step
+
+  // K steps [s_begin, s_end) of one expert for NB blocks of CW columns of its rows from row r0 on (CW 4: 4-bit only)
+  template <int NB, int CW>
   __device__ __forceinline__ static void run(const DecodeArgs& a, const Choice& c, int i, int r0, int s_begin, int s_end,
                                              int n0, unsigned char* lds, float* sums) {
-    constexpr int PF = W4 ? (NB > 1 ? 1 : 3) : (NB > 1 ? 2 : 4);  // steps of loads in flight
+    constexpr int PF = W4 ? (NB > 1 ? 1 : CW == 16 ? 3 : 4) : (NB > 1 ? 2 : 4);  // steps of loads in flight
+    constexpr int RPB = rows(CW), XV = W4 ? CW / 4 : RS::XV;
     const int lane = threadIdx.x & 63;
     const int K = a.F, H = a.H;
     const int64_t l = __builtin_amdgcn_readfirstlane(c.expert[i]);
@@ -688,7 +743,7 @@ struct Down {
     int cols[NB];
 #pragma unroll
     for (int nb = 0; nb < NB; ++nb) {
-      const int col = lane & 15, r = nb * RPB + col % RPB;
+      const int col = (lane & 15) % CW, r = nb * RPB + col % RPB;
       cols[nb] = r < cnt ? (r * pitch + (col >= RPB ? (int)part : 0)) * (int)sizeof(T) : -1;
     }
     f32x4 acc[CB][NB];
@@ -707,7 +762,7 @@ struct Down {
         const int s = min(st, s_end - 1);
         ws.load(rw[u], s, lane);
 #pragma unroll
-        for (int nb = 0; nb < NB; ++nb) WS::template load_col<2>(rx[u][nb], hr, cols[nb], s, K, lane);
+        for (int nb = 0; nb < NB; ++nb) WS::template load_col<2, CW>(rx[u][nb], hr, cols[nb], s, K, lane);
       };
       for (int s0 = s_begin; s0 < s_end;) {
         const int t0 = s0 >> 2, stop = min(s_end, (t0 + WS::CHUNK) * 4);
@@ -730,7 +785,7 @@ struct Down {
                   const u32x4 f[1] = {w4_to_bf16(rw[u][cb][j], sc[cb])};
 #pragma unroll
                   for (int nb = 0; nb < NB; ++nb) {
-                    const u32x4 b[1] = {rx[u][nb][j]};
+                    const u32x4 b[1] = {WS::template col<CW>(rx[u][nb], j)};
                     Op16::step(acc[cb][nb], f, b);
                   }
                 }
@@ -783,7 +838,8 @@ struct Down {
 #pragma unroll
         for (int cb = 0; cb < CB; ++cb)
 #pragma unroll
-          for (int q = 0; q < 4; ++q) acc[cb][nb][q] += dpp_f32<0x128>(acc[cb][nb][q]);  // row_ror 8: the other part
+          for (int q = 0; q < 4; ++q)
+            acc[cb][nb][q] += dpp_f32<0x120 + 16 - RPB>(acc[cb][nb][q]);  // row_ror: lane c adds the other part, c + RPB
       }
       const int col = lane & 15, r = nb * RPB + col;
       if (col < RPB && r < cnt) {
@@ -808,11 +864,13 @@ struct Down {
     for (int u = min(units, wave * per); u < u_end;) {
       const int i = __builtin_amdgcn_readfirstlane(u / ns), s = u - i * ns;
       const int n = min(ns - s, u_end - u);
-      const int nb = (c.row0[i + 1] - c.row0[i] + RPB - 1) / RPB;
+      const int cnt = c.row0[i + 1] - c.row0[i];
+      constexpr int RPB = rows(16);
       // more than two blocks: two at a time, the weights again from L2 (one expert's run is a few KB)
-      if (nb <= 1) run<1>(a, c, i, 0, s, s + n, n0, lds, sums);
+      if (W4 && cnt <= rows(4)) run<1, W4 ? 4 : 16>(a, c, i, 0, s, s + n, n0, lds, sums);
+      else if (cnt <= RPB) run<1, 16>(a, c, i, 0, s, s + n, n0, lds, sums);
       else
-        for (int r0 = 0; r0 < nb * RPB; r0 += 2 * RPB) run<2>(a, c, i, r0, s, s + n, n0, lds, sums);
+        for (int r0 = 0; r0 < cnt; r0 += 2 * RPB) run<2, 16>(a, c, i, r0, s, s + n, n0, lds, sums);
       u += n;
     }
     __syncthreads();
@@ -864,15 +922,15 @@ void launch_route_rows(const T* x, const float* w, const float* bias, int64_t bi
 
 template <typename T, bool W4>
 void launch_experts(const DecodeArgs& a, int num_cus, hipStream_t stream) {
-  using G = GateUp<T, W4, 1>;
+  using G = std::conditional_t<W4, GateUpW4, GateUp<T, 1>>;
   using D = Down<T, W4>;
   const int64_t gu = (int64_t)std::min(a.T * a.k, a.El) * ceil_div_host(a.F, G::COLS);
   const int grid = (int)std::min<int64_t>(gu, 2 * num_cus);
-  if constexpr (!W4) {
-    if (a.T > 16) decode_gate_up_kernel<T, W4, 2><<<grid, G::NTH, 0, stream>>>(a);
-    else decode_gate_up_kernel<T, W4, 1><<<grid, G::NTH, 0, stream>>>(a);
+  if constexpr (W4) {
+    decode_gate_up_kernel<GateUpW4><<<grid, GateUpW4::NTH, 0, stream>>>(a);
   } else {
-    decode_gate_up_kernel<T, W4, 1><<<grid, G::NTH, 0, stream>>>(a);
+    if (a.T <= 16) decode_gate_up_kernel<GateUp<T, 1>><<<grid, GateUp<T, 1>::NTH, 0, stream>>>(a);
+    else decode_gate_up_kernel<GateUp<T, 2>><<<grid, GateUp<T, 2>::NTH, 0, stream>>>(a);
   }
   decode_down_kernel<T, W4><<<std::min(ceil_div_host(a.H, D::COLS), 16 / D::NW * num_cus), D::NTH, 0, stream>>>(a);
 }
