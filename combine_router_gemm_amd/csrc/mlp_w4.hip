@@ -418,13 +418,14 @@ void launch_gemms(const W4Args& gu, const W4Args& dn, int64_t rows, int64_t mtil
 
 // Parts of the down pass's K with 32-row tiles: as many as give every CU its four workgroups, of 16 stages at least, and
 // no more than F / H, so that the parts' sums take no more workspace than h's two parts. 8 experts of 16 rows, H 4096,
-// F 14336 (128 tiles of 224 stages): the whole pass 241 -> 186 us; 4
-// experts of 16 rows, H 512, F 8192: 73 -> 30 us
-constexpr int kSplitMaxRows = 64;  // rows per expert
+// F 14336 (128 tiles of 224 stages): the whole pass 241 -> 186 us; 4 experts of 16 rows, H 512, F 8192: 73 -> 30 us, of
+// 256 rows: 110 -> 69 us; 3 experts of 1248 rows, H 224, F 10752: 215 -> 175 us.
+// Only up to 128 tiles of rows, as the workspace leaves room for the sums without knowing H.
+constexpr int kSplitMaxTiles = 128;
+int64_t row_tiles32(int64_t rows_max, int El) { return El * ceil_div_host64(ceil_div_host64(rows_max, El), 32); }
 int w4_split(int64_t rows_max, int El, int H, int F, int num_cus) {
-  const int64_t per = ceil_div_host64(rows_max, El);
-  if (per > kSplitMaxRows) return 1;
-  const int64_t tiles = El * ceil_div_host64(per, 32) * ceil_div_host(H, 256);
+  if (row_tiles32(rows_max, El) > kSplitMaxTiles) return 1;
+  const int64_t tiles = row_tiles32(rows_max, El) * ceil_div_host(H, 256);
   const int64_t s = std::min<int64_t>({kPerCu32 * num_cus / tiles, F / H, F / 64 / 16});
   return s < 2 ? 1 : (int)s;
 }
@@ -467,7 +468,7 @@ bool mlp_w4_fits(int64_t rows, int H, int F) { return rows * std::max<int64_t>(H
 size_t mlp_w4_workspace_bytes(int64_t rows, int El, int F) {
   return align256(mlp_plan_ints(El) * sizeof(int)) + align256((size_t)rows * sizeof(int)) +
          2 * align256((size_t)rows * (size_t)F * 2) +
-         (ceil_div_host64(rows, El) <= kSplitMaxRows ? align256((size_t)rows * (size_t)F * 4) : 0);
+         (row_tiles32(rows, El) <= kSplitMaxTiles ? align256((size_t)rows * (size_t)F * 4) : 0);
 }
 
 hipError_t launch_expert_mlp_w4(const void* send_buf, const moe_layout_t& L, const uint8_t* gu_codes,
