@@ -7,11 +7,11 @@
 //
 // What bounds it: the bytes of the chosen experts' weights, each read once. The weights are the M operand of the
 // matrix unit (16 output columns per tile) and an expert's tokens its N operand, gathered by the loads. No partial
-// result is added atomically: the down kernel adds a token's experts in expert order.
+// result is added atomically: the down kernel adds a token's experts in expert order, and where an H of few tiles has
+// it split, decode_sum_kernel adds the parts in theirs.
 #include <algorithm>
 #include <climits>
 #include <type_traits>
-#include <climits>
 
 #include "common.h"
 #include "kernels.h"
@@ -42,6 +42,8 @@ struct DecodeArgs {
   Choice* choice;       // written by the gate/up kernel, read by the down kernel
   void* h;              // [T * k, F] by row of Choice: fp32, or for bf16 layers the bf16 nearest to h and then
                         // [T * k, F] its remainder; with 4-bit weights rows of both parts, at w4_place2
+  float* partial;       // [split, T, H] sums of the down kernel's parts, where it is split
+  int split;
 };
 
 // With 4-bit weights the matrix step j of 128 k takes k = 32 g + 8 j .. + 7 from lane group g (W4Step). Rows of x and h
@@ -853,15 +855,18 @@ struct Down {
     }
   }
 
-  __device__ __forceinline__ static void tile(const DecodeArgs& a, const Choice& c, int n0, unsigned char* smem) {
+  // part: which of the a.split equal parts of the units
+  __device__ __forceinline__ static void tile(const DecodeArgs& a, const Choice& c, int n0, int part,
+                                              unsigned char* smem) {
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int ns = (a.F + STEP - 1) / STEP, units = c.n * ns;
-    const int per = (units + NW - 1) / NW;
-    const int u_end = min(units, (wave + 1) * per);
+    const int runs = NW * a.split, run_id = part * NW + wave;
+    const int per = (units + runs - 1) / runs;
+    const int u_end = min(units, (run_id + 1) * per);
     unsigned char* lds = smem + wave * WAVE_LDS;
     float* sums = reinterpret_cast<float*>(lds + STAGE);
     for (int o = lane; o < a.T * COLS; o += 64) sums[o] = 0.f;
-    for (int u = min(units, wave * per); u < u_end;) {
+    for (int u = min(units, run_id * per); u < u_end;) {
       const int i = __builtin_amdgcn_readfirstlane(u / ns), s = u - i * ns;
       const int n = min(ns - s, u_end - u);
       const int cnt = c.row0[i + 1] - c.row0[i];
@@ -880,7 +885,8 @@ struct Down {
         float v = 0.f;
 #pragma unroll
         for (int w = 0; w < NW; ++w) v += reinterpret_cast<const float*>(smem + w * WAVE_LDS + STAGE)[o];
-        static_cast<T*>(a.y)[(int64_t)t * a.H + n0 + r] = from_f32<T>(v);
+        if (a.split > 1) a.partial[((int64_t)part * a.T + t) * a.H + n0 + r] = v;
+        else static_cast<T*>(a.y)[(int64_t)t * a.H + n0 + r] = from_f32<T>(v);
       }
     }
     __syncthreads();
@@ -895,8 +901,40 @@ __global__ __launch_bounds__((Down<T, W4>::NTH), 4) void decode_down_kernel(Deco
   for (int x = threadIdx.x; x < (int)(sizeof(Choice) / 4); x += D::NTH)
     reinterpret_cast<int*>(&c)[x] = reinterpret_cast<const int*>(a.choice)[x];
   __syncthreads();
-  const int total = (a.H + D::COLS - 1) / D::COLS;
-  for (int tile = blockIdx.x; tile < total; tile += gridDim.x) D::tile(a, c, tile * D::COLS, smem);
+  const int total = (a.H + D::COLS - 1) / D::COLS * a.split;
+  for (int tile = blockIdx.x; tile < total; tile += gridDim.x)
+    D::tile(a, c, tile / a.split * D::COLS, tile % a.split, smem);
+}
+
+// y of a split down kernel: the parts' sums, added in their order
+template <typename T>
+__global__ __launch_bounds__(256) void decode_sum_kernel(DecodeArgs a) {
+  const int64_t n = (int64_t)a.T * a.H, i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4;
+  if (i >= n) return;
+  f32x4 v = {0.f, 0.f, 0.f, 0.f};
+  for (int p = 0; p < a.split; ++p) v += *reinterpret_cast<const f32x4*>(a.partial + p * n + i);
+#pragma unroll
+  for (int q = 0; q < 4; ++q) static_cast<T*>(a.y)[i + q] = from_f32<T>(v[q]);
+}
+
+// Parts of the down kernel's units, for an H whose tiles leave half of the CUs idle: as many as give every CU its
+// workgroups, with eight steps per wave at least, since adding the parts takes one more launch. Whole layers (us,
+// without and with; T tokens, E experts, k of them each):
+//   f32  T 13, E 37, k 4, H 968, F 4992      587   403
+//   bf16 T 32, E 64, k 8, H 1024, F 1024     155   109
+//   bf16 T  8, E  8, k 2, H 2048, F 8192     146   138
+//   bf16 T  4, E 16, k 2, H 3584, F 4096     108   115   (224 tiles: not split)
+//   w4   T 16, E 64, k 4, H 1024, F 4096     142    85
+//   w4   T 16, E 32, k 4, H 2880, F 2880     122   102
+//   w4   T  1, E 128, k 8, H 2048, F 768    18.1  18.4
+constexpr int kDownSplit = 8;         // parts at most
+constexpr int kDownSplitMaxH = 4096;  // no wider: the workspace has no room for the parts there
+int down_split(const DecodeArgs& a, int cols, int step, int nw, int num_cus) {
+  const int tiles = ceil_div_host(a.H, cols);
+  if (a.H > kDownSplitMaxH || tiles > num_cus / 2) return 1;
+  const int64_t units = (int64_t)std::min(a.T * a.k, a.El) * ceil_div_host(a.F, step);
+  const int64_t s = std::min<int64_t>({kDownSplit, 16 / nw * num_cus / tiles, units / nw / 8});
+  return s < 2 ? 1 : (int)s;
 }
 
 template <typename T>
@@ -921,7 +959,7 @@ void launch_route_rows(const T* x, const float* w, const float* bias, int64_t bi
 }
 
 template <typename T, bool W4>
-void launch_experts(const DecodeArgs& a, int num_cus, hipStream_t stream) {
+void launch_experts(DecodeArgs a, int num_cus, hipStream_t stream) {
   using G = std::conditional_t<W4, GateUpW4, GateUp<T, 1>>;
   using D = Down<T, W4>;
   const int64_t gu = (int64_t)std::min(a.T * a.k, a.El) * ceil_div_host(a.F, G::COLS);
@@ -932,14 +970,19 @@ void launch_experts(const DecodeArgs& a, int num_cus, hipStream_t stream) {
     if (a.T <= 16) decode_gate_up_kernel<GateUp<T, 1>><<<grid, GateUp<T, 1>::NTH, 0, stream>>>(a);
     else decode_gate_up_kernel<GateUp<T, 2>><<<grid, GateUp<T, 2>::NTH, 0, stream>>>(a);
   }
-  decode_down_kernel<T, W4><<<std::min(ceil_div_host(a.H, D::COLS), 16 / D::NW * num_cus), D::NTH, 0, stream>>>(a);
+  a.split = down_split(a, D::COLS, D::STEP, D::NW, num_cus);
+  const int tiles = ceil_div_host(a.H, D::COLS) * a.split;
+  decode_down_kernel<T, W4><<<std::min(tiles, 16 / D::NW * num_cus), D::NTH, 0, stream>>>(a);
+  if (a.split > 1)
+    decode_sum_kernel<T><<<(unsigned)ceil_div_host64((int64_t)a.T * a.H, 1024), 256, 0, stream>>>(a);
 }
 
 }  // namespace
 
 size_t decode_workspace_bytes(int T, int H, int k, int F) {
   return align256(sizeof(Choice)) + align256((size_t)T * k * (size_t)w4_pitch(F) * 4) +
-         align256((size_t)T * (size_t)w4_pitch(H) * 2);
+         align256((size_t)T * (size_t)w4_pitch(H) * 2) +
+         (H <= kDownSplitMaxH ? (size_t)kDownSplit * T * (size_t)H * 4 : 0);
 }
 
 hipError_t launch_layer_decode(const DecodeCall& d, int num_cus, hipStream_t stream) {
@@ -950,6 +993,7 @@ hipError_t launch_layer_decode(const DecodeCall& d, int num_cus, hipStream_t str
   a.h = ws;
   ws += align256((size_t)d.T * d.k * (size_t)w4_pitch(d.F) * 4);
   bf16_t* placed = d.s_gu ? reinterpret_cast<bf16_t*>(ws) : nullptr;
+  a.partial = reinterpret_cast<float*>(ws + align256((size_t)d.T * (size_t)w4_pitch(d.H) * 2));
   if (d.bf16)
     launch_route_rows(static_cast<const bf16_t*>(d.x), d.w_router, d.bias, d.bias_stride, d.T, d.H, d.E, d.logits,
                       placed, stream);

@@ -93,6 +93,10 @@ CASES = [
     ("experts_512", 6, 96, 512, 8, 32, 8, 2, "uniform"),
     ("long_k", 2, 2056, 6, 2, 1048, 1, 2, "uniform"),
     ("smallest", 1, 8, 2, 1, 8, 1, 1, "uniform"),
+    # H narrow and F long: the down product is split, into more parts than there are steps of chosen experts in the last
+    ("split_down", 9, 224, 24, 4, 1504, 2, 9, "uniform"),
+    ("split_down_wide_f", 20, 96, 40, 4, 2080, 1, 20, "zipf"),
+    ("split_down_few_chosen", 32, 64, 64, 2, 1056, 1, 32, "hot8"),
 ]
 
 
