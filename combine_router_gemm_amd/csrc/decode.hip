@@ -587,29 +587,41 @@ struct GateUp {
 // 4-bit weights: a tile is 32 columns of h for up to 16 rows of one expert; an expert of more rows is more than one tile,
 // its codes read again (a second block of columns costs 19 registers more than two workgroups per CU leave, and a
 // spilled register is reloaded behind every load in flight). Each wave takes a run of K, because scales come by four
-// steps.
+// steps. The eight waves share a tile's K, or four, two or one of them do where that leaves a wave fewer than eight
+// steps, so that it spends its time on filling and draining its loads, and there are tiles enough for every workgroup.
+// Whole layers (us, eight always and by this rule): 16 tokens, 64 experts, k 4, H 1024, F 4096 98 -> 72; 32 tokens, 128
+// experts, k 8, H 2048, F 768 100 -> 90; 8 tokens, 8 experts, k 2, H 2048, F 8192 62 -> 55. With sixteen steps for eight,
+// 32 tokens, 48 experts, k 2, H 7168, F 2048 160 -> 173; with tiles for every workgroup twice, the first 80.
+// ANY_KW: the kernel that can do so; a launch of too few tiles takes the other, 0.5 us faster for one token.
+template <bool ANY_KW>
 struct GateUpW4 {
   static constexpr int NW = DEC_GU_NW, NTH = NW * 64;
   static constexpr int COLS = 32;
   using WS = W4Step<4>;  // gate, gate, up, up
   static constexpr int RED = 4 * 4 * 64 * 4;
   static constexpr int WAVE_LDS = RED > WS::LDS_BYTES ? RED : WS::LDS_BYTES;
+  static constexpr int LW = 3, MIN_STEPS = 8;
+  static_assert(NW == 1 << LW, "");
+  // whether half of 2^lw waves are better for each of `total` tiles of ns steps
+  __host__ __device__ static constexpr bool narrow(int ns, int64_t total, int grid, int lw) {
+    return ns < (MIN_STEPS << lw) && (total << lw) / 2 >= (int64_t)NW * grid;
+  }
 
+  // K of one tile for kw waves, this one the wk-th; its sums to its LDS
   template <int CW>
-  __device__ __forceinline__ static void tile(const DecodeArgs& a, const Choice& c, int i, int r0, int f0,
-                                              unsigned char* smem) {
+  __device__ __forceinline__ static void multiply(const DecodeArgs& a, const Choice& c, int i, int r0, int f0, int kw,
+                                                  int wk, unsigned char* lds) {
     constexpr int PF = 2;  // steps of loads in flight per wave; three: 24.8 -> 26.1 us (one token, DeepSeek-V3 share)
-    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int lane = threadIdx.x & 63;
     const int K = a.H, F = a.F, pitch = w4_pitch(K);
     const int64_t l = __builtin_amdgcn_readfirstlane(c.expert[i]);
     const int row0 = __builtin_amdgcn_readfirstlane(c.row0[i]) + r0;
     const int cnt = __builtin_amdgcn_readfirstlane(c.row0[i + 1]) - row0;
-    unsigned char* lds = smem + wave * WAVE_LDS;
     const __amdgpu_buffer_rsrc_t xr =
         __builtin_amdgcn_make_buffer_rsrc((void*)a.x, (short)0, a.T * pitch * 2, 0x00020000);
     const int col = (lane & 15) % CW < cnt ? c.token[row0 + (lane & 15) % CW] * pitch * 2 : -1;
     const int ns = pitch / WS::STEP, ks = (K + W4_STILE_K - 1) / W4_STILE_K;
-    const int per = (ns + NW - 1) / NW, begin = wave * per, end = min(ns, begin + per);
+    const int per = (ns + kw - 1) / kw, begin = wk * per, end = min(ns, begin + per);
     WS ws;
 #pragma unroll
     for (int b = 0; b < 4; ++b) ws.block(b, a.w_gu, a.s_gu, (l * 2 * F + (b >> 1) * F + f0) / 16 + (b & 1), K);
@@ -657,17 +669,27 @@ struct GateUpW4 {
     for (int b = 0; b < 4; ++b)
 #pragma unroll
       for (int q = 0; q < 4; ++q) red[(b * 4 + q) * 64 + lane] = acc[b][q];
-    __syncthreads();
-    for (int o = tid; o < 512; o += NTH) {
-      const int ln = o & 63, q = (o >> 6) & 3, cb = o >> 8;
-      const int r = ln & 15, f = f0 + cb * 16 + (ln >> 4) * 4 + q;
-      if (r < min(cnt, CW) && f < F) {
+  }
+
+  // h of one tile from the sums of kw waves, whose LDS starts at lds, by the same waves
+  __device__ __forceinline__ static void activate(const DecodeArgs& a, const Choice& c, int i, int r0, int f0, int kw,
+                                                  int wk, const unsigned char* lds) {
+    const int row0 = c.row0[i] + r0, cnt = c.row0[i + 1] - row0, F = a.F;
+    const int ln = threadIdx.x & 63, r = ln & 15;
+    for (int o = wk; o < 8; o += kw) {
+      const int q = o & 3, cb = o >> 2, f = f0 + cb * 16 + (ln >> 4) * 4 + q;
+      if (r < cnt && f < F) {
         float g = 0.f, u = 0.f;
+        auto add = [&](int w) {
+          const float* red = reinterpret_cast<const float*>(lds + w * WAVE_LDS);
+          g += red[(cb * 4 + q) * 64 + ln];
+          u += red[((2 + cb) * 4 + q) * 64 + ln];
+        };
+        if (!ANY_KW || kw == NW) {
 #pragma unroll
-        for (int w = 0; w < NW; ++w) {
-          const float* red_w = reinterpret_cast<const float*>(smem + w * WAVE_LDS);
-          g += red_w[(cb * 4 + q) * 64 + ln];
-          u += red_w[((2 + cb) * 4 + q) * 64 + ln];
+          for (int w = 0; w < NW; ++w) add(w);
+        } else {
+          for (int w = 0; w < kw; ++w) add(w);
         }
         const float h = silu(g) * u;
         // the two parts of 32 elements side by side: a 128-byte line per row and fragment load
@@ -676,17 +698,30 @@ struct GateUpW4 {
         to[32] = (bf16_t)bf16_rest(h);
       }
     }
-    __syncthreads();
   }
 
   __device__ __forceinline__ static void run(const DecodeArgs& a, const Choice& c, unsigned char* smem) {
-    const int nft = (a.F + COLS - 1) / COLS, total = c.n * nft;
-    for (int t = blockIdx.x; t < total; t += gridDim.x) {
-      const int i = t / nft, f0 = (t - i * nft) * COLS;
-      const int n = c.row0[i + 1] - c.row0[i];
-      if (n <= 4) tile<4>(a, c, i, 0, f0, smem);
-      else
-        for (int r0 = 0; r0 < n; r0 += 16) tile<16>(a, c, i, r0, f0, smem);
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), passes = a.T > 16 ? 2 : 1;
+    const int nft = (a.F + COLS - 1) / COLS, total = __builtin_amdgcn_readfirstlane(c.n) * nft;
+    const int ns = (a.H + WS::STEP - 1) / WS::STEP;
+    int lw = LW;  // log2 of the waves of a tile
+    if (ANY_KW)
+      while (lw > 0 && narrow(ns, total, gridDim.x, lw)) --lw;
+    const int kw = 1 << lw, wk = wave & (kw - 1), tiles = NW >> lw;
+    unsigned char* lds = smem + wave * WAVE_LDS;
+    for (int t0 = blockIdx.x * tiles; t0 < total; t0 += gridDim.x * tiles) {
+      const int t = t0 + (wave >> lw), i = min(t, total - 1) / nft, f0 = (t - i * nft) * COLS;
+      const int n = t < total ? __builtin_amdgcn_readfirstlane(c.row0[i + 1] - c.row0[i]) : 0;
+      for (int pass = 0; pass < passes; ++pass) {  // as many for every wave, for the barriers
+        const int r0 = pass * 16;
+        if (r0 < n) {
+          if (n <= 4) multiply<4>(a, c, i, 0, f0, kw, wk, lds);
+          else multiply<16>(a, c, i, r0, f0, kw, wk, lds);
+        }
+        if (kw > 1) __syncthreads();  // one wave's LDS accesses are in order by themselves
+        if (r0 < n) activate(a, c, i, r0, f0, kw, wk, lds - wk * WAVE_LDS);
+        if (kw > 1) __syncthreads();
+      }
     }
   }
 };
@@ -960,12 +995,15 @@ void launch_route_rows(const T* x, const float* w, const float* bias, int64_t bi
 
 template <typename T, bool W4>
 void launch_experts(DecodeArgs a, int num_cus, hipStream_t stream) {
-  using G = std::conditional_t<W4, GateUpW4, GateUp<T, 1>>;
+  using G = std::conditional_t<W4, GateUpW4<false>, GateUp<T, 1>>;
   using D = Down<T, W4>;
   const int64_t gu = (int64_t)std::min(a.T * a.k, a.El) * ceil_div_host(a.F, G::COLS);
   const int grid = (int)std::min<int64_t>(gu, 2 * num_cus);
   if constexpr (W4) {
-    decode_gate_up_kernel<GateUpW4><<<grid, GateUpW4::NTH, 0, stream>>>(a);
+    if (G::narrow(ceil_div_host(a.H, W4_TILE_K), gu, grid, G::LW))
+      decode_gate_up_kernel<GateUpW4<true>><<<grid, G::NTH, 0, stream>>>(a);
+    else
+      decode_gate_up_kernel<G><<<grid, G::NTH, 0, stream>>>(a);
   } else {
     if (a.T <= 16) decode_gate_up_kernel<GateUp<T, 1>><<<grid, GateUp<T, 1>::NTH, 0, stream>>>(a);
     else decode_gate_up_kernel<GateUp<T, 2>><<<grid, GateUp<T, 2>::NTH, 0, stream>>>(a);

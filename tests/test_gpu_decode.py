@@ -97,6 +97,9 @@ CASES = [
     ("split_down", 9, 224, 24, 4, 1504, 2, 9, "uniform"),
     ("split_down_wide_f", 20, 96, 40, 4, 2080, 1, 20, "zipf"),
     ("split_down_few_chosen", 32, 64, 64, 2, 1056, 1, 32, "hot8"),
+    # H short and tiles enough: fewer waves share a tile of gate/up
+    ("many_tiles", 24, 96, 64, 8, 3104, 1, 24, "uniform"),
+    ("many_tiles_hot", 32, 160, 40, 4, 3360, 1, 32, "zipf"),
 ]
 
 
