@@ -381,8 +381,8 @@ int moe_expert_mlp_w4(const void* send_buf, const moe_layout_t* layout, const ui
 
 /*
  * moe_layer_decode -- the whole layer (route, dispatch, expert MLP, combine) for at most
- * MOE_DECODE_MAX_TOKENS tokens in three launches (router; choice of experts and gate/up; down and combine), with
- * no send buffer and no layout.
+ * MOE_DECODE_MAX_TOKENS tokens in three launches (router; choice of experts and gate/up; down and combine; a
+ * fourth adds the parts of a down pass split for its narrow H), with no send buffer and no layout.
  *   logits, topk_ids, topk_w  as moe_route defines them
  *   y[t] = sum over kept slots j of topk_w[t,j] * (silu(x Wg[l]^T) * (x Wu[l]^T)) Wd[l]^T with l = e mod El
  *          for expert e = topk_ids[t,j] (El = E / R); pair (t, j) is kept iff fewer than C earlier tokens
@@ -398,8 +398,8 @@ int moe_expert_mlp_w4(const void* send_buf, const moe_layout_t* layout, const ui
  *   logits       [T, E] fp32, topk_ids [T, k] int32, topk_w [T, k] fp32, y [T, H] (xdt): outputs
  *   workspace    device scratch of at least moe_layer_decode_workspace_bytes(T, H, E, k, F, xdt) bytes; no
  *                contents need clearing between calls, and calls that overlap must use separate workspaces
- * Requires 0 <= T <= MOE_DECODE_MAX_TOKENS (more is MOE_ERR_UNSUPPORTED: the four calls take it), H % 8 == 0
- * and F % 8 == 0; T == 0 is a no-op.
+ * Requires 0 <= T <= MOE_DECODE_MAX_TOKENS (more is MOE_ERR_UNSUPPORTED: the four calls take it), H % 8 == 0,
+ * F % 8 == 0, H <= 2^23 and F <= 2^20 (else MOE_ERR_UNSUPPORTED); T == 0 is a no-op.
  */
 #define MOE_DECODE_MAX_TOKENS 32
 size_t moe_layer_decode_workspace_bytes(int T, int H, int E, int k, int F, moe_dtype_t xdt);
