@@ -463,7 +463,12 @@ int w4_rows(int64_t rows_max, int El, int H, int F, int num_cus) {
 
 }  // namespace
 
-bool mlp_w4_fits(int64_t rows, int H, int F) { return rows * std::max<int64_t>(H, 2 * (int64_t)F) * 2 < 0x7ffffe00ll; }
+// Rows of either pass, one expert's scales and a 16-row block's codes are addressed by 31-bit byte offsets
+bool mlp_w4_fits(int64_t rows, int H, int F) {
+  auto scales = [](int64_t n, int64_t k) { return n / 16 * ceil_div_host64(k, W4_STILE_K) * W4_SCALE_TILE; };
+  return rows * std::max<int64_t>(H, 2 * (int64_t)F) * 2 < 0x7ffffe00ll && std::max(H, F) < 1 << 27 &&
+         std::max(scales(2 * (int64_t)F, H), scales(H, F)) <= INT32_MAX;
+}
 
 size_t mlp_w4_workspace_bytes(int64_t rows, int El, int F) {
   return align256(mlp_plan_ints(El) * sizeof(int)) + align256((size_t)rows * sizeof(int)) +

@@ -372,8 +372,8 @@ size_t moe_expert_mlp_w4_workspace_bytes(int T, int k, int E, int R, int C, int 
  *   out_buf    [rows_max, H] bf16 output, row-aligned with send_buf; rows >= total are left as they were
  *   workspace  device scratch of at least moe_expert_mlp_w4_workspace_bytes(...) bytes; no contents need
  *              clearing between calls, and calls that overlap must use separate workspaces
- * Requires H % 32 == 0, F % 32 == 0 and rows_max * max(H, 2 F) * 2 bytes below 2 GiB - 512 (else
- * MOE_ERR_UNSUPPORTED).
+ * Requires H % 32 == 0, F % 32 == 0, H and F below 2^27, and below 2 GiB - 512 rows_max * max(H, 2 F) * 2 bytes and
+ * the packed scales of one expert's [2F, H] or [H, F] (else MOE_ERR_UNSUPPORTED).
  */
 int moe_expert_mlp_w4(const void* send_buf, const moe_layout_t* layout, const uint8_t* gu_codes,
                       const uint8_t* gu_scales, const uint8_t* dn_codes, const uint8_t* dn_scales, int F,

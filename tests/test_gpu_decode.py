@@ -245,3 +245,46 @@ def test_streams_workspaces_and_graphs(w4):
             r.ws.fill_(rep)
         assert same(runs[0]().outputs(), refs[0])
         torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("w4", [False, True])
+def test_weights_past_4_gib(w4):
+    # the last experts of 4.5 GiB of gate/up codes, or of 5 GiB of bf16 gate/up weights
+    El, H, F, T, k = (330, 7168, 2048, 3, 2) if w4 else (160, 4096, 2048, 3, 2)
+    if torch.cuda.mem_get_info()[0] < 16 << 30:
+        pytest.skip("needs 16 GiB")
+    g = torch.Generator(device=DEV).manual_seed(15)
+    cpu = torch.Generator().manual_seed(16)
+    x = torch.randn(T, H, generator=cpu).to(torch.bfloat16)
+    wr = torch.randn(El, H, generator=cpu) * 0.02
+    bias = torch.zeros(El)
+    bias[-2:] = 1000.0  # every token chooses the last two
+    inp = {"x": x.to(DEV), "w_router": wr.to(DEV), "bias": bias.to(DEV), "w_gate_up": None,
+           "w_down": torch.empty(0, H, F)}
+    if w4:
+        packs = []
+        for N, K in ((2 * F, H), (H, F)):
+            cs, ss = moe.moe_w4_shapes(El, N, K)
+            packs += [torch.randint(0, 256, cs, dtype=torch.uint8, device=DEV, generator=g),
+                      torch.randint(118, 122, ss, dtype=torch.uint8, device=DEV, generator=g)]
+
+        def weights(N, K, c, s):
+            w = torch.empty(N, K, dtype=torch.bfloat16, device=DEV)
+            moe.moe_dequantize_w4(c, s, w)
+            return w.cpu()
+        gu, dn = {}, {}
+        for l in (El - 2, El - 1):
+            gu[l], dn[l] = weights(2 * F, H, packs[0][l], packs[1][l]), weights(H, F, packs[2][l], packs[3][l])
+    else:
+        packs = None
+        inp["w_gate_up"] = torch.empty(El, 2 * F, H, dtype=torch.bfloat16, device=DEV).normal_(0, 0.02, generator=g)
+        inp["w_down"] = torch.empty(El, H, F, dtype=torch.bfloat16, device=DEV).normal_(0, 0.02, generator=g)
+        gu = {l: inp["w_gate_up"][l].cpu() for l in (El - 2, El - 1)}
+        dn = {l: inp["w_down"][l].cpu() for l in (El - 2, El - 1)}
+    r = Run(inp, k, 1, T, packs)()
+    torch.cuda.synchronize()
+    ids = r.ids.cpu().long()
+    assert sorted(ids[0].tolist()) == [El - 2, El - 1]
+    ref = layer(x.double(), wr.double(), bias.double(), k, 1, T, ids, lambda l: (gu[l].double(), dn[l].double()),
+                2.0 ** -16)
+    assert within(r.y.cpu(), ref["y"], ref["dy"], torch.bfloat16) <= 1.0

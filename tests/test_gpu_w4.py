@@ -210,3 +210,29 @@ def test_expert_mlp_w4_graph_and_side_stream():
         torch.cuda.synchronize()
         assert torch.equal(out, ref)
         ws.fill_(0x3C)
+
+
+def test_expert_mlp_w4_weights_past_4_gib():
+    El, H, F, T = 330, 7168, 2048, 9  # 4.5 GiB of gate/up codes
+    if torch.cuda.mem_get_info()[0] < 12 << 30:
+        pytest.skip("needs 12 GiB")
+    counts = [0] * El
+    counts[0], counts[El - 1] = 4, 5
+    L = layout_of(counts, T, 1, 1, T, H)
+    g = torch.Generator(device=DEV).manual_seed(5)
+    packs = []
+    for N, K in ((2 * F, H), (H, F)):
+        cs, ss = moe.moe_w4_shapes(El, N, K)
+        packs += [torch.randint(0, 256, cs, dtype=torch.uint8, device=DEV, generator=g),
+                  torch.randint(118, 122, ss, dtype=torch.uint8, device=DEV, generator=g)]
+    send = torch.randn(L.rows_max, H, generator=torch.Generator().manual_seed(6)).to(torch.bfloat16)
+    out = torch.zeros(L.rows_max, H, dtype=torch.bfloat16, device=DEV)
+    moe.moe_expert_mlp_w4(send.to(DEV), L, *packs, out)
+    for l, rows in ((0, slice(0, 4)), (El - 1, slice(4, 9))):
+        v = []
+        for (N, K), c, s in (((2 * F, H), *packs[:2]), ((H, F), *packs[2:])):
+            w = torch.empty(N, K, dtype=torch.bfloat16, device=DEV)
+            moe.moe_dequantize_w4(c[l], s[l], w)
+            v.append(w.double().cpu())
+        ref, b = expert(send[rows].double(), v[0], v[1], 2.0 ** -8)
+        assert within(out[rows].cpu(), ref, b, torch.bfloat16) <= 1.0

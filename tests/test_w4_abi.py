@@ -73,6 +73,10 @@ def test_expert_mlp_refusals(lib):
     for a in ("send", "gc", "gs", "dc", "ds", "out", "ws"):
         assert call(**{a: None}) == INVALID
         assert call(**{a: ODD}) == INVALID
+    # one expert's scales past 31 bits, though its rows are few
+    assert call(F=1 << 28, T=1, k=1, E=1, R=1, C=1) == UNSUPPORTED
+    assert call(F=1 << 27, T=1, k=1, E=1, R=1, C=1) == UNSUPPORTED
+    assert call(F=1 << 26, H=1 << 13, T=1, k=1, E=1, R=1, C=1) == UNSUPPORTED
     assert lib.moe_expert_mlp_w4(P, None, P, P, P, P, 64, P, P, 1 << 40, None) == INVALID
 
 
@@ -101,6 +105,8 @@ def test_layer_refusals(lib, w4):
     if w4:
         assert call(H=72) == UNSUPPORTED
         assert call(F=40) == UNSUPPORTED
+    assert call(H=(1 << 23) + 32) == UNSUPPORTED
+    assert call(F=(1 << 20) + 32) == UNSUPPORTED
     assert call(bias=P, stride=-1) == INVALID
     assert call(wsb=16) == INVALID
     names = ["x", "wr", "gu", "dn", "lg", "ids", "w", "y", "ws"] + (["gs", "ds"] if w4 else [])
