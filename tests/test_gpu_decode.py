@@ -288,3 +288,36 @@ def test_weights_past_4_gib(w4):
     ref = layer(x.double(), wr.double(), bias.double(), k, 1, T, ids, lambda l: (gu[l].double(), dn[l].double()),
                 2.0 ** -16)
     assert within(r.y.cpu(), ref["y"], ref["dy"], torch.bfloat16) <= 1.0
+
+
+@pytest.mark.parametrize("w4", [False, True])
+def test_split_layers_in_graphs_that_share_a_workspace(w4):
+    """Two layers whose down pass is split, captured with one workspace and replayed one after the other, with the
+    workspace overwritten between; more tokens than a tile of gate/up has rows."""
+    T, H, E, k, F, R = 24, 96, 40, 4, 2080, 1
+    runs, refs, graphs = [], [], []
+    side = torch.cuda.Stream()
+    for i in range(2):
+        inp = inputs("split_graphs", T, H, E, k, F, R, torch.bfloat16, "zipf", 70 + i)
+        packs = pack4(inp["w_gate_up"])[0] + pack4(inp["w_down"])[0] if w4 else None
+        runs.append(Run(inp, k, R, T, packs))
+        runs[i].ws = runs[0].ws
+        with torch.cuda.stream(side):
+            runs[i]()
+        torch.cuda.synchronize()
+        refs.append(runs[i].outputs())
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            runs[i]()
+        graphs.append(g)
+    for rep in range(3):
+        for r in runs:
+            r.y.fill_(-1.0)
+        for g in graphs:
+            g.replay()
+        torch.cuda.synchronize()
+        for r, ref in zip(runs, refs):
+            assert same(r.outputs(), ref)
+        runs[0].ws.fill_(0xFF - rep)
+        assert same(runs[1]().outputs(), refs[1])
+        torch.cuda.synchronize()
