@@ -584,11 +584,13 @@ struct GateUp {
   }
 };
 
-// 4-bit weights: a tile is 32 columns of h for up to 16 rows of one expert; an expert of more rows is more than one tile,
-// its codes read again (a second block of columns costs 19 registers more than two workgroups per CU leave, and a
-// spilled register is reloaded behind every load in flight). Each wave takes a run of K, because scales come by four
-// steps. The eight waves share a tile's K, or four, two or one of them do where that leaves a wave fewer than eight
-// steps, so that it spends its time on filling and draining its loads, and there are tiles enough for every workgroup.
+// 4-bit weights: a tile is 32 columns of h for all rows of one expert. More than 16 rows take two blocks of columns with
+// one step of loads in flight instead of two, and their scales are stored before the columns are loaded: no more
+// registers are left with two workgroups per CU, and a spilled one is reloaded behind every load in flight (32 tokens of
+// a Kimi-K2 share, some of whose experts have that many rows: 157.5 us with the codes read twice, 145.8 so).
+// Each wave takes a run of K, because scales come by four steps. The eight waves share a tile's K, or four, two or one
+// of them do where that leaves a wave fewer than eight steps, so that it spends its time on filling and draining its
+// loads, and there are tiles enough for every workgroup.
 // Whole layers (us, eight always and by this rule): 16 tokens, 64 experts, k 4, H 1024, F 4096 98 -> 72; 32 tokens, 128
 // experts, k 8, H 2048, F 768 100 -> 90; 8 tokens, 8 experts, k 2, H 2048, F 8192 62 -> 55. With sixteen steps for eight,
 // 32 tokens, 48 experts, k 2, H 7168, F 2048 160 -> 173; with tiles for every workgroup twice, the first 80.
@@ -597,8 +599,9 @@ template <bool ANY_KW>
 struct GateUpW4 {
   static constexpr int NW = DEC_GU_NW, NTH = NW * 64;
   static constexpr int COLS = 32;
+  static constexpr int NBMAX = MOE_DECODE_MAX_TOKENS / 16;
   using WS = W4Step<4>;  // gate, gate, up, up
-  static constexpr int RED = 4 * 4 * 64 * 4;
+  static constexpr int RED = 4 * NBMAX * 4 * 64 * 4;
   static constexpr int WAVE_LDS = RED > WS::LDS_BYTES ? RED : WS::LDS_BYTES;
   static constexpr int LW = 3, MIN_STEPS = 8;
   static_assert(NW == 1 << LW, "");
@@ -608,39 +611,52 @@ struct GateUpW4 {
   }
 
   // K of one tile for kw waves, this one the wk-th; its sums to its LDS
-  template <int CW>
-  __device__ __forceinline__ static void multiply(const DecodeArgs& a, const Choice& c, int i, int r0, int f0, int kw,
-                                                  int wk, unsigned char* lds) {
-    constexpr int PF = 2;  // steps of loads in flight per wave; three: 24.8 -> 26.1 us (one token, DeepSeek-V3 share)
+  template <int CW, int NB>
+  __device__ __forceinline__ static void multiply(const DecodeArgs& a, const Choice& c, int i, int f0, int kw, int wk,
+                                                  unsigned char* lds) {
+    // steps of loads in flight per wave; three for one block: 24.8 -> 26.1 us (one token, DeepSeek-V3 share)
+    constexpr int PF = NB == 1 ? 2 : 1;
     const int lane = threadIdx.x & 63;
     const int K = a.H, F = a.F, pitch = w4_pitch(K);
     const int64_t l = __builtin_amdgcn_readfirstlane(c.expert[i]);
-    const int row0 = __builtin_amdgcn_readfirstlane(c.row0[i]) + r0;
+    const int row0 = __builtin_amdgcn_readfirstlane(c.row0[i]);
     const int cnt = __builtin_amdgcn_readfirstlane(c.row0[i + 1]) - row0;
     const __amdgpu_buffer_rsrc_t xr =
         __builtin_amdgcn_make_buffer_rsrc((void*)a.x, (short)0, a.T * pitch * 2, 0x00020000);
-    const int col = (lane & 15) % CW < cnt ? c.token[row0 + (lane & 15) % CW] * pitch * 2 : -1;
+    int cols[NB];
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb) {
+      const int r = nb * 16 + (lane & 15) % CW;
+      cols[nb] = r < cnt ? c.token[row0 + r] * pitch * 2 : -1;
+    }
     const int ns = pitch / WS::STEP, ks = (K + W4_STILE_K - 1) / W4_STILE_K;
     const int per = (ns + kw - 1) / kw, begin = wk * per, end = min(ns, begin + per);
     WS ws;
 #pragma unroll
     for (int b = 0; b < 4; ++b) ws.block(b, a.w_gu, a.s_gu, (l * 2 * F + (b >> 1) * F + f0) / 16 + (b & 1), K);
-    f32x4 acc[4];
+    f32x4 acc[NB][4];
 #pragma unroll
-    for (int b = 0; b < 4; ++b) acc[b] = f32x4{0.f, 0.f, 0.f, 0.f};
-    u32x4 rw[PF][4], rx[PF][CW / 4];
+    for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+      for (int b = 0; b < 4; ++b) acc[nb][b] = f32x4{0.f, 0.f, 0.f, 0.f};
+    u32x4 rw[PF][4], rx[PF][NB][CW / 4];
     auto load = [&](int st, int u) {
       const int s = min(st, end - 1);
       ws.load(rw[u], s, lane);
-      WS::template load_col<1, CW>(rx[u], xr, col, s, K, lane);
+#pragma unroll
+      for (int nb = 0; nb < NB; ++nb) WS::template load_col<1, CW>(rx[u][nb], xr, cols[nb], s, K, lane);
     };
     for (int s0 = begin; s0 < end;) {
       const int t0 = s0 >> 2, stop = min(end, (t0 + WS::CHUNK) * 4);
       u32x4 sv[4];
       ws.load_scales(sv, t0, ks, lane);
+      if (NB > 1) {  // the scales' registers are needed for the columns
+        WS::store_scales(sv, lds, lane);
+        __builtin_amdgcn_sched_barrier(0);
+      }
 #pragma unroll
       for (int u = 0; u < PF; ++u) load(s0 + u, u);
-      WS::store_scales(sv, lds, lane);
+      if (NB == 1) WS::store_scales(sv, lds, lane);
       for (; s0 < stop; s0 += PF) {
 #pragma unroll
         for (int u = 0; u < PF; ++u) {
@@ -651,11 +667,14 @@ struct GateUpW4 {
             for (int b = 0; b < 4; ++b) sc[b] = WS::scale(lds, b, t0, st, lane);
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-              const u32x4 x[1] = {WS::template col<CW>(rx[u], j)};
+              u32x4 x[NB][1];
+#pragma unroll
+              for (int nb = 0; nb < NB; ++nb) x[nb][0] = WS::template col<CW>(rx[u][nb], j);
 #pragma unroll
               for (int b = 0; b < 4; ++b) {
                 const u32x4 f[1] = {w4_to_bf16(rw[u][b][j], sc[b])};
-                Op16::step(acc[b], f, x);
+#pragma unroll
+                for (int nb = 0; nb < NB; ++nb) Op16::step(acc[nb][b], f, x[nb]);
               }
             }
             load(st + PF, u);
@@ -666,24 +685,26 @@ struct GateUpW4 {
     }
     float* red = reinterpret_cast<float*>(lds);
 #pragma unroll
-    for (int b = 0; b < 4; ++b)
+    for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-      for (int q = 0; q < 4; ++q) red[(b * 4 + q) * 64 + lane] = acc[b][q];
+      for (int b = 0; b < 4; ++b)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) red[((nb * 4 + b) * 4 + q) * 64 + lane] = acc[nb][b][q];
   }
 
   // h of one tile from the sums of kw waves, whose LDS starts at lds, by the same waves
-  __device__ __forceinline__ static void activate(const DecodeArgs& a, const Choice& c, int i, int r0, int f0, int kw,
-                                                  int wk, const unsigned char* lds) {
-    const int row0 = c.row0[i] + r0, cnt = c.row0[i + 1] - row0, F = a.F;
-    const int ln = threadIdx.x & 63, r = ln & 15;
-    for (int o = wk; o < 8; o += kw) {
-      const int q = o & 3, cb = o >> 2, f = f0 + cb * 16 + (ln >> 4) * 4 + q;
+  __device__ __forceinline__ static void activate(const DecodeArgs& a, const Choice& c, int i, int f0, int kw, int wk,
+                                                  const unsigned char* lds) {
+    const int row0 = c.row0[i], cnt = c.row0[i + 1] - row0, F = a.F;
+    const int ln = threadIdx.x & 63;
+    for (int o = wk; o < (cnt > 16 ? 16 : 8); o += kw) {
+      const int q = o & 3, cb = (o >> 2) & 1, r = (o >> 3) * 16 + (ln & 15), f = f0 + cb * 16 + (ln >> 4) * 4 + q;
       if (r < cnt && f < F) {
         float g = 0.f, u = 0.f;
         auto add = [&](int w) {
           const float* red = reinterpret_cast<const float*>(lds + w * WAVE_LDS);
-          g += red[(cb * 4 + q) * 64 + ln];
-          u += red[((2 + cb) * 4 + q) * 64 + ln];
+          g += red[(((o >> 3) * 4 + cb) * 4 + q) * 64 + ln];
+          u += red[(((o >> 3) * 4 + 2 + cb) * 4 + q) * 64 + ln];
         };
         if (!ANY_KW || kw == NW) {
 #pragma unroll
@@ -701,7 +722,7 @@ struct GateUpW4 {
   }
 
   __device__ __forceinline__ static void run(const DecodeArgs& a, const Choice& c, unsigned char* smem) {
-    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), passes = a.T > 16 ? 2 : 1;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int nft = (a.F + COLS - 1) / COLS, total = __builtin_amdgcn_readfirstlane(c.n) * nft;
     const int ns = (a.H + WS::STEP - 1) / WS::STEP;
     int lw = LW;  // log2 of the waves of a tile
@@ -712,16 +733,12 @@ struct GateUpW4 {
     for (int t0 = blockIdx.x * tiles; t0 < total; t0 += gridDim.x * tiles) {
       const int t = t0 + (wave >> lw), i = min(t, total - 1) / nft, f0 = (t - i * nft) * COLS;
       const int n = t < total ? __builtin_amdgcn_readfirstlane(c.row0[i + 1] - c.row0[i]) : 0;
-      for (int pass = 0; pass < passes; ++pass) {  // as many for every wave, for the barriers
-        const int r0 = pass * 16;
-        if (r0 < n) {
-          if (n <= 4) multiply<4>(a, c, i, 0, f0, kw, wk, lds);
-          else multiply<16>(a, c, i, r0, f0, kw, wk, lds);
-        }
-        if (kw > 1) __syncthreads();  // one wave's LDS accesses are in order by themselves
-        if (r0 < n) activate(a, c, i, r0, f0, kw, wk, lds - wk * WAVE_LDS);
-        if (kw > 1) __syncthreads();
-      }
+      if (n > 16) multiply<16, 2>(a, c, i, f0, kw, wk, lds);
+      else if (n > 4) multiply<16, 1>(a, c, i, f0, kw, wk, lds);
+      else if (n > 0) multiply<4, 1>(a, c, i, f0, kw, wk, lds);
+      if (kw > 1) __syncthreads();  // one wave's LDS accesses are in order by themselves
+      if (n > 0) activate(a, c, i, f0, kw, wk, lds - wk * WAVE_LDS);
+      if (kw > 1) __syncthreads();
     }
   }
 };
