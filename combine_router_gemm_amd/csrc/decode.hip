@@ -400,8 +400,8 @@ __device__ __forceinline__ uint32_t dpp_u32(uint32_t v) {
 // a time, through LDS of the wave's own, and several blocks share a column's fragments. Where only four columns are in use (CW 4, not 16) one load takes what four
 // would: lane c of 16 takes column c % 4's fragment of step c / 4, and a rotation within the 16 lanes brings it to its
 // column when that step comes. What then stands in the other columns is never looked at. One token of a DeepSeek-V3
-// share: gate/up 25.4 -> 24.8 us, down 17.0 -> 15.7 us; eight columns in two loads gave nothing (Kimi-K2 share, 32
-// tokens).
+// share: down 17.0 -> 15.7 us, and gate/up has registers for a third step in flight; eight columns in two loads gave
+// nothing (Kimi-K2 share, 32 tokens).
 template <int BL>
 struct W4Step {
   static constexpr int STEP = W4_TILE_K;
@@ -458,6 +458,31 @@ struct W4Step {
   }
 };
 
+// Steps s, s + D, ... below stop through PF slots of registers, whose first loads are under way: use(st, u) a step from
+// slot u, load(st, u) one into it. No load is issued past the end: runs are short (7 to 45 steps), and loads that
+// repeat the last step to keep one loop body took as long on the load path as the others (gate/up and down, us: 16 tokens
+// of a Kimi-K2 share in bf16 349 -> 333 and 198 -> 187; one token of a DeepSeek-V3 share in 4 bits 25.1 -> 23.6 and 16.0
+// -> 12.8).
+template <int PF, int D, typename Use, typename Load>
+__device__ __forceinline__ void pipeline(int s, int stop, Use use, Load load) {
+  for (; s + (2 * PF - 1) * D < stop; s += PF * D) {
+#pragma unroll
+    for (int u = 0; u < PF; ++u) {
+      use(s + u * D, u);
+      load(s + (u + PF) * D, u);
+    }
+  }
+#pragma unroll
+  for (int u = 0; u < PF; ++u)
+    if (s + u * D < stop) {
+      use(s + u * D, u);
+      if (s + (u + PF) * D < stop) load(s + (u + PF) * D, u);
+    }
+#pragma unroll
+  for (int u = 0; u < PF - 1; ++u)
+    if (s + (u + PF) * D < stop) use(s + (u + PF) * D, u);
+}
+
 __device__ __forceinline__ float silu(float g) { return g / (1.0f + expf(-g)); }
 
 // ------------------------------------------------------------------------------------------------
@@ -465,13 +490,15 @@ __device__ __forceinline__ float silu(float g) { return g / (1.0f + expf(-g)); }
 // ------------------------------------------------------------------------------------------------
 // Row-major weights: a tile is 16 columns of h for NB blocks of 16 rows of one expert (two for more than 16 tokens).
 // The eight waves split its K and add their sums through LDS in wave order; the next tile's first loads are requested
-// before that, so the weight stream does not stop at a tile's end (Mixtral layer, one token, 79.8 -> 77.9 us).
+// before that, so the weight stream does not stop at a tile's end (Mixtral layer, one token, 79.8 -> 77.9 us). The f32
+// kernel of two blocks has registers for one step of loads in flight; two spill (whole layer of 32 tokens, 37 experts,
+// H 968, F 4992: 507 us against 425).
 template <typename T, int NB>
 struct GateUp {
   static constexpr int NW = DEC_GU_NW, NTH = NW * 64;
   using RS = RowStep<T, 2>;
   static constexpr int COLS = 16;
-  static constexpr int PF = NB == 1 ? 3 : 2;  // steps of loads in flight per wave
+  static constexpr int PF = NB == 1 ? 3 : sizeof(T) == 2 ? 2 : 1;  // steps of loads in flight per wave
   static constexpr int RED = 2 * NB * 4 * 64 * 4;
   static constexpr int WAVE_LDS = RED > RS::LDS_BYTES ? RED : RS::LDS_BYTES;
 
@@ -523,30 +550,24 @@ struct GateUp {
       for (int s = 0; s < 2; ++s)
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb) acc[s][nb] = f32x4{0.f, 0.f, 0.f, 0.f};
-      for (int s0 = wave; s0 < ns; s0 += PF * NW) {
+      auto use = [&](int st, int u) {
+        RS::stage(rw[u], lds, st, K, lane);
 #pragma unroll
-        for (int u = 0; u < PF; ++u) {
-          const int st = s0 + u * NW;
-          if (st < ns) {
-            RS::stage(rw[u], lds, st, K, lane);
+        for (int kk = 0; kk < RS::KST; ++kk) {
+          u32x4 fg[RS::VPF], fu[RS::VPF];
+          RS::frag(lds, 0, kk, lane, fg);
+          RS::frag(lds, 1, kk, lane, fu);
 #pragma unroll
-            for (int kk = 0; kk < RS::KST; ++kk) {
-              u32x4 fg[RS::VPF], fu[RS::VPF];
-              RS::frag(lds, 0, kk, lane, fg);
-              RS::frag(lds, 1, kk, lane, fu);
+          for (int nb = 0; nb < NB; ++nb) {
+            u32x4 b[RS::VPF];
 #pragma unroll
-              for (int nb = 0; nb < NB; ++nb) {
-                u32x4 b[RS::VPF];
-#pragma unroll
-                for (int q = 0; q < RS::VPF; ++q) b[q] = rx[u][nb][kk * RS::VPF + q];
-                DecOp<T>::step(acc[0][nb], fg, b);
-                DecOp<T>::step(acc[1][nb], fu, b);
-              }
-            }
-            load(st + PF * NW, u);
+            for (int q = 0; q < RS::VPF; ++q) b[q] = rx[u][nb][kk * RS::VPF + q];
+            DecOp<T>::step(acc[0][nb], fg, b);
+            DecOp<T>::step(acc[1][nb], fu, b);
           }
         }
-      }
+      };
+      pipeline<PF, NW>(wave, ns, use, load);
       float* red = reinterpret_cast<float*>(lds);
 #pragma unroll
       for (int s = 0; s < 2; ++s)
@@ -589,11 +610,11 @@ struct GateUp {
 // registers are left with two workgroups per CU, and a spilled one is reloaded behind every load in flight (32 tokens of
 // a Kimi-K2 share, some of whose experts have that many rows: 157.5 us with the codes read twice, 145.8 so).
 // Each wave takes a run of K, because scales come by four steps. The eight waves share a tile's K, or four, two or one
-// of them do where that leaves a wave fewer than eight steps, so that it spends its time on filling and draining its
+// of them do where that leaves a wave fewer than seven steps, so that it spends its time on filling and draining its
 // loads, and there are tiles enough for every workgroup.
-// Whole layers (us, eight always and by this rule): 16 tokens, 64 experts, k 4, H 1024, F 4096 98 -> 72; 32 tokens, 128
-// experts, k 8, H 2048, F 768 100 -> 90; 8 tokens, 8 experts, k 2, H 2048, F 8192 62 -> 55. With sixteen steps for eight,
-// 32 tokens, 48 experts, k 2, H 7168, F 2048 160 -> 173; with tiles for every workgroup twice, the first 80.
+// Whole layers (us, eight always and by this rule): 16 tokens, 64 experts, k 4, H 1024, F 4096 93 -> 67; 32 tokens, 128
+// experts, k 8, H 2048, F 768 86 -> 79; 8 tokens, 8 experts, k 2, H 2048, F 8192 46 -> 43. With four steps for seven the
+// second took 85.
 // ANY_KW: the kernel that can do so; a launch of too few tiles takes the other, 0.5 us faster for one token.
 template <bool ANY_KW>
 struct GateUpW4 {
@@ -603,7 +624,7 @@ struct GateUpW4 {
   using WS = W4Step<4>;  // gate, gate, up, up
   static constexpr int RED = 4 * NBMAX * 4 * 64 * 4;
   static constexpr int WAVE_LDS = RED > WS::LDS_BYTES ? RED : WS::LDS_BYTES;
-  static constexpr int LW = 3, MIN_STEPS = 8;
+  static constexpr int LW = 3, MIN_STEPS = 7;
   static_assert(NW == 1 << LW, "");
   // whether half of 2^lw waves are better for each of `total` tiles of ns steps
   __host__ __device__ static constexpr bool narrow(int ns, int64_t total, int grid, int lw) {
@@ -614,8 +635,9 @@ struct GateUpW4 {
   template <int CW, int NB>
   __device__ __forceinline__ static void multiply(const DecodeArgs& a, const Choice& c, int i, int f0, int kw, int wk,
                                                   unsigned char* lds) {
-    // steps of loads in flight per wave; three for one block: 24.8 -> 26.1 us (one token, DeepSeek-V3 share)
-    constexpr int PF = NB == 1 ? 2 : 1;
+    // steps of loads in flight per wave, as the registers allow; two for four columns: 22.9 -> 23.6 us (one token,
+    // DeepSeek-V3 share), 140 -> 147 us (32 tokens, Kimi-K2 share)
+    constexpr int PF = NB == 2 ? 1 : CW == 4 ? 3 : 2;
     const int lane = threadIdx.x & 63;
     const int K = a.H, F = a.F, pitch = w4_pitch(K);
     const int64_t l = __builtin_amdgcn_readfirstlane(c.expert[i]);
@@ -657,30 +679,24 @@ struct GateUpW4 {
 #pragma unroll
       for (int u = 0; u < PF; ++u) load(s0 + u, u);
       if (NB == 1) WS::store_scales(sv, lds, lane);
-      for (; s0 < stop; s0 += PF) {
+      auto use = [&](int st, int u) {
+        float sc[4];
 #pragma unroll
-        for (int u = 0; u < PF; ++u) {
-          const int st = s0 + u;
-          if (st < stop) {
-            float sc[4];
+        for (int b = 0; b < 4; ++b) sc[b] = WS::scale(lds, b, t0, st, lane);
 #pragma unroll
-            for (int b = 0; b < 4; ++b) sc[b] = WS::scale(lds, b, t0, st, lane);
+        for (int j = 0; j < 4; ++j) {
+          u32x4 x[NB][1];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              u32x4 x[NB][1];
+          for (int nb = 0; nb < NB; ++nb) x[nb][0] = WS::template col<CW>(rx[u][nb], j);
 #pragma unroll
-              for (int nb = 0; nb < NB; ++nb) x[nb][0] = WS::template col<CW>(rx[u][nb], j);
+          for (int b = 0; b < 4; ++b) {
+            const u32x4 f[1] = {w4_to_bf16(rw[u][b][j], sc[b])};
 #pragma unroll
-              for (int b = 0; b < 4; ++b) {
-                const u32x4 f[1] = {w4_to_bf16(rw[u][b][j], sc[b])};
-#pragma unroll
-                for (int nb = 0; nb < NB; ++nb) Op16::step(acc[nb][b], f, x[nb]);
-              }
-            }
-            load(st + PF, u);
+            for (int nb = 0; nb < NB; ++nb) Op16::step(acc[nb][b], f, x[nb]);
           }
         }
-      }
+      };
+      pipeline<PF, 1>(s0, stop, use, load);
       s0 = stop;
     }
     float* red = reinterpret_cast<float*>(lds);
@@ -825,29 +841,24 @@ struct Down {
 #pragma unroll
         for (int u = 0; u < PF; ++u) load(s0 + u, u);
         WS::store_scales(sv, lds, lane);
-        for (; s0 < stop; s0 += PF) {
+        auto use = [&](int st, int u) {
+          float sc[CB];
 #pragma unroll
-          for (int u = 0; u < PF; ++u) {
-            if (s0 + u < stop) {
-              float sc[CB];
+          for (int b = 0; b < CB; ++b) sc[b] = WS::scale(lds, b, t0, st, lane);
 #pragma unroll
-              for (int b = 0; b < CB; ++b) sc[b] = WS::scale(lds, b, t0, s0 + u, lane);
+          for (int j = 0; j < 4; ++j) {
 #pragma unroll
-              for (int j = 0; j < 4; ++j) {
+            for (int cb = 0; cb < CB; ++cb) {
+              const u32x4 f[1] = {w4_to_bf16(rw[u][cb][j], sc[cb])};
 #pragma unroll
-                for (int cb = 0; cb < CB; ++cb) {
-                  const u32x4 f[1] = {w4_to_bf16(rw[u][cb][j], sc[cb])};
-#pragma unroll
-                  for (int nb = 0; nb < NB; ++nb) {
-                    const u32x4 b[1] = {WS::template col<CW>(rx[u][nb], j)};
-                    Op16::step(acc[cb][nb], f, b);
-                  }
-                }
+              for (int nb = 0; nb < NB; ++nb) {
+                const u32x4 b[1] = {WS::template col<CW>(rx[u][nb], j)};
+                Op16::step(acc[cb][nb], f, b);
               }
-              load(s0 + u + PF, u);
             }
           }
-        }
+        };
+        pipeline<PF, 1>(s0, stop, use, load);
         s0 = stop;
       }
     } else {
@@ -864,27 +875,22 @@ struct Down {
       };
 #pragma unroll
       for (int u = 0; u < PF; ++u) load(s_begin + u, u);
-      for (int s0 = s_begin; s0 < s_end; s0 += PF) {
+      auto use = [&](int st, int u) {
+        RS::stage(rw[u], lds, st, K, lane);
 #pragma unroll
-        for (int u = 0; u < PF; ++u) {
-          if (s0 + u < s_end) {
-            RS::stage(rw[u], lds, s0 + u, K, lane);
+        for (int kk = 0; kk < RS::KST; ++kk) {
+          u32x4 f[RS::VPF];
+          RS::frag(lds, 0, kk, lane, f);
 #pragma unroll
-            for (int kk = 0; kk < RS::KST; ++kk) {
-              u32x4 f[RS::VPF];
-              RS::frag(lds, 0, kk, lane, f);
+          for (int nb = 0; nb < NB; ++nb) {
+            u32x4 b[RS::VPF];
 #pragma unroll
-              for (int nb = 0; nb < NB; ++nb) {
-                u32x4 b[RS::VPF];
-#pragma unroll
-                for (int q = 0; q < RS::VPF; ++q) b[q] = rx[u][nb][kk * RS::VPF + q];
-                DecOp<T>::step(acc[0][nb], f, b);
-              }
-            }
-            load(s0 + u + PF, u);
+            for (int q = 0; q < RS::VPF; ++q) b[q] = rx[u][nb][kk * RS::VPF + q];
+            DecOp<T>::step(acc[0][nb], f, b);
           }
         }
-      }
+      };
+      pipeline<PF, 1>(s_begin, s_end, use, load);
     }
 #pragma unroll
     for (int nb = 0; nb < NB; ++nb) {
@@ -972,13 +978,13 @@ __global__ __launch_bounds__(256) void decode_sum_kernel(DecodeArgs a) {
 // Parts of the down kernel's units, for an H whose tiles leave half of the CUs idle: as many as give every CU its
 // workgroups, with eight steps per wave at least, since adding the parts takes one more launch. Whole layers (us,
 // without and with; T tokens, E experts, k of them each):
-//   f32  T 13, E 37, k 4, H 968, F 4992      587   403
-//   bf16 T 32, E 64, k 8, H 1024, F 1024     155   109
-//   bf16 T  8, E  8, k 2, H 2048, F 8192     146   138
+//   f32  T 13, E 37, k 4, H 968, F 4992      477   323
+//   bf16 T 32, E 64, k 8, H 1024, F 1024     127    92
+//   bf16 T  8, E  8, k 2, H 2048, F 8192     149   142
 //   bf16 T  4, E 16, k 2, H 3584, F 4096     108   115   (224 tiles: not split)
-//   w4   T 16, E 64, k 4, H 1024, F 4096     142    85
-//   w4   T 16, E 32, k 4, H 2880, F 2880     122   102
-//   w4   T  1, E 128, k 8, H 2048, F 768    18.1  18.4
+//   w4   T 16, E 64, k 4, H 1024, F 4096     115    67
+//   w4   T 16, E 32, k 4, H 2880, F 2880     104    89
+//   w4   T  1, E 128, k 8, H 2048, F 768    17.3  17.3   (too few steps: not split)
 constexpr int kDownSplit = 8;         // parts at most
 constexpr int kDownSplitMaxH = 4096;  // no wider: the workspace has no room for the parts there
 int down_split(const DecodeArgs& a, int cols, int step, int nw, int num_cus) {
