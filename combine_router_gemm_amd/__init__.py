@@ -23,7 +23,7 @@ __all__ = ["MOE_F32", "MOE_BF16", "MOE_FP8_BLOCK", "MoeError", "Layout", "librar
            "moe_combine_send", "moe_combine_recv", "moe_expert_mlp_combine", "moe_dispatch_noalloc",
            "MOE_DISPATCH_NOALLOC_MAX_WORKSPACE", "MOE_W4_GROUP", "MOE_DECODE_MAX_TOKENS", "moe_w4_shapes",
            "moe_w4_codes_bytes", "moe_w4_scales_bytes", "moe_quantize_w4", "moe_dequantize_w4", "moe_expert_mlp_w4",
-           "moe_expert_mlp_w4_workspace_bytes", "moe_layer_decode", "moe_layer_decode_w4",
+           "moe_expert_mlp_w4_workspace_bytes", "moe_expert_mlp_w4_tiling", "moe_layer_decode", "moe_layer_decode_w4",
            "moe_layer_decode_workspace_bytes",
            "moe_expert_mlp_combine_workspace_bytes", "moe_rows_max", "moe_route_workspace_bytes", "moe_dispatch_workspace_bytes",
            "moe_expert_mlp_workspace_bytes", "moe_status_string", "EXPORTED_SYMBOLS"]
@@ -43,7 +43,8 @@ EXPORTED_SYMBOLS = ("moe_status_string", "moe_rows_max", "moe_route_workspace_by
                     "moe_expert_mlp", "moe_combine", "moe_dispatch_fp8", "moe_expert_mlp_fp8", "moe_combine_send",
                     "moe_combine_recv", "moe_expert_mlp_combine", "moe_expert_mlp_combine_workspace_bytes",
                     "moe_dispatch_noalloc", "moe_w4_codes_bytes", "moe_w4_scales_bytes", "moe_quantize_w4",
-                    "moe_dequantize_w4", "moe_expert_mlp_w4_workspace_bytes", "moe_expert_mlp_w4",
+                    "moe_dequantize_w4", "moe_expert_mlp_w4_workspace_bytes", "moe_expert_mlp_w4_tiling",
+                    "moe_expert_mlp_w4",
                     "moe_layer_decode_workspace_bytes", "moe_layer_decode", "moe_layer_decode_w4")
 
 
@@ -118,6 +119,8 @@ def load_library():
     lib.moe_dequantize_w4.restype = i32
     lib.moe_expert_mlp_w4_workspace_bytes.argtypes = [i32, i32, i32, i32, i32, i32]
     lib.moe_expert_mlp_w4_workspace_bytes.restype = sz
+    lib.moe_expert_mlp_w4_tiling.argtypes = [i32] * 7 + [ctypes.POINTER(ctypes.c_int)] * 2
+    lib.moe_expert_mlp_w4_tiling.restype = i32
     lib.moe_expert_mlp_w4.argtypes = [vp, ctypes.POINTER(_CLayout), vp, vp, vp, vp, i32, vp, vp, sz, vp]
     lib.moe_expert_mlp_w4.restype = i32
     lib.moe_layer_decode_workspace_bytes.argtypes = [i32, i32, i32, i32, i32, i32]
@@ -224,6 +227,14 @@ def moe_w4_shapes(*shape: int) -> tuple:
 
 def moe_expert_mlp_w4_workspace_bytes(T: int, k: int, E: int, R: int, C: int, F: int) -> int:
     return int(load_library().moe_expert_mlp_w4_workspace_bytes(T, k, E, R, C, F))
+
+
+def moe_expert_mlp_w4_tiling(T: int, k: int, E: int, R: int, C: int, H: int, F: int) -> tuple:
+    """(rows per tile, parts of the down pass) that moe_expert_mlp_w4 takes for these sizes on the current device."""
+    rows, parts = ctypes.c_int(), ctypes.c_int()
+    st = load_library().moe_expert_mlp_w4_tiling(T, k, E, R, C, H, F, ctypes.byref(rows), ctypes.byref(parts))
+    _check(st, "moe_expert_mlp_w4_tiling")
+    return rows.value, parts.value
 
 
 def moe_layer_decode_workspace_bytes(T: int, H: int, E: int, k: int, F: int, xdt: int) -> int:

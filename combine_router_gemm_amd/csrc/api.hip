@@ -370,17 +370,39 @@ size_t moe_expert_mlp_w4_workspace_bytes(int T, int k, int E, int R, int C, int 
   return moe::mlp_w4_workspace_bytes(moe_rows_max(T, k, E, C), E / R, F);
 }
 
+namespace {
+// The widths moe_expert_mlp_w4 takes for `rows` rows
+int check_w4_widths(int64_t rows, int H, int F) {
+  if (F < 1) return MOE_ERR_INVALID;
+  if (H % MOE_W4_GROUP != 0 || F % MOE_W4_GROUP != 0) return MOE_ERR_UNSUPPORTED;
+  if ((int64_t)2 * F > (int64_t)INT32_MAX / 2 || H > INT32_MAX / 4) return MOE_ERR_UNSUPPORTED;
+  return moe::mlp_w4_fits(rows, H, F) ? MOE_OK : MOE_ERR_UNSUPPORTED;
+}
+}  // namespace
+
+int moe_expert_mlp_w4_tiling(int T, int k, int E, int R, int C, int H, int F, int* tile_rows, int* down_parts) {
+  if (T < 0 || C < 0 || E < 1 || E > MOE_MAX_EXPERTS || R < 1 || E % R != 0 || k < 1 || k > MOE_MAX_TOPK || k > E ||
+      H < 1 || !tile_rows || !down_parts)
+    return MOE_ERR_INVALID;
+  if ((int64_t)T * k > (int64_t)INT32_MAX) return MOE_ERR_UNSUPPORTED;
+  const int64_t rows = moe_rows_max(T, k, E, C);
+  const int st = check_w4_widths(rows, H, F);
+  if (st != MOE_OK) return st;
+  const moe::W4Tiling t = moe::mlp_w4_tiling(rows, E / R, H, F, device_cus());
+  *tile_rows = t.rows;
+  *down_parts = t.parts;
+  return MOE_OK;
+}
+
 int moe_expert_mlp_w4(const void* send_buf, const moe_layout_t* layout, const uint8_t* gu_codes,
                       const uint8_t* gu_scales, const uint8_t* dn_codes, const uint8_t* dn_scales, int F,
                       void* out_buf, void* workspace, size_t workspace_bytes, hipStream_t stream) {
   const int st = check_layout(layout);
   if (st != MOE_OK) return st;
   const moe_layout_t& L = *layout;
-  if (F < 1) return MOE_ERR_INVALID;
-  if (L.H % MOE_W4_GROUP != 0 || F % MOE_W4_GROUP != 0) return MOE_ERR_UNSUPPORTED;
-  if ((int64_t)2 * F > (int64_t)INT32_MAX / 2 || L.H > INT32_MAX / 4) return MOE_ERR_UNSUPPORTED;
   const int64_t rows = moe_rows_max(L.T, L.k, L.E, L.C);
-  if (!moe::mlp_w4_fits(rows, L.H, F)) return MOE_ERR_UNSUPPORTED;
+  const int wst = check_w4_widths(rows, L.H, F);
+  if (wst != MOE_OK) return wst;
   if (!gu_codes || !gu_scales || !dn_codes || !dn_scales) return MOE_ERR_INVALID;
   if (rows > 0 && (!send_buf || !out_buf)) return MOE_ERR_INVALID;
   if (!al16(send_buf) || !al16(gu_codes) || !al16(gu_scales) || !al16(dn_codes) || !al16(dn_scales) ||

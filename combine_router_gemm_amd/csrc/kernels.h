@@ -78,6 +78,11 @@ hipError_t launch_dequantize_w4(const uint8_t* codes, const uint8_t* scales, int
 // rows and both parts of h are read at 31-bit byte offsets
 bool mlp_w4_fits(int64_t rows, int H, int F);
 size_t mlp_w4_workspace_bytes(int64_t rows, int El, int F);
+// what a call is cut into: rows per tile, parts of the down pass's K and the 64-k stages of each
+struct W4Tiling {
+  int rows, parts, stages;
+};
+W4Tiling mlp_w4_tiling(int64_t rows, int El, int H, int F, int num_cus);
 hipError_t launch_expert_mlp_w4(const void* send_buf, const moe_layout_t& L, const uint8_t* gu_codes,
                                 const uint8_t* gu_scales, const uint8_t* dn_codes, const uint8_t* dn_scales, int F,
                                 void* out_buf, void* workspace, int num_cus, hipStream_t stream);

@@ -463,6 +463,18 @@ int w4_rows(int64_t rows_max, int El, int H, int F, int num_cus) {
 
 }  // namespace
 
+W4Tiling mlp_w4_tiling(int64_t rows, int El, int H, int F, int num_cus) {
+  if (rows == 0) return {32, 1, 0};  // nothing runs
+  W4Tiling t{w4_rows(rows, El, H, F, num_cus), 1, 0};
+  if (t.rows == 32) {
+    const int nk = ceil_div_host(F, 64);
+    t.parts = w4_split(rows, El, H, F, num_cus);
+    t.stages = (ceil_div_host(nk, t.parts) + 7) & ~7;
+    t.parts = ceil_div_host(nk, t.stages);  // every part has stages
+  }
+  return t;
+}
+
 // Rows of either pass, one expert's scales and a 16-row block's codes are addressed by 31-bit byte offsets
 bool mlp_w4_fits(int64_t rows, int H, int F) {
   auto scales = [](int64_t n, int64_t k) { return n / 16 * ceil_div_host64(k, W4_STILE_K) * W4_SCALE_TILE; };
@@ -489,7 +501,8 @@ hipError_t launch_expert_mlp_w4(const void* send_buf, const moe_layout_t& L, con
   ws += align256((size_t)rows * sizeof(int));
   bf16_t* h = reinterpret_cast<bf16_t*>(ws);
   const int64_t h_part = (int64_t)(align256((size_t)rows * (size_t)F * 2) / 2);
-  const int bm = w4_rows(rows, El, L.H, F, num_cus);
+  const W4Tiling tiling = mlp_w4_tiling(rows, El, L.H, F, num_cus);
+  const int bm = tiling.rows;
   launch_mlp_plan(L, bm, plan, perm, stream);
   W4Args gu{};
   gu.A = static_cast<const bf16_t*>(send_buf);
@@ -517,10 +530,8 @@ hipError_t launch_expert_mlp_w4(const void* send_buf, const moe_layout_t& L, con
   dn.plan = plan;
   dn.El = El;
   if (bm == 32) {
-    const int nk = ceil_div_host(F, 64);
-    dn.split = w4_split(rows, El, L.H, F, num_cus);
-    dn.split_stages = (ceil_div_host(nk, dn.split) + 7) & ~7;
-    dn.split = ceil_div_host(nk, dn.split_stages);  // every part has stages
+    dn.split = tiling.parts;
+    dn.split_stages = tiling.stages;
     dn.partial = reinterpret_cast<float*>(h + 2 * h_part);
     dn.partial_stride = rows * L.H;
   }

@@ -364,7 +364,7 @@ size_t moe_expert_mlp_w4_workspace_bytes(int T, int k, int E, int R, int C, int 
 /*
  * moe_expert_mlp_w4 -- moe_expert_mlp with 4-bit weights: every weight enters the GEMMs as the bf16 value its
  * code stands for (exact); everything else is moe_expert_mlp in bf16, but that h keeps 16 significant bits (two
- * bf16 parts) where 32-row tiles run (few rows per expert, or few tiles).
+ * bf16 parts) where 32-row tiles run (few rows per expert, or few tiles; moe_expert_mlp_w4_tiling tells).
  *   send_buf   [rows_max, H] bf16 rows written by moe_dispatch
  *   layout     the layout moe_dispatch filled (expert_kept / expert_offset are read on the device)
  *   gu_codes, gu_scales  packed [El, 2F, H]: rows 0..F-1 of an expert are Wg, rows F..2F-1 are Wu
@@ -378,6 +378,15 @@ size_t moe_expert_mlp_w4_workspace_bytes(int T, int k, int E, int R, int C, int 
 int moe_expert_mlp_w4(const void* send_buf, const moe_layout_t* layout, const uint8_t* gu_codes,
                       const uint8_t* gu_scales, const uint8_t* dn_codes, const uint8_t* dn_scales, int F,
                       void* out_buf, void* workspace, size_t workspace_bytes, hipStream_t stream);
+
+/*
+ * moe_expert_mlp_w4_tiling -- what moe_expert_mlp_w4 cuts a call of these sizes into on the current device, computed on
+ * the host from the sizes alone.
+ *   tile_rows   rows per tile: 32 (h keeps 16 significant bits), 128 or 256 (h is one bf16, as in moe_expert_mlp)
+ *   down_parts  parts of the down pass's F whose fp32 sums a further launch adds, 1 where it is not split
+ * Returns what moe_expert_mlp_w4 would return for the sizes, and writes nothing unless that is MOE_OK.
+ */
+int moe_expert_mlp_w4_tiling(int T, int k, int E, int R, int C, int H, int F, int* tile_rows, int* down_parts);
 
 /*
  * moe_layer_decode -- the whole layer (route, dispatch, expert MLP, combine) for at most
