@@ -99,6 +99,10 @@ __device__ __forceinline__ float bf16_rest(float v) {
   const float d = v - (float)(bf16_t)v;
   return fabsf(d) <= 3.4e38f ? d : 0.f;
 }
+// The sum of what the two bf16 parts gave in a product with the same weights. The second part is at most 2^-8 of the
+// first: where the first's sum is infinite (an infinite weight, a sum beyond float32) the second's may be an infinity of
+// the other sign or 0 * inf, so the first's stands alone.
+__device__ __forceinline__ float join_parts(float hi, float lo) { return fabsf(hi) < INFINITY ? hi + lo : hi; }
 
 // ------------------------------------------------------------------------------------------------
 // wave helpers

@@ -899,7 +899,8 @@ struct Down {
         for (int cb = 0; cb < CB; ++cb)
 #pragma unroll
           for (int q = 0; q < 4; ++q)
-            acc[cb][nb][q] += dpp_f32<0x120 + 16 - RPB>(acc[cb][nb][q]);  // row_ror: lane c adds the other part, c + RPB
+            // row_ror: lane c adds the other part, c + RPB
+            acc[cb][nb][q] = join_parts(acc[cb][nb][q], dpp_f32<0x120 + 16 - RPB>(acc[cb][nb][q]));
       }
       const int col = lane & 15, r = nb * RPB + col;
       if (col < RPB && r < cnt) {

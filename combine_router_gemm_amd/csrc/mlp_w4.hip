@@ -310,7 +310,7 @@ __global__ __launch_bounds__(WM * WN * 64) void w4_gemm_kernel(W4Args a, int a_b
 #pragma unroll
       for (int b = 0; b < 2; ++b)
 #pragma unroll
-        for (int q = 0; q < 16; ++q) acc[0][b][q] += __shfl_xor(acc[0][b][q], 16, 64);
+        for (int q = 0; q < 16; ++q) acc[0][b][q] = join_parts(acc[0][b][q], __shfl_xor(acc[0][b][q], 16, 64));
     }
     if constexpr (SPLIT) {
       // lane l holds row l % 32 of a block and four consecutive columns per group of registers

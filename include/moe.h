@@ -365,6 +365,7 @@ size_t moe_expert_mlp_w4_workspace_bytes(int T, int k, int E, int R, int C, int 
  * moe_expert_mlp_w4 -- moe_expert_mlp with 4-bit weights: every weight enters the GEMMs as the bf16 value its
  * code stands for (exact); everything else is moe_expert_mlp in bf16, but that h keeps 16 significant bits (two
  * bf16 parts) where 32-row tiles run (few rows per expert, or few tiles; moe_expert_mlp_w4_tiling tells).
+ * In 32-row tiles a product of h and a down weight beyond float32's range gives an infinity or NaN.
  *   send_buf   [rows_max, H] bf16 rows written by moe_dispatch
  *   layout     the layout moe_dispatch filled (expert_kept / expert_offset are read on the device)
  *   gu_codes, gu_scales  packed [El, 2F, H]: rows 0..F-1 of an expert are Wg, rows F..2F-1 are Wu
@@ -399,7 +400,8 @@ int moe_expert_mlp_w4_tiling(int T, int k, int E, int R, int C, int H, int F, in
  *   Sums are fp32 and y is rounded once to xdt. Unlike moe_expert_mlp, which stores h and the expert outputs
  *   as xdt, bf16 layers keep 16 significant bits of h (two bf16 parts) and fp32 expert outputs, so y is
  *   nearer the formula than the four calls'. A token's y depends on its own kept experts only: an infinity
- *   or NaN in an expert's weights or in another token's x does not reach it.
+ *   or NaN in an expert's weights or in another token's x does not reach it. Infinite weights and sums beyond
+ *   float32 give what they give in fp32 with h rounded to bf16 (an infinity, or NaN where infinities cancel).
  *   x            [T, H] activations (xdt)
  *   w_router     [E, H] fp32; logit_bias, bias_row_stride as for moe_route
  *   C            per-expert capacity, >= 0 (T: no drop)
