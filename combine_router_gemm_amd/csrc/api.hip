@@ -422,8 +422,6 @@ size_t moe_layer_decode_workspace_bytes(int T, int H, int E, int k, int F, moe_d
 }
 
 namespace {
-constexpr int kDecodeMaxWidth = 1 << 23;
-
 // Shared by moe_layer_decode and moe_layer_decode_w4 (packed): validation and launch. `unit` divides H and F.
 int layer_decode(moe::DecodeCall& d, moe_dtype_t xdt, bool packed, size_t workspace_bytes, hipStream_t stream) {
   if (!valid_dtype(xdt)) return MOE_ERR_UNSUPPORTED;
@@ -433,7 +431,7 @@ int layer_decode(moe::DecodeCall& d, moe_dtype_t xdt, bool packed, size_t worksp
   const int unit = packed ? MOE_W4_GROUP : 8;
   if (d.T > MOE_DECODE_MAX_TOKENS || d.H % unit != 0 || d.F % unit != 0) return MOE_ERR_UNSUPPORTED;
   // x, and h of one expert's rows in its two parts, are read at 31-bit byte offsets
-  if (d.H > kDecodeMaxWidth || d.F > kDecodeMaxWidth / MOE_MAX_TOPK) return MOE_ERR_UNSUPPORTED;
+  if (d.H > moe::kDecodeMaxH || d.F > moe::kDecodeMaxF) return MOE_ERR_UNSUPPORTED;
   if (d.bias && d.bias_stride < 0) return MOE_ERR_INVALID;
   if (d.T == 0) return MOE_OK;
   if (!d.x || !d.w_router || !d.w_gu || !d.w_dn || (packed && (!d.s_gu || !d.s_dn)) || !d.logits || !d.ids || !d.wts ||

@@ -334,7 +334,12 @@ struct DecOp<float> {
 
 // Columns (rows of x or h) are read with buffer loads: a lane without one, or past K, reads at an offset beyond the
 // buffer, which the hardware answers with zeros and without a memory request.
-constexpr int DEC_NONE = 0x7fffff00;
+constexpr int DEC_NONE = 0x7ffff000;
+constexpr int DEC_COL_MAX = 3 * 64 * 2;  // the most that is added to it: the fourth step of h's two parts (W4Step)
+static_assert((int64_t)DEC_NONE + DEC_COL_MAX + 16 <= INT32_MAX, "offsets are signed 32-bit sums");
+static_assert((int64_t)MOE_DECODE_MAX_TOKENS * kDecodeMaxH * 4 <= DEC_NONE &&
+                  (int64_t)(MOE_DECODE_MAX_TOKENS * MOE_MAX_TOPK + MOE_DECODE_MAX_TOKENS) * kDecodeMaxF * 4 <= DEC_NONE,
+              "past the end of the rows of x and of both parts of h");
 __device__ __forceinline__ u32x4 ld_col(__amdgpu_buffer_rsrc_t r, int off) {
   return __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(r, off, 0, 0));
 }
@@ -439,7 +444,10 @@ struct W4Step {
     const int off =
         in ? row + step * (STEP * 2 * PARTS) + (lane >> 4) * 16 + (lane & 15) / CW * (64 * PARTS) : DEC_NONE;
 #pragma unroll
-    for (int q = 0; q < CW / 4; ++q) x[q] = ld_col(r, off + q * (64 * PARTS));
+    for (int q = 0; q < CW / 4; ++q) {
+      static_assert((CW / 4 - 1) * 64 * PARTS <= DEC_COL_MAX, "");
+      x[q] = ld_col(r, off + q * (64 * PARTS));
+    }
   }
   // the fragments of matrix step j
   template <int CW>

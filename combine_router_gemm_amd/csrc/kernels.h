@@ -88,6 +88,8 @@ hipError_t launch_expert_mlp_w4(const void* send_buf, const moe_layout_t& L, con
                                 void* out_buf, void* workspace, int num_cus, hipStream_t stream);
 
 // ---- the whole layer for a few tokens ----
+constexpr int kDecodeMaxH = 1 << 23;
+constexpr int kDecodeMaxF = kDecodeMaxH / MOE_MAX_TOPK;
 struct DecodeCall {
   const void* x;
   int bf16;
