@@ -328,13 +328,20 @@ int moe_combine_recv(const void* partial, moe_dtype_t xdt, const moe_layout_t* l
   return hip_status(moe::launch_combine_recv(partial, xdt == MOE_BF16, L, y, stream));
 }
 
+namespace {
+// sizes a packed matrix may have: whole groups and row blocks, and no more weights than bytes can be counted for
+bool w4_sizes(int64_t rows, int K) {
+  return rows % 16 == 0 && K % MOE_W4_GROUP == 0 && K <= INT32_MAX - 512 && rows <= INT64_MAX / 4 / K;
+}
+}  // namespace
+
 size_t moe_w4_codes_bytes(int64_t rows, int K) {
-  if (rows <= 0 || K <= 0 || rows % 16 != 0 || K % MOE_W4_GROUP != 0) return 0;
+  if (rows <= 0 || K <= 0 || !w4_sizes(rows, K)) return 0;
   return (size_t)(rows / 16) * (size_t)moe::ceil_div_host(K, 128) * 1024;
 }
 
 size_t moe_w4_scales_bytes(int64_t rows, int K) {
-  if (rows <= 0 || K <= 0 || rows % 16 != 0 || K % MOE_W4_GROUP != 0) return 0;
+  if (rows <= 0 || K <= 0 || !w4_sizes(rows, K)) return 0;
   return (size_t)(rows / 16) * (size_t)moe::ceil_div_host(K, 512) * 256;
 }
 
@@ -343,8 +350,7 @@ namespace {
 int check_w4(const void* w, moe_dtype_t wdt, int64_t rows, int K, const void* codes, const void* scales) {
   if (!valid_dtype(wdt)) return MOE_ERR_UNSUPPORTED;
   if (rows < 0 || K < 1) return MOE_ERR_INVALID;
-  if (rows % 16 != 0 || K % MOE_W4_GROUP != 0 || K > INT32_MAX - 512) return MOE_ERR_UNSUPPORTED;
-  if (rows > INT64_MAX / 4 / K) return MOE_ERR_UNSUPPORTED;
+  if (!w4_sizes(rows, K)) return MOE_ERR_UNSUPPORTED;
   if (rows > 0 && (!w || !codes || !scales)) return MOE_ERR_INVALID;
   if (!al16(w) || !al16(codes) || !al16(scales)) return MOE_ERR_INVALID;
   return MOE_OK;
@@ -367,7 +373,9 @@ int moe_dequantize_w4(const uint8_t* codes, const uint8_t* scales, int64_t rows,
 
 size_t moe_expert_mlp_w4_workspace_bytes(int T, int k, int E, int R, int C, int F) {
   if (E <= 0 || R <= 0 || E % R != 0 || F <= 0) return 0;
-  return moe::mlp_w4_workspace_bytes(moe_rows_max(T, k, E, C), E / R, F);
+  const int64_t rows = moe_rows_max(T, k, E, C);
+  if (rows > INT32_MAX || !moe::mlp_w4_fits(rows, MOE_W4_GROUP, F)) return 0;  // for no H
+  return moe::mlp_w4_workspace_bytes(rows, E / R, F);
 }
 
 namespace {
@@ -416,7 +424,7 @@ int moe_expert_mlp_w4(const void* send_buf, const moe_layout_t* layout, const ui
 
 size_t moe_layer_decode_workspace_bytes(int T, int H, int E, int k, int F, moe_dtype_t xdt) {
   if (T <= 0 || T > MOE_DECODE_MAX_TOKENS || H <= 0 || E <= 0 || k <= 0 || k > MOE_MAX_TOPK || F <= 0 ||
-      !valid_dtype(xdt))
+      !valid_dtype(xdt) || H > moe::kDecodeMaxH || F > moe::kDecodeMaxF)
     return 0;
   return moe::decode_workspace_bytes(T, H, k, F);
 }

@@ -334,8 +334,9 @@ int moe_expert_mlp_fp8(const uint8_t* send_q, const float* send_scale, const moe
  */
 #define MOE_W4_GROUP 32
 
-/* Bytes of the packed codes / scales of `rows` rows of length K (0 unless rows % 16 == 0, K % 32 == 0 and
- * both are positive). `rows` counts the rows of every matrix of a batch: El * 2F for w_gate_up. */
+/* Bytes of the packed codes / scales of `rows` rows of length K (0 unless both are positive and moe_quantize_w4 takes
+ * them: rows % 16 == 0, K % 32 == 0, K below 2^31 - 512, rows * K below 2^61). `rows` counts the rows of every
+ * matrix of a batch: El * 2F for w_gate_up. */
 size_t moe_w4_codes_bytes(int64_t rows, int K);
 size_t moe_w4_scales_bytes(int64_t rows, int K);
 
@@ -345,7 +346,8 @@ size_t moe_w4_scales_bytes(int64_t rows, int K);
  *           unspecified)
  *   codes   moe_w4_codes_bytes(rows, K) bytes (output)
  *   scales  moe_w4_scales_bytes(rows, K) bytes (output)
- * Requires rows % 16 == 0 and K % 32 == 0 (else MOE_ERR_UNSUPPORTED); rows == 0 is a no-op.
+ * Requires rows % 16 == 0, K % 32 == 0, K < 2^31 - 512 and rows * K < 2^61 (else MOE_ERR_UNSUPPORTED); rows == 0 is a
+ * no-op.
  */
 int moe_quantize_w4(const void* w, moe_dtype_t wdt, int64_t rows, int K, uint8_t* codes, uint8_t* scales,
                     hipStream_t stream);
@@ -358,7 +360,7 @@ int moe_quantize_w4(const void* w, moe_dtype_t wdt, int64_t rows, int K, uint8_t
 int moe_dequantize_w4(const uint8_t* codes, const uint8_t* scales, int64_t rows, int K, void* w, moe_dtype_t wdt,
                       hipStream_t stream);
 
-/* Bytes of scratch `workspace` moe_expert_mlp_w4 needs for this layout and FFN width. */
+/* Bytes of scratch `workspace` moe_expert_mlp_w4 needs for this layout and FFN width (0 where it takes them with no H). */
 size_t moe_expert_mlp_w4_workspace_bytes(int T, int k, int E, int R, int C, int F);
 
 /*
@@ -413,6 +415,7 @@ int moe_expert_mlp_w4_tiling(int T, int k, int E, int R, int C, int H, int F, in
  * F % 8 == 0, H <= 2^23 and F <= 2^20 (else MOE_ERR_UNSUPPORTED); T == 0 is a no-op.
  */
 #define MOE_DECODE_MAX_TOKENS 32
+/* Bytes of scratch `workspace` moe_layer_decode needs (0 for T == 0 and for sizes beyond its limits). */
 size_t moe_layer_decode_workspace_bytes(int T, int H, int E, int k, int F, moe_dtype_t xdt);
 int moe_layer_decode(const void* x, moe_dtype_t xdt, const float* w_router, const float* logit_bias,
                      int64_t bias_row_stride, int T, int H, int E, int R, int k, int C, int F,
