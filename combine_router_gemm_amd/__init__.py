@@ -562,6 +562,8 @@ def moe_expert_mlp_w4(send_buf: torch.Tensor, layout: Layout, gu_codes: torch.Te
     F = gu_codes.shape[1] * 8
     gc, gs, dc, ds = _expert_shapes(L.E // L.R, F, L.H)
     u8, rows = torch.uint8, (L.rows_max, L.H)
+    for name, n in (("expert_kept", L.E), ("expert_offset", L.E + 1)):  # the arrays that the kernels read
+        _arg(getattr(L, name), "layout." + name, torch.int32, (n,), dev)
     need = _size("moe_expert_mlp_w4_workspace_bytes", L.T, L.k, L.E, L.R, L.C, F)
     p_ws, n_ws, ws = _scratch(need, workspace, dev, stream)
     cl = L.c_struct()
