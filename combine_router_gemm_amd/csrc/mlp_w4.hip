@@ -7,7 +7,7 @@
 //
 //   w4_gemm_kernel  BM rows x 64 WN weight rows per tile on v_mfma_f32_32x32x16_bf16. Rows go to LDS directly; the
 //                   codes go from memory to the registers of the wave that multiplies them and never pass LDS.
-//                   BM = 32 (four waves, up to four workgroups per CU) streams the codes of experts with few rows and
+//                   BM = 32 (four waves, four or three workgroups per CU) streams the codes of experts with few rows and
 //                   is bound by their bytes; BM = 128 and 256 (eight waves, one workgroup per CU) are bound by the
 //                   matrix units.
 #include <algorithm>
@@ -87,7 +87,7 @@ __device__ __forceinline__ void wait_loads() {
 // down pass's doubled matrix work is free, and one where the matrix units are the bound.
 // SPLIT: the down pass with K cut over workgroups, where its tiles are few and its K long (see w4_split).
 template <int BM, int WM, int WN, bool GATED, int PARTS, bool SPLIT = false>
-__global__ __launch_bounds__(WM * WN * 64) void w4_gemm_kernel(W4Args a, int a_bytes) {
+__global__ __launch_bounds__(WM * WN * 64, BM == 32 ? 4 : 1) void w4_gemm_kernel(W4Args a, int a_bytes) {
   static_assert(!SPLIT || !GATED, "the gate/up pass is not split");
   constexpr int NW = WM * WN, NTH = NW * 64, S = 32, NS = 4;
   constexpr int WTM = BM / WM, TM = WTM / S;
@@ -395,66 +395,78 @@ int w4_grid(int64_t tiles, int64_t most) {
   return (int)std::max<int64_t>(g, 1);
 }
 
-// workgroups per CU: the registers and LDS of BM = 32 let four stay resident
-constexpr int kPerCu32 = 4;
+// Workgroups that stay resident on a CU with 32-row tiles. Gate/up: four of 123 registers (and 28 KB of LDS; without the
+// bound of four waves per SIMD the compiler takes 132). Down: three, of 45 KB of LDS. Whole passes with the grids and the
+// split for four each while only three were resident, and as it is (us): 8 experts of 16 rows, H 4096, F 14336 194 ->
+// 182, of 64 rows 313 -> 305; 3 experts of 1248 rows, H 224, F 10752 186 -> 170-176.
+constexpr int kPerCuGateUp32 = 4, kPerCuDown32 = 3;
 template <int BM, int WM, int WN, int PARTS>
 void launch_gemms(const W4Args& gu, const W4Args& dn, int64_t rows, int64_t mtiles, int num_cus, hipStream_t stream) {
-  constexpr int PER_CU = BM == 32 ? kPerCu32 : 1, NTH = WM * WN * 64;
+  constexpr int GU_PER_CU = BM == 32 ? kPerCuGateUp32 : 1, DN_PER_CU = BM == 32 ? kPerCuDown32 : 1, NTH = WM * WN * 64;
   w4_gemm_kernel<BM, WM, WN, true, PARTS>
-      <<<w4_grid(mtiles * ceil_div_host(gu.N, WN * 32), PER_CU * num_cus), NTH, 0, stream>>>(gu, (int)(rows * gu.K * 2));
+      <<<w4_grid(mtiles * ceil_div_host(gu.N, WN * 32), GU_PER_CU * num_cus), NTH, 0, stream>>>(gu, (int)(rows * gu.K * 2));
   const int a_bytes = (int)((PARTS == 2 ? dn.part * 2 : 0) + rows * dn.K * 2);
   const int64_t tiles = mtiles * ceil_div_host(dn.N, WN * 64);
   if constexpr (BM == 32) {
     if (dn.split > 1) {
       w4_gemm_kernel<BM, WM, WN, false, PARTS, true>
-          <<<w4_grid(tiles * dn.split, PER_CU * num_cus), NTH, 0, stream>>>(dn, a_bytes);
+          <<<w4_grid(tiles * dn.split, DN_PER_CU * num_cus), NTH, 0, stream>>>(dn, a_bytes);
       w4_sum_kernel<<<(unsigned)ceil_div_host64(rows * dn.N / 8, 256), 256, 0, stream>>>(
           dn.partial, dn.split, dn.partial_stride, dn.plan, dn.out_perm, dn.N, dn.Out);
       return;
     }
   }
-  w4_gemm_kernel<BM, WM, WN, false, PARTS><<<w4_grid(tiles, PER_CU * num_cus), NTH, 0, stream>>>(dn, a_bytes);
+  w4_gemm_kernel<BM, WM, WN, false, PARTS><<<w4_grid(tiles, DN_PER_CU * num_cus), NTH, 0, stream>>>(dn, a_bytes);
 }
 
-// Parts of the down pass's K with 32-row tiles: as many as give every CU its four workgroups, of 16 stages at least, and
+// Parts of the down pass's K with 32-row tiles: as many as give every CU its three workgroups, of 16 stages at least, and
 // no more than F / H, so that the parts' sums take no more workspace than h's two parts. 8 experts of 16 rows, H 4096,
-// F 14336 (128 tiles of 224 stages): the whole pass 241 -> 186 us; 4 experts of 16 rows, H 512, F 8192: 73 -> 30 us, of
-// 256 rows: 110 -> 69 us; 3 experts of 1248 rows, H 224, F 10752: 215 -> 175 us.
+// F 14336 (128 tiles of 224 stages): the whole pass 233 -> 181 us; 4 experts of 16 rows, H 512, F 8192: 78 -> 32 us, of
+// 256 rows: 113 -> 68 us; 3 experts of 1248 rows, H 224, F 10752: 211 -> 170 us.
 // Only up to 128 tiles of rows, as the workspace leaves room for the sums without knowing H.
 constexpr int kSplitMaxTiles = 128;
 int64_t row_tiles32(int64_t rows_max, int El) { return El * ceil_div_host64(ceil_div_host64(rows_max, El), 32); }
 int w4_split(int64_t rows_max, int El, int H, int F, int num_cus) {
   if (row_tiles32(rows_max, El) > kSplitMaxTiles) return 1;
   const int64_t tiles = row_tiles32(rows_max, El) * ceil_div_host(H, 256);
-  const int64_t s = std::min<int64_t>({kPerCu32 * num_cus / tiles, F / H, F / 64 / 16});
+  const int64_t s = std::min<int64_t>({kPerCuDown32 * num_cus / tiles, F / H, F / 64 / 16});
   return s < 2 ? 1 : (int)s;
 }
 
 // Rows per M tile, by the time both passes would take with each, from the largest tile counts the capacity allows. A
-// round of 256-row tiles, one per CU, is the unit for every k; a round of 128-row tiles takes 0.57 of it, and 32-row
-// tiles, up to four per CU, 0.2 and 0.27 for each tile a CU holds: they wait on memory, not on the matrix units.
+// round of 256-row tiles, one per CU, is the unit for every k; a round of 128-row tiles takes 0.57 of it. 32-row tiles
+// wait on memory, not on the matrix units, and share a CU: each of a full round's takes 0.28, and those of the last one
+// 0.22 and 0.1 together.
 // Whole passes (us):
 //   experts, H, F, rows each      32     128     256
-//   32, 7168, 2048, 32           198     252     377
-//   32, 7168, 2048, 96           408     353     436
-//   32, 7168, 2048, 192          814     662     584
-//   8, 4096, 14336, 128          559     461     563
-//   8, 4096, 14336, 256         1054     720     798
-//   4, 2048, 1024, 256            39      56      88
-//   4, 2048, 1024, 1024           93      70      99
-//   12, 1184, 736, 64             28      35      50
+//   32, 7168, 2048, 32           193     253     376
+//   32, 7168, 2048, 64           287     292     394
+//   32, 7168, 2048, 96           407     346     432
+//   32, 7168, 2048, 192          722     656     569
+//   8, 4096, 14336, 96           414     403     519
+//   8, 4096, 14336, 256          931     713     772
+//   4, 2048, 1024, 256            41      58      90
+//   4, 2048, 1024, 512            53      62      93
+//   4, 2048, 1024, 1024           85      68     100
+//   16, 2048, 768, 100            48      57      69
+//   16, 2048, 768, 200            67      62      87
+//   8, 2048, 2048, 128            57      72      88
+//   8, 288, 2016, 640             71      74      99
+//   8, 288, 2016, 1280           119     101     123
+//   12, 1184, 736, 256            46      49      74
 // (64-row tiles with two workgroups per CU were never more than 8 % better than the best of these, and often worse.)
 int w4_rows(int64_t rows_max, int El, int H, int F, int num_cus) {
   const int64_t per = ceil_div_host64(rows_max, El);
-  auto rounds = [&](int bm, int64_t n_tiles) {
+  auto rounds = [&](int bm, int64_t n_tiles, int per_cu32) {
     const double t = (double)El * ceil_div_host64(per, bm) * n_tiles / num_cus;  // tiles per CU
     if (bm == 256) return std::ceil(t);
     if (bm == 128) return 0.57 * std::ceil(t);
-    const double full = std::floor(t / kPerCu32), rest = t - kPerCu32 * full;
-    return full * 1.28 + (rest > 0 ? 0.2 + 0.27 * rest : 0.0);
+    const double full = std::floor(t / per_cu32), rest = t - per_cu32 * full;
+    return full * 0.28 * per_cu32 + (rest > 0 ? 0.1 + 0.22 * rest : 0.0);
   };
   auto cost = [&](int bm, int split) {
-    return H * rounds(bm, ceil_div_host(F, 128)) + (double)F / split * rounds(bm, (int64_t)ceil_div_host(H, 256) * split);
+    return H * rounds(bm, ceil_div_host(F, 128), kPerCuGateUp32) +
+           (double)F / split * rounds(bm, (int64_t)ceil_div_host(H, 256) * split, kPerCuDown32);
   };
   const double c32 = cost(32, w4_split(rows_max, El, H, F, num_cus)), c128 = cost(128, 1), c256 = cost(256, 1);
   if (c32 <= c128 && c32 <= c256) return 32;

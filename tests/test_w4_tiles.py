@@ -15,9 +15,9 @@ CASES = [
     ("t32_ranks", [17, 64, 0, 31, 2, 40, 33, 1], 100, 2, 2, 64, 288, 352, 32, 1),
     ("t32_split", [9, 0, 32, 1], 42, 1, 1, 42, 160, 2304, 32, 2),
     ("t32_split_ranks", [3, 16, 0, 1, 7, 20], 47, 1, 2, 20, 64, 4160, 32, 3),
-    ("t128", [640, 129, 0, 1, 257, 500, 64, 33], 2560, 2, 1, 2560, 288, 2016, 128, 1),
-    ("t128_ranks", [512, 1, 0, 300, 255, 17, 128, 33, 256, 0, 31, 90, 1, 400, 64, 129], 2560, 2, 2, 512, 288, 2016, 128,
-     1),
+    ("t128", [640, 129, 0, 1, 257, 500, 64, 33], 5120, 2, 1, 5120, 288, 2016, 128, 1),
+    ("t128_ranks", [512, 1, 0, 300, 255, 17, 128, 33, 256, 0, 31, 90, 1, 400, 64, 129], 5120, 2, 2, 1024, 288, 2016,
+     128, 1),
     ("t256", [2049, 255, 0, 1400], 8192, 1, 1, 8192, 1056, 544, 256, 1),
     ("t256_ranks", [511, 1, 0, 300, 700, 256, 33, 1025], 4096, 2, 2, 2048, 1056, 544, 256, 1),
 ]
