@@ -400,13 +400,13 @@ __device__ __forceinline__ uint32_t dpp_u32(uint32_t v) {
 
 // Packed 4-bit weights of BL 16-row blocks, 128 k per step. One load is a code tile, and a lane's 16 bytes are the 32
 // k of one row that share a scale. The word j of them is its fragment of matrix step j, whose k are (lane / 16) * 32
-// + 8 j on: the columns' fragments follow that order. The load path is what these kernels run out of first (it takes
-// as long over a byte per lane as over sixteen), so scales come sixteen bytes per lane, four tiles at a time, through
-// LDS of the wave's own, and several blocks share a column's fragments. Where only four columns are in use (CW 4, not
-// 16) one load takes what four would: lane c of 16 takes column c % 4's fragment of step c / 4, and a rotation within
-// the 16 lanes brings it to its column when that step comes. What then stands in the other columns is never looked
-// at. One token of a DeepSeek-V3 share: down 17.0 -> 15.7 us, and gate/up has registers for a third step in flight;
-// eight columns in two loads gave nothing (Kimi-K2 share, 32 tokens).
+// + 8 j on: the columns' fragments follow that order. A load of a byte per lane takes as long as one of sixteen, so
+// scales come sixteen bytes per lane, four tiles at a time, through LDS of the wave's own, and several blocks share a
+// column's fragments. Where only four columns are in use (CW 4, not 16) one load takes what four would: lane c of 16
+// takes column c % 4's fragment of step c / 4, and a rotation within the 16 lanes brings it to its column when that
+// step comes. What then stands in the other columns is never looked at. One token of a DeepSeek-V3 share: down 17.0 ->
+// 15.7 us, and gate/up has registers for a third step in flight; eight columns in two loads gave nothing (Kimi-K2
+// share, 32 tokens).
 template <int BL>
 struct W4Step {
   static constexpr int STEP = W4_TILE_K;
@@ -468,7 +468,7 @@ struct W4Step {
 
 // Steps s, s + D, ... below stop through PF slots of registers, whose first loads are under way: use(st, u) a step
 // from slot u, load(st, u) one into it. No load is issued past the end: runs are short (7 to 45 steps), and loads
-// that repeat the last step to keep one loop body took as long on the load path as the others (gate/up and down, us:
+// that repeat the last step to keep one loop body take as long as the others (gate/up and down, us:
 // 16 tokens of a Kimi-K2 share in bf16 349 -> 333 and 198 -> 187; one token of a DeepSeek-V3 share in 4 bits 25.1 ->
 // 23.6 and 16.0 -> 12.8).
 template <int PF, int D, typename Use, typename Load>

@@ -64,3 +64,10 @@ def test_down_over_several_chunks_of_scales(monkeypatch, T, El):
 def test_four_waves_to_a_gate_up_tile(monkeypatch, T, El, k, F, H):
     print(f"\n[gpu] layer w4 four waves T {T} experts {El} H {H} F {F}", flush=True)
     check(monkeypatch, T, H, El, k, F, 740 + T)
+
+
+# every (token, slot) pair chooses an expert of its own: 256 rows and as many experts, the most a call can have
+@pytest.mark.parametrize("El", [256, 512])
+def test_as_many_experts_as_pairs(monkeypatch, El):
+    print(f"\n[gpu] layer w4 256 rows of 256 experts of {El}", flush=True)
+    check(monkeypatch, 32, 96, El, 8, 64, 760)
