@@ -132,7 +132,7 @@ CASES = [
     ("split", [9, 0, 32, 1], 42, 1, 1, 42, 160, 2304),
     ("split_ranks", [3, 16, 0, 1, 7, 20], 47, 1, 2, 20, 64, 4160),
     ("split_many_rows", [150, 70], 220, 1, 1, 220, 96, 4160),
-    # enough tiles for 256 CUs that the 128- and the 256-row tiles run
+    # many tiles (tests/test_w4_tiles.py has the cases of the 128- and 256-row tiles)
     ("tile_128", [640, 129, 0, 1, 257, 500, 64, 33], 2560, 2, 1, 2560, 288, 2016),
     ("tile_256_ranks", [512, 1, 0, 300, 255, 17, 128, 33, 256, 0, 31, 90, 1, 700, 64, 129], 2048, 2, 2, 2048, 160, 2016),
 ]
