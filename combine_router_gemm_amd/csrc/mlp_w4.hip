@@ -8,8 +8,9 @@
 //   w4_gemm_kernel  BM rows x 64 WN weight rows per tile on v_mfma_f32_32x32x16_bf16. Rows go to LDS directly; the
 //                   codes go from memory to the registers of the wave that multiplies them and never pass LDS.
 //                   BM = 32 (four waves, four or three workgroups per CU) streams the codes of experts with few rows and
-//                   is bound by their bytes; BM = 128 and 256 (eight waves, one workgroup per CU) are bound by the
-//                   matrix units.
+//                   is bound by their bytes; BM = 128 and 256 (eight waves, one workgroup per CU) decode a code for more
+//                   rows: at 1024 rows per expert the matrix units are busy 53 to 57 % of the cycles, at 100 to 250
+//                   neither they nor the bytes are reached (1.4 to 1.9 times the longer of the two).
 #include <algorithm>
 #include <cmath>
 #include <type_traits>

@@ -5,6 +5,7 @@ import pytest
 import torch
 
 import tests._layer_ref as ref
+import tests.test_sparse_experts as sparse
 from tests._layer_ref import layer, within
 from tests.test_gpu_decode import DEV, Run, pack4
 from tests.test_sparse_experts import expert, rows_of, weights
@@ -71,3 +72,10 @@ def test_four_waves_to_a_gate_up_tile(monkeypatch, T, El, k, F, H):
 def test_as_many_experts_as_pairs(monkeypatch, El):
     print(f"\n[gpu] layer w4 256 rows of 256 experts of {El}", flush=True)
     check(monkeypatch, 32, 96, El, 8, 64, 760)
+
+
+# R == E: one weight set, so a token's kept choices are one row with the sum of their weights; with a capacity and without
+@pytest.mark.parametrize("kind", ["f32", "bf16", "w4"])
+@pytest.mark.parametrize("T,C", [(1, 1), (7, 2), (32, 32)])
+def test_one_weight_set_for_every_expert(monkeypatch, T, C, kind):
+    sparse.test_layer(monkeypatch, "one_set", T, 96, 8, 8, 64, 8, C, "uniform", kind)

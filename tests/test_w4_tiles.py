@@ -13,6 +13,7 @@ from tests.test_gpu_w4 import DEV, case
 CASES = [
     ("t32", [33, 0, 16, 70, 1, 5], 130, 1, 1, 70, 160, 96, 32, 1),
     ("t32_ranks", [17, 64, 0, 31, 2, 40, 33, 1], 100, 2, 2, 64, 288, 352, 32, 1),
+    ("t32_one_set", [5, 0, 40, 3, 33, 1], 90, 1, 6, 40, 96, 160, 32, 1),  # every rank's rows share one weight set
     ("t32_split", [9, 0, 32, 1], 42, 1, 1, 42, 160, 2304, 32, 2),
     ("t32_split_ranks", [3, 16, 0, 1, 7, 20], 47, 1, 2, 20, 64, 4160, 32, 3),
     ("t128", [640, 129, 0, 1, 257, 500, 64, 33], 5120, 2, 1, 5120, 288, 2016, 128, 1),
