@@ -24,7 +24,10 @@ __all__ = ["MOE_F32", "MOE_BF16", "MOE_FP8_BLOCK", "MoeError", "Layout", "librar
            "MOE_DISPATCH_NOALLOC_MAX_WORKSPACE", "MOE_W4_GROUP", "MOE_DECODE_MAX_TOKENS", "moe_w4_shapes",
            "moe_w4_codes_bytes", "moe_w4_scales_bytes", "moe_quantize_w4", "moe_dequantize_w4", "moe_expert_mlp_w4",
            "moe_expert_mlp_w4_workspace_bytes", "moe_expert_mlp_w4_tiling", "moe_layer_decode", "moe_layer_decode_w4",
-           "moe_layer_decode_workspace_bytes",
+           "moe_layer_decode_workspace_bytes", "moe_quantize_i8", "moe_dequantize_i8", "moe_dispatch_i8",
+           "moe_expert_mlp_i8", "moe_expert_mlp_i8_workspace_bytes", "moe_balance_loss",
+           "moe_balance_loss_workspace_bytes", "moe_combine_backward", "moe_route_backward",
+           "moe_route_backward_workspace_bytes",
            "moe_expert_mlp_combine_workspace_bytes", "moe_rows_max", "moe_route_workspace_bytes", "moe_dispatch_workspace_bytes",
            "moe_expert_mlp_workspace_bytes", "moe_status_string", "EXPORTED_SYMBOLS"]
 
@@ -45,7 +48,10 @@ EXPORTED_SYMBOLS = ("moe_status_string", "moe_rows_max", "moe_route_workspace_by
                     "moe_dispatch_noalloc", "moe_w4_codes_bytes", "moe_w4_scales_bytes", "moe_quantize_w4",
                     "moe_dequantize_w4", "moe_expert_mlp_w4_workspace_bytes", "moe_expert_mlp_w4_tiling",
                     "moe_expert_mlp_w4",
-                    "moe_layer_decode_workspace_bytes", "moe_layer_decode", "moe_layer_decode_w4")
+                    "moe_layer_decode_workspace_bytes", "moe_layer_decode", "moe_layer_decode_w4", "moe_quantize_i8",
+                    "moe_dequantize_i8", "moe_dispatch_i8", "moe_expert_mlp_i8_workspace_bytes", "moe_expert_mlp_i8",
+                    "moe_balance_loss_workspace_bytes", "moe_balance_loss", "moe_combine_backward",
+                    "moe_route_backward_workspace_bytes", "moe_route_backward")
 
 
 class MoeError(RuntimeError):
@@ -129,6 +135,26 @@ def load_library():
     lib.moe_layer_decode.restype = i32
     lib.moe_layer_decode_w4.argtypes = [vp, vp, vp, i64] + [i32] * 7 + [vp] * 9 + [sz, vp]
     lib.moe_layer_decode_w4.restype = i32
+    lib.moe_quantize_i8.argtypes = [vp, i32, i64, i32, vp, vp, vp]
+    lib.moe_quantize_i8.restype = i32
+    lib.moe_dequantize_i8.argtypes = [vp, vp, i64, i32, vp, i32, vp]
+    lib.moe_dequantize_i8.restype = i32
+    lib.moe_dispatch_i8.argtypes = [vp, i32, vp, ctypes.POINTER(_CLayout), vp, vp, vp, sz, vp]
+    lib.moe_dispatch_i8.restype = i32
+    lib.moe_expert_mlp_i8_workspace_bytes.argtypes = [i32] * 7
+    lib.moe_expert_mlp_i8_workspace_bytes.restype = sz
+    lib.moe_expert_mlp_i8.argtypes = [vp, vp, ctypes.POINTER(_CLayout), vp, vp, vp, vp, i32, vp, vp, sz, vp]
+    lib.moe_expert_mlp_i8.restype = i32
+    lib.moe_balance_loss_workspace_bytes.argtypes = [i32, i32, i32]
+    lib.moe_balance_loss_workspace_bytes.restype = sz
+    lib.moe_balance_loss.argtypes = [vp] * 4 + [i32] * 4 + [ctypes.c_float] + [vp] * 4 + [sz, vp]
+    lib.moe_balance_loss.restype = i32
+    lib.moe_combine_backward.argtypes = [vp, i32, vp, ctypes.POINTER(_CLayout), vp, vp, vp, vp]
+    lib.moe_combine_backward.restype = i32
+    lib.moe_route_backward_workspace_bytes.argtypes = [i32, i32, i32, i32]
+    lib.moe_route_backward_workspace_bytes.restype = sz
+    lib.moe_route_backward.argtypes = [vp, i32] + [vp] * 5 + [i32] * 4 + [vp] * 5 + [sz, vp]
+    lib.moe_route_backward.restype = i32
     _lib = lib
     return lib
 
@@ -239,6 +265,18 @@ def moe_expert_mlp_w4_tiling(T: int, k: int, E: int, R: int, C: int, H: int, F: 
 
 def moe_layer_decode_workspace_bytes(T: int, H: int, E: int, k: int, F: int, xdt: int) -> int:
     return int(load_library().moe_layer_decode_workspace_bytes(T, H, E, k, F, xdt))
+
+
+def moe_expert_mlp_i8_workspace_bytes(T: int, k: int, E: int, R: int, C: int, H: int, F: int) -> int:
+    return int(load_library().moe_expert_mlp_i8_workspace_bytes(T, k, E, R, C, H, F))
+
+
+def moe_balance_loss_workspace_bytes(T: int, E: int, S: int) -> int:
+    return int(load_library().moe_balance_loss_workspace_bytes(T, E, S))
+
+
+def moe_route_backward_workspace_bytes(T: int, H: int, E: int, xdt: int) -> int:
+    return int(load_library().moe_route_backward_workspace_bytes(T, H, E, xdt))
 
 
 # ------------------------------------------------------------------------------------------------
@@ -629,3 +667,148 @@ def moe_layer_decode_w4(x: torch.Tensor, w_router: torch.Tensor, logit_bias: Opt
                (dn_scales, "dn_scales", u8, ds))
     _layer("moe_layer_decode_w4", x, w_router, logit_bias, k, R, C, F, weights, logits, topk_ids, topk_w, y,
            workspace, stream)
+
+
+# ------------------------------------------------------------------------------------------------
+# int8 experts
+# ------------------------------------------------------------------------------------------------
+
+def _opt(t: Optional[torch.Tensor], name: str, dtype, shape, dev: int) -> Optional[int]:
+    """_arg of a tensor that may be left out."""
+    return None if t is None else _arg(t, name, dtype, shape, dev)
+
+
+def _layout_args(L: Layout, names, dev: int) -> None:
+    """Checks the layout arrays that a call's kernels read or write."""
+    shapes = {"expert_offset": (L.E + 1,), "row_token": (L.rows_max,), "row_slot": (L.rows_max,), "pair_row": (L.T, L.k)}
+    for name in names:
+        _arg(getattr(L, name), "layout." + name, torch.int32, shapes.get(name, (L.E,)), dev)
+
+
+_LAYOUT_ALL = ("expert_count", "expert_kept", "expert_overflow", "expert_offset", "row_token", "row_slot", "pair_row")
+
+
+def moe_quantize_i8(w: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor, stream=None) -> None:
+    """Rows of w [.., K] (f32 or bf16) to int8 codes [.., K] and one float32 scale per row [..]."""
+    dev, K = _device(w, "w"), w.shape[-1]
+    st = load_library().moe_quantize_i8(
+        _arg(w, "w", w.dtype, w.shape, dev), _dtype_code(w), w.numel() // K if K else 0, K,
+        _arg(codes, "codes", torch.int8, w.shape, dev), _arg(scales, "scales", torch.float32, w.shape[:-1], dev),
+        _raw_stream(stream, dev))
+    if st:
+        _check(st, "moe_quantize_i8")
+
+
+def moe_dequantize_i8(codes: torch.Tensor, scales: torch.Tensor, w: torch.Tensor, stream=None) -> None:
+    """code * scale into w [.., K] (f32 or bf16)."""
+    dev, K = _device(w, "w"), w.shape[-1]
+    st = load_library().moe_dequantize_i8(
+        _arg(codes, "codes", torch.int8, w.shape, dev), _arg(scales, "scales", torch.float32, w.shape[:-1], dev),
+        w.numel() // K if K else 0, K, _arg(w, "w", w.dtype, w.shape, dev), _dtype_code(w), _raw_stream(stream, dev))
+    if st:
+        _check(st, "moe_dequantize_i8")
+
+
+def moe_dispatch_i8(x: torch.Tensor, topk_ids: torch.Tensor, layout: Layout, send_q: torch.Tensor,
+                    send_scale: torch.Tensor, workspace: Optional[torch.Tensor] = None, stream=None) -> None:
+    """moe_dispatch with int8 send rows: codes [rows_max, H] and one float32 scale per row. x must be bf16."""
+    dev = _device(x, "x")
+    L = layout
+    _layout_args(L, _LAYOUT_ALL, dev)
+    p_ws, n_ws, ws = _scratch(_size("moe_dispatch_workspace_bytes", L.T, L.k, L.E), workspace, dev, stream)
+    cl = L.c_struct()
+    st = load_library().moe_dispatch_i8(
+        _arg(x, "x", torch.bfloat16, (L.T, L.H), dev), MOE_BF16, _arg(topk_ids, "topk_ids", torch.int32, (L.T, L.k), dev),
+        ctypes.byref(cl), _arg(send_q, "send_q", torch.int8, (L.rows_max, L.H), dev),
+        _arg(send_scale, "send_scale", torch.float32, (L.rows_max,), dev), p_ws, n_ws, _raw_stream(stream, dev))
+    if st:
+        _check(st, "moe_dispatch_i8")
+
+
+def moe_expert_mlp_i8(send_q: torch.Tensor, send_scale: torch.Tensor, layout: Layout, gu_codes: torch.Tensor,
+                      gu_scales: torch.Tensor, dn_codes: torch.Tensor, dn_scales: torch.Tensor, out_buf: torch.Tensor,
+                      workspace: Optional[torch.Tensor] = None, stream=None) -> None:
+    """Expert SwiGLU MLP on int8 rows with int8 weights (codes [El, 2F, H] and [El, H, F], a scale per output channel);
+    out_buf is bf16."""
+    dev = _device(send_q, "send_q")
+    L = layout
+    El, F = L.E // L.R, gu_codes.shape[1] // 2
+    i8, f32 = torch.int8, torch.float32
+    _layout_args(L, ("expert_kept", "expert_offset"), dev)
+    need = _size("moe_expert_mlp_i8_workspace_bytes", L.T, L.k, L.E, L.R, L.C, L.H, F)
+    p_ws, n_ws, ws = _scratch(need, workspace, dev, stream)
+    cl = L.c_struct()
+    st = load_library().moe_expert_mlp_i8(
+        _arg(send_q, "send_q", i8, (L.rows_max, L.H), dev), _arg(send_scale, "send_scale", f32, (L.rows_max,), dev),
+        ctypes.byref(cl), _arg(gu_codes, "gu_codes", i8, (El, 2 * F, L.H), dev),
+        _arg(gu_scales, "gu_scales", f32, (El, 2 * F), dev), _arg(dn_codes, "dn_codes", i8, (El, L.H, F), dev),
+        _arg(dn_scales, "dn_scales", f32, (El, L.H), dev), F,
+        _arg(out_buf, "out_buf", torch.bfloat16, (L.rows_max, L.H), dev), p_ws, n_ws, _raw_stream(stream, dev))
+    if st:
+        _check(st, "moe_expert_mlp_i8")
+
+
+# ------------------------------------------------------------------------------------------------
+# training the router
+# ------------------------------------------------------------------------------------------------
+
+def moe_balance_loss(logits: torch.Tensor, topk_ids: torch.Tensor, weight: float, loss: torch.Tensor,
+                     expert_count: torch.Tensor, d_logits: Optional[torch.Tensor] = None,
+                     seq_offset: Optional[torch.Tensor] = None, token_mask: Optional[torch.Tensor] = None,
+                     workspace: Optional[torch.Tensor] = None, stream=None) -> None:
+    """Per-expert counts [S, E], balance loss [1] and its gradient [T, E] over S sequences (seq_offset [S + 1]; one of all
+    tokens without it). token_mask [T] is uint8 or bool, 0 for tokens that do not count."""
+    dev = _device(logits, "logits")
+    T, E = logits.shape
+    k = topk_ids.shape[1]
+    S = 1 if seq_offset is None else seq_offset.shape[0] - 1
+    f32, i32 = torch.float32, torch.int32
+    mask_t = torch.bool if token_mask is not None and token_mask.dtype is torch.bool else torch.uint8
+    p_ws, n_ws, ws = _scratch(_size("moe_balance_loss_workspace_bytes", T, E, S), workspace, dev, stream)
+    st = load_library().moe_balance_loss(
+        _arg(logits, "logits", f32, (T, E), dev), _arg(topk_ids, "topk_ids", i32, (T, k), dev),
+        _opt(seq_offset, "seq_offset", i32, (S + 1,), dev), _opt(token_mask, "token_mask", mask_t, (T,), dev), T, E, k, S,
+        weight, _arg(loss, "loss", f32, (1,), dev), _arg(expert_count, "expert_count", i32, (S, E), dev),
+        _opt(d_logits, "d_logits", f32, (T, E), dev), p_ws, n_ws, _raw_stream(stream, dev))
+    if st:
+        _check(st, "moe_balance_loss")
+
+
+def moe_combine_backward(dy: torch.Tensor, out_buf: torch.Tensor, layout: Layout, topk_w: torch.Tensor,
+                         d_topk_w: torch.Tensor, d_out_buf: Optional[torch.Tensor] = None, stream=None) -> None:
+    """Gradients of moe_combine: d_topk_w [T, k], and d_out_buf [rows_max, H] unless it is left out."""
+    dev = _device(dy, "dy")
+    L, f32 = layout, torch.float32
+    _layout_args(L, ("pair_row",), dev)
+    cl = L.c_struct()
+    st = load_library().moe_combine_backward(
+        _arg(dy, "dy", dy.dtype, (L.T, L.H), dev), _dtype_code(dy),
+        _arg(out_buf, "out_buf", dy.dtype, (L.rows_max, L.H), dev), ctypes.byref(cl),
+        _arg(topk_w, "topk_w", f32, (L.T, L.k), dev), _arg(d_topk_w, "d_topk_w", f32, (L.T, L.k), dev),
+        _opt(d_out_buf, "d_out_buf", dy.dtype, (L.rows_max, L.H), dev), _raw_stream(stream, dev))
+    if st:
+        _check(st, "moe_combine_backward")
+
+
+def moe_route_backward(x: torch.Tensor, w_router: torch.Tensor, topk_ids: torch.Tensor, topk_w: torch.Tensor,
+                       d_topk_w: Optional[torch.Tensor], d_logits_in: Optional[torch.Tensor], d_logits: torch.Tensor,
+                       d_x: Optional[torch.Tensor] = None, d_w_router: Optional[torch.Tensor] = None,
+                       d_bias: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
+                       stream=None) -> None:
+    """Gradients of moe_route from those of the routing weights (d_topk_w) and of the logits (d_logits_in), either of which
+    may be None: d_logits [T, E], and d_x [T, H], d_w_router [E, H], d_bias [E] unless they are left out."""
+    dev, dt = _device(x, "x"), x.dtype
+    T, H = x.shape
+    E, k = w_router.shape[0], topk_ids.shape[1]
+    f32 = torch.float32
+    code = _dtype_code(x)
+    p_ws, n_ws, ws = _scratch(_size("moe_route_backward_workspace_bytes", T, H, E, code), workspace, dev, stream)
+    st = load_library().moe_route_backward(
+        _arg(x, "x", dt, (T, H), dev), code, _arg(w_router, "w_router", f32, (E, H), dev),
+        _arg(topk_ids, "topk_ids", torch.int32, (T, k), dev), _arg(topk_w, "topk_w", f32, (T, k), dev),
+        _opt(d_topk_w, "d_topk_w", f32, (T, k), dev), _opt(d_logits_in, "d_logits_in", f32, (T, E), dev), T, H, E, k,
+        _arg(d_logits, "d_logits", f32, (T, E), dev), _opt(d_x, "d_x", dt, (T, H), dev),
+        _opt(d_w_router, "d_w_router", f32, (E, H), dev), _opt(d_bias, "d_bias", f32, (E,), dev), p_ws, n_ws,
+        _raw_stream(stream, dev))
+    if st:
+        _check(st, "moe_route_backward")

@@ -475,4 +475,147 @@ int moe_layer_decode_w4(const void* x, const float* w_router, const float* logit
   return layer_decode(d, MOE_BF16, true, workspace_bytes, stream);
 }
 
+
+namespace {
+// Shared by moe_quantize_i8 and moe_dequantize_i8
+int check_i8(const void* w, moe_dtype_t wdt, int64_t rows, int K, const void* codes, const void* scales) {
+  if (!valid_dtype(wdt)) return MOE_ERR_UNSUPPORTED;
+  if (rows < 0 || K < 1) return MOE_ERR_INVALID;
+  if (K % 16 != 0 || rows > INT64_MAX / 4 / K) return MOE_ERR_UNSUPPORTED;
+  if (rows > 0 && (!w || !codes || !scales)) return MOE_ERR_INVALID;
+  if (!al16(w) || !al16(codes) || !al4(scales)) return MOE_ERR_INVALID;
+  return MOE_OK;
+}
+}  // namespace
+
+int moe_quantize_i8(const void* w, moe_dtype_t wdt, int64_t rows, int K, int8_t* codes, float* scales,
+                    hipStream_t stream) {
+  const int st = check_i8(w, wdt, rows, K, codes, scales);
+  if (st != MOE_OK || rows == 0) return st;
+  return hip_status(moe::launch_quantize_i8(w, wdt == MOE_BF16, rows, K, codes, scales, stream));
+}
+
+int moe_dequantize_i8(const int8_t* codes, const float* scales, int64_t rows, int K, void* w, moe_dtype_t wdt,
+                      hipStream_t stream) {
+  const int st = check_i8(w, wdt, rows, K, codes, scales);
+  if (st != MOE_OK || rows == 0) return st;
+  return hip_status(moe::launch_dequantize_i8(codes, scales, rows, K, w, wdt == MOE_BF16, stream));
+}
+
+int moe_dispatch_i8(const void* x, moe_dtype_t xdt, const int32_t* topk_ids, const moe_layout_t* layout, int8_t* send_q,
+                    float* send_scale, void* workspace, size_t workspace_bytes, hipStream_t stream) {
+  if (xdt != MOE_BF16) return MOE_ERR_UNSUPPORTED;
+  const int st = check_layout(layout);
+  if (st != MOE_OK) return st;
+  const moe_layout_t& L = *layout;
+  if (L.H % 16 != 0) return MOE_ERR_UNSUPPORTED;
+  const int64_t rows = moe_rows_max(L.T, L.k, L.E, L.C);
+  if (L.T > 0 && (!x || !topk_ids)) return MOE_ERR_INVALID;
+  if (rows > 0 && (!send_q || !send_scale)) return MOE_ERR_INVALID;
+  if (!al16(x) || !al16(send_q) || !al16(workspace) || !al4(send_scale) || !al4(topk_ids)) return MOE_ERR_INVALID;
+  const size_t need = moe_dispatch_workspace_bytes(L.T, L.k, L.E);
+  if (need > 0 && (!workspace || workspace_bytes < need)) return MOE_ERR_INVALID;
+  char* ws = static_cast<char*>(workspace);
+  int* blk_count = reinterpret_cast<int*>(ws);
+  int* pair_local =
+      reinterpret_cast<int*>(ws + moe::align256((size_t)moe::dispatch_num_blocks(L.T) * L.E * sizeof(int)));
+  return hip_status(moe::launch_dispatch_i8(x, topk_ids, L, send_q, send_scale, blk_count, pair_local, stream));
+}
+
+namespace {
+// The widths moe_expert_mlp_i8 takes for `rows` rows
+int check_i8_widths(int64_t rows, int H, int F) {
+  if (F < 1) return MOE_ERR_INVALID;
+  if (H % 16 != 0 || F % 16 != 0) return MOE_ERR_UNSUPPORTED;
+  return moe::mlp_i8_fits(rows, H, F) ? MOE_OK : MOE_ERR_UNSUPPORTED;
+}
+}  // namespace
+
+size_t moe_expert_mlp_i8_workspace_bytes(int T, int k, int E, int R, int C, int H, int F) {
+  if (E <= 0 || R <= 0 || E % R != 0 || H <= 0 || F <= 0) return 0;
+  const int64_t rows = moe_rows_max(T, k, E, C);
+  if (rows > INT32_MAX || !moe::mlp_i8_fits(rows, H, F)) return 0;
+  return moe::mlp_i8_workspace_bytes(rows, E / R, H, F);
+}
+
+int moe_expert_mlp_i8(const int8_t* send_q, const float* send_scale, const moe_layout_t* layout, const int8_t* gu_codes,
+                      const float* gu_scales, const int8_t* dn_codes, const float* dn_scales, int F, void* out_buf,
+                      void* workspace, size_t workspace_bytes, hipStream_t stream) {
+  const int st = check_layout(layout);
+  if (st != MOE_OK) return st;
+  const moe_layout_t& L = *layout;
+  const int64_t rows = moe_rows_max(L.T, L.k, L.E, L.C);
+  const int wst = check_i8_widths(rows, L.H, F);
+  if (wst != MOE_OK) return wst;
+  if (!gu_codes || !gu_scales || !dn_codes || !dn_scales) return MOE_ERR_INVALID;
+  if (rows > 0 && (!send_q || !send_scale || !out_buf)) return MOE_ERR_INVALID;
+  if (!al16(send_q) || !al4(send_scale) || !al16(gu_codes) || !al4(gu_scales) || !al16(dn_codes) || !al4(dn_scales) ||
+      !al16(out_buf) || !al16(workspace))
+    return MOE_ERR_INVALID;
+  if (!workspace || workspace_bytes < moe_expert_mlp_i8_workspace_bytes(L.T, L.k, L.E, L.R, L.C, L.H, F))
+    return MOE_ERR_INVALID;
+  return hip_status(moe::launch_expert_mlp_i8(send_q, send_scale, L, gu_codes, gu_scales, dn_codes, dn_scales, F,
+                                              out_buf, workspace, device_cus(), stream));
+}
+
+size_t moe_balance_loss_workspace_bytes(int T, int E, int S) {
+  if (T < 0 || E < 1 || E > MOE_MAX_EXPERTS || S < 1) return 0;
+  return moe::balance_workspace_bytes(T, E, S);
+}
+
+int moe_balance_loss(const float* logits, const int32_t* topk_ids, const int32_t* seq_offset, const uint8_t* token_mask,
+                     int T, int E, int k, int S, float weight, float* loss, int32_t* expert_count, float* d_logits,
+                     void* workspace, size_t workspace_bytes, hipStream_t stream) {
+  if (T < 0 || E < 1 || E > MOE_MAX_EXPERTS || k < 1 || k > MOE_MAX_TOPK || k > E || S < 1) return MOE_ERR_INVALID;
+  if (!seq_offset && S != 1) return MOE_ERR_INVALID;
+  if ((int64_t)T * k > (int64_t)INT32_MAX || (int64_t)S * E > (int64_t)INT32_MAX) return MOE_ERR_UNSUPPORTED;
+  if (!loss || !expert_count || (T > 0 && (!logits || !topk_ids))) return MOE_ERR_INVALID;
+  if (!al4(logits) || !al4(topk_ids) || !al4(seq_offset) || !al4(loss) || !al4(expert_count) || !al4(d_logits) ||
+      !al16(workspace))
+    return MOE_ERR_INVALID;
+  if (!workspace || workspace_bytes < moe_balance_loss_workspace_bytes(T, E, S)) return MOE_ERR_INVALID;
+  return hip_status(moe::launch_balance(logits, topk_ids, seq_offset, token_mask, T, E, k, S, weight, loss, expert_count,
+                                        d_logits, workspace, stream));
+}
+
+int moe_combine_backward(const void* dy, moe_dtype_t xdt, const void* out_buf, const moe_layout_t* layout,
+                         const float* topk_w, float* d_topk_w, void* d_out_buf, hipStream_t stream) {
+  if (!valid_dtype(xdt)) return MOE_ERR_UNSUPPORTED;
+  const int st = check_layout(layout);
+  if (st != MOE_OK) return st;
+  const moe_layout_t& L = *layout;
+  if (L.T == 0) return MOE_OK;
+  const int64_t rows = moe_rows_max(L.T, L.k, L.E, L.C);
+  if (!dy || !topk_w || !d_topk_w) return MOE_ERR_INVALID;
+  if (rows > 0 && !out_buf) return MOE_ERR_INVALID;
+  if (!al16(dy) || !al16(out_buf) || !al4(topk_w) || !al4(d_topk_w) || !al16(d_out_buf)) return MOE_ERR_INVALID;
+  return hip_status(
+      moe::launch_combine_backward(dy, xdt == MOE_BF16, out_buf, L, topk_w, d_topk_w, d_out_buf, stream));
+}
+
+size_t moe_route_backward_workspace_bytes(int T, int H, int E, moe_dtype_t xdt) {
+  if (T <= 0 || H <= 0 || E <= 0 || !valid_dtype(xdt)) return 0;
+  return moe::route_backward_workspace_bytes(T, H, E, xdt == MOE_BF16);
+}
+
+int moe_route_backward(const void* x, moe_dtype_t xdt, const float* w_router, const int32_t* topk_ids,
+                       const float* topk_w, const float* d_topk_w, const float* d_logits_in, int T, int H, int E, int k,
+                       float* d_logits, void* d_x, float* d_w_router, float* d_bias, void* workspace,
+                       size_t workspace_bytes, hipStream_t stream) {
+  if (!valid_dtype(xdt)) return MOE_ERR_UNSUPPORTED;
+  if (T < 0 || H < 1 || E < 1 || E > MOE_MAX_EXPERTS || k < 1 || k > MOE_MAX_TOPK || k > E) return MOE_ERR_INVALID;
+  if (H % 8 != 0 || (int64_t)T * E > (int64_t)INT32_MAX) return MOE_ERR_UNSUPPORTED;
+  if (T > 0 && (!d_logits || (!d_topk_w && !d_logits_in) || (d_topk_w && (!topk_ids || !topk_w)) ||
+                (d_x && !w_router) || (d_w_router && !x)))
+    return MOE_ERR_INVALID;
+  if (!al16(x) || !al16(w_router) || !al4(topk_ids) || !al4(topk_w) || !al4(d_topk_w) || !al4(d_logits_in) ||
+      !al4(d_logits) || !al16(d_x) || !al16(d_w_router) || !al4(d_bias) || !al16(workspace))
+    return MOE_ERR_INVALID;
+  const size_t need = moe_route_backward_workspace_bytes(T, H, E, xdt);
+  if (need > 0 && (!workspace || workspace_bytes < need)) return MOE_ERR_INVALID;
+  moe::RouteBackward r{x, xdt == MOE_BF16, w_router, topk_ids, topk_w, d_topk_w, d_logits_in, T, H, E, k, d_logits, d_x,
+                       d_w_router, d_bias, workspace};
+  return hip_status(moe::launch_route_backward(r, stream));
+}
+
 }  // extern "C"

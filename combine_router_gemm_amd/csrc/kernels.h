@@ -87,6 +87,45 @@ hipError_t launch_expert_mlp_w4(const void* send_buf, const moe_layout_t& L, con
                                 const uint8_t* gu_scales, const uint8_t* dn_codes, const uint8_t* dn_scales, int F,
                                 void* out_buf, void* workspace, int num_cus, hipStream_t stream);
 
+// ---- int8 rows and experts ----
+hipError_t launch_quantize_i8(const void* w, int bf16, int64_t rows, int K, int8_t* codes, float* scales,
+                              hipStream_t stream);
+hipError_t launch_dequantize_i8(const int8_t* codes, const float* scales, int64_t rows, int K, void* w, int bf16,
+                                hipStream_t stream);
+hipError_t launch_dispatch_i8(const void* x, const int* ids, const moe_layout_t& L, int8_t* send_q, float* send_scale,
+                              int* blk_count, int* pair_local, hipStream_t stream);
+bool mlp_i8_fits(int64_t rows, int H, int F);
+size_t mlp_i8_workspace_bytes(int64_t rows, int El, int H, int F);
+hipError_t launch_expert_mlp_i8(const int8_t* send_q, const float* send_scale, const moe_layout_t& L,
+                                const int8_t* gu_codes, const float* gu_scales, const int8_t* dn_codes,
+                                const float* dn_scales, int F, void* out_buf, void* workspace, int num_cus,
+                                hipStream_t stream);
+
+// ---- training the router ----
+size_t balance_workspace_bytes(int T, int E, int S);
+hipError_t launch_balance(const float* logits, const int* ids, const int* seq_offset, const uint8_t* mask, int T, int E,
+                          int k, int S, float weight, float* loss, int* count, float* d_logits, void* workspace,
+                          hipStream_t stream);
+hipError_t launch_combine_backward(const void* dy, int bf16, const void* out_buf, const moe_layout_t& L,
+                                   const float* topk_w, float* d_w, void* d_out, hipStream_t stream);
+struct RouteBackward {
+  const void* x;
+  int bf16;
+  const float* w_router;
+  const int* ids;
+  const float* w;
+  const float* d_w;   // or nullptr
+  const float* d_in;  // or nullptr
+  int T, H, E, k;
+  float* d_logits;
+  void* d_x;          // these three: or nullptr
+  float* d_w_router;
+  float* d_bias;
+  void* workspace;
+};
+size_t route_backward_workspace_bytes(int T, int H, int E, int bf16);
+hipError_t launch_route_backward(const RouteBackward& r, hipStream_t stream);
+
 // ---- the whole layer for a few tokens ----
 constexpr int kDecodeMaxH = 1 << 23;
 constexpr int kDecodeMaxF = kDecodeMaxH / MOE_MAX_TOPK;

@@ -48,4 +48,24 @@ struct OpF32 {
   static __device__ __forceinline__ int out_row(int lane, int q) { return (lane >> 4) * 4 + q; }
 };
 
+// int8 operands, int32 sums: each lane supplies 16 consecutive K of fragment row (l % S).
+//   OpI16: v_mfma_i32_16x16x64_i8 (S = 16, KS = 64), OpI32: v_mfma_i32_32x32x32_i8 (S = 32, KS = 32); output rows as above
+struct OpI16 {
+  static constexpr int S = 16, KS = 64, NR = 4;
+  using Acc = i32x4;
+  static __device__ __forceinline__ void step(Acc& acc, u32x4 a, u32x4 b) {
+    acc = __builtin_amdgcn_mfma_i32_16x16x64_i8(__builtin_bit_cast(i32x4, a), __builtin_bit_cast(i32x4, b), acc, 0, 0, 0);
+  }
+  static __device__ __forceinline__ int out_row(int lane, int q) { return (lane >> 4) * 4 + q; }
+};
+
+struct OpI32 {
+  static constexpr int S = 32, KS = 32, NR = 16;
+  using Acc = i32x16;
+  static __device__ __forceinline__ void step(Acc& acc, u32x4 a, u32x4 b) {
+    acc = __builtin_amdgcn_mfma_i32_32x32x32_i8(__builtin_bit_cast(i32x4, a), __builtin_bit_cast(i32x4, b), acc, 0, 0, 0);
+  }
+  static __device__ __forceinline__ int out_row(int lane, int q) { return (q >> 2) * 8 + (lane >> 5) * 4 + (q & 3); }
+};
+
 }  // namespace moe

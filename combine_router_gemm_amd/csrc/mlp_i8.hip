@@ -1,0 +1,466 @@
+// Expert SwiGLU MLP on dispatched int8 rows with int8 expert weights (moe_expert_mlp_i8).
+//
+//   gate/up   g = s_row s_ch (sum_k q_x q_w), u alike: the products are int8, their sums int32 and exact; h = silu(g) u
+//             in float32, and the largest |h| of each row of a tile
+//   h rows    a row's maximum is that of its tiles; h to int8 codes with the row's scale
+//   down      out = s_h s_ch (sum_f q_h q_w), rounded once to bf16
+// The plan (rows grouped by local expert, mlp.hip) is moe_expert_mlp's. h stays float32 until its codes: any shorter form
+// would move codes over their borders, which a row's maximum, known only after the whole pass, decides.
+//
+//   i8_gemm_kernel  rows and weight rows go to LDS directly, in stages of 128 k (128 bytes of a row: whole cache lines), NS
+//                   stages in flight.
+#include <algorithm>
+
+#include "common.h"
+#include "i8.h"
+#include "kernels.h"
+#include "mfma.h"
+#include "tiles.h"
+
+namespace moe {
+
+namespace {
+
+struct I8Args {
+  const int8_t* A;       // rows [., K]: the send rows, or the codes of h in plan order
+  const int* a_perm;     // source row of a plan row, or nullptr (A in plan order)
+  const float* a_scale;  // [rows of A]
+  const int8_t* W;       // [El, w_rows, K]
+  const float* w_scale;  // [El, w_rows]
+  int K, N;              // N: output columns (F or H)
+  int w_rows;            // weight rows per expert (2F or H)
+  int up;                // weight row of the up half (gate/up only)
+  float* h;              // gate/up: [., N] in plan order
+  uint32_t* h_top;       // gate/up: [., h_tiles] bits of the largest |h| of a row in each tile of columns
+  int h_tiles;
+  bf16_t* out;           // down: [., N]
+  const int* out_perm;   // down: destination row of a plan row
+  const int* plan;
+  int El;
+  // SPLIT: K in `split` parts of split_stages stages each, their int32 sums to partial [split, rows, N]
+  int split, split_stages;
+  int* partial;
+  int64_t partial_stride;  // elements of one part
+};
+
+__device__ __forceinline__ float silu(float g) { return g / (1.0f + expf(-g)); }
+
+// A stage's rows: 128 bytes each, 16-byte chunk c of row r at c ^ ((r >> 1) & 7), so that a fragment read touches every
+// bank once.
+__device__ __forceinline__ int swizzle(int r) { return (r >> 1) & 7; }
+
+// BM rows x BN weight rows per tile (gate/up: the gate and the up rows of BN / 2 columns), WM x WN waves.
+template <typename Op, int BM, int BN, int WM, int WN, int NS, int PER_CU, bool GATED, bool SPLIT = false>
+__global__ __launch_bounds__(WM * WN * 64, PER_CU * WM * WN / 4 > 1 ? PER_CU * WM * WN / 4 : 1) void i8_gemm_kernel(
+    I8Args a, int a_bytes) {
+  static_assert(!SPLIT || !GATED, "the gate/up pass is not split");
+  constexpr int S = Op::S, NW = WM * WN, NTH = NW * 64, ROWB = 128, RPI = 8;
+  constexpr int STAGE = (BM + BN) * ROWB, A_INS = BM / RPI, LPW = (BM + BN) / RPI / NW;
+  static_assert((BM + BN) / RPI % NW == 0, "wave loads must split evenly");
+  constexpr int OUTC = GATED ? BN / 2 : BN;
+  constexpr int WTM = BM / WM, TM = WTM / S, WTN = OUTC / WN, TN = WTN / S;
+  constexpr int NACC = GATED ? 2 * TN : TN, KSTEPS = ROWB / Op::KS;
+  static_assert(TM >= 1 && TN >= 1, "wave tile too small");
+  constexpr int OUT_BYTES = GATED || SPLIT ? 0 : BM * OUTC * 2;
+  constexpr int BODY = NS * STAGE > OUT_BYTES ? NS * STAGE : OUT_BYTES;
+  constexpr int OOB = 0x7ffffff0;
+  // the only LDS object (a second one makes the compiler wait for every load in flight before LDS reads): the stages, which
+  // the output tile reuses; the tile's row scales and destination rows; the waves' row maxima; the plan's starts
+  constexpr int SCALE_OFF = BODY, ROW_OFF = SCALE_OFF + BM * 4, TOP_OFF = ROW_OFF + BM * 4;
+  constexpr int PLAN_OFF = TOP_OFF + (GATED ? WN * BM * 4 : 0);
+  __shared__ __attribute__((aligned(1024))) unsigned char smem[PLAN_OFF + 2 * (MOE_MAX_EXPERTS + 1) * 4];
+  float* s_scale = reinterpret_cast<float*>(smem + SCALE_OFF);
+  int* s_row = reinterpret_cast<int*>(smem + ROW_OFF);
+  uint32_t* s_top = reinterpret_cast<uint32_t*>(smem + TOP_OFF);
+  int* row_start = reinterpret_cast<int*>(smem + PLAN_OFF);
+  int* tile_start = row_start + MOE_MAX_EXPERTS + 1;
+  int tid = threadIdx.x, lane = tid & 63;  // made opaque at each tile start (below)
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wm = wave / WN, wn = wave % WN;
+  int fr = lane % S, fq = lane / S;
+  const int K = a.K, nk = (K + ROWB - 1) / ROWB;
+  for (int i = tid; i <= a.El; i += NTH) {
+    row_start[i] = a.plan[2 + i];
+    tile_start[i] = a.plan[3 + a.El + i];
+  }
+  const int n_tiles = (a.N + OUTC - 1) / OUTC;
+  lds_barrier();
+  const Tiles mine = my_tiles(a.plan[0] * n_tiles * (SPLIT ? a.split : 1));
+  const __amdgpu_buffer_rsrc_t a_rsrc = __builtin_amdgcn_make_buffer_rsrc((void*)a.A, (short)0, a_bytes, 0x00020000);
+  int l = 0;
+  for (int unit = mine.begin; unit < mine.end; unit += mine.step) {
+    const int tile = SPLIT ? unit / a.split : unit, sp = SPLIT ? unit - tile * a.split : 0;
+    const int s_begin = SPLIT ? sp * a.split_stages : 0, s_end = SPLIT ? min(nk, s_begin + a.split_stages) : nk;
+    // per-lane values are computed again in each tile: kept across the tile loop they do not fit the registers next
+    // to the accumulators
+    asm volatile("" : "+v"(tid), "+v"(lane), "+v"(fr), "+v"(fq));
+    // tiles list (expert, N tile, M tile) in expert order and a workgroup's tiles increase: scan on
+    while (__builtin_amdgcn_readfirstlane(tile_start[l + 1]) * n_tiles <= tile) ++l;
+    const int ts = __builtin_amdgcn_readfirstlane(tile_start[l]);
+    const int mt_l = __builtin_amdgcn_readfirstlane(tile_start[l + 1]) - ts;
+    const int local = tile - ts * n_tiles;
+    const int nt = local / mt_l, mt = local % mt_l;
+    const int p0 = __builtin_amdgcn_readfirstlane(row_start[l]) + mt * BM;
+    const int m_rows = min(BM, __builtin_amdgcn_readfirstlane(row_start[l + 1]) - p0);
+    const int n0 = nt * OUTC;
+    const __amdgpu_buffer_rsrc_t b_rsrc = __builtin_amdgcn_make_buffer_rsrc(
+        (void*)(a.W + (int64_t)l * a.w_rows * K), (short)0, a.w_rows * K, 0x00020000);
+    const float* w_scale = a.w_scale + (int64_t)l * a.w_rows;
+
+    // this wave's LPW loads of a stage, 8 rows each: the byte offset without k. The source rows are looked up together.
+    int voff[LPW];
+#pragma unroll
+    for (int q = 0; q < LPW; ++q) {
+      const int p = p0 + min((wave * LPW + q) * RPI + (lane >> 3), m_rows - 1);
+      voff[q] = a.a_perm && wave * LPW + q < A_INS ? a.a_perm[p] : p;
+    }
+    wait_loads<0>();
+    lds_barrier();  // the previous tile has left LDS
+    for (int r = tid; r < BM; r += NTH) {
+      const int p = p0 + min(r, m_rows - 1);
+      s_scale[r] = a.a_scale[a.a_perm ? a.a_perm[p] : p];
+      s_row[r] = a.out_perm ? a.out_perm[p] : p;
+    }
+    int tail = 0;  // bit q: this lane's chunk of load q lies within K in the last stage
+#pragma unroll
+    for (int q = 0; q < LPW; ++q) {
+      const int ins = wave * LPW + q;
+      const int r = (ins < A_INS ? ins : ins - A_INS) * RPI + (lane >> 3);
+      const int chunk = (lane & 7) ^ swizzle(r);
+      tail |= ((nk - 1) * ROWB + chunk * 16 < K ? 1 : 0) << q;
+      if (ins < A_INS) {
+        voff[q] = r < m_rows ? voff[q] * K + chunk * 16 : OOB;
+      } else {
+        const int half = GATED ? r / OUTC : 0, col = n0 + (GATED ? r % OUTC : r);
+        voff[q] = col < a.N ? (col + half * a.up) * K + chunk * 16 : OOB;
+      }
+    }
+    auto issue = [&](int st) {
+      unsigned char* base = smem + (st % NS) * STAGE;
+      const bool last = st == nk - 1, past = st >= s_end;
+#pragma unroll
+      for (int q = 0; q < LPW; ++q) {
+        const int ins = wave * LPW + q;  // wave-uniform
+        auto* dst = (__attribute__((address_space(3))) void*)(base + ins * 1024);
+        const int vo = voff[q] == OOB || past || (last && !((tail >> q) & 1)) ? OOB : voff[q] + st * ROWB;
+        if (ins < A_INS) __builtin_amdgcn_raw_ptr_buffer_load_lds(a_rsrc, dst, 16, vo, 0, 0, 0);
+        else __builtin_amdgcn_raw_ptr_buffer_load_lds(b_rsrc, dst, 16, vo, 0, 0, BM <= 64 ? 2 : 0);
+      }
+    };
+    typename Op::Acc acc[TM][NACC];
+#pragma unroll
+    for (int i = 0; i < TM; ++i)
+#pragma unroll
+      for (int j = 0; j < NACC; ++j)
+#pragma unroll
+        for (int q = 0; q < Op::NR; ++q) acc[i][j][q] = 0;
+    const int mb = min(TM, max(0, (m_rows - wm * WTM + S - 1) / S));  // blocks with rows (wave-uniform)
+    const int sw = swizzle(fr);  // blocks start at multiples of 16 rows
+    auto multiply = [&](int st) {
+      const unsigned char* base = smem + (st % NS) * STAGE + fr * ROWB;
+#pragma unroll
+      for (int ks = 0; ks < KSTEPS; ++ks) {
+        const int xo = ((ks * (Op::KS / 16) + fq) ^ sw) << 4;
+        u32x4 fa[TM], fb[NACC];
+#pragma unroll
+        for (int j = 0; j < NACC; ++j) {
+          const int r0 = BM + (GATED ? (j / TN) * OUTC + wn * WTN + (j % TN) * S : wn * WTN + j * S);
+          fb[j] = ld16(base + r0 * ROWB + xo);
+        }
+#pragma unroll
+        for (int i = 0; i < TM; ++i) fa[i] = ld16(base + (wm * WTM + i * S) * ROWB + xo);
+#pragma unroll
+        for (int i = 0; i < TM; ++i)
+          if (i < mb) {
+#pragma unroll
+            for (int j = 0; j < NACC; ++j) Op::step(acc[i][j], fa[i], fb[j]);
+          }
+      }
+    };
+    wait_loads<0>();  // the scale and row lookups: the waits below count stage loads only
+#pragma unroll
+    for (int i = 0; i < NS - 1; ++i) issue(s_begin + i);
+    for (int st = s_begin; st < s_end; ++st) {
+      wait_loads<(NS - 2) * LPW>();
+      lds_barrier();  // stage st has landed for every wave, and stage st - 1 has been read
+      issue(st + NS - 1);
+      multiply(st);
+    }
+
+    const int c_lane = n0 + wn * WTN + fr;  // column of block j: + j * S
+    if constexpr (SPLIT) {
+#pragma unroll
+      for (int i = 0; i < TM; ++i)
+#pragma unroll
+        for (int q = 0; q < Op::NR; ++q) {
+          const int r = wm * WTM + i * S + Op::out_row(lane, q);
+          if (r < m_rows) {
+            int* o = a.partial + sp * a.partial_stride + (int64_t)(p0 + r) * a.N;
+#pragma unroll
+            for (int j = 0; j < TN; ++j)
+              if (c_lane + j * S < a.N) o[c_lane + j * S] = acc[i][j][q];
+          }
+        }
+    } else if constexpr (GATED) {
+      float sg[TN], su[TN];
+#pragma unroll
+      for (int j = 0; j < TN; ++j) {
+        const int c = min(c_lane + j * S, a.N - 1);
+        sg[j] = w_scale[c];
+        su[j] = w_scale[a.up + c];
+      }
+#pragma unroll
+      for (int i = 0; i < TM; ++i)
+#pragma unroll
+        for (int q = 0; q < Op::NR; ++q) {
+          const int r = wm * WTM + i * S + Op::out_row(lane, q);
+          const float sr = s_scale[r];
+          uint32_t top = 0;
+#pragma unroll
+          for (int j = 0; j < TN; ++j) {
+            const float g = (float)acc[i][j][q] * sr * sg[j], u = (float)acc[i][j + TN][q] * sr * su[j];
+            const float v = silu(g) * u;
+            const bool in = c_lane + j * S < a.N;
+            if (in) top = max(top, abs_bits(v));
+            if (in && r < m_rows) a.h[(int64_t)(p0 + r) * a.N + c_lane + j * S] = v;
+          }
+#pragma unroll
+          for (int off = S / 2; off > 0; off >>= 1) top = max(top, (uint32_t)__shfl_xor((int)top, off, 64));
+          if (fr == 0) s_top[wn * BM + r] = top;
+        }
+      lds_barrier();
+      for (int r = tid; r < m_rows; r += NTH) {
+        uint32_t top = 0;
+#pragma unroll
+        for (int w = 0; w < WN; ++w) top = max(top, s_top[w * BM + r]);
+        a.h_top[(int64_t)(p0 + r) * a.h_tiles + nt] = top;
+      }
+    } else {
+      wait_loads<0>();
+      lds_barrier();  // every wave is past its last stage, whose LDS takes the output tile
+      float sd[TN];
+#pragma unroll
+      for (int j = 0; j < TN; ++j) sd[j] = w_scale[min(c_lane + j * S, a.N - 1)];
+      constexpr int CPO = OUTC / 8;  // chunk c of output row r at c ^ (4 * ((r >> 2) & 1))
+#pragma unroll
+      for (int i = 0; i < TM; ++i)
+#pragma unroll
+        for (int q = 0; q < Op::NR; ++q) {
+          const int r = wm * WTM + i * S + Op::out_row(lane, q);
+          const float sr = s_scale[r];
+#pragma unroll
+          for (int j = 0; j < TN; ++j) {
+            const int c = wn * WTN + j * S + fr;
+            *reinterpret_cast<bf16_t*>(smem + r * OUTC * 2 + (((c >> 3) ^ (((r >> 2) & 1) << 2)) << 4) + (c & 7) * 2) =
+                (bf16_t)((float)acc[i][j][q] * sr * sd[j]);
+          }
+        }
+      lds_barrier();
+      for (int o = tid; o < BM * CPO; o += NTH) {
+        const int r = o / CPO, ch = o % CPO, col = n0 + ch * 8;
+        if (r < m_rows && col < a.N)
+          st16(a.out + (int64_t)s_row[r] * a.N + col, ld16(smem + r * OUTC * 2 + ((ch ^ (((r >> 2) & 1) << 2)) << 4)));
+      }
+    }
+  }
+}
+
+// Codes of h: a workgroup per row and 2048 columns. Every wave finds the row's maximum from its tiles' itself.
+constexpr int kHCols = 2048;
+__global__ __launch_bounds__(256) void i8_h_kernel(const float* __restrict__ h, const uint32_t* __restrict__ h_top,
+                                                   int h_tiles, const int* __restrict__ plan, int F,
+                                                   int8_t* __restrict__ codes, float* __restrict__ scale) {
+  const int rows = plan[1];
+  const int c = blockIdx.x * kHCols + threadIdx.x * 8;
+  for (int64_t p = blockIdx.y; p < rows; p += gridDim.y) {
+    u32x4 lo{0u, 0u, 0u, 0u}, hi{0u, 0u, 0u, 0u};
+    if (c < F) {
+      lo = ld16_nt(h + p * F + c);
+      hi = ld16_nt(h + p * F + c + 4);
+    }
+    uint32_t top = 0;
+    for (int i = lane_id(); i < h_tiles; i += 64) top = max(top, h_top[p * h_tiles + i]);
+    const I8Row r = i8_row(wave_top(top));
+    if (blockIdx.x == 0 && threadIdx.x == 0) scale[p] = r.scale;
+    if (c < F) {
+      float v[8];
+      unpack(lo, *reinterpret_cast<float(*)[4]>(&v[0]));
+      unpack(hi, *reinterpret_cast<float(*)[4]>(&v[4]));
+      uint32_t w[2];
+      i8_codes(v, r, w);
+      *reinterpret_cast<u32x2*>(codes + p * F + c) = u32x2{w[0], w[1]};
+    }
+  }
+}
+
+// The parts of a split down pass added (int32: exact in any order), scaled, rounded once and put into their rows: eight
+// columns per thread.
+__global__ __launch_bounds__(256) void i8_sum_kernel(I8Args a) {
+  const int64_t at = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 8;
+  const int p = (int)(at / a.N), c = (int)(at - (int64_t)p * a.N);
+  if (p >= a.plan[1]) return;
+  int l = 0, hi = a.El;  // the expert of plan row p: the last l with row_start[l] <= p
+  while (hi - l > 1) {
+    const int mid = (l + hi) >> 1;
+    if (a.plan[2 + mid] <= p) l = mid;
+    else hi = mid;
+  }
+  int v[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+  for (int s = 0; s < a.split; ++s)
+#pragma unroll
+    for (int q4 = 0; q4 < 2; ++q4) {
+      const i32x4 w = *reinterpret_cast<const i32x4*>(a.partial + s * a.partial_stride + at + 4 * q4);
+#pragma unroll
+      for (int q = 0; q < 4; ++q) v[4 * q4 + q] += w[q];
+    }
+  const float sr = a.a_scale[p];
+  const float* sd = a.w_scale + (int64_t)l * a.w_rows + c;
+  float o[8];
+#pragma unroll
+  for (int q = 0; q < 8; ++q) o[q] = (float)v[q] * sr * sd[q];
+  st16(a.out + (int64_t)a.out_perm[p] * a.N + c, pack(o));
+}
+
+int i8_grid(int64_t tiles, int64_t most) {
+  int64_t g = std::min(tiles, most);
+  if (g >= 8) g &= ~7ll;
+  return (int)std::max<int64_t>(g, 1);
+}
+
+constexpr int kPlanCus = 256;   // what a call is cut into is a function of its sizes alone, as its workspace is
+constexpr int kSmallCols = 64;  // columns of a 32-row tile, of either pass
+template <typename Op, int BM, int WM, int WN, int GUN, int GUNS, int DNN, int DNNS, int PER_CU>
+void launch_gemms(const I8Args& gu, const I8Args& dn, int64_t rows, int64_t mtiles, int num_cus, hipStream_t stream) {
+  constexpr int NTH = WM * WN * 64;
+  i8_gemm_kernel<Op, BM, GUN, WM, WN, GUNS, PER_CU, true>
+      <<<i8_grid(mtiles * ceil_div_host(gu.N, GUN / 2), PER_CU * num_cus), NTH, 0, stream>>>(gu, (int)(rows * gu.K));
+  const dim3 hg(ceil_div_host(gu.N, kHCols), (unsigned)std::min<int64_t>(rows, 65535));
+  i8_h_kernel<<<hg, 256, 0, stream>>>(gu.h, gu.h_top, gu.h_tiles, gu.plan, gu.N, const_cast<int8_t*>(dn.A),
+                                      const_cast<float*>(dn.a_scale));
+  const int64_t tiles = mtiles * ceil_div_host(dn.N, DNN);
+  if constexpr (BM == 32) {
+    if (dn.split > 1) {
+      i8_gemm_kernel<Op, BM, DNN, WM, WN, DNNS, PER_CU, false, true>
+          <<<i8_grid(tiles * dn.split, PER_CU * num_cus), NTH, 0, stream>>>(dn, (int)(rows * dn.K));
+      i8_sum_kernel<<<(unsigned)ceil_div_host64(rows * dn.N / 8, 256), 256, 0, stream>>>(dn);
+      return;
+    }
+  }
+  i8_gemm_kernel<Op, BM, DNN, WM, WN, DNNS, PER_CU, false>
+      <<<i8_grid(tiles, PER_CU * num_cus), NTH, 0, stream>>>(dn, (int)(rows * dn.K));
+}
+
+int64_t row_tiles(int64_t rows_max, int El, int bm) { return El * ceil_div_host64(ceil_div_host64(rows_max, El), bm); }
+
+// Parts of the down pass's K with 32-row tiles: as many as give every CU its two workgroups, of at least 8 stages.
+int i8_split(int64_t rows_max, int El, int H, int F) {
+  const int64_t tiles = row_tiles(rows_max, El, 32) * ceil_div_host(H, kSmallCols);
+  const int64_t s = std::min<int64_t>(2 * kPlanCus / tiles, F / 128 / 8);
+  return s < 2 ? 1 : (int)s;
+}
+
+struct I8Plan {
+  int bm, split, stages;
+};
+I8Plan i8_plan(int64_t rows_max, int El, int H, int F) {
+  const int64_t per = ceil_div_host64(rows_max, El);
+  I8Plan p{per <= 64 ? 32 : per <= 384 ? 128 : 256, 1, 0};
+  if (p.bm == 32) {
+    const int nk = ceil_div_host(F, 128);
+    p.split = i8_split(rows_max, El, H, F);
+    p.stages = ceil_div_host(nk, p.split);
+    p.split = ceil_div_host(nk, p.stages);  // every part has stages
+  }
+  return p;
+}
+
+int h_tiles(int bm, int F) { return ceil_div_host(F, bm == 32 ? kSmallCols : 128); }
+
+// the workspace: plan, row map, h, its tiles' maxima, its codes and scales, the parts of a split down pass
+struct I8Scratch {
+  size_t plan, perm, h, top, codes, scale, partial, total;
+};
+I8Scratch i8_scratch(int64_t rows, int El, int H, int F, const I8Plan& p) {
+  I8Scratch s;
+  size_t at = 0;
+  auto take = [&](size_t bytes) {
+    const size_t here = at;
+    at += align256(bytes);
+    return here;
+  };
+  s.plan = take(mlp_plan_ints(El) * sizeof(int));
+  s.perm = take((size_t)rows * sizeof(int));
+  s.h = take((size_t)rows * (size_t)F * sizeof(float));
+  s.top = take((size_t)rows * (size_t)h_tiles(p.bm, F) * sizeof(uint32_t));
+  s.codes = take((size_t)rows * (size_t)F);
+  s.scale = take((size_t)rows * sizeof(float));
+  s.partial = take(p.split > 1 ? (size_t)p.split * (size_t)rows * (size_t)H * sizeof(int) : 0);
+  s.total = at;
+  return s;
+}
+
+}  // namespace
+
+// Rows of either pass and one expert's weights are addressed by 31-bit byte offsets; K products of codes of either sign
+// (128 * 128 at most) stay within an int32 sum
+bool mlp_i8_fits(int64_t rows, int H, int F) {
+  return std::max(H, F) < 1 << 17 && rows * std::max<int64_t>(H, F) < 0x7ffffe00ll &&
+         2 * (int64_t)F * H < 0x7ffffe00ll;
+}
+
+size_t mlp_i8_workspace_bytes(int64_t rows, int El, int H, int F) {
+  return i8_scratch(rows, El, H, F, i8_plan(rows, El, H, F)).total;
+}
+
+hipError_t launch_expert_mlp_i8(const int8_t* send_q, const float* send_scale, const moe_layout_t& L,
+                                const int8_t* gu_codes, const float* gu_scales, const int8_t* dn_codes,
+                                const float* dn_scales, int F, void* out_buf, void* workspace, int num_cus,
+                                hipStream_t stream) {
+  const int El = L.E / L.R;
+  const int64_t rows = moe_rows_max(L.T, L.k, L.E, L.C);
+  if (rows == 0) return hipSuccess;
+  const I8Plan p = i8_plan(rows, El, L.H, F);
+  const I8Scratch at = i8_scratch(rows, El, L.H, F, p);
+  char* ws = static_cast<char*>(workspace);
+  int* plan = reinterpret_cast<int*>(ws + at.plan);
+  int* perm = reinterpret_cast<int*>(ws + at.perm);
+  launch_mlp_plan(L, p.bm, plan, perm, stream);
+  I8Args gu{};
+  gu.A = send_q;
+  gu.a_perm = perm;
+  gu.a_scale = send_scale;
+  gu.W = gu_codes;
+  gu.w_scale = gu_scales;
+  gu.K = L.H;
+  gu.N = F;
+  gu.w_rows = 2 * F;
+  gu.up = F;
+  gu.h = reinterpret_cast<float*>(ws + at.h);
+  gu.h_top = reinterpret_cast<uint32_t*>(ws + at.top);
+  gu.h_tiles = h_tiles(p.bm, F);
+  gu.plan = plan;
+  gu.El = El;
+  I8Args dn{};
+  dn.A = reinterpret_cast<int8_t*>(ws + at.codes);
+  dn.a_scale = reinterpret_cast<float*>(ws + at.scale);
+  dn.W = dn_codes;
+  dn.w_scale = dn_scales;
+  dn.K = F;
+  dn.N = L.H;
+  dn.w_rows = L.H;
+  dn.out = static_cast<bf16_t*>(out_buf);
+  dn.out_perm = perm;
+  dn.plan = plan;
+  dn.El = El;
+  dn.split = p.split;
+  dn.split_stages = p.stages;
+  dn.partial = reinterpret_cast<int*>(ws + at.partial);
+  dn.partial_stride = rows * L.H;
+  const int64_t mtiles = ceil_div_host64(rows, p.bm) + El;
+  if (p.bm == 32) launch_gemms<OpI16, 32, 1, 4, 2 * kSmallCols, 3, kSmallCols, 4, 2>(gu, dn, rows, mtiles, num_cus, stream);
+  else if (p.bm == 128) launch_gemms<OpI32, 128, 2, 4, 256, 3, 256, 3, 1>(gu, dn, rows, mtiles, num_cus, stream);
+  else launch_gemms<OpI32, 256, 4, 2, 256, 2, 256, 2, 1>(gu, dn, rows, mtiles, num_cus, stream);
+  return hipGetLastError();
+}
+
+}  // namespace moe

@@ -18,6 +18,7 @@
 #include "common.h"
 #include "kernels.h"
 #include "mfma.h"
+#include "tiles.h"
 #include "w4.h"
 
 namespace moe {
@@ -46,31 +47,9 @@ struct W4Args {
 
 __device__ __forceinline__ float silu(float g) { return g / (1.0f + expf(-g)); }
 
-// This workgroup's tiles out of `total`: the list is cut into eight contiguous ranges, one per XCD (workgroup b runs
-// on XCD b % 8), so tiles that share weights or rows meet in one L2.
-struct Tiles {
-  int begin, end, step;
-};
-__device__ __forceinline__ Tiles my_tiles(int total) {
-  const int G = gridDim.x;
-  Tiles t{(int)blockIdx.x, total, G};
-  if ((G & 7) == 0) {
-    const int x = blockIdx.x & 7, per = (total + 7) >> 3;
-    t.begin = x * per + (blockIdx.x >> 3);
-    t.end = min(total, (x + 1) * per);
-    t.step = G >> 3;
-  }
-  return t;
-}
-
 // ------------------------------------------------------------------------------------------------
 // the GEMM
 // ------------------------------------------------------------------------------------------------
-template <int N>
-__device__ __forceinline__ void wait_loads() {
-  asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
-}
-
 // BM rows x 64 WN weight rows per tile; WM x WN waves, each BM / WM rows x 64 weight rows: the gate and the up rows of 32
 // columns of h, or 64 down rows. K goes in stages of 64:
 //  - rows: 128 bytes each, straight to LDS, NS slots. 16-byte chunk c of row r sits at c ^ ((r >> 1) & 7), so that a

@@ -10,7 +10,9 @@
  *
  * plus an fp8 variant of the dispatch and of the expert MLP (moe_dispatch_fp8, moe_expert_mlp_fp8), an
  * expert MLP on 4-bit weights (moe_quantize_w4, moe_dequantize_w4, moe_expert_mlp_w4), and the whole layer
- * for a few tokens in one call (moe_layer_decode, moe_layer_decode_w4).
+ * for a few tokens in one call (moe_layer_decode, moe_layer_decode_w4), int8 experts (moe_quantize_i8,
+ * moe_dequantize_i8, moe_dispatch_i8, moe_expert_mlp_i8), and what training the router takes (moe_balance_loss,
+ * moe_combine_backward, moe_route_backward).
  *
  * Sources (cited by page title and section):
  *   [EPM] "Efficient and portable mixture-of-experts communication" (Perplexity, 2025)
@@ -434,6 +436,128 @@ int moe_layer_decode_w4(const void* x, const float* w_router, const float* logit
                         const uint8_t* gu_scales, const uint8_t* dn_codes, const uint8_t* dn_scales, float* logits,
                         int32_t* topk_ids, float* topk_w, void* y, void* workspace, size_t workspace_bytes,
                         hipStream_t stream);
+
+/*
+ * int8 experts.
+ *   A row of K values v (an output channel of a weight matrix, a token's hidden row, a row of h) has one scale: with
+ *   a = max|v|, code = round-half-even(127 v / a), where a tie is one of the exact quotient, and scale = a / 127 in
+ *   float32; a code stands for code * scale. A row of zeros has codes 0 and scale 0. A row that holds an infinity or NaN
+ *   has codes 0 and scale NaN, so that everything computed from it is NaN. Codes are row-major int8, [rows, K].
+ */
+
+/*
+ * moe_quantize_i8 -- rows of a matrix to int8 codes and scales. For the experts' weights `rows` counts the rows of every
+ * matrix of a batch (El * 2F for w_gate_up): one scale per output channel.
+ *   w       [rows, K] (wdt: MOE_F32 or MOE_BF16)
+ *   codes   [rows, K] int8, 16-byte aligned (output)
+ *   scales  [rows] fp32 (output)
+ * Requires K % 16 == 0 and rows * K < 2^61 (else MOE_ERR_UNSUPPORTED); rows == 0 is a no-op.
+ */
+int moe_quantize_i8(const void* w, moe_dtype_t wdt, int64_t rows, int K, int8_t* codes, float* scales,
+                    hipStream_t stream);
+
+/* moe_dequantize_i8 -- w [rows, K] (wdt, output) = code * scale, the float32 product rounded once to wdt. */
+int moe_dequantize_i8(const int8_t* codes, const float* scales, int64_t rows, int K, void* w, moe_dtype_t wdt,
+                      hipStream_t stream);
+
+/*
+ * moe_dispatch_i8 -- moe_dispatch whose send rows are int8 codes with a scale per row instead of copies of x: half the
+ * bytes to write, and to send. The layout is exactly the one moe_dispatch writes.
+ *   x           [T, H] bf16 activations (xdt must be MOE_BF16)
+ *   topk_ids    [T, k] int32 expert ids
+ *   layout      as for moe_dispatch
+ *   send_q      [rows_max, H] int8 codes, send_scale [rows_max] fp32 (outputs); rows >= expert_offset[E] are left as
+ *               they were
+ *   workspace   device scratch of at least moe_dispatch_workspace_bytes(T, k, E) bytes
+ * Requires H % 16 == 0 (else MOE_ERR_UNSUPPORTED).
+ */
+int moe_dispatch_i8(const void* x, moe_dtype_t xdt, const int32_t* topk_ids, const moe_layout_t* layout, int8_t* send_q,
+                    float* send_scale, void* workspace, size_t workspace_bytes, hipStream_t stream);
+
+/* Bytes of scratch `workspace` moe_expert_mlp_i8 needs (0 for sizes beyond its limits). */
+size_t moe_expert_mlp_i8_workspace_bytes(int T, int k, int E, int R, int C, int H, int F);
+
+/*
+ * moe_expert_mlp_i8 -- moe_expert_mlp on int8 rows with int8 weights. A row of global expert e uses l = e mod El:
+ *   g = (sum_k q[k] Wg[l][f][k]) * send_scale * gu_scale[l][f], u alike with rows F + f, the sums exact in int32;
+ *   h = silu(g) * u in fp32, quantised like any row: codes qh with scale sh = max|h| / 127;
+ *   out[c] = (sum_f qh[f] Wd[l][c][f]) * sh * dn_scale[l][c], rounded once to bf16.
+ * A row with a scale of NaN, or an h that is not finite, gives a row of NaN and touches no other.
+ *   send_q, send_scale  rows written by moe_dispatch_i8
+ *   layout     the layout moe_dispatch_i8 filled (expert_kept / expert_offset are read on the device)
+ *   gu_codes   [El, 2F, H] int8, gu_scales [El, 2F] fp32: rows 0..F-1 of an expert are Wg, rows F..2F-1 are Wu
+ *   dn_codes   [El, H, F] int8, dn_scales [El, H] fp32
+ *   out_buf    [rows_max, H] bf16 output, row-aligned with send_q (feeds moe_combine); rows >= total are left as they were
+ *   workspace  device scratch of at least moe_expert_mlp_i8_workspace_bytes(...) bytes; no contents need clearing between
+ *              calls, and calls that overlap must use separate workspaces
+ * Requires H % 16 == 0, F % 16 == 0, H and F below 2^17, and rows_max * max(H, F) and 2 F * H below 2^31 - 512 (else
+ * MOE_ERR_UNSUPPORTED).
+ */
+int moe_expert_mlp_i8(const int8_t* send_q, const float* send_scale, const moe_layout_t* layout, const int8_t* gu_codes,
+                      const float* gu_scales, const int8_t* dn_codes, const float* dn_scales, int F, void* out_buf,
+                      void* workspace, size_t workspace_bytes, hipStream_t stream);
+
+/* Bytes of scratch `workspace` moe_balance_loss needs. */
+size_t moe_balance_loss_workspace_bytes(int T, int E, int S);
+
+/*
+ * moe_balance_loss -- how evenly a router spreads its tokens: per-expert counts, the balance loss and its gradient.
+ *   Sequence s holds n_s counted tokens; count[s, e] of their k choices each are expert e; f[s, e] = count[s, e] / (k n_s);
+ *   p[t] = softmax(logits[t]) over all E experts.
+ *   loss = weight / S' * sum over sequences of E / n_s * sum_t sum_e f[s, e] p[t, e], S' the sequences with n_s > 0
+ *          (loss 0 if there are none): `weight` where the choices and the probabilities are even, more where they agree on
+ *          few experts. f is a constant of the gradient.
+ *   d_logits[t, e] = weight / S' * E / n_s * p[t, e] * (f[s, e] - sum_e' f[s, e'] p[t, e'])
+ *   logits      [T, E] fp32, as moe_route writes them
+ *   topk_ids    [T, k] int32; an id outside [0, E) is not counted
+ *   seq_offset  [S + 1] int32, not decreasing: sequence s is tokens [seq_offset[s], seq_offset[s + 1]); or NULL with S = 1:
+ *               one sequence of all tokens. Tokens of no sequence are not counted.
+ *   token_mask  [T] uint8, 0 for tokens that are not counted (padding); or NULL
+ *   loss        [1] fp32, expert_count [S, E] int32, d_logits [T, E] fp32 or NULL (outputs). Tokens that are not counted get
+ *               a gradient of 0, whatever their logits hold; so does a token whose logits are all -inf (its p is 0).
+ *   workspace   device scratch of at least moe_balance_loss_workspace_bytes(T, E, S) bytes; no contents need clearing, and
+ *               calls that overlap must use separate workspaces
+ * Requires T * k and S * E below 2^31. T == 0 writes a loss and counts of 0.
+ */
+int moe_balance_loss(const float* logits, const int32_t* topk_ids, const int32_t* seq_offset, const uint8_t* token_mask,
+                     int T, int E, int k, int S, float weight, float* loss, int32_t* expert_count, float* d_logits,
+                     void* workspace, size_t workspace_bytes, hipStream_t stream);
+
+/*
+ * moe_combine_backward -- gradients of moe_combine.
+ *   d_topk_w[t, j] = sum_h dy[t, h] * out_buf[pair_row[t, j], h] in fp32, 0 for a dropped pair
+ *   d_out_buf[pair_row[t, j]] = topk_w[t, j] * dy[t], rounded once to xdt
+ *   dy         [T, H] (xdt) gradient of y
+ *   out_buf    [rows_max, H] (xdt), layout and topk_w as moe_combine took them
+ *   d_topk_w   [T, k] fp32 (output)
+ *   d_out_buf  [rows_max, H] (xdt, output; not out_buf itself), or NULL: frozen experts need none. Rows >= total are left as
+ *              they were.
+ * (The gradient of moe_dispatch, d_x[t] = the sum of its kept rows' gradients, is moe_combine of them with weights of 1.)
+ */
+int moe_combine_backward(const void* dy, moe_dtype_t xdt, const void* out_buf, const moe_layout_t* layout,
+                         const float* topk_w, float* d_topk_w, void* d_out_buf, hipStream_t stream);
+
+/* Bytes of scratch `workspace` moe_route_backward needs (may be 0). */
+size_t moe_route_backward_workspace_bytes(int T, int H, int E, moe_dtype_t xdt);
+
+/*
+ * moe_route_backward -- gradients of moe_route: of the softmax over the selected logits, and of the router's product.
+ *   d_logits[t, e] = d_logits_in[t, e] + sum over j with topk_ids[t, j] = e of
+ *                    topk_w[t, j] * (d_topk_w[t, j] - sum_i topk_w[t, i] * d_topk_w[t, i])
+ *   d_x = d_logits w_router (rounded once to xdt), d_w_router = d_logits^T x, d_bias = sum_t d_logits[t], sums in fp32 or
+ *   more (d_logits itself is the gradient of a [T, E] bias)
+ *   x            [T, H] (xdt), w_router [E, H] fp32, topk_ids and topk_w [T, k] as moe_route took and wrote them
+ *   d_topk_w     [T, k] fp32 (moe_combine_backward), or NULL: none
+ *   d_logits_in  [T, E] fp32, what other losses add (moe_balance_loss), or NULL: none; not both may be NULL
+ *   d_logits     [T, E] fp32 (output); may be d_logits_in itself
+ *   d_x          [T, H] (xdt), d_w_router [E, H] fp32, d_bias [E] fp32: outputs, each may be NULL
+ *   workspace    device scratch of at least moe_route_backward_workspace_bytes(T, H, E, xdt) bytes
+ * Requires H % 8 == 0 and T * E < 2^31 (else MOE_ERR_UNSUPPORTED). T == 0 writes zeros to d_w_router and d_bias.
+ */
+int moe_route_backward(const void* x, moe_dtype_t xdt, const float* w_router, const int32_t* topk_ids,
+                       const float* topk_w, const float* d_topk_w, const float* d_logits_in, int T, int H, int E, int k,
+                       float* d_logits, void* d_x, float* d_w_router, float* d_bias, void* workspace,
+                       size_t workspace_bytes, hipStream_t stream);
 
 #ifdef __cplusplus
 }
