@@ -604,7 +604,7 @@ int moe_route_backward(const void* x, moe_dtype_t xdt, const float* w_router, co
                        size_t workspace_bytes, hipStream_t stream) {
   if (!valid_dtype(xdt)) return MOE_ERR_UNSUPPORTED;
   if (T < 0 || H < 1 || E < 1 || E > MOE_MAX_EXPERTS || k < 1 || k > MOE_MAX_TOPK || k > E) return MOE_ERR_INVALID;
-  if (H % 8 != 0 || (int64_t)T * E > (int64_t)INT32_MAX) return MOE_ERR_UNSUPPORTED;
+  if (H % 8 != 0 || H > 1 << 21 || (int64_t)T * E > (int64_t)INT32_MAX) return MOE_ERR_UNSUPPORTED;
   if (T > 0 && (!d_logits || (!d_topk_w && !d_logits_in) || (d_topk_w && (!topk_ids || !topk_w)) ||
                 (d_x && !w_router) || (d_w_router && !x)))
     return MOE_ERR_INVALID;

@@ -6,6 +6,7 @@
 // router: w = softmax over the selected logits, logits = x Wr^T + b. With c_j = w_j (d_w_j - sum_i w_i d_w_i), the gradient of
 //   the logits is d_in plus c_j at the selected experts; then d_x = d_logits Wr, d_Wr = d_logits^T x, d_b = the column sums.
 #include <algorithm>
+#include <type_traits>
 
 #include "common.h"
 #include "kernels.h"
@@ -80,55 +81,93 @@ __global__ __launch_bounds__(NTH) void combine_backward_kernel(const T* __restri
 }
 
 // ---- router ----
-// Three products share one operand, the gradient of the logits, of T x E values: small, but the factor of 2 T E H operations
-// with either matrix. bf16 layers run them on bf16 MFMA, whose products are exact in fp32, with the fp32 operands cut into
-// bf16 parts of 8 bits: d_w_router (fp32) takes d_logits in three parts, which hold all of it, and x as it is; d_x, rounded to
-// bf16 in the end, takes d_logits and the weight in two parts each (16 bits) and three of their four products. fp32 layers run
-// on fp32 MFMA.
-//   route_grad_prep   d_logits, its column sums per 32 tokens, and the parts, laid out as the matrix unit takes them: a
-//                     fragment (32 rows x 16 k) is the 1 KB that a wave loads at once, lane l row l % 32, k = 8 (l / 32) on.
-//                     The transposes are made here, where they cost little.
-//   route_dx          the weight's parts of 64 or 128 columns stay in LDS while the tokens stream past.
-//   route_dw          x is transposed on its way to LDS: a thread loads 8 x 8 values and puts pairs of rows together.
-constexpr int kRows = 32, kStep = 16, kFrag = 1024;  // rows and k of a fragment, its bytes
-constexpr int kPairCols = 64;  // columns of x that two fragments of the weight hold, the even ones and the odd ones
+// The gradient of the logits, T x E values, is small, but a factor of both products (2 T E H operations each).
+//   bf16 layers: d_w_router (fp32) is x, exact, times d_logits in three bf16 parts, which hold all of its 24 bits, on bf16 MFMA:
+//     every product is exact and the sums are fp32. d_x is rounded to bf16, so its operands are fp16 with a power of two for
+//     each token and each column of x that puts the largest value at 2^14: off by 2^-11 of itself each at most (2^-39 of the
+//     largest for what becomes subnormal), against 2^-8 of the result in its own rounding. One product instead of the three that two
+//     bf16 parts of each take: 57 -> 37 us for 4096 x 256 x 7168 (28 now).
+//   fp32 layers: fp32 MFMA.
+// Fragments: 32 rows x STEP k are the 1 KB that a wave loads at once, lane l row l % 32 and the 16 bytes of k from (l / 32) *
+// STEP / 2 on. All operands but x are laid out in fragments by route_grad_prep, their transposes made on the way:
+//   route_grad_prep   d_logits, its column sums per 32 tokens, and the fragments of it and of the weight
+//   route_dx          the weight's fragments of 32 NJ columns stay in LDS while the tokens stream past
+//   route_dw          x is transposed on its way to LDS; the tokens are split over workgroups where the tiles are few
+constexpr int kRows = 32, kFrag = 1024;  // rows of a fragment, its bytes
+
+struct GradBf16 {
+  using X = bf16_t;
+  static constexpr int STEP = 16, PARTS = 3;  // k of a fragment; parts of d_logits in d_w_router
+  static constexpr bool SCALED = true;
+  static __device__ __forceinline__ void dx(f32x16& acc, u32x4 a, u32x4 b) {
+    acc = __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b), acc, 0, 0, 0);
+  }
+  static __device__ __forceinline__ void dw(f32x16& acc, u32x4 a, u32x4 b) {
+    acc = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), acc, 0, 0, 0);
+  }
+  // eight values times 2^e in fp16
+  static __device__ __forceinline__ u32x4 dx_operand(const float (&v)[8], int e) {
+    f16x8 o;
+#pragma unroll
+    for (int q = 0; q < 8; ++q) o[q] = (_Float16)ldexpf(v[q], e);
+    return __builtin_bit_cast(u32x4, o);
+  }
+  static __device__ __forceinline__ u32x4 dw_part(float (&v)[8]) {  // and what it leaves
+    const u32x4 o = pack(v);
+#pragma unroll
+    for (int q = 0; q < 8; ++q) v[q] = bf16_rest(v[q]);
+    return o;
+  }
+};
+struct GradF32 {
+  using X = float;
+  static constexpr int STEP = 8, PARTS = 1;
+  static constexpr bool SCALED = false;
+  static __device__ __forceinline__ void dx(f32x16& acc, u32x4 a, u32x4 b) {
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+      acc = __builtin_amdgcn_mfma_f32_32x32x2f32(__uint_as_float(a[q]), __uint_as_float(b[q]), acc, 0, 0, 0);
+  }
+  static __device__ __forceinline__ void dw(f32x16& acc, u32x4 a, u32x4 b) { dx(acc, a, b); }
+  static __device__ __forceinline__ u32x4 dx_operand(const float (&v)[4], int) { return pack(v); }
+  static __device__ __forceinline__ u32x4 dw_part(float (&v)[4]) { return pack(v); }
+};
 
 struct GradArgs {
   RouteBackward r;
-  int tb, ek, eb, hb;    // 32-token blocks, 16-expert steps, 32-expert blocks, 64-column blocks
-  unsigned char* px;     // [tb][ek][2 parts] fragments: rows tokens, k experts
-  unsigned char* pw;     // [eb][2 tb][3 parts] fragments: rows experts, k tokens
-  unsigned char* wt;     // [hb][ek][2 columns parities][2 parts] fragments: rows columns of x, k experts
-  float* bias_part;      // [tb][E]
-  float* partial;        // [splits][E][H]
+  int tb, ek, eb, hb, nj;  // blocks of 32 tokens, k steps and blocks of 32 experts, blocks of 32 nj columns
+  unsigned char* px;       // [tb][ek] fragments: rows tokens, k experts
+  unsigned char* pw;       // [eb][tb 32 / STEP][PARTS] fragments: rows experts, k tokens
+  unsigned char* wt;       // [hb][ek][nj] fragments: rows columns of x, k experts; row c of fragment j is column nj c + j
+  int* t_exp;              // [32 tb], h_exp [32 nj hb]: the powers of two of the fp16 operands
+  int* h_exp;
+  float* bias_part;        // [tb][E]
+  float* partial;          // [splits][E][H]
   int splits, chunks_per_split;
 };
 
-// Eight values as N bf16 parts, each the nearest bf16 of what the parts before it leave.
-template <int N>
-__device__ __forceinline__ void store_parts(float (&v)[8], unsigned char* frag, int lane) {
-#pragma unroll
-  for (int p = 0; p < N; ++p) {
-    st16(frag + p * kFrag + lane * 16, pack(v));
-    if (p + 1 < N) {
-#pragma unroll
-      for (int q = 0; q < 8; ++q) v[q] = bf16_rest(v[q]);
-    }
-  }
+// The power of two that puts a largest value, given by its bits, into [2^14, 2^15); 0 for zero, infinities and NaN.
+__device__ __forceinline__ int fp16_exp(uint32_t top) {
+  if (top == 0 || top >= 0x7f800000u) return 0;
+  return 15 - (int)(__builtin_amdgcn_frexp_expf(__uint_as_float(top)));
 }
 
-// Workgroups [0, tb): 32 tokens each. The others: 64 columns x 32 experts of the weight each.
-__global__ __launch_bounds__(NTH) void route_grad_prep_kernel(GradArgs a) {
-  constexpr int PITCH = MOE_MAX_EXPERTS + 1;
-  __shared__ float s[kRows * PITCH];
+// Workgroups [0, tb): 32 tokens each. The others: 32 columns of the weight each.
+constexpr int kPrepThreads = 1024;
+template <typename G>
+__global__ __launch_bounds__(kPrepThreads) void route_grad_prep_kernel(GradArgs a) {
+  constexpr int PITCH = MOE_MAX_EXPERTS + 1, WP = kRows + 1, N = G::STEP / 2, NW = kPrepThreads / 64;
+  __shared__ float s[kRows * PITCH > MOE_MAX_EXPERTS * WP ? kRows * PITCH : MOE_MAX_EXPERTS * WP];
+  __shared__ uint32_t s_top[kPrepThreads / kRows][kRows];
+  __shared__ int s_exp[kRows];
   const RouteBackward& r = a.r;
-  const int tid = threadIdx.x, E = r.E, k = r.k;
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, E = r.E, k = r.k;
   if ((int)blockIdx.x < a.tb) {
     const int64_t t0 = (int64_t)blockIdx.x * kRows;
     const int n = (int)min((int64_t)kRows, r.T - t0);
     const int ep = a.eb * kRows;  // experts with the padding of a fragment, zeros
-    for (int i = tid >> 6; i < kRows; i += NTH / 64)
-      for (int e = tid & 63; e < ep; e += 64) s[i * PITCH + e] = r.d_in && i < n && e < E ? r.d_in[(t0 + i) * E + e] : 0.f;
+    for (int i = wave; i < kRows; i += NW)
+      for (int e = lane; e < ep; e += 64) s[i * PITCH + e] = r.d_in && i < n && e < E ? r.d_in[(t0 + i) * E + e] : 0.f;
     __syncthreads();
     if (r.d_w && tid < n) {  // a thread per token, so that an id given twice gets both
       const int64_t at = (t0 + tid) * k;
@@ -148,124 +187,177 @@ __global__ __launch_bounds__(NTH) void route_grad_prep_kernel(GradArgs a) {
         if (id[j] >= 0 && id[j] < E) s[tid * PITCH + id[j]] += w[j] * (d[j] - sum);
     }
     __syncthreads();
-    for (int i = tid >> 6; i < n; i += NTH / 64)
-      for (int e = tid & 63; e < E; e += 64) r.d_logits[(t0 + i) * E + e] = s[i * PITCH + e];
+    for (int i = wave; i < kRows; i += NW) {
+      uint32_t top = 0;
+      for (int e = lane; e < E; e += 64) {
+        const float v = s[i * PITCH + e];
+        if (i < n) r.d_logits[(t0 + i) * E + e] = v;
+        top = max(top, __float_as_uint(v) & 0x7fffffffu);
+      }
+      if (G::SCALED && a.px) {
+#pragma unroll
+        for (int off = 32; off > 0; off >>= 1) top = max(top, (uint32_t)__shfl_xor((int)top, off, 64));
+        if (lane == 0) {
+          s_exp[i] = fp16_exp(top);
+          a.t_exp[t0 + i] = s_exp[i];
+        }
+      }
+    }
     if (r.d_bias)
-      for (int e = tid; e < E; e += NTH) {
+      for (int e = tid; e < E; e += kPrepThreads) {
         float v = 0.f;
         for (int i = 0; i < n; ++i) v += s[i * PITCH + e];
         a.bias_part[(int64_t)blockIdx.x * E + e] = v;
       }
-    if (a.px)
-      for (int i = tid; i < a.ek * 64; i += NTH) {
-        const int lane = i & 63, step = i >> 6;
-        float v[8];
-#pragma unroll
-        for (int q = 0; q < 8; ++q) v[q] = s[(lane & 31) * PITCH + step * kStep + (lane >> 5) * 8 + q];
-        store_parts<2>(v, a.px + ((int64_t)blockIdx.x * a.ek + step) * 2 * kFrag, lane);
-      }
     if (a.pw)
-      for (int i = tid; i < a.eb * 2 * 64; i += NTH) {
-        const int lane = i & 63, half = (i >> 6) & 1, b = i >> 7;
-        float v[8];
+      for (int i = tid; i < a.eb * (kRows / G::STEP) * 64; i += kPrepThreads) {
+        const int l = i & 63, step = (i >> 6) % (kRows / G::STEP), b = (i >> 6) / (kRows / G::STEP);
+        float v[N];
 #pragma unroll
-        for (int q = 0; q < 8; ++q) v[q] = s[(half * kStep + (lane >> 5) * 8 + q) * PITCH + b * kRows + (lane & 31)];
-        store_parts<3>(v, a.pw + ((int64_t)b * a.tb * 2 + (int64_t)blockIdx.x * 2 + half) * 3 * kFrag, lane);
+        for (int q = 0; q < N; ++q) v[q] = s[(step * G::STEP + (l >> 5) * N + q) * PITCH + b * kRows + (l & 31)];
+        unsigned char* f = a.pw + (((int64_t)b * a.tb + blockIdx.x) * (kRows / G::STEP) + step) * G::PARTS * kFrag + l * 16;
+#pragma unroll
+        for (int p = 0; p < G::PARTS; ++p) st16(f + p * kFrag, G::dw_part(v));
+      }
+    __syncthreads();  // s_exp
+    if (a.px)
+      for (int i = tid; i < a.ek * 64; i += kPrepThreads) {
+        const int l = i & 63, step = i >> 6;
+        float v[N];
+#pragma unroll
+        for (int q = 0; q < N; ++q) v[q] = s[(l & 31) * PITCH + step * G::STEP + (l >> 5) * N + q];
+        st16(a.px + ((int64_t)blockIdx.x * a.ek + step) * kFrag + l * 16, G::dx_operand(v, G::SCALED ? s_exp[l & 31] : 0));
       }
     return;
   }
-  constexpr int WP = kPairCols + 4;
-  const int i = blockIdx.x - a.tb, b = i / a.eb, e0 = i % a.eb * kRows, h0 = b * kPairCols;
-  for (int v = tid; v < kRows * kPairCols / 4; v += NTH) {
-    const int e = v / (kPairCols / 4), c = v % (kPairCols / 4) * 4;
-    const bool in = e0 + e < E && h0 + c < r.H;
-    *reinterpret_cast<u32x4*>(s + e * WP + c) = in ? ld16(r.w_router + (int64_t)(e0 + e) * r.H + h0 + c) : u32x4{0u, 0u, 0u, 0u};
+  const int c = tid & 31, g = tid >> 5;  // column of the 32, and which experts
+  const int h0 = (blockIdx.x - a.tb) * kRows, ep = a.ek * G::STEP;
+  uint32_t top = 0;
+  for (int e = g; e < ep; e += kPrepThreads / kRows) {
+    const float v = e < E && h0 + c < r.H ? r.w_router[(int64_t)e * r.H + h0 + c] : 0.f;
+    s[e * WP + c] = v;
+    top = max(top, __float_as_uint(v) & 0x7fffffffu);
+  }
+  if constexpr (G::SCALED) {
+    s_top[g][c] = top;
+    __syncthreads();
+    if (tid < kRows) {
+      for (int i = 1; i < kPrepThreads / kRows; ++i) top = max(top, s_top[i][c]);
+      s_exp[c] = fp16_exp(top);
+      a.h_exp[h0 + c] = s_exp[c];
+    }
   }
   __syncthreads();
-  const int lane = tid & 63, odd = (tid >> 6) & 1, step = tid >> 7;
-  if (e0 / kStep + step < a.ek) {
-    float v[8];
+  const int per = 32 / a.nj;  // this workgroup's rows of each fragment: column nj row + j
+  for (int i = tid; i < a.ek * a.nj * 2 * per; i += kPrepThreads) {
+    const int row = i % per, half = i / per & 1, j = i / (2 * per) % a.nj, step = i / (2 * per * a.nj);
+    const int col = a.nj * row + j, b = h0 / (32 * a.nj), row0 = h0 % (32 * a.nj) / a.nj;
+    float v[N];
 #pragma unroll
-    for (int q = 0; q < 8; ++q) v[q] = s[(step * kStep + (lane >> 5) * 8 + q) * WP + 2 * (lane & 31) + odd];
-    store_parts<2>(v, a.wt + (((int64_t)b * a.ek + e0 / kStep + step) * 2 + odd) * 2 * kFrag, lane);
+    for (int q = 0; q < N; ++q) v[q] = s[(step * G::STEP + half * N + q) * WP + col];
+    st16(a.wt + (((int64_t)b * a.ek + step) * a.nj + j) * kFrag + (half * 32 + row0 + row) * 16,
+         G::dx_operand(v, G::SCALED ? s_exp[col] : 0));
   }
 }
 
-// d_x: a wave computes 64 tokens x 64 columns, WT x WH waves. The columns' parts are in LDS for good; the tokens' fragments come
-// from memory one step ahead, across the ends of the token tiles.
-template <int WT, int WH>
-__global__ __launch_bounds__(WT * WH * 64) void route_dx_kernel(GradArgs a) {
-  constexpr int NT = WT * WH * 64;
+// d_x: a wave computes 32 TI tokens x 32 NJ columns, WT waves. The columns' fragments are in LDS for good; the tokens' come from
+// memory D - 1 steps ahead, across the ends of the token tiles. A lane has NJ neighbouring columns of a row.
+template <typename G, int NJ, int TI, int WT>
+__global__ __launch_bounds__(WT * 64, TI == 1 ? 4 : 2) void route_dx_kernel(GradArgs a) {
+  constexpr int NT = WT * 64, D = 4;
+  using X = typename G::X;
   extern __shared__ __attribute__((aligned(1024))) unsigned char s_w[];
   const RouteBackward& r = a.r;
   const int tid = threadIdx.x, lane = tid & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int wh = wave % WH, wt = wave / WH;
-  const int b0 = blockIdx.x * WH;
-  const int per_block = a.ek * 4 * kFrag;  // bytes of a 64-column block
-  for (int i = tid * 16; i < min(WH, a.hb - b0) * per_block; i += NT * 16) st16(s_w + i, ld16(a.wt + (int64_t)b0 * per_block + i));
-  __syncthreads();
-  if (b0 + wh >= a.hb) return;
-  const unsigned char* w = s_w + wh * per_block + lane * 16;
-  const int tiles = (a.tb + 2 * WT - 1) / (2 * WT);  // of 64 WT tokens
-  u32x4 fa[2][2][2];  // buffer, 32-token block, part
-  auto load = [&](int tile, int step, u32x4 (&f)[2][2]) {
+  const int wt = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int block = a.ek * NJ * kFrag;
+  for (int i = tid * 16; i < block; i += NT * 16 * 8) {
+    u32x4 v[8];
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int tb = min((tile * WT + wt) * 2 + i, a.tb - 1);
+    for (int q = 0; q < 8; ++q)
+      if (i + q * NT * 16 < block) v[q] = ld16(a.wt + (int64_t)blockIdx.x * block + i + q * NT * 16);
 #pragma unroll
-      for (int p = 0; p < 2; ++p) f[i][p] = ld16(a.px + (((int64_t)tb * a.ek + step) * 2 + p) * kFrag + lane * 16);
+    for (int q = 0; q < 8; ++q)
+      if (i + q * NT * 16 < block) st16(s_w + i + q * NT * 16, v[q]);
+  }
+  const int tiles = (a.tb + TI * WT - 1) / (TI * WT);  // of 32 TI WT tokens
+  u32x4 fa[D][TI];  // 32-token blocks
+  int tile = blockIdx.y, step = 0, ltile = blockIdx.y, lstep = 0;
+  // the next step that is not on its way yet; past the last one a valid address, as a branch around loads makes the compiler
+  // wait for all of them
+  auto load = [&](u32x4 (&f)[TI]) {
+#pragma unroll
+    for (int i = 0; i < TI; ++i) {
+      const int tb = min((ltile * WT + wt) * TI + i, a.tb - 1);
+      f[i] = ld16(a.px + ((int64_t)tb * a.ek + lstep) * kFrag + lane * 16);
+    }
+    if (++lstep == a.ek) {
+      lstep = 0;
+      ltile += gridDim.y;
     }
   };
-  f32x16 acc[2][2];
+  f32x16 acc[TI][NJ];
   auto clear = [&] {
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
+    for (int i = 0; i < TI; ++i)
 #pragma unroll
-      for (int j = 0; j < 2; ++j)
+      for (int j = 0; j < NJ; ++j)
 #pragma unroll
         for (int q = 0; q < 16; ++q) acc[i][j][q] = 0.f;
   };
   clear();
-  int tile = blockIdx.y, step = 0;
-  if (tile < tiles) load(tile, 0, fa[0]);
-  auto one = [&](u32x4 (&now)[2][2], u32x4 (&next)[2][2]) {
-    const int nstep = step + 1 < a.ek ? step + 1 : 0, ntile = nstep ? tile : tile + (int)gridDim.y;
-    if (ntile < tiles) load(ntile, nstep, next);
-    u32x4 fb[2][2];
 #pragma unroll
-    for (int j = 0; j < 2; ++j)
+  for (int i = 0; i < D - 1; ++i) load(fa[i]);
+  const int h = blockIdx.x * 32 * NJ + NJ * (lane & 31);
+  int he[NJ];
 #pragma unroll
-      for (int p = 0; p < 2; ++p) fb[j][p] = ld16(w + ((step * 2 + j) * 2 + p) * kFrag);
+  for (int j = 0; j < NJ; ++j) he[j] = G::SCALED ? a.h_exp[h + j] : 0;
+  __syncthreads();
+  auto one = [&](auto U) {
+    constexpr int u = decltype(U)::value;
+    load(fa[(u + D - 1) % D]);
+    u32x4 fb[NJ];
 #pragma unroll
-    for (int pp = 2; pp >= 0; --pp) {  // second parts first
-      const int pa = pp == 1, pb = pp == 2;
+    for (int j = 0; j < NJ; ++j) fb[j] = ld16(s_w + (step * NJ + j) * kFrag + lane * 16);
 #pragma unroll
-      for (int i = 0; i < 2; ++i)
+    for (int i = 0; i < TI; ++i)
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          const u32x4 x[1] = {now[i][pa]}, y[1] = {fb[j][pb]};
-          Op32::step(acc[i][j], x, y);
-        }
-    }
-    if (nstep == 0) {
+      for (int j = 0; j < NJ; ++j) G::dx(acc[i][j], fa[u][i], fb[j]);
+    if (++step == a.ek) {
 #pragma unroll
-      for (int i = 0; i < 2; ++i)
+      for (int i = 0; i < TI; ++i) {
+        const int tb = (tile * WT + wt) * TI + i;
+        const int64_t t0 = (int64_t)tb * kRows;
+        // the powers of two of the block's tokens, by scalar loads: vector loads would wait for the fragments on their way
+        const auto* te = (const __attribute__((address_space(4))) int*)(a.t_exp + (int64_t)min(tb, a.tb - 1) * kRows);
+        if (t0 < r.T)
 #pragma unroll
-        for (int q = 0; q < 16; ++q) {
-          const int64_t t = (int64_t)((tile * WT + wt) * 2 + i) * kRows + Op32::out_row(lane, q);
-          const int h = (b0 + wh) * kPairCols + 2 * (lane & 31);
-          if (t < r.T && h < r.H)
-            *reinterpret_cast<uint32_t*>(static_cast<bf16_t*>(r.d_x) + t * r.H + h) = pack2_bf16(acc[i][0][q], acc[i][1][q]);
-        }
+          for (int q = 0; q < 16; ++q) {
+            const int64_t t = t0 + Op32::out_row(lane, q);
+            const int ti = !G::SCALED ? 0 : lane < 32 ? te[Op32::out_row(0, q)] : te[Op32::out_row(32, q)];
+            if (t < r.T && h < r.H) {
+              X* o = static_cast<X*>(r.d_x) + t * r.H + h;
+              float v[NJ];
+#pragma unroll
+              for (int j = 0; j < NJ; ++j) v[j] = G::SCALED ? ldexpf(acc[i][j][q], -ti - he[j]) : acc[i][j][q];
+              if constexpr (sizeof(X) == 4 && NJ == 4) *reinterpret_cast<u32x4*>(o) = pack(v);
+              else if constexpr (sizeof(X) == 4) *reinterpret_cast<f32x2*>(o) = f32x2{v[0], v[1]};
+              else  // (non-temporal: 29.4 -> 27.7 us)
+                __builtin_nontemporal_store(u32x2{pack2_bf16(v[0], v[1]), pack2_bf16(v[2], v[3])},
+                                            reinterpret_cast<u32x2*>(o));
+            }
+          }
+      }
       clear();
+      step = 0;
+      tile += gridDim.y;
     }
-    tile = ntile;
-    step = nstep;
   };
   while (tile < tiles) {
-    one(fa[0], fa[1]);
-    if (tile < tiles) one(fa[1], fa[0]);
+    one(std::integral_constant<int, 0>{});
+    if (tile < tiles) one(std::integral_constant<int, 1>{});
+    if (tile < tiles) one(std::integral_constant<int, 2>{});
+    if (tile < tiles) one(std::integral_constant<int, 3>{});
   }
 }
 
@@ -289,47 +381,65 @@ __global__ __launch_bounds__(512) void route_dbias_kernel(GradArgs a) {
 }
 
 // d_w_router: eight waves, WE along the experts (32 each) and 8 / WE along the tokens, whose sums are added in the end; 128
-// columns of x. Tokens go in chunks of 256: a thread loads 8 tokens x 8 columns of the next chunk while this one is multiplied.
-// In LDS the chunk is fragments [16 steps][4 column blocks]; in a fragment the 16 bytes of column c are at place
-// c ^ (its group of 8 in the 128 columns), so that the writes of a wave, at a stride of 8 columns, touch all banks.
+// columns of x. Tokens go in chunks of 16 steps: a thread loads 8 tokens x 16 bytes of the next chunk while this one is
+// multiplied. In LDS the chunk is fragments [16 steps][4 column blocks]; in a fragment the 16 bytes of column c are at place
+// c ^ (its group of 8 in the 128 columns), so that the writes of a wave, at a stride of 4 or 8 columns, touch all banks.
 // Workgroups past the column tiles add up the bias.
-constexpr int kDwCols = 128, kDwChunk = 256;
-template <int WE>
+constexpr int kDwCols = 128, kDwSteps = 16, kDwChunkBytes = kDwSteps * 4 * kFrag;
+template <typename G, int WE>
 __global__ __launch_bounds__(512) void route_dw_kernel(GradArgs a, int col_tiles) {
-  constexpr int KW = 8 / WE, CHUNK = kDwChunk * kDwCols * 2;
+  constexpr int KW = 8 / WE, P = G::PARTS, VN = Vec<typename G::X>::N, CT = kDwSteps * G::STEP;
   extern __shared__ __attribute__((aligned(1024))) unsigned char s_x[];  // two chunks
   const RouteBackward& r = a.r;
   const int tid = threadIdx.x, lane = tid & 63;
-  if ((int)blockIdx.x >= col_tiles) {
-    if (blockIdx.y == 0 && blockIdx.z == 0) bias_sums(a, blockIdx.x - col_tiles, reinterpret_cast<double*>(s_x));
+  // a workgroup's unit: splits of the tokens are the slowest index and an XCD takes neighbouring units, so that its L2 holds the
+  // d_logits of one split
+  const int e_tiles = (a.eb + 7) / 8, units = col_tiles * e_tiles * a.splits, per = (units + 7) >> 3;
+  const int unit = (blockIdx.x & 7) * per + (blockIdx.x >> 3);
+  if ((int)blockIdx.x >= per * 8) {
+    bias_sums(a, blockIdx.x - per * 8, reinterpret_cast<double*>(s_x));
     return;
   }
+  if (unit >= units) return;
+  const int split = unit / (col_tiles * e_tiles), e_tile = unit / col_tiles % e_tiles;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int we = wave % WE, kw = wave / WE;
-  const int eb = blockIdx.z * 8 + we;  // this wave's 32 experts
-  const int h0 = blockIdx.x * kDwCols;
-  const int steps = a.tb * 2, chunks = (steps + 15) / 16;
-  const int c0 = blockIdx.y * a.chunks_per_split, c1 = min(chunks, c0 + a.chunks_per_split);
-  const bf16_t* x = static_cast<const bf16_t*>(r.x);
-  const int g8 = tid & 15, t8 = tid >> 4;  // this thread's 8 columns and 8 tokens of a chunk
-  const bool in_h = h0 + g8 * 8 < r.H;
+  const int eb = e_tile * 8 + we;  // this wave's 32 experts
+  const int h0 = unit % col_tiles * kDwCols;
+  const int steps = a.tb * (kRows / G::STEP), chunks = (steps + kDwSteps - 1) / kDwSteps;
+  const int c0 = split * a.chunks_per_split, c1 = min(chunks, c0 + a.chunks_per_split);
+  const typename G::X* x = static_cast<const typename G::X*>(r.x);
+  const int gv = tid % (kDwCols / VN), t8 = tid / (kDwCols / VN);  // this thread's VN columns and 8 tokens of a chunk
+  const bool in_h = h0 + gv * VN < r.H;
   u32x4 raw[8];
+  // rows of chunk c; past the last token, and in lanes past H, the offset reads zeros. All loads here are unconditional: a
+  // branch around some makes the compiler wait for more of them than it needs.
+  const int voff = in_h ? (t8 * 8 * r.H + h0 + gv * VN) * (int)sizeof(*x) : 0x7ffffff0;
   auto load = [&](int c) {
+    const int64_t t0 = min((int64_t)c * CT, (int64_t)r.T);
+    const __amdgpu_buffer_rsrc_t rsrc = __builtin_amdgcn_make_buffer_rsrc(
+        (void*)(x + t0 * r.H), (short)0, (int)(min((int64_t)CT, r.T - t0) * r.H * (int)sizeof(*x)), 0x00020000);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int64_t t = (int64_t)c * kDwChunk + t8 * 8 + i;
-      raw[i] = in_h && t < r.T ? ld16_nt(x + t * r.H + h0 + g8 * 8) : u32x4{0u, 0u, 0u, 0u};
-    }
+    for (int i = 0; i < 8; ++i)
+      raw[i] = __builtin_bit_cast(
+          u32x4, __builtin_amdgcn_raw_buffer_load_b128(rsrc, in_h ? voff + i * r.H * (int)sizeof(*x) : voff, 0, 2));
   };
   auto store = [&](int slot) {
-    unsigned char* base = s_x + slot * CHUNK + (((t8 >> 1) * 4 + (g8 >> 2)) * 64 + (t8 & 1) * 32 + (g8 & 3) * 8) * 16;
+    const int col = gv * VN, g8 = col >> 3;
+    unsigned char* base = s_x + slot * kDwChunkBytes + (((t8 * 8 / G::STEP) * 4 + (col >> 5)) * 64 + (col & 24)) * 16;
 #pragma unroll
-    for (int c = 0; c < 8; ++c) {
-      u32x4 v;
+    for (int c = 0; c < VN; ++c) {
+      unsigned char* o = base + ((((col & 7) + c) ^ g8) & 7) * 16;
+      if constexpr (VN == 8) {
+        u32x4 v;
 #pragma unroll
-      for (int p = 0; p < 4; ++p)  // tokens 2 p and 2 p + 1 of column c
-        v[p] = __builtin_amdgcn_perm(raw[2 * p + 1][c >> 1], raw[2 * p][c >> 1], c & 1 ? 0x07060302u : 0x05040100u);
-      st16(base + ((c ^ g8) & 7) * 16, v);
+        for (int p = 0; p < 4; ++p)  // tokens 2 p and 2 p + 1 of column c
+          v[p] = __builtin_amdgcn_perm(raw[2 * p + 1][c >> 1], raw[2 * p][c >> 1], c & 1 ? 0x07060302u : 0x05040100u);
+        st16(o + (t8 & 1) * 512, v);
+      } else {
+        st16(o, u32x4{raw[0][c], raw[1][c], raw[2][c], raw[3][c]});
+        st16(o + 512, u32x4{raw[4][c], raw[5][c], raw[6][c], raw[7][c]});
+      }
     }
   };
   f32x16 acc[4];
@@ -337,7 +447,7 @@ __global__ __launch_bounds__(512) void route_dw_kernel(GradArgs a, int col_tiles
   for (int j = 0; j < 4; ++j)
 #pragma unroll
     for (int q = 0; q < 16; ++q) acc[j][q] = 0.f;
-  const unsigned char* pw = a.pw + (int64_t)min(eb, a.eb - 1) * steps * 3 * kFrag + lane * 16;
+  const unsigned char* pw = a.pw + (int64_t)min(eb, a.eb - 1) * steps * P * kFrag + lane * 16;
   int rd[4];  // this lane's column in the four blocks
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
@@ -348,34 +458,44 @@ __global__ __launch_bounds__(512) void route_dw_kernel(GradArgs a, int col_tiles
     load(c0);
     store(0);
   }
+  constexpr int U = kDwSteps / KW, D = U < 4 ? U : 4;  // a wave's steps of a chunk; buffers of d_logits' fragments
+  static_assert(U % D == 0, "a chunk takes every buffer as often");
+  u32x4 fa[D][P];
+  auto load_a = [&](int s, u32x4 (&f)[P]) {  // step s of all
+#pragma unroll
+    for (int p = 0; p < P; ++p) f[p] = ld16(pw + ((int64_t)max(0, min(s, steps - 1)) * P + p) * kFrag);
+  };
+  if (steps > 0) {
+#pragma unroll
+    for (int u = 0; u < D - 1; ++u) load_a(c0 * kDwSteps + kw + u * KW, fa[u]);
+  }
+  // One chunk; its last steps are past the tokens in the last chunk only. The columns' fragments are read one step ahead.
+  auto chunk = [&](int c) {
+    const unsigned char* base = s_x + ((c - c0) & 1) * kDwChunkBytes;
+    u32x4 fb[2][4];
+    auto read_b = [&](int s, u32x4 (&f)[4]) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) f[j] = ld16(base + s * 4 * kFrag + rd[j]);
+    };
+    read_b(kw, fb[0]);
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int s = kw + u * KW;
+      load_a(c * kDwSteps + s + (D - 1) * KW, fa[(u + D - 1) % D]);
+      if (u == 0) load(c + 1);  // (spread over the steps: 65 against 56 us)
+      if (u + 1 < U) read_b(s + KW, fb[(u + 1) & 1]);
+      if (c * kDwSteps + s < steps) {
+#pragma unroll
+        for (int p = P - 1; p >= 0; --p)  // the smallest part first
+#pragma unroll
+          for (int j = 0; j < 4; ++j) G::dw(acc[j], fa[u % D][p], fb[u & 1][j]);
+      }
+      __builtin_amdgcn_sched_barrier(0);
+    }
+  };
   for (int c = c0; c < c1; ++c) {
     lds_barrier();  // chunk c is in LDS, and chunk c - 1 has been read
-    if (c + 1 < c1) load(c + 1);
-    const unsigned char* base = s_x + ((c - c0) & 1) * CHUNK;
-    const int s_end = min(16, steps - c * 16);
-    u32x4 fa[2][3];
-    auto load_a = [&](int s, u32x4 (&f)[3]) {
-#pragma unroll
-      for (int p = 0; p < 3; ++p) f[p] = ld16(pw + ((int64_t)(c * 16 + s) * 3 + p) * kFrag);
-    };
-    if (kw < s_end) load_a(kw, fa[0]);
-#pragma unroll
-    for (int u = 0; u < 16 / KW; ++u) {
-      const int s = kw + u * KW;
-      if (s < s_end) {
-        if (s + KW < s_end) load_a(s + KW, fa[(u + 1) & 1]);
-        u32x4 fb[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) fb[j] = ld16(base + s * 4 * kFrag + rd[j]);
-#pragma unroll
-        for (int p = 2; p >= 0; --p)  // the smallest part first
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const u32x4 va[1] = {fa[u & 1][p]}, vb[1] = {fb[j]};
-            Op32::step(acc[j], va, vb);
-          }
-      }
-    }
+    chunk(c);
     if (c + 1 < c1) store((c + 1 - c0) & 1);
   }
   if constexpr (KW > 1) {  // add the waves' sums, in the order of kw, through LDS
@@ -396,7 +516,7 @@ __global__ __launch_bounds__(512) void route_dw_kernel(GradArgs a, int col_tiles
 #pragma unroll
         for (int q = 0; q < 16; ++q) acc[j][q] += s[((w * WE + we) * 64 + j * 16 + q) * 64 + lane];
   }
-  float* out = a.splits > 1 ? a.partial + (int64_t)blockIdx.y * r.E * r.H : r.d_w_router;
+  float* out = a.splits > 1 ? a.partial + (int64_t)split * r.E * r.H : r.d_w_router;
 #pragma unroll
   for (int j = 0; j < 4; ++j)
 #pragma unroll
@@ -419,43 +539,6 @@ __global__ __launch_bounds__(NTH) void route_dw_sum_kernel(const float* __restri
     for (int q = 0; q < 4; ++q) v[q] += p[q];
   }
   st16(out + at, pack(v));
-}
-
-// C[m, n] = sum_k A(m, k) B[k, n] in fp32 on v_mfma_f32_32x32x2_f32, B's rows contiguous in n. TRANS: A(m, k) = A[k, m], else
-// A[m, k]. 64 x 64 tiles, four waves of 32 x 32, K in steps of 16 through LDS.
-template <bool TRANS>
-__global__ __launch_bounds__(NTH) void route_grad_gemm_kernel(const float* __restrict__ A, const float* __restrict__ B, int M,
-                                                             int N, int K, int lda, float* __restrict__ C) {
-  constexpr int BM = 64, BN = 64, BK = 16, PAD = 4;
-  __shared__ float s_a[BK][BM + PAD], s_b[BK][BN + PAD];
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const int m0 = blockIdx.y * BM, n0 = blockIdx.x * BN;
-  const int wm = (wave >> 1) * 32, wn = (wave & 1) * 32;
-  f32x16 acc;
-#pragma unroll
-  for (int q = 0; q < 16; ++q) acc[q] = 0.f;
-  for (int k0 = 0; k0 < K; k0 += BK) {
-    __syncthreads();
-    for (int i = tid; i < BK * BM; i += NTH) {
-      const int kk = TRANS ? i / BM : i % BK, mm = TRANS ? i % BM : i / BK;
-      const bool in = k0 + kk < K && m0 + mm < M;
-      s_a[kk][mm] = !in ? 0.f : TRANS ? A[(int64_t)(k0 + kk) * lda + m0 + mm] : A[(int64_t)(m0 + mm) * lda + k0 + kk];
-    }
-    for (int i = tid; i < BK * BN; i += NTH) {
-      const int kk = i / BN, nn = i % BN;
-      s_b[kk][nn] = k0 + kk < K && n0 + nn < N ? B[(int64_t)(k0 + kk) * N + n0 + nn] : 0.f;
-    }
-    __syncthreads();
-#pragma unroll
-    for (int kk = 0; kk < BK; kk += 2)
-      acc = __builtin_amdgcn_mfma_f32_32x32x2f32(s_a[kk + (lane >> 5)][wm + (lane & 31)],
-                                                 s_b[kk + (lane >> 5)][wn + (lane & 31)], acc, 0, 0, 0);
-  }
-#pragma unroll
-  for (int q = 0; q < 16; ++q) {
-    const int m = m0 + wm + Op32::out_row(lane, q), n = n0 + wn + (lane & 31);
-    if (m < M && n < N) C[(int64_t)m * N + n] = acc[q];
-  }
 }
 
 }  // namespace
@@ -482,17 +565,19 @@ hipError_t launch_combine_backward(const void* dy, int bf16, const void* out_buf
 namespace {
 
 struct GradSizes {
-  int tb, ek, eb, hb, splits, chunks_per_split;
-  size_t px, pw, wt, bias, partial, total;
+  int tb, ek, eb, hb, nj, splits, chunks_per_split;
+  size_t px, pw, wt, t_exp, h_exp, bias, partial, total;
 };
-GradSizes grad_sizes(int T, int H, int E, int bf16) {
+template <typename G>
+GradSizes grad_sizes(int T, int H, int E) {
   GradSizes g{};
   g.tb = ceil_div_host(T, kRows);
-  g.ek = ceil_div_host(E, kStep);
+  g.ek = ceil_div_host(E, G::STEP);
   g.eb = ceil_div_host(E, kRows);
-  g.hb = ceil_div_host(H, kPairCols);
+  g.nj = g.ek <= 32 ? 4 : 2;  // the weight's fragments of 32 nj columns take 1 KB ek nj of LDS, 128 KB at most
+  g.hb = ceil_div_host(H, 32 * g.nj);
   // d_w_router: parts of the tokens, as many as give every CU a workgroup
-  const int chunks = std::max(1, ceil_div_host(T, kDwChunk));
+  const int chunks = std::max(1, ceil_div_host(T, kDwSteps * G::STEP));
   const int tiles = ceil_div_host(H, kDwCols) * ceil_div_host(g.eb, 8);
   g.chunks_per_split = ceil_div_host(chunks, std::max(1, std::min(chunks, 256 / tiles)));
   g.splits = ceil_div_host(chunks, g.chunks_per_split);
@@ -503,44 +588,37 @@ GradSizes grad_sizes(int T, int H, int E, int bf16) {
     return here;
   };
   g.bias = take((size_t)g.tb * E * sizeof(float));
-  if (bf16) {
-    g.px = take((size_t)g.tb * g.ek * 2 * kFrag);
-    g.pw = take((size_t)g.eb * g.tb * 2 * 3 * kFrag);
-    g.wt = take((size_t)g.hb * g.ek * 4 * kFrag);
-    g.partial = take(g.splits > 1 ? (size_t)g.splits * E * H * sizeof(float) : 0);
-  }
+  g.px = take((size_t)g.tb * g.ek * kFrag);
+  g.pw = take((size_t)g.eb * g.tb * (kRows / G::STEP) * G::PARTS * kFrag);
+  g.wt = take((size_t)g.hb * g.ek * g.nj * kFrag);
+  g.t_exp = take((size_t)g.tb * kRows * sizeof(int));
+  g.h_exp = take((size_t)g.hb * 32 * g.nj * sizeof(int));
+  g.partial = take(g.splits > 1 ? (size_t)g.splits * E * H * sizeof(float) : 0);
   g.total = at;
   return g;
 }
 
-template <int WE>
+template <typename G, int WE>
 hipError_t launch_dw(const GradArgs& a, hipStream_t stream) {
-  const int lds = 2 * kDwChunk * kDwCols * 2, tiles = ceil_div_host(a.r.H, kDwCols);
+  const int lds = 2 * kDwChunkBytes, tiles = ceil_div_host(a.r.H, kDwCols);
   const int bias = a.r.d_bias ? ceil_div_host(a.r.E, 64) : 0;
-  const hipError_t st = hipFuncSetAttribute(reinterpret_cast<const void*>(route_dw_kernel<WE>),
-                                            hipFuncAttributeMaxDynamicSharedMemorySize, lds);
-  if (st != hipSuccess) return st;
-  route_dw_kernel<WE><<<dim3(tiles + bias, a.splits, ceil_div_host(a.eb, 8)), 512, lds, stream>>>(a, tiles);
+  const int units = tiles * a.splits * ceil_div_host(a.eb, 8);
+  route_dw_kernel<G, WE><<<ceil_div_host(units, 8) * 8 + bias, 512, lds, stream>>>(a, tiles);
   return hipGetLastError();
 }
 
-template <int WT, int WH>
+template <typename G, int NJ, int TI, int WT>
 hipError_t launch_dx(const GradArgs& a, hipStream_t stream) {
-  const int lds = WH * a.ek * 4 * kFrag;
-  const hipError_t st = hipFuncSetAttribute(reinterpret_cast<const void*>(route_dx_kernel<WT, WH>),
-                                            hipFuncAttributeMaxDynamicSharedMemorySize, lds);
-  if (st != hipSuccess) return st;
-  const int cols = ceil_div_host(a.hb, WH), tiles = ceil_div_host(a.tb, 2 * WT);
-  route_dx_kernel<WT, WH><<<dim3(cols, std::max(1, std::min(tiles, 256 / cols))), WT * WH * 64, lds, stream>>>(a);
+  const int tiles = ceil_div_host(a.tb, TI * WT);
+  // two workgroups per CU, whose stores and products overlap, where the LDS takes them
+  const dim3 grid(a.hb, std::max(1, std::min(tiles, 512 / a.hb)));
+  route_dx_kernel<G, NJ, TI, WT><<<grid, WT * 64, a.ek * NJ * kFrag, stream>>>(a);
   return hipGetLastError();
 }
 
-}  // namespace
-
-size_t route_backward_workspace_bytes(int T, int H, int E, int bf16) { return grad_sizes(T, H, E, bf16).total; }
-
-hipError_t launch_route_backward(const RouteBackward& r, hipStream_t stream) {
-  const GradSizes g = grad_sizes(r.T, r.H, r.E, r.bf16);
+template <typename G>
+hipError_t launch_route_backward_t(const RouteBackward& r, hipStream_t stream) {
+  const GradSizes g = grad_sizes<G>(r.T, r.H, r.E);
   unsigned char* ws = static_cast<unsigned char*>(r.workspace);
   GradArgs a{};
   a.r = r;
@@ -548,51 +626,50 @@ hipError_t launch_route_backward(const RouteBackward& r, hipStream_t stream) {
   a.ek = g.ek;
   a.eb = g.eb;
   a.hb = g.hb;
+  a.nj = g.nj;
   a.splits = g.splits;
   a.chunks_per_split = g.chunks_per_split;
   a.bias_part = reinterpret_cast<float*>(ws + g.bias);
-  if (r.bf16) {
-    a.px = r.d_x ? ws + g.px : nullptr;
-    a.pw = r.d_w_router ? ws + g.pw : nullptr;
-    a.wt = ws + g.wt;
-    a.partial = reinterpret_cast<float*>(ws + g.partial);
-  }
+  a.px = r.d_x ? ws + g.px : nullptr;
+  a.pw = r.d_w_router ? ws + g.pw : nullptr;
+  a.wt = ws + g.wt;
+  a.t_exp = reinterpret_cast<int*>(ws + g.t_exp);
+  a.h_exp = reinterpret_cast<int*>(ws + g.h_exp);
+  a.partial = reinterpret_cast<float*>(ws + g.partial);
+  hipError_t st = hipSuccess;
   if (r.T > 0) {
-    route_grad_prep_kernel<<<a.tb + (a.px ? a.hb * a.eb : 0), NTH, 0, stream>>>(a);
-    const hipError_t st = hipGetLastError();
+    route_grad_prep_kernel<G><<<a.tb + (r.d_x ? a.hb * a.nj : 0), kPrepThreads, 0, stream>>>(a);
+    st = hipGetLastError();
+    if (st == hipSuccess && r.d_x) {
+      const bool few = a.tb <= 4;  // tokens for two waves at most
+      if (a.nj == 4)
+        st = few ? launch_dx<G, 4, 1, 4>(a, stream) : a.ek <= 16 ? launch_dx<G, 4, 1, 8>(a, stream) : launch_dx<G, 4, 2, 8>(a, stream);
+      else if constexpr (!G::SCALED) st = few ? launch_dx<G, 2, 1, 4>(a, stream) : launch_dx<G, 2, 2, 8>(a, stream);
+    }
     if (st != hipSuccess) return st;
   }
-  if (r.bf16) {
-    hipError_t st = hipSuccess;
-    if (r.d_x && r.T > 0) {
-      st = a.ek <= 16 ? launch_dx<4, 2>(a, stream) : launch_dx<8, 1>(a, stream);
-      if (st != hipSuccess) return st;
-    }
-    if (r.d_w_router) {
-      st = a.eb <= 1 ? launch_dw<1>(a, stream) : a.eb <= 2 ? launch_dw<2>(a, stream)
-           : a.eb <= 4 ? launch_dw<4>(a, stream) : launch_dw<8>(a, stream);
-      if (st != hipSuccess) return st;
-      if (a.splits > 1) {
-        const int64_t n = (int64_t)r.E * r.H;
-        route_dw_sum_kernel<<<(unsigned)ceil_div_host64(n / 4, NTH), NTH, 0, stream>>>(a.partial, a.splits, n, r.d_w_router);
-      }
-    } else if (r.d_bias) {
-      route_dbias_kernel<<<ceil_div_host(r.E, 64), 512, 0, stream>>>(a);
-    }
-    return hipGetLastError();
-  }
-  if (r.d_x && r.T > 0) {
-    const dim3 grid(ceil_div_host(r.H, 64), ceil_div_host(r.T, 64));
-    route_grad_gemm_kernel<false><<<grid, NTH, 0, stream>>>(r.d_logits, r.w_router, r.T, r.H, r.E, r.E,
-                                                           static_cast<float*>(r.d_x));
-  }
   if (r.d_w_router) {
-    const dim3 grid(ceil_div_host(r.H, 64), ceil_div_host(r.E, 64));
-    route_grad_gemm_kernel<true><<<grid, NTH, 0, stream>>>(r.d_logits, static_cast<const float*>(r.x), r.E, r.H, r.T, r.E,
-                                                          r.d_w_router);
+    st = a.eb <= 1 ? launch_dw<G, 1>(a, stream) : a.eb <= 2 ? launch_dw<G, 2>(a, stream)
+         : a.eb <= 4 ? launch_dw<G, 4>(a, stream) : launch_dw<G, 8>(a, stream);
+    if (st != hipSuccess) return st;
+    if (a.splits > 1) {
+      const int64_t n = (int64_t)r.E * r.H;
+      route_dw_sum_kernel<<<(unsigned)ceil_div_host64(n / 4, NTH), NTH, 0, stream>>>(a.partial, a.splits, n, r.d_w_router);
+    }
+  } else if (r.d_bias) {
+    route_dbias_kernel<<<ceil_div_host(r.E, 64), 512, 0, stream>>>(a);
   }
-  if (r.d_bias) route_dbias_kernel<<<ceil_div_host(r.E, 64), 512, 0, stream>>>(a);
   return hipGetLastError();
+}
+
+}  // namespace
+
+size_t route_backward_workspace_bytes(int T, int H, int E, int bf16) {
+  return bf16 ? grad_sizes<GradBf16>(T, H, E).total : grad_sizes<GradF32>(T, H, E).total;
+}
+
+hipError_t launch_route_backward(const RouteBackward& r, hipStream_t stream) {
+  return r.bf16 ? launch_route_backward_t<GradBf16>(r, stream) : launch_route_backward_t<GradF32>(r, stream);
 }
 
 }  // namespace moe

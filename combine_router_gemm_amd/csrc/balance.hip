@@ -14,12 +14,13 @@
 #include "common.h"
 #include "kernels.h"
 #include "tiles.h"
+#include "topk.h"
 
 namespace moe {
 
 namespace {
 
-constexpr int NTH = 256;
+constexpr int NTH = 1024, NW = NTH / 64;
 
 struct BalanceArgs {
   const float* logits;
@@ -43,66 +44,95 @@ __device__ __forceinline__ void seq_range(const BalanceArgs& a, int s, int& begi
 }
 
 // Workgroup (split, s): the ids of one part of sequence s into LDS counters, and from there to the part's own place.
-__global__ __launch_bounds__(1024) void balance_count_kernel(BalanceArgs a) {
+__global__ __launch_bounds__(NTH) void balance_count_kernel(BalanceArgs a) {
   __shared__ int s_count[MOE_MAX_EXPERTS + 1];
   const int tid = threadIdx.x;
   if (blockIdx.x == 0 && blockIdx.y == 0 && tid == 0) *a.ticket = 0;
   for (int s = blockIdx.y; s < a.S; s += gridDim.y) {
-    for (int e = tid; e <= a.E; e += 1024) s_count[e] = 0;
+    for (int e = tid; e <= a.E; e += NTH) s_count[e] = 0;
     __syncthreads();
     int begin, end;
     seq_range(a, s, begin, end);
     const int64_t per = ((int64_t)(end - begin) + a.splits - 1) / a.splits;
     const int64_t t0 = begin + blockIdx.x * per, t1 = min((int64_t)end, t0 + per);
     int tokens = 0;
-    for (int64_t t = t0 + tid; t < t1; t += 1024) tokens += !a.mask || a.mask[t] != 0;
-    for (int64_t i = t0 * a.k + tid; i < t1 * a.k; i += 1024) {
-      const int e = a.ids[i];
-      if ((!a.mask || a.mask[(unsigned)i / (unsigned)a.k] != 0) && e >= 0 && e < a.E) atomicAdd(&s_count[e], 1);
+    for (int64_t t = t0 + tid; t < t1; t += NTH) tokens += !a.mask || a.mask[t] != 0;
+    for (int64_t i0 = t0 * a.k + tid; i0 < t1 * a.k; i0 += 8 * NTH) {  // eight loads in flight
+      int e[8];
+#pragma unroll
+      for (int q = 0; q < 8; ++q) {
+        const int64_t i = i0 + q * NTH;
+        const bool in = i < t1 * a.k;
+        e[q] = in ? a.ids[i] : -1;
+        if (a.mask && in && a.mask[(unsigned)i / (unsigned)a.k] == 0) e[q] = -1;
+      }
+#pragma unroll
+      for (int q = 0; q < 8; ++q)
+        if (e[q] >= 0 && e[q] < a.E) atomicAdd(&s_count[e[q]], 1);
     }
     if (tokens) atomicAdd(&s_count[a.E], tokens);
     __syncthreads();
     int* out = a.part + ((int64_t)s * a.splits + blockIdx.x) * (a.E + 1);
-    for (int e = tid; e <= a.E; e += 1024) out[e] = s_count[e];
+    for (int e = tid; e <= a.E; e += NTH) out[e] = s_count[e];
     __syncthreads();
   }
 }
 
-// Sum and maximum over a group of G lanes, in every lane, in a fixed order
+// Sum and maximum over a group of 4, 16 or 64 lanes, in every lane, in a fixed order (DPP within the 16 lanes of a row)
 template <int G>
 __device__ __forceinline__ float group_sum(float v) {
-#pragma unroll
-  for (int off = 1; off < G; off <<= 1) v += __shfl_xor(v, off, 64);
+  if constexpr (G == 64) return wave_sum(v);
+  v += dpp_f32<0xB1>(v);
+  v += dpp_f32<0x4E>(v);
+  if constexpr (G == 16) {
+    v += dpp_f32<0x141>(v);
+    v += dpp_f32<0x140>(v);
+  }
   return v;
 }
 template <int G>
 __device__ __forceinline__ float group_max(float v) {
-#pragma unroll
-  for (int off = 1; off < G; off <<= 1) v = fmaxf(v, __shfl_xor(v, off, 64));
+  if constexpr (G == 64) return wave_max(v);
+  v = fmaxf(v, dpp_f32<0xB1>(v));
+  v = fmaxf(v, dpp_f32<0x4E>(v));
+  if constexpr (G == 16) {
+    v = fmaxf(v, dpp_f32<0x141>(v));
+    v = fmaxf(v, dpp_f32<0x140>(v));
+  }
   return v;
+}
+
+// Entry e of sequence s over its parts, whose loads go out together (one after another they are 16 round trips: 7 us)
+constexpr int kMaxSplits = 16;
+__device__ __forceinline__ int part_sum(const BalanceArgs& a, int64_t s, int64_t e) {
+  int v[kMaxSplits], c = 0;
+#pragma unroll
+  for (int i = 0; i < kMaxSplits; ++i) v[i] = i < a.splits ? a.part[(s * a.splits + i) * (a.E + 1) + e] : 0;
+#pragma unroll
+  for (int i = 0; i < kMaxSplits; ++i) c += v[i];
+  return c;
 }
 
 // G lanes per token, NV vectors of VW logits per lane: lane i of the group holds logits (i + j G) VW .. of j < NV.
 // A workgroup takes `tokens` consecutive tokens; where they belong to several sequences it goes through these in turn, with
-// the sequence's f in LDS.
+// the sequence's f in LDS. A group loads U tokens at once: a large batch is one such round, and its loads are what it waits for
+// (one token after another: 30 us for 16384 x 256, 14 with four at once).
 template <int G, int VW, int NV>
 __global__ __launch_bounds__(NTH) void balance_rows_kernel(BalanceArgs a, int tokens) {
-  constexpr int TPP = NTH / G;  // tokens per pass
+  constexpr int TPP = NTH / G, U = NV > 2 ? 2 : 4;  // tokens per pass, passes at once
   __shared__ float s_f[MOE_MAX_EXPERTS];
-  __shared__ double s_sum[NTH / 64];
+  __shared__ double s_sum[NW];
   __shared__ int s_n, s_used, s_last;
   const int tid = threadIdx.x, gl = tid % G;
   const int t_begin = blockIdx.x * tokens, t_end = min(a.T, t_begin + tokens);
   // sequences with counted tokens
   if (tid == 0) s_used = 0;
   __syncthreads();
-  int used = 0;
-  for (int s = tid; s < a.S; s += NTH) {
-    int n = 0;
-    for (int i = 0; i < a.splits; ++i) n += a.part[((int64_t)s * a.splits + i) * (a.E + 1) + a.E];
-    used += n > 0;
+  if (a.S > 1) {
+    int used = 0;
+    for (int s = tid; s < a.S; s += NTH) used += part_sum(a, s, a.E) > 0;
+    if (used) atomicAdd(&s_used, used);
   }
-  if (used) atomicAdd(&s_used, used);
   // the sequence of the first token: the last one that begins at or before it
   int s = 0;
   for (int hi = a.S; hi - s > 1;) {
@@ -126,8 +156,7 @@ __global__ __launch_bounds__(NTH) void balance_rows_kernel(BalanceArgs a, int to
       __syncthreads();  // s_f has been read
       if (in) {
         for (int e = tid; e <= a.E; e += NTH) {
-          int c = 0;
-          for (int i = 0; i < a.splits; ++i) c += a.part[((int64_t)s * a.splits + i) * (a.E + 1) + e];
+          const int c = part_sum(a, s, e);
           if (e < a.E) s_f[e] = (float)c;
           else s_n = c;
         }
@@ -135,7 +164,7 @@ __global__ __launch_bounds__(NTH) void balance_rows_kernel(BalanceArgs a, int to
       __syncthreads();
       const int n = in ? s_n : 0;
       const float unit = n > 0 ? 1.f / ((float)a.k * (float)n) : 0.f;
-      const float factor = n > 0 ? a.weight * (float)a.E / ((float)n * (float)s_used) : 0.f;
+      const float factor = n > 0 ? a.weight * (float)a.E / ((float)n * (float)(a.S > 1 ? s_used : 1)) : 0.f;
       float f[NV][VW];
 #pragma unroll
       for (int j = 0; j < NV; ++j)
@@ -144,50 +173,62 @@ __global__ __launch_bounds__(NTH) void balance_rows_kernel(BalanceArgs a, int to
           const int e = (gl + j * G) * VW + q;
           f[j][q] = n > 0 && e < a.E ? s_f[e] * unit : 0.f;
         }
-      for (int t = t0 + tid / G; t < t1; t += TPP) {
-        const bool live = n > 0 && (!a.mask || a.mask[t] != 0);
-        const float* row = a.logits + (int64_t)t * a.E;
-        float x[NV][VW], m = -INFINITY;
+      for (int tu = t0 + tid / G; tu < t1; tu += TPP * U) {
+        float x[U][NV][VW];
+        bool live[U];
 #pragma unroll
-        for (int j = 0; j < NV; ++j) {
-          const int e = (gl + j * G) * VW;
-          if constexpr (VW == 4) {
-            u32x4 v{0xff800000u, 0xff800000u, 0xff800000u, 0xff800000u};
-            if (live && e < a.E) v = ld16_nt(row + e);
-            unpack(v, x[j]);
-          } else {
-            x[j][0] = live && e < a.E ? row[e] : -INFINITY;
-          }
-#pragma unroll
-          for (int q = 0; q < VW; ++q) m = fmaxf(m, x[j][q]);
-        }
-        m = group_max<G>(m);
-        const float base = m == -INFINITY ? 0.f : m;  // every logit -inf: p is 0 and the token adds nothing
-        float z = 0.f, d = 0.f;
-#pragma unroll
-        for (int j = 0; j < NV; ++j)
-#pragma unroll
-          for (int q = 0; q < VW; ++q) {
-            x[j][q] = expf(x[j][q] - base);
-            z += x[j][q];
-            d = fmaf(x[j][q], f[j][q], d);
-          }
-        z = group_sum<G>(z);
-        d = group_sum<G>(d);
-        const float iz = z > 0.f ? 1.f / z : z == 0.f ? 0.f : z;  // NaN stays NaN
-        const float dot = d * iz;
-        if (gl == 0 && live) sum += (double)(factor * dot);
-        if (a.d_logits) {
-          float* out = a.d_logits + (int64_t)t * a.E;
+        for (int u = 0; u < U; ++u) {
+          const int t = tu + u * TPP;
+          live[u] = n > 0 && t < t1 && (!a.mask || a.mask[t] != 0);
+          const float* row = a.logits + (int64_t)t * a.E;
 #pragma unroll
           for (int j = 0; j < NV; ++j) {
             const int e = (gl + j * G) * VW;
-            if (e < a.E) {
-              float o[VW];
+            if constexpr (VW == 4) {
+              u32x4 v{0xff800000u, 0xff800000u, 0xff800000u, 0xff800000u};
+              if (live[u] && e < a.E) v = ld16_nt(row + e);
+              unpack(v, x[u][j]);
+            } else {
+              x[u][j][0] = live[u] && e < a.E ? row[e] : -INFINITY;
+            }
+          }
+        }
 #pragma unroll
-              for (int q = 0; q < VW; ++q) o[q] = live ? factor * (x[j][q] * iz) * (f[j][q] - dot) : 0.f;
-              if constexpr (VW == 4) st16_nt(out + e, pack(o));
-              else out[e] = o[0];
+        for (int u = 0; u < U; ++u) {
+          const int t = tu + u * TPP;
+          float m = -INFINITY;
+#pragma unroll
+          for (int j = 0; j < NV; ++j)
+#pragma unroll
+            for (int q = 0; q < VW; ++q) m = fmaxf(m, x[u][j][q]);
+          m = group_max<G>(m);
+          const float base = m == -INFINITY ? 0.f : m;  // every logit -inf: p is 0 and the token adds nothing
+          float z = 0.f, d = 0.f;
+#pragma unroll
+          for (int j = 0; j < NV; ++j)
+#pragma unroll
+            for (int q = 0; q < VW; ++q) {
+              x[u][j][q] = expf(x[u][j][q] - base);
+              z += x[u][j][q];
+              d = fmaf(x[u][j][q], f[j][q], d);
+            }
+          z = group_sum<G>(z);
+          d = group_sum<G>(d);
+          const float iz = z > 0.f ? 1.f / z : z == 0.f ? 0.f : z;  // NaN stays NaN
+          const float dot = d * iz;
+          if (gl == 0 && live[u]) sum += (double)(factor * dot);
+          if (a.d_logits && t < t1) {
+            float* out = a.d_logits + (int64_t)t * a.E;
+#pragma unroll
+            for (int j = 0; j < NV; ++j) {
+              const int e = (gl + j * G) * VW;
+              if (e < a.E) {
+                float o[VW];
+#pragma unroll
+                for (int q = 0; q < VW; ++q) o[q] = live[u] ? factor * (x[u][j][q] * iz) * (f[j][q] - dot) : 0.f;
+                if constexpr (VW == 4) st16_nt(out + e, pack(o));
+                else out[e] = o[0];
+              }
             }
           }
         }
@@ -198,10 +239,8 @@ __global__ __launch_bounds__(NTH) void balance_rows_kernel(BalanceArgs a, int to
   }
   // counts of the whole batch, a slice per workgroup
   for (int64_t i = (int64_t)blockIdx.x * NTH + tid; i < (int64_t)a.S * a.E; i += (int64_t)gridDim.x * NTH) {
-    const int64_t sq = i / a.E, e = i - sq * a.E;
-    int c = 0;
-    for (int p = 0; p < a.splits; ++p) c += a.part[(sq * a.splits + p) * (a.E + 1) + e];
-    a.count[i] = c;
+    const int64_t sq = i / a.E;
+    a.count[i] = part_sum(a, sq, i - sq * a.E);
   }
   // the workgroup's partial, at agent scope; the last workgroup to have stored its own adds them all
 #pragma unroll
@@ -210,7 +249,7 @@ __global__ __launch_bounds__(NTH) void balance_rows_kernel(BalanceArgs a, int to
   __syncthreads();
   if (tid == 0) {
     double v = 0.0;
-    for (int w = 0; w < NTH / 64; ++w) v += s_sum[w];
+    for (int w = 0; w < NW; ++w) v += s_sum[w];
     __hip_atomic_store(&a.partial[blockIdx.x], v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
     // an agent-scope store writes through to where every XCD reads it: its acknowledgement is all the order it needs, and
     // a fence's write-back of the L2 would flush the gradients as well
@@ -228,15 +267,15 @@ __global__ __launch_bounds__(NTH) void balance_rows_kernel(BalanceArgs a, int to
   __syncthreads();
   if (tid == 0) {
     v = 0.0;
-    for (int w = 0; w < NTH / 64; ++w) v += s_sum[w];
+    for (int w = 0; w < NW; ++w) v += s_sum[w];
     *a.loss = (float)v;
   }
 }
 
-// Tokens per workgroup of balance_rows: enough workgroups for every CU, at most kMaxGroups partials
-constexpr int kMaxGroups = 2048;
+// Tokens per workgroup of balance_rows: a workgroup for every CU. More of them would queue for the one ticket.
+constexpr int kMaxGroups = 256;
 int rows_per_group(int T) { return std::max(16, ceil_div_host(T, kMaxGroups)); }
-int count_splits(int T, int S) { return std::max(1, std::min(16 / S, T / 256)); }
+int count_splits(int T, int S) { return std::max(1, std::min(kMaxSplits / S, T / 256)); }
 
 }  // namespace
 
@@ -267,7 +306,7 @@ hipError_t launch_balance(const float* logits, const int* ids, const int* seq_of
   a.loss = loss;
   a.count = count;
   a.d_logits = d_logits;
-  balance_count_kernel<<<dim3(a.splits, std::min(S, 65535)), 1024, 0, stream>>>(a);
+  balance_count_kernel<<<dim3(a.splits, std::min(S, 65535)), NTH, 0, stream>>>(a);
   const hipError_t st = hipGetLastError();
   if (st != hipSuccess) return st;
 #define MOE_BALANCE(G, VW, NV) balance_rows_kernel<G, VW, NV><<<groups, NTH, 0, stream>>>(a, tokens)

@@ -552,7 +552,8 @@ size_t moe_route_backward_workspace_bytes(int T, int H, int E, moe_dtype_t xdt);
  *   d_logits     [T, E] fp32 (output); may be d_logits_in itself
  *   d_x          [T, H] (xdt), d_w_router [E, H] fp32, d_bias [E] fp32: outputs, each may be NULL
  *   workspace    device scratch of at least moe_route_backward_workspace_bytes(T, H, E, xdt) bytes
- * Requires H % 8 == 0 and T * E < 2^31 (else MOE_ERR_UNSUPPORTED). T == 0 writes zeros to d_w_router and d_bias.
+ * Requires H % 8 == 0, H <= 2^21 and T * E < 2^31 (else MOE_ERR_UNSUPPORTED). T == 0 writes zeros to d_w_router and
+ * d_bias.
  */
 int moe_route_backward(const void* x, moe_dtype_t xdt, const float* w_router, const int32_t* topk_ids,
                        const float* topk_w, const float* d_topk_w, const float* d_logits_in, int T, int H, int E, int k,

@@ -62,8 +62,11 @@ def combine_backward(dy, out, pair_row, w):
 
 
 def route_backward(x, wr, ids, w, d_w, d_in, split):
-    """Gradients of the router in float64: each with its bound. split: x is bf16, and d_x takes its operands in two bf16 parts,
-    each off by at most 2^-16, without the product of the two second parts, another 2^-16."""
+    """Gradients of the router in float64: each with its bound. split: x is bf16, and d_x takes its operands in fp16, scaled by
+    a power of two for each token of d_logits and each column of the weight that puts the largest value into [2^14, 2^15). Half
+    a step of fp16 is 2^-11 of a value down to 2^-14, and 2^-25 below, which is 2^-39 of that largest value at most. So with
+    a' = a (1 + d) + s, |d| <= 2^-11, |s| <= 2^-39 max|a|, and b' alike, |a' b' - a b| is at most
+    (2^-10 + 2^-22) |a b| + 1.01 (|s_a| |b| + |s_b| |a|) + |s_a s_b|."""
     T, H = x.shape
     E = wr.shape[0]
     dl = torch.zeros(T, E, dtype=torch.float64) if d_in is None else d_in.clone()
@@ -80,9 +83,13 @@ def route_backward(x, wr, ids, w, d_w, d_in, split):
                     dl[t, ids[t, j]] += c[t, j]
                     db[t, ids[t, j]] += e[t, j]
         db += (k + 1) * U * (dl.abs() + db)
-    part = 3.1 * 2.0 ** -16 if split else 0.0
+    part = 2.0 ** -10 + 2.0 ** -22 if split else 0.0
     d_x = dl @ wr
     bx = ((E + 2) * U + part) * ((dl.abs() + db) @ wr.abs()) + db @ wr.abs()
+    if split and T:
+        low = 2.0 ** -39
+        sa, sb = low * (dl.abs() + db).amax(1, keepdim=True), low * wr.abs().amax(0, keepdim=True)
+        bx = bx + 1.01 * (sa * wr.abs().sum(0) + sb * (dl.abs() + db).sum(1, keepdim=True)) + E * sa * sb
     d_wr = dl.T @ x
     bw = (T + 2) * U * ((dl.abs() + db).T @ x.abs()) + db.T @ x.abs()
     return dict(d_logits=(dl, db), d_x=(d_x, bx), d_w_router=(d_wr, bw),

@@ -69,6 +69,7 @@ def test_route_backward_refusals(lib):
     assert call(H=0) == INVALID
     assert call(H=60) == UNSUPPORTED
     assert call(T=1 << 28, E=8) == UNSUPPORTED
+    assert call(H=(1 << 21) + 8) == UNSUPPORTED
     assert call(dl=None) == INVALID
     assert call(dw=None, di=None) == INVALID         # no gradient at all
     assert call(ids=None) == INVALID
