@@ -25,7 +25,7 @@ __all__ = ["MOE_F32", "MOE_BF16", "MOE_FP8_BLOCK", "MoeError", "Layout", "librar
            "moe_w4_codes_bytes", "moe_w4_scales_bytes", "moe_quantize_w4", "moe_dequantize_w4", "moe_expert_mlp_w4",
            "moe_expert_mlp_w4_workspace_bytes", "moe_expert_mlp_w4_tiling", "moe_layer_decode", "moe_layer_decode_w4",
            "moe_layer_decode_workspace_bytes", "moe_quantize_i8", "moe_dequantize_i8", "moe_dispatch_i8",
-           "moe_expert_mlp_i8", "moe_expert_mlp_i8_workspace_bytes", "moe_balance_loss",
+           "moe_expert_mlp_i8", "moe_expert_mlp_i8_workspace_bytes", "moe_expert_mlp_i8_tiling", "moe_balance_loss",
            "moe_balance_loss_workspace_bytes", "moe_combine_backward", "moe_route_backward",
            "moe_route_backward_workspace_bytes",
            "moe_expert_mlp_combine_workspace_bytes", "moe_rows_max", "moe_route_workspace_bytes", "moe_dispatch_workspace_bytes",
@@ -50,7 +50,7 @@ EXPORTED_SYMBOLS = ("moe_status_string", "moe_rows_max", "moe_route_workspace_by
                     "moe_expert_mlp_w4",
                     "moe_layer_decode_workspace_bytes", "moe_layer_decode", "moe_layer_decode_w4", "moe_quantize_i8",
                     "moe_dequantize_i8", "moe_dispatch_i8", "moe_expert_mlp_i8_workspace_bytes", "moe_expert_mlp_i8",
-                    "moe_balance_loss_workspace_bytes", "moe_balance_loss", "moe_combine_backward",
+                    "moe_expert_mlp_i8_tiling", "moe_balance_loss_workspace_bytes", "moe_balance_loss", "moe_combine_backward",
                     "moe_route_backward_workspace_bytes", "moe_route_backward")
 
 
@@ -143,6 +143,8 @@ def load_library():
     lib.moe_dispatch_i8.restype = i32
     lib.moe_expert_mlp_i8_workspace_bytes.argtypes = [i32] * 7
     lib.moe_expert_mlp_i8_workspace_bytes.restype = sz
+    lib.moe_expert_mlp_i8_tiling.argtypes = [i32] * 7 + [ctypes.POINTER(ctypes.c_int)] * 3
+    lib.moe_expert_mlp_i8_tiling.restype = i32
     lib.moe_expert_mlp_i8.argtypes = [vp, vp, ctypes.POINTER(_CLayout), vp, vp, vp, vp, i32, vp, vp, sz, vp]
     lib.moe_expert_mlp_i8.restype = i32
     lib.moe_balance_loss_workspace_bytes.argtypes = [i32, i32, i32]
@@ -269,6 +271,13 @@ def moe_layer_decode_workspace_bytes(T: int, H: int, E: int, k: int, F: int, xdt
 
 def moe_expert_mlp_i8_workspace_bytes(T: int, k: int, E: int, R: int, C: int, H: int, F: int) -> int:
     return int(load_library().moe_expert_mlp_i8_workspace_bytes(T, k, E, R, C, H, F))
+
+
+def moe_expert_mlp_i8_tiling(T: int, k: int, E: int, R: int, C: int, H: int, F: int) -> tuple:
+    """(rows per tile, parts of the gate/up pass, parts of the down pass) that moe_expert_mlp_i8 takes for these sizes."""
+    n = [ctypes.c_int() for _ in range(3)]
+    _check(load_library().moe_expert_mlp_i8_tiling(T, k, E, R, C, H, F, *map(ctypes.byref, n)), "moe_expert_mlp_i8_tiling")
+    return tuple(v.value for v in n)
 
 
 def moe_balance_loss_workspace_bytes(T: int, E: int, S: int) -> int:

@@ -538,6 +538,22 @@ size_t moe_expert_mlp_i8_workspace_bytes(int T, int k, int E, int R, int C, int 
   return moe::mlp_i8_workspace_bytes(rows, E / R, H, F);
 }
 
+int moe_expert_mlp_i8_tiling(int T, int k, int E, int R, int C, int H, int F, int* tile_rows, int* gate_up_parts,
+                             int* down_parts) {
+  if (T < 0 || C < 0 || E < 1 || E > MOE_MAX_EXPERTS || R < 1 || E % R != 0 || k < 1 || k > MOE_MAX_TOPK || k > E ||
+      H < 1 || !tile_rows || !gate_up_parts || !down_parts)
+    return MOE_ERR_INVALID;
+  if ((int64_t)T * k > (int64_t)INT32_MAX) return MOE_ERR_UNSUPPORTED;
+  const int64_t rows = moe_rows_max(T, k, E, C);
+  const int st = check_i8_widths(rows, H, F);
+  if (st != MOE_OK) return st;
+  const moe::I8Tiling t = moe::mlp_i8_tiling(rows, E / R, H, F);
+  *tile_rows = t.rows;
+  *gate_up_parts = t.gu_parts;
+  *down_parts = t.dn_parts;
+  return MOE_OK;
+}
+
 int moe_expert_mlp_i8(const int8_t* send_q, const float* send_scale, const moe_layout_t* layout, const int8_t* gu_codes,
                       const float* gu_scales, const int8_t* dn_codes, const float* dn_scales, int F, void* out_buf,
                       void* workspace, size_t workspace_bytes, hipStream_t stream) {

@@ -316,14 +316,13 @@ __global__ __launch_bounds__(SCATTER_WAVES * 64) void dispatch_scatter_kernel(
 // LDS), workgroup 0 writes count / kept / overflow / offsets, and then each wave scatters one token as
 // dispatch_scatter does. This saves a launch and its dependent global round trips on decode batches.
 //
-// dispatch_small_rows: all of that but the scatter. Returns the token of this wave, with `row` as resolve_pair_row gives
-// it, or -1 for a wave without one.
+// dispatch_small_rows: all of that but the scatter. The row of pair (t, lane) for lanes < k, as resolve_pair_row gives it, with
+// the layout entries written when `write` is set; -1 for a t past the batch.
 __device__ __forceinline__ int dispatch_small_rows(const int* __restrict__ ids, int T_, int k, int E, int C,
                                                    int* __restrict__ count, int* __restrict__ kept,
                                                    int* __restrict__ overflow, int* __restrict__ offset,
                                                    int* __restrict__ row_token, int* __restrict__ row_slot,
-                                                   int* __restrict__ pair_row, int& row) {
-  static_assert(DR_THREADS == SCATTER_WAVES * 64, "one wave per token");
+                                                   int* __restrict__ pair_row, int t, bool write) {
   __shared__ int cnt[DR_WAVES][MOE_MAX_EXPERTS];
   __shared__ int s_tot[MOE_MAX_EXPERTS];
   __shared__ int s_off[MOE_MAX_EXPERTS];
@@ -348,20 +347,21 @@ __device__ __forceinline__ int dispatch_small_rows(const int* __restrict__ ids, 
     }
   }
   __syncthreads();
-  const int t = blockIdx.x * SCATTER_WAVES + wave;
-  row = -1;
-  if (t >= T_) return -1;
+  int row = -1;
+  if (t >= T_) return row;
   if (lane < k) {
     const int p = t * k + lane;
     const int e = s_exp[p], pos = s_pos[p];
     if (e >= 0 && pos < C) row = s_off[e] + pos;
-    pair_row[p] = row;
-    if (row >= 0) {
-      row_token[row] = t;
-      row_slot[row] = lane;
+    if (write) {
+      pair_row[p] = row;
+      if (row >= 0) {
+        row_token[row] = t;
+        row_slot[row] = lane;
+      }
     }
   }
-  return t;
+  return row;
 }
 
 template <typename T, int VPL>
@@ -369,9 +369,11 @@ __global__ __launch_bounds__(DR_THREADS) void dispatch_small_kernel(
     const T* __restrict__ x, const int* __restrict__ ids, int T_, int H, int k, int E, int C, int* __restrict__ count,
     int* __restrict__ kept, int* __restrict__ overflow, int* __restrict__ offset, int* __restrict__ row_token,
     int* __restrict__ row_slot, int* __restrict__ pair_row, T* __restrict__ send_buf) {
-  int row;
-  const int t = dispatch_small_rows(ids, T_, k, E, C, count, kept, overflow, offset, row_token, row_slot, pair_row, row);
-  if (t >= 0) copy_token_row<T, VPL>(x, t, H, row, send_buf);
+  static_assert(DR_THREADS == SCATTER_WAVES * 64, "one wave per token");
+  const int t = blockIdx.x * SCATTER_WAVES + (int)(threadIdx.x >> 6);
+  const int row =
+      dispatch_small_rows(ids, T_, k, E, C, count, kept, overflow, offset, row_token, row_slot, pair_row, t, true);
+  if (t < T_) copy_token_row<T, VPL>(x, t, H, row, send_buf);
 }
 
 template <typename T, int VPL>
@@ -469,80 +471,83 @@ __global__ __launch_bounds__(SCATTER_WAVES * 64) void dispatch_scatter_fp8_kerne
 }
 
 // ---- int8 rows ----
-// One wave quantises token row t of x (i8.h) and stores codes and scale to its kept rows (lane j < k holds the row of
-// pair (t, j), -1 if dropped). Up to VPL 16-byte slices per lane stay in registers between the row's maximum and its codes;
-// what a longer row has beyond them is read twice.
-template <int VPL>
+// One workgroup quantises token row t of x (i8.h) and stores codes and scale to its kept rows (lane j < k of every wave holds
+// the row of pair (t, j), -1 if dropped). Up to VPT 16-byte slices per thread stay in registers between the row's maximum and
+// its codes; what a longer row has beyond them is read twice. A wave per token took 22 us where this takes 10 (128 tokens,
+// H 7168), and 61 against 58 for 4096 tokens.
+template <int VPT>
 __device__ __forceinline__ void quantize_token_row(const bf16_t* __restrict__ x, int t, int H, int row,
                                                    int8_t* __restrict__ send_q, float* __restrict__ send_scale) {
-  const int lane = lane_id();
+  __shared__ uint32_t s_top[DR_WAVES];
+  const int tid = threadIdx.x;
   const uint64_t kept = __ballot(row >= 0);
-  if (kept == 0) return;
+  if (kept == 0) return;  // the same in every wave
   const int nvec = H / 8;
   const bf16_t* src = x + (int64_t)t * H;
-  u32x4 val[VPL];
+  u32x4 val[VPT];
   uint32_t top = 0;
 #pragma unroll
-  for (int i = 0; i < VPL; ++i) {
-    const int v = lane + i * 64;
+  for (int i = 0; i < VPT; ++i) {
+    const int v = tid + i * DR_THREADS;
     val[i] = v < nvec ? ld16(src + (int64_t)v * 8) : u32x4{0u, 0u, 0u, 0u};
   }
 #pragma unroll
-  for (int i = 0; i < VPL; ++i) {
+  for (int i = 0; i < VPT; ++i) {
     float f[8];
     unpack(val[i], f);
     top = abs_top(f, top);
   }
-  for (int v = VPL * 64 + lane; v < nvec; v += 64) {
+  for (int v = VPT * DR_THREADS + tid; v < nvec; v += DR_THREADS) {
     float f[8];
     unpack(ld16(src + (int64_t)v * 8), f);
     top = abs_top(f, top);
   }
-  const I8Row r = i8_row(wave_top(top));
-  if (row >= 0) send_scale[row] = r.scale;
-  for (int base = 0; base < nvec; base += 64 * VPL) {
-    uint32_t q[VPL][2];
+  top = wave_top(top);
+  if ((tid & 63) == 0) s_top[tid >> 6] = top;
+  __syncthreads();
 #pragma unroll
-    for (int i = 0; i < VPL; ++i) {
-      const int v = base + lane + i * 64;
-      if (base > 0 && v < nvec) val[i] = ld16(src + (int64_t)v * 8);
-      float f[8];
-      unpack(val[i], f);
-      i8_codes(f, r, q[i]);
-    }
-    for (uint64_t m = kept; m; m &= m - 1) {
-      int8_t* dst = send_q + (int64_t)__shfl(row, __builtin_ctzll(m), 64) * H;
+  for (int i = 0; i < DR_WAVES; ++i) top = max(top, s_top[i]);
+  const I8Row r = i8_row(top);
+  if (tid < 64 && row >= 0) send_scale[row] = r.scale;
+  auto put = [&](u32x4 raw, int v) {
+    float f[8];
+    uint32_t q[2];
+    unpack(raw, f);
+    i8_codes(f, r, q);
+    for (uint64_t m = kept; m; m &= m - 1)
+      *reinterpret_cast<u32x2*>(send_q + (int64_t)__builtin_amdgcn_readlane(row, __builtin_ctzll(m)) * H + (int64_t)v * 8) =
+          u32x2{q[0], q[1]};
+  };
 #pragma unroll
-      for (int i = 0; i < VPL; ++i) {
-        const int v = base + lane + i * 64;
-        if (v < nvec) *reinterpret_cast<u32x2*>(dst + (int64_t)v * 8) = u32x2{q[i][0], q[i][1]};
-      }
-    }
+  for (int i = 0; i < VPT; ++i) {
+    const int v = tid + i * DR_THREADS;
+    if (v < nvec) put(val[i], v);
   }
+  for (int v = VPT * DR_THREADS + tid; v < nvec; v += DR_THREADS) put(ld16(src + (int64_t)v * 8), v);
 }
 
-template <int VPL>
-__global__ __launch_bounds__(SCATTER_WAVES * 64) void dispatch_scatter_i8_kernel(
+template <int VPT>
+__global__ __launch_bounds__(DR_THREADS) void dispatch_scatter_i8_kernel(
     const bf16_t* __restrict__ x, const int* __restrict__ ids, int T_, int H, int k, int E, int C,
     const int* __restrict__ blk_base, const int* __restrict__ pair_local, const int* __restrict__ offset,
     int* __restrict__ row_token, int* __restrict__ row_slot, int* __restrict__ pair_row, int8_t* __restrict__ send_q,
     float* __restrict__ send_scale) {
-  const int t = blockIdx.x * SCATTER_WAVES + (int)(threadIdx.x >> 6);
-  if (t >= T_) return;
-  const int row =
-      resolve_pair_row(t, lane_id(), ids, k, E, C, blk_base, pair_local, offset, row_token, row_slot, pair_row);
-  quantize_token_row<VPL>(x, t, H, row, send_q, send_scale);
+  const int t = blockIdx.x;
+  const int row = resolve_pair_row(t, lane_id(), ids, k, E, C, blk_base, pair_local, offset, row_token, row_slot, pair_row,
+                                   threadIdx.x < 64);
+  quantize_token_row<VPT>(x, t, H, row, send_q, send_scale);
 }
 
-template <int VPL>
+template <int VPT>
 __global__ __launch_bounds__(DR_THREADS) void dispatch_small_i8_kernel(
     const bf16_t* __restrict__ x, const int* __restrict__ ids, int T_, int H, int k, int E, int C,
     int* __restrict__ count, int* __restrict__ kept, int* __restrict__ overflow, int* __restrict__ offset,
     int* __restrict__ row_token, int* __restrict__ row_slot, int* __restrict__ pair_row, int8_t* __restrict__ send_q,
     float* __restrict__ send_scale) {
-  int row;
-  const int t = dispatch_small_rows(ids, T_, k, E, C, count, kept, overflow, offset, row_token, row_slot, pair_row, row);
-  if (t >= 0) quantize_token_row<VPL>(x, t, H, row, send_q, send_scale);
+  const int t = blockIdx.x;
+  const int row = dispatch_small_rows(ids, T_, k, E, C, count, kept, overflow, offset, row_token, row_slot, pair_row, t,
+                                      threadIdx.x < 64);
+  quantize_token_row<VPT>(x, t, H, row, send_q, send_scale);
 }
 
 }  // namespace
@@ -628,15 +633,14 @@ hipError_t launch_dispatch_fp8(const void* x, const int* ids, const moe_layout_t
 hipError_t launch_dispatch_i8(const void* x, const int* ids, const moe_layout_t& L, int8_t* send_q, float* send_scale,
                               int* blk_count, int* pair_local, hipStream_t stream) {
   const int nvec = L.H / 8;
-  const unsigned blocks = (unsigned)ceil_div_host(L.T, SCATTER_WAVES);
   const bf16_t* xp = static_cast<const bf16_t*>(x);
 #define MOE_PER_WIDTH(GO)     \
-  if (nvec > 256) GO(16);     \
-  else if (nvec > 64) GO(4);  \
+  if (nvec > 512) GO(4);      \
+  else if (nvec > 256) GO(2); \
   else GO(1)
   if (L.T > 0 && dispatch_num_blocks(L.T) == 1) {  // one launch: every workgroup ranks the whole batch
-#define MOE_SMALL_I8(VPL)                                                                                      \
-  dispatch_small_i8_kernel<VPL><<<blocks, DR_THREADS, 0, stream>>>(xp, ids, L.T, L.H, L.k, L.E, L.C, L.expert_count, \
+#define MOE_SMALL_I8(VPT)                                                                                      \
+  dispatch_small_i8_kernel<VPT><<<L.T, DR_THREADS, 0, stream>>>(xp, ids, L.T, L.H, L.k, L.E, L.C, L.expert_count, \
                                                                    L.expert_kept, L.expert_overflow,           \
                                                                    L.expert_offset, L.row_token, L.row_slot,   \
                                                                    L.pair_row, send_q, send_scale)
@@ -646,8 +650,8 @@ hipError_t launch_dispatch_i8(const void* x, const int* ids, const moe_layout_t&
   }
   const hipError_t st = launch_counts(ids, L, blk_count, pair_local, stream);
   if (st != hipSuccess || L.T == 0) return st;
-#define MOE_SCATTER_I8(VPL)                                                                                      \
-  dispatch_scatter_i8_kernel<VPL><<<blocks, SCATTER_WAVES * 64, 0, stream>>>(xp, ids, L.T, L.H, L.k, L.E, L.C, blk_count, \
+#define MOE_SCATTER_I8(VPT)                                                                                      \
+  dispatch_scatter_i8_kernel<VPT><<<L.T, DR_THREADS, 0, stream>>>(xp, ids, L.T, L.H, L.k, L.E, L.C, blk_count, \
                                                                              pair_local, L.expert_offset, L.row_token, \
                                                                              L.row_slot, L.pair_row, send_q, send_scale)
   MOE_PER_WIDTH(MOE_SCATTER_I8);

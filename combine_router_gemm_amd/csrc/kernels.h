@@ -95,6 +95,11 @@ hipError_t launch_dequantize_i8(const int8_t* codes, const float* scales, int64_
 hipError_t launch_dispatch_i8(const void* x, const int* ids, const moe_layout_t& L, int8_t* send_q, float* send_scale,
                               int* blk_count, int* pair_local, hipStream_t stream);
 bool mlp_i8_fits(int64_t rows, int H, int F);
+// what a call is cut into: rows per tile, parts of each pass's K
+struct I8Tiling {
+  int rows, gu_parts, dn_parts;
+};
+I8Tiling mlp_i8_tiling(int64_t rows, int El, int H, int F);
 size_t mlp_i8_workspace_bytes(int64_t rows, int El, int H, int F);
 hipError_t launch_expert_mlp_i8(const int8_t* send_q, const float* send_scale, const moe_layout_t& L,
                                 const int8_t* gu_codes, const float* gu_scales, const int8_t* dn_codes,

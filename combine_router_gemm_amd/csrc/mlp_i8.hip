@@ -8,8 +8,10 @@
 // would move codes over their borders, which a row's maximum, known only after the whole pass, decides.
 //
 //   i8_gemm_kernel  rows and weight rows go to LDS directly, in stages of 128 k (128 bytes of a row: whole cache lines), NS
-//                   stages in flight.
+//                   stages in flight; 32- and 64-row tiles stream the weights of experts with few rows and are bound by their
+//                   bytes, 128- and 256-row ones by the matrix units and the power that they draw.
 #include <algorithm>
+#include <type_traits>
 
 #include "common.h"
 #include "i8.h"
@@ -35,9 +37,12 @@ struct I8Args {
   int h_tiles;
   bf16_t* out;           // down: [., N]
   const int* out_perm;   // down: destination row of a plan row
-  const int* plan;
+  // row_start [El + 1]: first plan row of each expert, the last entry all rows. tile_start [El + 1]: first tile of BM rows, or
+  // nullptr: each workgroup counts the tiles itself
+  const int* row_start;
+  const int* tile_start;
   int El;
-  // SPLIT: K in `split` parts of split_stages stages each, their int32 sums to partial [split, rows, N]
+  // SPLIT: K in `split` parts of split_stages stages each, their int32 sums to partial [split, rows, w_rows]
   int split, split_stages;
   int* partial;
   int64_t partial_stride;  // elements of one part
@@ -50,10 +55,13 @@ __device__ __forceinline__ float silu(float g) { return g / (1.0f + expf(-g)); }
 __device__ __forceinline__ int swizzle(int r) { return (r >> 1) & 7; }
 
 // BM rows x BN weight rows per tile (gate/up: the gate and the up rows of BN / 2 columns), WM x WN waves.
-template <typename Op, int BM, int BN, int WM, int WN, int NS, int PER_CU, bool GATED, bool SPLIT = false>
+// PP: eight waves in two groups, one of each on every SIMD, that run the same sequence (read half a stage of fragments,
+// barrier, multiply them, barrier) one barrier apart: while one group reads and loads the other keeps the matrix units busy.
+// SPLIT: K cut over workgroups, where the tiles are few (see i8_plan).
+template <typename Op, int BM, int BN, int WM, int WN, int NS, int PER_CU, bool PP, bool GATED, bool SPLIT = false>
 __global__ __launch_bounds__(WM * WN * 64, PER_CU * WM * WN / 4 > 1 ? PER_CU * WM * WN / 4 : 1) void i8_gemm_kernel(
     I8Args a, int a_bytes) {
-  static_assert(!SPLIT || !GATED, "the gate/up pass is not split");
+  static_assert(!PP || (NS == 2 && WM * WN == 8 && !SPLIT), "ping-pong");
   constexpr int S = Op::S, NW = WM * WN, NTH = NW * 64, ROWB = 128, RPI = 8;
   constexpr int STAGE = (BM + BN) * ROWB, A_INS = BM / RPI, LPW = (BM + BN) / RPI / NW;
   static_assert((BM + BN) / RPI % NW == 0, "wave loads must split evenly");
@@ -80,12 +88,31 @@ __global__ __launch_bounds__(WM * WN * 64, PER_CU * WM * WN / 4 > 1 ? PER_CU * W
   int fr = lane % S, fq = lane / S;
   const int K = a.K, nk = (K + ROWB - 1) / ROWB;
   for (int i = tid; i <= a.El; i += NTH) {
-    row_start[i] = a.plan[2 + i];
-    tile_start[i] = a.plan[3 + a.El + i];
+    row_start[i] = a.row_start[i];
+    if (a.tile_start) tile_start[i] = a.tile_start[i];
   }
   const int n_tiles = (a.N + OUTC - 1) / OUTC;
-  lds_barrier();
-  const Tiles mine = my_tiles(a.plan[0] * n_tiles * (SPLIT ? a.split : 1));
+  __syncthreads();
+  if (!a.tile_start) {
+    if (wave == 0) {  // an exclusive scan of the experts' tiles, 64 at a time
+      int before = 0;
+      for (int i0 = 0; i0 < a.El; i0 += 64) {
+        const int i = i0 + lane;
+        const int n = i < a.El ? (row_start[i + 1] - row_start[i] + BM - 1) / BM : 0;
+        int sum = n;
+#pragma unroll
+        for (int off = 1; off < 64; off <<= 1) {
+          const int up = __shfl_up(sum, off, 64);
+          if (lane >= off) sum += up;
+        }
+        if (i < a.El) tile_start[i] = before + sum - n;
+        before += __shfl(sum, 63, 64);
+      }
+      if (lane == 0) tile_start[a.El] = before;
+    }
+    __syncthreads();
+  }
+  const Tiles mine = my_tiles(__builtin_amdgcn_readfirstlane(tile_start[a.El]) * n_tiles * (SPLIT ? a.split : 1));
   const __amdgpu_buffer_rsrc_t a_rsrc = __builtin_amdgcn_make_buffer_rsrc((void*)a.A, (short)0, a_bytes, 0x00020000);
   int l = 0;
   for (int unit = mine.begin; unit < mine.end; unit += mine.step) {
@@ -178,13 +205,63 @@ __global__ __launch_bounds__(WM * WN * 64, PER_CU * WM * WN / 4 > 1 ? PER_CU * W
       }
     };
     wait_loads<0>();  // the scale and row lookups: the waits below count stage loads only
+    if constexpr (PP) {
+      constexpr int KPH = 2, PHASES = KSTEPS / KPH;  // K steps per phase, phases of a stage
+      const int grp = wave >> 2;
+      u32x4 frag[KPH][TM + NACC];
+      auto phase_end = [&](bool wait) {
+        if (wait) wait_loads<0>();
+        __builtin_amdgcn_sched_barrier(0);
+        lds_barrier();
+        __builtin_amdgcn_sched_barrier(0);
+      };
+      auto phase = [&](int st, auto J) {
+        constexpr int j = decltype(J)::value;
+        // stage st + 1 goes where stage st - 1 was, which both groups finished reading before this phase
+        if (j == 0 && st >= 1) issue(st + 1);
+        const unsigned char* base = smem + (st & 1) * STAGE + fr * ROWB;
 #pragma unroll
-    for (int i = 0; i < NS - 1; ++i) issue(s_begin + i);
-    for (int st = s_begin; st < s_end; ++st) {
-      wait_loads<(NS - 2) * LPW>();
-      lds_barrier();  // stage st has landed for every wave, and stage st - 1 has been read
-      issue(st + NS - 1);
-      multiply(st);
+        for (int k = 0; k < KPH; ++k) {
+          const int xo = (((j * KPH + k) * (Op::KS / 16) + fq) ^ sw) << 4;
+#pragma unroll
+          for (int i = 0; i < TM; ++i) frag[k][i] = ld16(base + (wm * WTM + i * S) * ROWB + xo);
+#pragma unroll
+          for (int n = 0; n < NACC; ++n) {
+            const int r0 = BM + (GATED ? (n / TN) * OUTC + wn * WTN + (n % TN) * S : wn * WTN + n * S);
+            frag[k][TM + n] = ld16(base + r0 * ROWB + xo);
+          }
+        }
+        // stage st + 1 has to have landed when the group that runs first starts on it
+        phase_end(j == PHASES - 1 && grp == 1);
+        __builtin_amdgcn_s_setprio(1);
+#pragma unroll
+        for (int k = 0; k < KPH; ++k)
+#pragma unroll
+          for (int i = 0; i < TM; ++i)
+#pragma unroll
+            for (int n = 0; n < NACC; ++n) Op::step(acc[i][n], frag[k][i], frag[k][TM + n]);
+        __builtin_amdgcn_s_setprio(0);
+        phase_end(j == PHASES - 1 && grp == 0);
+      };
+      issue(0);
+      issue(1);
+      wait_loads<LPW>();
+      lds_barrier();
+      if (grp == 1) phase_end(false);
+      for (int st = 0; st < nk; ++st) {
+        phase(st, std::integral_constant<int, 0>{});
+        phase(st, std::integral_constant<int, 1>{});
+      }
+      if (grp == 0) phase_end(false);
+    } else {
+#pragma unroll
+      for (int i = 0; i < NS - 1; ++i) issue(s_begin + i);
+      for (int st = s_begin; st < s_end; ++st) {
+        wait_loads<(NS - 2) * LPW>();
+        lds_barrier();  // stage st has landed for every wave, and stage st - 1 has been read
+        issue(st + NS - 1);
+        multiply(st);
+      }
     }
 
     const int c_lane = n0 + wn * WTN + fr;  // column of block j: + j * S
@@ -195,10 +272,13 @@ __global__ __launch_bounds__(WM * WN * 64, PER_CU * WM * WN / 4 > 1 ? PER_CU * W
         for (int q = 0; q < Op::NR; ++q) {
           const int r = wm * WTM + i * S + Op::out_row(lane, q);
           if (r < m_rows) {
-            int* o = a.partial + sp * a.partial_stride + (int64_t)(p0 + r) * a.N;
+            int* o = a.partial + sp * a.partial_stride + (int64_t)(p0 + r) * a.w_rows;  // w_rows sums of a row
 #pragma unroll
             for (int j = 0; j < TN; ++j)
-              if (c_lane + j * S < a.N) o[c_lane + j * S] = acc[i][j][q];
+              if (c_lane + j * S < a.N) {
+                o[c_lane + j * S] = acc[i][j][q];
+                if constexpr (GATED) o[a.up + c_lane + j * S] = acc[i][j + TN][q];
+              }
           }
         }
     } else if constexpr (GATED) {
@@ -268,9 +348,9 @@ __global__ __launch_bounds__(WM * WN * 64, PER_CU * WM * WN / 4 > 1 ? PER_CU * W
 // Codes of h: a workgroup per row and 2048 columns. Every wave finds the row's maximum from its tiles' itself.
 constexpr int kHCols = 2048;
 __global__ __launch_bounds__(256) void i8_h_kernel(const float* __restrict__ h, const uint32_t* __restrict__ h_top,
-                                                   int h_tiles, const int* __restrict__ plan, int F,
+                                                   int h_tiles, const int* __restrict__ total, int F,
                                                    int8_t* __restrict__ codes, float* __restrict__ scale) {
-  const int rows = plan[1];
+  const int rows = *total;
   const int c = blockIdx.x * kHCols + threadIdx.x * 8;
   for (int64_t p = blockIdx.y; p < rows; p += gridDim.y) {
     u32x4 lo{0u, 0u, 0u, 0u}, hi{0u, 0u, 0u, 0u};
@@ -293,18 +373,45 @@ __global__ __launch_bounds__(256) void i8_h_kernel(const float* __restrict__ h, 
   }
 }
 
-// The parts of a split down pass added (int32: exact in any order), scaled, rounded once and put into their rows: eight
-// columns per thread.
+// The expert of plan row p: the last l with row_start[l] <= p
+__device__ __forceinline__ int row_expert(const I8Args& a, int p) {
+  int l = 0;
+  for (int hi = a.El; hi - l > 1;) {
+    const int mid = (l + hi) >> 1;
+    if (a.row_start[mid] <= p) l = mid;
+    else hi = mid;
+  }
+  return l;
+}
+
+// The parts of a split gate/up pass added (int32: exact in any order), and h as i8_gemm_kernel makes it: a wave per row and
+// 64 columns, the tile of its maximum.
+__global__ __launch_bounds__(256) void i8_sum_h_kernel(I8Args a) {
+  const int64_t unit = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
+  const int p = (int)(unit / a.h_tiles), tile = (int)(unit - (int64_t)p * a.h_tiles);
+  if (p >= a.row_start[a.El]) return;
+  const int c = tile * 64 + lane_id();
+  const bool in = c < a.N;
+  int g = 0, u = 0;
+  for (int s = 0; s < a.split; ++s) {
+    const int* o = a.partial + s * a.partial_stride + (int64_t)p * a.w_rows + (in ? c : 0);
+    g += o[0];
+    u += o[a.up];
+  }
+  const float sr = a.a_scale[a.a_perm ? a.a_perm[p] : p];
+  const float* sw = a.w_scale + (int64_t)row_expert(a, p) * a.w_rows + (in ? c : 0);
+  const float v = silu((float)g * sr * sw[0]) * ((float)u * sr * sw[a.up]);
+  if (in) a.h[(int64_t)p * a.N + c] = v;
+  const uint32_t top = wave_top(in ? abs_bits(v) : 0u);
+  if (lane_id() == 0) a.h_top[(int64_t)p * a.h_tiles + tile] = top;
+}
+
+// The parts of a split down pass added, scaled, rounded once and put into their rows: eight columns per thread.
 __global__ __launch_bounds__(256) void i8_sum_kernel(I8Args a) {
   const int64_t at = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 8;
   const int p = (int)(at / a.N), c = (int)(at - (int64_t)p * a.N);
-  if (p >= a.plan[1]) return;
-  int l = 0, hi = a.El;  // the expert of plan row p: the last l with row_start[l] <= p
-  while (hi - l > 1) {
-    const int mid = (l + hi) >> 1;
-    if (a.plan[2 + mid] <= p) l = mid;
-    else hi = mid;
-  }
+  if (p >= a.row_start[a.El]) return;
+  const float* sd = a.w_scale + (int64_t)row_expert(a, p) * a.w_rows + c;
   int v[8] = {0, 0, 0, 0, 0, 0, 0, 0};
   for (int s = 0; s < a.split; ++s)
 #pragma unroll
@@ -314,11 +421,10 @@ __global__ __launch_bounds__(256) void i8_sum_kernel(I8Args a) {
       for (int q = 0; q < 4; ++q) v[4 * q4 + q] += w[q];
     }
   const float sr = a.a_scale[p];
-  const float* sd = a.w_scale + (int64_t)l * a.w_rows + c;
   float o[8];
 #pragma unroll
   for (int q = 0; q < 8; ++q) o[q] = (float)v[q] * sr * sd[q];
-  st16(a.out + (int64_t)a.out_perm[p] * a.N + c, pack(o));
+  st16(a.out + (int64_t)(a.out_perm ? a.out_perm[p] : p) * a.N + c, pack(o));
 }
 
 int i8_grid(int64_t tiles, int64_t most) {
@@ -327,56 +433,110 @@ int i8_grid(int64_t tiles, int64_t most) {
   return (int)std::max<int64_t>(g, 1);
 }
 
-constexpr int kPlanCus = 256;   // what a call is cut into is a function of its sizes alone, as its workspace is
-constexpr int kSmallCols = 64;  // columns of a 32-row tile, of either pass
-template <typename Op, int BM, int WM, int WN, int GUN, int GUNS, int DNN, int DNNS, int PER_CU>
+constexpr int kPlanCus = 256;  // what a call is cut into is a function of its sizes alone, as its workspace is
+
+// The tiles: rows, columns of h and of the output, workgroups per CU
+struct I8Tile {
+  int bm, gu_cols, dn_cols, per_cu;
+};
+constexpr I8Tile kTiles[] = {{32, 64, 64, 2}, {64, 64, 128, 2}, {128, 128, 256, 1}, {256, 128, 256, 1}};
+
+template <int I, typename Op, int WM, int WN, int GUNS, int DNNS, bool PP = false>
 void launch_gemms(const I8Args& gu, const I8Args& dn, int64_t rows, int64_t mtiles, int num_cus, hipStream_t stream) {
-  constexpr int NTH = WM * WN * 64;
-  i8_gemm_kernel<Op, BM, GUN, WM, WN, GUNS, PER_CU, true>
-      <<<i8_grid(mtiles * ceil_div_host(gu.N, GUN / 2), PER_CU * num_cus), NTH, 0, stream>>>(gu, (int)(rows * gu.K));
-  const dim3 hg(ceil_div_host(gu.N, kHCols), (unsigned)std::min<int64_t>(rows, 65535));
-  i8_h_kernel<<<hg, 256, 0, stream>>>(gu.h, gu.h_top, gu.h_tiles, gu.plan, gu.N, const_cast<int8_t*>(dn.A),
-                                      const_cast<float*>(dn.a_scale));
-  const int64_t tiles = mtiles * ceil_div_host(dn.N, DNN);
-  if constexpr (BM == 32) {
-    if (dn.split > 1) {
-      i8_gemm_kernel<Op, BM, DNN, WM, WN, DNNS, PER_CU, false, true>
-          <<<i8_grid(tiles * dn.split, PER_CU * num_cus), NTH, 0, stream>>>(dn, (int)(rows * dn.K));
-      i8_sum_kernel<<<(unsigned)ceil_div_host64(rows * dn.N / 8, 256), 256, 0, stream>>>(dn);
-      return;
+  constexpr I8Tile t = kTiles[I];
+  constexpr int NTH = WM * WN * 64, GUN = 2 * t.gu_cols, DNN = t.dn_cols;
+  auto grid = [&](int64_t tiles) { return i8_grid(tiles, t.per_cu * num_cus); };
+  const int64_t gu_tiles = mtiles * ceil_div_host(gu.N, t.gu_cols), dn_tiles = mtiles * ceil_div_host(dn.N, t.dn_cols);
+  bool gu_split = false, dn_split = false;
+  if constexpr (t.bm == 32) {
+    gu_split = gu.split > 1;
+    dn_split = dn.split > 1;
+    if (gu_split) {
+      i8_gemm_kernel<Op, t.bm, GUN, WM, WN, GUNS, t.per_cu, PP, true, true>
+          <<<grid(gu_tiles * gu.split), NTH, 0, stream>>>(gu, (int)(rows * gu.K));
+      i8_sum_h_kernel<<<(unsigned)ceil_div_host64(rows * gu.h_tiles, 4), 256, 0, stream>>>(gu);
     }
   }
-  i8_gemm_kernel<Op, BM, DNN, WM, WN, DNNS, PER_CU, false>
-      <<<i8_grid(tiles, PER_CU * num_cus), NTH, 0, stream>>>(dn, (int)(rows * dn.K));
+  if (!gu_split)
+    i8_gemm_kernel<Op, t.bm, GUN, WM, WN, GUNS, t.per_cu, PP, true>
+        <<<grid(gu_tiles), NTH, 0, stream>>>(gu, (int)(rows * gu.K));
+  const dim3 hg(ceil_div_host(gu.N, kHCols), (unsigned)std::min<int64_t>(rows, 65535));
+  i8_h_kernel<<<hg, 256, 0, stream>>>(gu.h, gu.h_top, gu.h_tiles, gu.row_start + gu.El, gu.N, const_cast<int8_t*>(dn.A),
+                                      const_cast<float*>(dn.a_scale));
+  if constexpr (t.bm == 32) {
+    if (dn_split) {
+      i8_gemm_kernel<Op, t.bm, DNN, WM, WN, DNNS, t.per_cu, PP, false, true>
+          <<<grid(dn_tiles * dn.split), NTH, 0, stream>>>(dn, (int)(rows * dn.K));
+      i8_sum_kernel<<<(unsigned)ceil_div_host64(rows * dn.N / 8, 256), 256, 0, stream>>>(dn);
+    }
+  }
+  if (!dn_split)
+    i8_gemm_kernel<Op, t.bm, DNN, WM, WN, DNNS, t.per_cu, PP, false>
+        <<<grid(dn_tiles), NTH, 0, stream>>>(dn, (int)(rows * dn.K));
 }
 
-int64_t row_tiles(int64_t rows_max, int El, int bm) { return El * ceil_div_host64(ceil_div_host64(rows_max, El), bm); }
-
-// Parts of the down pass's K with 32-row tiles: as many as give every CU its two workgroups, of at least 8 stages.
-int i8_split(int64_t rows_max, int El, int H, int F) {
-  const int64_t tiles = row_tiles(rows_max, El, 32) * ceil_div_host(H, kSmallCols);
-  const int64_t s = std::min<int64_t>(2 * kPlanCus / tiles, F / 128 / 8);
-  return s < 2 ? 1 : (int)s;
-}
-
+// What a call is cut into: the tile, and for 32-row tiles the parts of each pass's K and the stages of a part.
 struct I8Plan {
-  int bm, split, stages;
+  int tile, gu_split, gu_stages, dn_split, dn_stages;
 };
+
+// Tiles of a row block count when the rows are spread over the experts; fewer rows than experts reach as many at most
+int64_t row_tiles(int64_t rows_max, int El, int bm) {
+  const int64_t n = std::min<int64_t>(El, rows_max);
+  return n * ceil_div_host64(ceil_div_host64(rows_max, n), bm);
+}
+
+// The tile whose two passes take least, from the time of a round of stages: 2.3 us for 256 rows, 1.5 for 128, and for two
+// workgroups per CU 1.32 (64 rows) and 0.89 (32 rows); a last round of one workgroup per CU takes 1.15 and 0.85. Whole MLPs (us)
+// by rows of a tile, which this rule orders right but for ties:
+//   experts, H, F, rows each      32      64     128     256
+//   32, 7168, 2048, 32           246     247     286     346
+//   32, 7168, 2048, 64           412     277     308     366
+//   32, 7168, 2048, 128          745     460     352     395
+//   32, 7168, 2048, 256         1462     821     535     471
+//   8, 4096, 14336, 32           244     248     323     422
+//   8, 4096, 14336, 96           591     510     370     448
+//   12, 1184, 736, 64           29.9    30.3    38.6    46.3
+//   12, 1184, 736, 128          43.4    37.6    44.8    49.3
+//   12, 1184, 736, 384          87.4    67.8    50.2    62.7
+//   16, 2048, 768, 128          56.6    43.8    50.5    55.3
+//   48, 1024, 512, 96           60.8    54.2    46.6    50.9
+double tile_cost(int i, int64_t rows_max, int El, int H, int F) {
+  constexpr double full[] = {0.89, 1.32, 1.5, 2.3}, rest[] = {0.85, 1.15, 1.5, 2.3};
+  const int64_t m = row_tiles(rows_max, El, kTiles[i].bm), slots = kTiles[i].per_cu * kPlanCus;
+  auto pass = [&](int cols, int tile_cols, int K) {
+    const int64_t tiles = m * ceil_div_host(cols, tile_cols), left = tiles % slots;
+    return ceil_div_host(K, 128) * (tiles / slots * full[i] + (left == 0 ? 0.0 : left <= kPlanCus ? rest[i] : full[i]));
+  };
+  return pass(F, kTiles[i].gu_cols, H) + pass(H, kTiles[i].dn_cols, F);
+}
+
+// Parts of a pass's K with 32-row tiles: as many as give every CU its workgroups, of at least 8 stages each, as the parts' sums
+// take a launch of their own.
+void split_k(int64_t tiles, int K, int& split, int& stages) {
+  const int nk = ceil_div_host(K, 128);
+  split = (int)std::max<int64_t>(1, std::min<int64_t>(kTiles[0].per_cu * kPlanCus / tiles, nk / 8));
+  stages = ceil_div_host(nk, split);
+  split = ceil_div_host(nk, stages);  // every part has stages
+}
+
 I8Plan i8_plan(int64_t rows_max, int El, int H, int F) {
-  const int64_t per = ceil_div_host64(rows_max, El);
-  I8Plan p{per <= 64 ? 32 : per <= 384 ? 128 : 256, 1, 0};
-  if (p.bm == 32) {
-    const int nk = ceil_div_host(F, 128);
-    p.split = i8_split(rows_max, El, H, F);
-    p.stages = ceil_div_host(nk, p.split);
-    p.split = ceil_div_host(nk, p.stages);  // every part has stages
+  I8Plan p{0, 1, 0, 1, 0};
+  if (rows_max == 0) return p;
+  for (int i = 1; i < 4; ++i)
+    if (tile_cost(i, rows_max, El, H, F) < tile_cost(p.tile, rows_max, El, H, F)) p.tile = i;
+  if (p.tile == 0) {
+    const int64_t m = row_tiles(rows_max, El, 32);
+    split_k(m * ceil_div_host(F, kTiles[0].gu_cols), H, p.gu_split, p.gu_stages);
+    split_k(m * ceil_div_host(H, kTiles[0].dn_cols), F, p.dn_split, p.dn_stages);
   }
   return p;
 }
 
-int h_tiles(int bm, int F) { return ceil_div_host(F, bm == 32 ? kSmallCols : 128); }
+int h_tiles(const I8Plan& p, int F) { return ceil_div_host(F, kTiles[p.tile].gu_cols); }
 
-// the workspace: plan, row map, h, its tiles' maxima, its codes and scales, the parts of a split down pass
+// the workspace: plan, row map, h, its tiles' maxima, its codes and scales, the parts of a split pass (gate/up's are
+// done with before the down pass writes its own)
 struct I8Scratch {
   size_t plan, perm, h, top, codes, scale, partial, total;
 };
@@ -391,10 +551,11 @@ I8Scratch i8_scratch(int64_t rows, int El, int H, int F, const I8Plan& p) {
   s.plan = take(mlp_plan_ints(El) * sizeof(int));
   s.perm = take((size_t)rows * sizeof(int));
   s.h = take((size_t)rows * (size_t)F * sizeof(float));
-  s.top = take((size_t)rows * (size_t)h_tiles(p.bm, F) * sizeof(uint32_t));
+  s.top = take((size_t)rows * (size_t)h_tiles(p, F) * sizeof(uint32_t));
   s.codes = take((size_t)rows * (size_t)F);
   s.scale = take((size_t)rows * sizeof(float));
-  s.partial = take(p.split > 1 ? (size_t)p.split * (size_t)rows * (size_t)H * sizeof(int) : 0);
+  s.partial = take(std::max(p.gu_split > 1 ? (size_t)p.gu_split * 2 * (size_t)F : 0,
+                            p.dn_split > 1 ? (size_t)p.dn_split * (size_t)H : 0) * (size_t)rows * sizeof(int));
   s.total = at;
   return s;
 }
@@ -406,6 +567,11 @@ I8Scratch i8_scratch(int64_t rows, int El, int H, int F, const I8Plan& p) {
 bool mlp_i8_fits(int64_t rows, int H, int F) {
   return std::max(H, F) < 1 << 17 && rows * std::max<int64_t>(H, F) < 0x7ffffe00ll &&
          2 * (int64_t)F * H < 0x7ffffe00ll;
+}
+
+I8Tiling mlp_i8_tiling(int64_t rows, int El, int H, int F) {
+  const I8Plan p = i8_plan(rows, El, H, F);
+  return {kTiles[p.tile].bm, p.gu_split, p.dn_split};
 }
 
 size_t mlp_i8_workspace_bytes(int64_t rows, int El, int H, int F) {
@@ -424,10 +590,14 @@ hipError_t launch_expert_mlp_i8(const int8_t* send_q, const float* send_scale, c
   char* ws = static_cast<char*>(workspace);
   int* plan = reinterpret_cast<int*>(ws + at.plan);
   int* perm = reinterpret_cast<int*>(ws + at.perm);
-  launch_mlp_plan(L, p.bm, plan, perm, stream);
+  // with one rank the send rows are in plan order and the offsets are the row starts: no plan is needed
+  const bool ranks = L.R > 1;
+  if (ranks) launch_mlp_plan(L, kTiles[p.tile].bm, plan, perm, stream);
+  const int* row_start = ranks ? plan + 2 : L.expert_offset;
+  const int* tile_start = ranks ? plan + 3 + El : nullptr;
   I8Args gu{};
   gu.A = send_q;
-  gu.a_perm = perm;
+  gu.a_perm = ranks ? perm : nullptr;
   gu.a_scale = send_scale;
   gu.W = gu_codes;
   gu.w_scale = gu_scales;
@@ -437,8 +607,13 @@ hipError_t launch_expert_mlp_i8(const int8_t* send_q, const float* send_scale, c
   gu.up = F;
   gu.h = reinterpret_cast<float*>(ws + at.h);
   gu.h_top = reinterpret_cast<uint32_t*>(ws + at.top);
-  gu.h_tiles = h_tiles(p.bm, F);
-  gu.plan = plan;
+  gu.h_tiles = h_tiles(p, F);
+  gu.split = p.gu_split;
+  gu.split_stages = p.gu_stages;
+  gu.partial = reinterpret_cast<int*>(ws + at.partial);
+  gu.partial_stride = rows * 2 * F;
+  gu.row_start = row_start;
+  gu.tile_start = tile_start;
   gu.El = El;
   I8Args dn{};
   dn.A = reinterpret_cast<int8_t*>(ws + at.codes);
@@ -449,17 +624,19 @@ hipError_t launch_expert_mlp_i8(const int8_t* send_q, const float* send_scale, c
   dn.N = L.H;
   dn.w_rows = L.H;
   dn.out = static_cast<bf16_t*>(out_buf);
-  dn.out_perm = perm;
-  dn.plan = plan;
+  dn.out_perm = ranks ? perm : nullptr;
+  dn.row_start = row_start;
+  dn.tile_start = tile_start;
   dn.El = El;
-  dn.split = p.split;
-  dn.split_stages = p.stages;
+  dn.split = p.dn_split;
+  dn.split_stages = p.dn_stages;
   dn.partial = reinterpret_cast<int*>(ws + at.partial);
   dn.partial_stride = rows * L.H;
-  const int64_t mtiles = ceil_div_host64(rows, p.bm) + El;
-  if (p.bm == 32) launch_gemms<OpI16, 32, 1, 4, 2 * kSmallCols, 3, kSmallCols, 4, 2>(gu, dn, rows, mtiles, num_cus, stream);
-  else if (p.bm == 128) launch_gemms<OpI32, 128, 2, 4, 256, 3, 256, 3, 1>(gu, dn, rows, mtiles, num_cus, stream);
-  else launch_gemms<OpI32, 256, 4, 2, 256, 2, 256, 2, 1>(gu, dn, rows, mtiles, num_cus, stream);
+  const int64_t mtiles = ceil_div_host64(rows, kTiles[p.tile].bm) + std::min<int64_t>(El, rows);
+  if (p.tile == 0) launch_gemms<0, OpI16, 1, 4, 3, 4>(gu, dn, rows, mtiles, num_cus, stream);
+  else if (p.tile == 1) launch_gemms<1, OpI32, 2, 2, 3, 3>(gu, dn, rows, mtiles, num_cus, stream);
+  else if (p.tile == 2) launch_gemms<2, OpI32, 2, 4, 3, 3>(gu, dn, rows, mtiles, num_cus, stream);
+  else launch_gemms<3, OpI32, 4, 2, 2, 2, true>(gu, dn, rows, mtiles, num_cus, stream);
   return hipGetLastError();
 }
 

@@ -497,6 +497,16 @@ int moe_expert_mlp_i8(const int8_t* send_q, const float* send_scale, const moe_l
                       const float* gu_scales, const int8_t* dn_codes, const float* dn_scales, int F, void* out_buf,
                       void* workspace, size_t workspace_bytes, hipStream_t stream);
 
+/*
+ * moe_expert_mlp_i8_tiling -- what moe_expert_mlp_i8 cuts a call of these sizes into, from the sizes alone (the result does
+ * not depend on it: the sums are exact).
+ *   tile_rows       rows per tile: 32, 64, 128 or 256
+ *   gate_up_parts, down_parts  parts of the pass's K whose int32 sums a further launch adds, 1 where it is not split
+ * Returns what moe_expert_mlp_i8 would return for the sizes, and writes nothing unless that is MOE_OK.
+ */
+int moe_expert_mlp_i8_tiling(int T, int k, int E, int R, int C, int H, int F, int* tile_rows, int* gate_up_parts,
+                             int* down_parts);
+
 /* Bytes of scratch `workspace` moe_balance_loss needs. */
 size_t moe_balance_loss_workspace_bytes(int T, int E, int S);
 

@@ -146,32 +146,39 @@ def check(out, q, s, weights, counts, R, every=1):
 
 
 CASES = [
-    # name, counts, T, k, R, C, H, F
-    ("one_row", [1, 0, 0, 0], 1, 1, 1, 1, 16, 16),
-    ("empty", [0, 0, 0, 0], 4, 2, 1, 4, 64, 32),
-    ("ranks_ragged", [3, 0, 17, 1, 16, 2, 0, 15], 40, 2, 4, 17, 144, 80),
-    ("rows_16_32", [16, 33, 32, 31], 64, 2, 1, 33, 544, 288),
-    ("wide", [9, 23], 32, 1, 1, 32, 1184, 736),
-    # few tiles and a wide F: the down pass is split, its last part shorter; with two ranks
-    ("split", [9, 0, 32, 1], 42, 1, 1, 42, 160, 4304),
-    ("split_ranks", [3, 16, 0, 1, 7, 20], 47, 1, 2, 20, 64, 4160),
-    ("tile_128", [300, 129, 1, 513], 513, 2, 1, 513, 288, 368),
-    ("tile_128_ranks", [128, 1, 0, 127, 33, 200], 300, 2, 3, 200, 416, 272),
-    ("tile_256", [1025, 700, 256, 255], 1118, 2, 1, 1118, 144, 272),
-    ("tile_256_ranks", [257, 255, 256, 1, 400, 0], 1300, 1, 3, 500, 272, 144),
+    # name, counts, T, k, R, C, H, F, rows per tile, whether the gate/up and the down pass are split
+    ("one_row", [1, 0, 0, 0], 1, 1, 1, 1, 16, 16, 32, False, False),
+    ("empty", [0, 0, 0, 0], 4, 2, 1, 4, 64, 32, 32, False, False),
+    ("ranks_ragged", [3, 0, 17, 1, 16, 2, 0, 15], 40, 2, 4, 17, 144, 80, 32, False, False),
+    ("rows_16_32", [16, 33, 32, 31], 64, 2, 1, 33, 544, 288, 32, False, False),
+    ("wide", [9, 23], 32, 1, 1, 32, 1184, 736, 32, False, False),
+    # few tiles and a wide K: a pass is split, its last part shorter; with two ranks
+    ("split_down", [9, 0, 32, 1], 42, 1, 1, 42, 160, 4304, 32, False, True),
+    ("split_down_ranks", [3, 16, 0, 1, 7, 20], 47, 1, 2, 20, 64, 4160, 32, False, True),
+    ("split_gate_up", [9, 0, 32, 1], 42, 1, 1, 42, 4304, 160, 32, True, False),
+    ("split_gate_up_ranks", [3, 16, 0, 1, 7, 20], 47, 1, 2, 20, 4160, 48, 32, True, False),
+    ("split_both", [1, 1], 2, 1, 1, 1, 2064, 2320, 32, True, True),
+    ("tile_64", [64, 130, 1, 61], 256, 1, 1, 256, 4112, 4112, 64, False, False),
+    ("tile_64_ranks", [40, 24, 1, 33, 0, 34, 50, 66], 256, 1, 2, 70, 4112, 2064, 64, False, False),
+    ("tile_128", [300, 129, 1, 513] * 3, 2829, 1, 1, 700, 1184, 736, 128, False, False),
+    ("tile_128_ranks", [128, 1, 0, 127, 33, 200, 256, 255] * 3, 3000, 1, 2, 300, 1184, 736, 128, False, False),
+    ("tile_256", [1025, 700, 256, 255] * 3, 6708, 1, 1, 6708, 1184, 736, 256, False, False),
+    ("tile_256_ranks", [257, 255, 256, 1, 1400, 0, 700, 33] * 2, 6000, 1, 2, 6000, 1040, 720, 256, False, False),
 ]
 
 
-@pytest.mark.parametrize("name,counts,T,k,R,C,H,F", CASES, ids=[c[0] for c in CASES])
-def test_expert_mlp_i8(name, counts, T, k, R, C, H, F):
+@pytest.mark.parametrize("name,counts,T,k,R,C,H,F,rows,gu,dn", CASES, ids=[c[0] for c in CASES])
+def test_expert_mlp_i8(name, counts, T, k, R, C, H, F, rows, gu, dn):
     print(f"\n[gpu] expert MLP i8 {name}", flush=True)
+    tiling = moe.moe_expert_mlp_i8_tiling(T, k, len(counts), R, C, H, F)
+    assert (tiling[0], tiling[1] > 1, tiling[2] > 1) == (rows, gu, dn)
     L, q, s, weights = case(counts, T, k, R, C, H, F, 100 + len(name))
     n = moe.moe_expert_mlp_i8_workspace_bytes(T, k, len(counts), R, C, H, F)
     ws = torch.full((n,), 0xFF, dtype=torch.uint8, device=DEV)
     out = run(L, q, s, weights, torch.full((L.rows_max, H), -7.0, dtype=torch.bfloat16, device=DEV), workspace=ws)
     total = sum(counts)
     assert torch.all(out[total:] == -7.0)  # rows past the kept ones are left alone
-    assert check(out, q, s, weights, counts, R, 1 if total < 300 else 7) <= 1.0
+    assert check(out, q, s, weights, counts, R, 1 if total < 300 else 23) <= 1.0
     ws.fill_(0x11)
     again = run(L, q, s, weights, torch.full_like(out, -7.0), workspace=ws)
     assert torch.equal(out.view(torch.int16), again.view(torch.int16))

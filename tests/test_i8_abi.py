@@ -102,6 +102,24 @@ def test_workspace_sizes(lib):
     assert size(1 << 20, 1, 1, 1, 1 << 20, 64, 2032) >= (1 << 20) * 2032 * 5
 
 
+def test_tiling_query(lib):
+    """Every tile, and each split, is what some sizes take (tests/test_gpu_i8.py has the same sizes on the GPU)."""
+    from tests.test_gpu_i8 import CASES
+    seen = set()
+    for name, counts, T, k, R, C, H, F, rows, gu, dn in CASES:
+        t = moe.moe_expert_mlp_i8_tiling(T, k, len(counts), R, C, H, F)
+        assert (t[0], t[1] > 1, t[2] > 1) == (rows, gu, dn), (name, t)
+        seen.add(rows)
+    assert seen == {32, 64, 128, 256}
+    n = [ctypes.c_int(7) for _ in range(3)]
+    call = lambda T=4, k=2, E=8, R=1, C=4, H=64, F=64, out=n: lib.moe_expert_mlp_i8_tiling(
+        T, k, E, R, C, H, F, *[ctypes.byref(v) if v is not None else None for v in out])
+    assert call(H=72) == UNSUPPORTED and call(F=0) == INVALID and call(k=9, E=16) == INVALID and call(R=3) == INVALID
+    assert call(T=-1) == INVALID and call(out=[n[0], None, n[1]]) == INVALID and call(F=1 << 17) == UNSUPPORTED
+    assert [v.value for v in n] == [7, 7, 7]
+    assert call() == 0 and [v.value for v in n] != [7, 7, 7]
+
+
 def test_binding_refuses_host_tensors(lib):
     w, q, s = torch.zeros(32, 64), torch.zeros(32, 64, dtype=torch.int8), torch.zeros(32)
     with pytest.raises(moe.MoeError):
