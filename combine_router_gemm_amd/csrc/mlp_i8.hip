@@ -42,10 +42,15 @@ struct I8Args {
   const int* row_start;
   const int* tile_start;
   int El;
-  // SPLIT: K in `split` parts of split_stages stages each, their int32 sums to partial [split, rows, w_rows]
+  // SPLIT: K in `split` parts of split_stages stages each. Gate/up: their int32 sums to partial [split, rows, w_rows]. Down: a
+  // thread's sums of a part to partial [tile, split, .., thread], and the workgroup that completes a tile by its count in
+  // `ticket` (zeroed by the gate/up kernel) adds them.
   int split, split_stages;
   int* partial;
-  int64_t partial_stride;  // elements of one part
+  int64_t partial_stride;  // gate/up: elements of one part
+  int* ticket;
+  int* zero;               // gate/up: ints to zero for the down pass
+  int zero_n;
 };
 
 __device__ __forceinline__ float silu(float g) { return g / (1.0f + expf(-g)); }
@@ -58,24 +63,31 @@ __device__ __forceinline__ int swizzle(int r) { return (r >> 1) & 7; }
 // PP: eight waves in two groups, one of each on every SIMD, that run the same sequence (read half a stage of fragments,
 // barrier, multiply them, barrier) one barrier apart: while one group reads and loads the other keeps the matrix units busy.
 // SPLIT: K cut over workgroups, where the tiles are few (see i8_plan).
-template <typename Op, int BM, int BN, int WM, int WN, int NS, int PER_CU, bool PP, bool GATED, bool SPLIT = false>
+// FEW: a down pass of at most kFewRows rows in all, which takes h itself and makes the codes of its part of K while the first
+// weights are on their way, in place of a launch for them (one Mixtral-shaped token 85 -> 73 us with the join in the kernel).
+constexpr int kFewRows = 8, kFewStages = 32;
+template <typename Op, int BM, int BN, int WM, int WN, int NS, int PER_CU, bool PP, bool GATED, bool SPLIT = false,
+          bool FEW = false>
 __global__ __launch_bounds__(WM * WN * 64, PER_CU * WM * WN / 4 > 1 ? PER_CU * WM * WN / 4 : 1) void i8_gemm_kernel(
     I8Args a, int a_bytes) {
   static_assert(!PP || (NS == 2 && WM * WN == 8 && !SPLIT), "ping-pong");
+  static_assert(!FEW || (SPLIT && !GATED && WM == 1), "a few rows");
   constexpr int S = Op::S, NW = WM * WN, NTH = NW * 64, ROWB = 128, RPI = 8;
-  constexpr int STAGE = (BM + BN) * ROWB, A_INS = BM / RPI, LPW = (BM + BN) / RPI / NW;
-  static_assert((BM + BN) / RPI % NW == 0, "wave loads must split evenly");
+  constexpr int SA = FEW ? 0 : BM;                               // rows that a stage loads
+  constexpr int A_BYTES = FEW ? kFewStages * kFewRows * ROWB : 0;  // FEW: codes of all stages, before the weights' stages
+  constexpr int STAGE = (SA + BN) * ROWB, A_INS = SA / RPI, LPW = (SA + BN) / RPI / NW;
+  static_assert((SA + BN) / RPI % NW == 0, "wave loads must split evenly");
   constexpr int OUTC = GATED ? BN / 2 : BN;
   constexpr int WTM = BM / WM, TM = WTM / S, WTN = OUTC / WN, TN = WTN / S;
   constexpr int NACC = GATED ? 2 * TN : TN, KSTEPS = ROWB / Op::KS;
   static_assert(TM >= 1 && TN >= 1, "wave tile too small");
-  constexpr int OUT_BYTES = GATED || SPLIT ? 0 : BM * OUTC * 2;
-  constexpr int BODY = NS * STAGE > OUT_BYTES ? NS * STAGE : OUT_BYTES;
+  constexpr int OUT_BYTES = GATED ? 0 : BM * OUTC * 2;
+  constexpr int BODY = A_BYTES + NS * STAGE > OUT_BYTES ? A_BYTES + NS * STAGE : OUT_BYTES;
   constexpr int OOB = 0x7ffffff0;
   // the only LDS object (a second one makes the compiler wait for every load in flight before LDS reads): the stages, which
   // the output tile reuses; the tile's row scales and destination rows; the waves' row maxima; the plan's starts
   constexpr int SCALE_OFF = BODY, ROW_OFF = SCALE_OFF + BM * 4, TOP_OFF = ROW_OFF + BM * 4;
-  constexpr int PLAN_OFF = TOP_OFF + (GATED ? WN * BM * 4 : 0);
+  constexpr int PLAN_OFF = TOP_OFF + (GATED ? WN * BM * 4 : 16);
   __shared__ __attribute__((aligned(1024))) unsigned char smem[PLAN_OFF + 2 * (MOE_MAX_EXPERTS + 1) * 4];
   float* s_scale = reinterpret_cast<float*>(smem + SCALE_OFF);
   int* s_row = reinterpret_cast<int*>(smem + ROW_OFF);
@@ -87,6 +99,8 @@ __global__ __launch_bounds__(WM * WN * 64, PER_CU * WM * WN / 4 > 1 ? PER_CU * W
   const int wm = wave / WN, wn = wave % WN;
   int fr = lane % S, fq = lane / S;
   const int K = a.K, nk = (K + ROWB - 1) / ROWB;
+  if constexpr (GATED)
+    for (int i = blockIdx.x * NTH + tid; i < a.zero_n; i += gridDim.x * NTH) a.zero[i] = 0;
   for (int i = tid; i <= a.El; i += NTH) {
     row_start[i] = a.row_start[i];
     if (a.tile_start) tile_start[i] = a.tile_start[i];
@@ -145,9 +159,16 @@ __global__ __launch_bounds__(WM * WN * 64, PER_CU * WM * WN / 4 > 1 ? PER_CU * W
     lds_barrier();  // the previous tile has left LDS
     for (int r = tid; r < BM; r += NTH) {
       const int p = p0 + min(r, m_rows - 1);
-      s_scale[r] = a.a_scale[a.a_perm ? a.a_perm[p] : p];
+      if constexpr (!FEW) s_scale[r] = a.a_scale[a.a_perm ? a.a_perm[p] : p];
       s_row[r] = a.out_perm ? a.out_perm[p] : p;
     }
+    if constexpr (FEW)
+      for (int r = wave; r < BM; r += NW) {  // the rows' maxima, for now
+        uint32_t top = 0;
+        for (int i = lane; i < a.h_tiles; i += 64) top = max(top, a.h_top[(int64_t)(p0 + min(r, m_rows - 1)) * a.h_tiles + i]);
+        top = wave_top(top);
+        if (lane == 0) s_scale[r] = __uint_as_float(top);
+      }
     int tail = 0;  // bit q: this lane's chunk of load q lies within K in the last stage
 #pragma unroll
     for (int q = 0; q < LPW; ++q) {
@@ -163,7 +184,7 @@ __global__ __launch_bounds__(WM * WN * 64, PER_CU * WM * WN / 4 > 1 ? PER_CU * W
       }
     }
     auto issue = [&](int st) {
-      unsigned char* base = smem + (st % NS) * STAGE;
+      unsigned char* base = smem + A_BYTES + (st % NS) * STAGE;
       const bool last = st == nk - 1, past = st >= s_end;
 #pragma unroll
       for (int q = 0; q < LPW; ++q) {
@@ -184,18 +205,21 @@ __global__ __launch_bounds__(WM * WN * 64, PER_CU * WM * WN / 4 > 1 ? PER_CU * W
     const int mb = min(TM, max(0, (m_rows - wm * WTM + S - 1) / S));  // blocks with rows (wave-uniform)
     const int sw = swizzle(fr);  // blocks start at multiples of 16 rows
     auto multiply = [&](int st) {
-      const unsigned char* base = smem + (st % NS) * STAGE + fr * ROWB;
+      const unsigned char* base = smem + A_BYTES + (st % NS) * STAGE + fr * ROWB;
+      const unsigned char* few = smem + ((st - s_begin) * kFewRows + (fr & (kFewRows - 1))) * ROWB;
 #pragma unroll
       for (int ks = 0; ks < KSTEPS; ++ks) {
         const int xo = ((ks * (Op::KS / 16) + fq) ^ sw) << 4;
         u32x4 fa[TM], fb[NACC];
 #pragma unroll
         for (int j = 0; j < NACC; ++j) {
-          const int r0 = BM + (GATED ? (j / TN) * OUTC + wn * WTN + (j % TN) * S : wn * WTN + j * S);
+          const int r0 = SA + (GATED ? (j / TN) * OUTC + wn * WTN + (j % TN) * S : wn * WTN + j * S);
           fb[j] = ld16(base + r0 * ROWB + xo);
         }
 #pragma unroll
-        for (int i = 0; i < TM; ++i) fa[i] = ld16(base + (wm * WTM + i * S) * ROWB + xo);
+        for (int i = 0; i < TM; ++i)
+          fa[i] = FEW ? ld16(few + (((ks * (Op::KS / 16) + fq) ^ swizzle(fr & (kFewRows - 1))) << 4))
+                      : ld16(base + (wm * WTM + i * S) * ROWB + xo);
 #pragma unroll
         for (int i = 0; i < TM; ++i)
           if (i < mb) {
@@ -256,6 +280,26 @@ __global__ __launch_bounds__(WM * WN * 64, PER_CU * WM * WN / 4 > 1 ? PER_CU * W
     } else {
 #pragma unroll
       for (int i = 0; i < NS - 1; ++i) issue(s_begin + i);
+      if constexpr (FEW) {
+        // codes of the part's columns: 16 of a row per thread and round; past K they are zeros
+        lds_barrier();  // the maxima
+        const int units = m_rows * (s_end - s_begin) * 8;
+        for (int u = tid; u < units; u += NTH) {
+          const int r = u % m_rows, chunk = u / m_rows, c = s_begin * ROWB + chunk * 16;
+          const I8Row row = i8_row(__float_as_uint(s_scale[r]));
+          uint32_t w[4] = {0u, 0u, 0u, 0u};
+          if (c < K) {
+            float v[16];
+            const float* h = a.h + (int64_t)(p0 + r) * K + c;
+#pragma unroll
+            for (int q = 0; q < 4; ++q) unpack(ld16(h + 4 * q), *reinterpret_cast<float(*)[4]>(&v[4 * q]));
+            i8_codes(v, row, w);
+          }
+          st16(smem + ((chunk >> 3) * kFewRows + r) * ROWB + (((chunk & 7) ^ swizzle(r)) << 4), u32x4{w[0], w[1], w[2], w[3]});
+        }
+        lds_barrier();
+        if (tid < BM) s_scale[tid] = i8_row(__float_as_uint(s_scale[tid])).scale;
+      }
       for (int st = s_begin; st < s_end; ++st) {
         wait_loads<(NS - 2) * LPW>();
         lds_barrier();  // stage st has landed for every wave, and stage st - 1 has been read
@@ -264,8 +308,42 @@ __global__ __launch_bounds__(WM * WN * 64, PER_CU * WM * WN / 4 > 1 ? PER_CU * W
       }
     }
 
+    if constexpr (SPLIT && !GATED) {
+      if (a.split > 1) {  // (uniform)
+        constexpr int PV = TM * NACC * Op::NR / 2;  // pairs of sums per thread
+        const int64_t slot = ((int64_t)tile * a.split + sp) * PV * NTH + tid;
+        uint64_t* part = reinterpret_cast<uint64_t*>(a.partial);
+#pragma unroll
+        for (int v = 0; v < PV; ++v) {
+          const int q = 2 * v, i = q / (NACC * Op::NR), j = q / Op::NR % NACC, n = q % Op::NR;
+          __hip_atomic_store(part + slot + v * NTH,
+                             (uint64_t)(uint32_t)acc[i][j][n] | ((uint64_t)(uint32_t)acc[i][j][n + 1] << 32),
+                             __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        }
+        // agent-scope stores write through to where every XCD reads them, so their acknowledgement is all the order that
+        // the count needs. Nothing waits for another workgroup: the last to arrive finishes the tile.
+        int* s_last = reinterpret_cast<int*>(s_top);
+        wait_loads<0>();
+        lds_barrier();
+        if (tid == 0)
+          *s_last = __hip_atomic_fetch_add(a.ticket + tile, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) == a.split - 1;
+        lds_barrier();
+        if (!__builtin_amdgcn_readfirstlane(*s_last)) continue;
+        for (int o = 0; o < a.split; ++o) {  // int32 sums: exact in any order
+          if (o == sp) continue;
+          const int64_t from = ((int64_t)tile * a.split + o) * PV * NTH + tid;
+#pragma unroll
+          for (int v = 0; v < PV; ++v) {
+            const int q = 2 * v, i = q / (NACC * Op::NR), j = q / Op::NR % NACC, n = q % Op::NR;
+            const uint64_t w = __hip_atomic_load(part + from + v * NTH, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+            acc[i][j][n] += (int)(uint32_t)w;
+            acc[i][j][n + 1] += (int)(uint32_t)(w >> 32);
+          }
+        }
+      }
+    }
     const int c_lane = n0 + wn * WTN + fr;  // column of block j: + j * S
-    if constexpr (SPLIT) {
+    if constexpr (SPLIT && GATED) {
 #pragma unroll
       for (int i = 0; i < TM; ++i)
 #pragma unroll
@@ -277,7 +355,7 @@ __global__ __launch_bounds__(WM * WN * 64, PER_CU * WM * WN / 4 > 1 ? PER_CU * W
             for (int j = 0; j < TN; ++j)
               if (c_lane + j * S < a.N) {
                 o[c_lane + j * S] = acc[i][j][q];
-                if constexpr (GATED) o[a.up + c_lane + j * S] = acc[i][j + TN][q];
+                o[a.up + c_lane + j * S] = acc[i][j + TN][q];
               }
           }
         }
@@ -406,27 +484,6 @@ __global__ __launch_bounds__(256) void i8_sum_h_kernel(I8Args a) {
   if (lane_id() == 0) a.h_top[(int64_t)p * a.h_tiles + tile] = top;
 }
 
-// The parts of a split down pass added, scaled, rounded once and put into their rows: eight columns per thread.
-__global__ __launch_bounds__(256) void i8_sum_kernel(I8Args a) {
-  const int64_t at = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 8;
-  const int p = (int)(at / a.N), c = (int)(at - (int64_t)p * a.N);
-  if (p >= a.row_start[a.El]) return;
-  const float* sd = a.w_scale + (int64_t)row_expert(a, p) * a.w_rows + c;
-  int v[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-  for (int s = 0; s < a.split; ++s)
-#pragma unroll
-    for (int q4 = 0; q4 < 2; ++q4) {
-      const i32x4 w = *reinterpret_cast<const i32x4*>(a.partial + s * a.partial_stride + at + 4 * q4);
-#pragma unroll
-      for (int q = 0; q < 4; ++q) v[4 * q4 + q] += w[q];
-    }
-  const float sr = a.a_scale[p];
-  float o[8];
-#pragma unroll
-  for (int q = 0; q < 8; ++q) o[q] = (float)v[q] * sr * sd[q];
-  st16(a.out + (int64_t)(a.out_perm ? a.out_perm[p] : p) * a.N + c, pack(o));
-}
-
 int i8_grid(int64_t tiles, int64_t most) {
   int64_t g = std::min(tiles, most);
   if (g >= 8) g &= ~7ll;
@@ -437,9 +494,9 @@ constexpr int kPlanCus = 256;  // what a call is cut into is a function of its s
 
 // The tiles: rows, columns of h and of the output, workgroups per CU
 struct I8Tile {
-  int bm, gu_cols, dn_cols, per_cu;
+  int bm, gu_cols, dn_cols, per_cu, dn_per_cu;  // (down, 32 rows, Kimi-K2 decode: 120 us with two workgroups per CU, 113 with 3)
 };
-constexpr I8Tile kTiles[] = {{32, 64, 64, 2}, {64, 64, 128, 2}, {128, 128, 256, 1}, {256, 128, 256, 1}};
+constexpr I8Tile kTiles[] = {{32, 64, 64, 2, 3}, {64, 64, 128, 2, 2}, {128, 128, 256, 1, 1}, {256, 128, 256, 1, 1}};
 
 template <int I, typename Op, int WM, int WN, int GUNS, int DNNS, bool PP = false>
 void launch_gemms(const I8Args& gu, const I8Args& dn, int64_t rows, int64_t mtiles, int num_cus, hipStream_t stream) {
@@ -460,6 +517,13 @@ void launch_gemms(const I8Args& gu, const I8Args& dn, int64_t rows, int64_t mtil
   if (!gu_split)
     i8_gemm_kernel<Op, t.bm, GUN, WM, WN, GUNS, t.per_cu, PP, true>
         <<<grid(gu_tiles), NTH, 0, stream>>>(gu, (int)(rows * gu.K));
+  if constexpr (t.bm == 32) {
+    if (rows <= kFewRows) {
+      i8_gemm_kernel<Op, 16, DNN, WM, WN, DNNS, t.per_cu, PP, false, true, true>
+          <<<grid(dn_tiles * dn.split), NTH, 0, stream>>>(dn, 0);
+      return;
+    }
+  }
   const dim3 hg(ceil_div_host(gu.N, kHCols), (unsigned)std::min<int64_t>(rows, 65535));
   i8_h_kernel<<<hg, 256, 0, stream>>>(gu.h, gu.h_top, gu.h_tiles, gu.row_start + gu.El, gu.N, const_cast<int8_t*>(dn.A),
                                       const_cast<float*>(dn.a_scale));
@@ -467,12 +531,11 @@ void launch_gemms(const I8Args& gu, const I8Args& dn, int64_t rows, int64_t mtil
     if (dn_split) {
       i8_gemm_kernel<Op, t.bm, DNN, WM, WN, DNNS, t.per_cu, PP, false, true>
           <<<grid(dn_tiles * dn.split), NTH, 0, stream>>>(dn, (int)(rows * dn.K));
-      i8_sum_kernel<<<(unsigned)ceil_div_host64(rows * dn.N / 8, 256), 256, 0, stream>>>(dn);
     }
   }
   if (!dn_split)
-    i8_gemm_kernel<Op, t.bm, DNN, WM, WN, DNNS, t.per_cu, PP, false>
-        <<<grid(dn_tiles), NTH, 0, stream>>>(dn, (int)(rows * dn.K));
+    i8_gemm_kernel<Op, t.bm, DNN, WM, WN, DNNS, t.dn_per_cu, PP, false>
+        <<<i8_grid(dn_tiles, t.dn_per_cu * num_cus), NTH, 0, stream>>>(dn, (int)(rows * dn.K));
 }
 
 // What a call is cut into: the tile, and for 32-row tiles the parts of each pass's K and the stages of a part.
@@ -512,10 +575,10 @@ double tile_cost(int i, int64_t rows_max, int El, int H, int F) {
 }
 
 // Parts of a pass's K with 32-row tiles: as many as give every CU its workgroups, of at least 8 stages each, as the parts' sums
-// take a launch of their own.
-void split_k(int64_t tiles, int K, int& split, int& stages) {
+// take a launch of their own (gate/up) or a wait for the last part; at most `most` stages.
+void split_k(int64_t tiles, int K, int most, int& split, int& stages) {
   const int nk = ceil_div_host(K, 128);
-  split = (int)std::max<int64_t>(1, std::min<int64_t>(kTiles[0].per_cu * kPlanCus / tiles, nk / 8));
+  split = (int)std::max<int64_t>(ceil_div_host(nk, most), std::min<int64_t>(kTiles[0].per_cu * kPlanCus / tiles, nk / 8));
   stages = ceil_div_host(nk, split);
   split = ceil_div_host(nk, stages);  // every part has stages
 }
@@ -523,12 +586,12 @@ void split_k(int64_t tiles, int K, int& split, int& stages) {
 I8Plan i8_plan(int64_t rows_max, int El, int H, int F) {
   I8Plan p{0, 1, 0, 1, 0};
   if (rows_max == 0) return p;
-  for (int i = 1; i < 4; ++i)
+  for (int i = 1; i < 4 && rows_max > kFewRows; ++i)
     if (tile_cost(i, rows_max, El, H, F) < tile_cost(p.tile, rows_max, El, H, F)) p.tile = i;
   if (p.tile == 0) {
     const int64_t m = row_tiles(rows_max, El, 32);
-    split_k(m * ceil_div_host(F, kTiles[0].gu_cols), H, p.gu_split, p.gu_stages);
-    split_k(m * ceil_div_host(H, kTiles[0].dn_cols), F, p.dn_split, p.dn_stages);
+    split_k(m * ceil_div_host(F, kTiles[0].gu_cols), H, 1 << 30, p.gu_split, p.gu_stages);
+    split_k(m * ceil_div_host(H, kTiles[0].dn_cols), F, rows_max <= kFewRows ? kFewStages : 1 << 30, p.dn_split, p.dn_stages);
   }
   return p;
 }
@@ -536,10 +599,12 @@ I8Plan i8_plan(int64_t rows_max, int El, int H, int F) {
 int h_tiles(const I8Plan& p, int F) { return ceil_div_host(F, kTiles[p.tile].gu_cols); }
 
 // the workspace: plan, row map, h, its tiles' maxima, its codes and scales, the parts of a split pass (gate/up's are
-// done with before the down pass writes its own)
+// done with before the down pass writes its own) and the down tiles' tickets
 struct I8Scratch {
-  size_t plan, perm, h, top, codes, scale, partial, total;
+  size_t plan, perm, h, top, codes, scale, partial, ticket, total;
+  int tickets;
 };
+int64_t row_tiles_most(int64_t rows, int El, int bm) { return ceil_div_host64(rows, bm) + std::min<int64_t>(El, rows); }
 I8Scratch i8_scratch(int64_t rows, int El, int H, int F, const I8Plan& p) {
   I8Scratch s;
   size_t at = 0;
@@ -554,8 +619,12 @@ I8Scratch i8_scratch(int64_t rows, int El, int H, int F, const I8Plan& p) {
   s.top = take((size_t)rows * (size_t)h_tiles(p, F) * sizeof(uint32_t));
   s.codes = take((size_t)rows * (size_t)F);
   s.scale = take((size_t)rows * sizeof(float));
-  s.partial = take(std::max(p.gu_split > 1 ? (size_t)p.gu_split * 2 * (size_t)F : 0,
-                            p.dn_split > 1 ? (size_t)p.dn_split * (size_t)H : 0) * (size_t)rows * sizeof(int));
+  // down: 32 x 64 sums a tile and part
+  const int64_t dn_tiles = p.dn_split > 1 ? row_tiles_most(rows, El, 32) * ceil_div_host(H, kTiles[0].dn_cols) : 0;
+  s.tickets = (int)dn_tiles;
+  s.partial = take(std::max(p.gu_split > 1 ? (size_t)p.gu_split * 2 * (size_t)F * (size_t)rows : 0,
+                            (size_t)dn_tiles * p.dn_split * 32 * kTiles[0].dn_cols) * sizeof(int));
+  s.ticket = take((size_t)s.tickets * sizeof(int));
   s.total = at;
   return s;
 }
@@ -612,6 +681,8 @@ hipError_t launch_expert_mlp_i8(const int8_t* send_q, const float* send_scale, c
   gu.split_stages = p.gu_stages;
   gu.partial = reinterpret_cast<int*>(ws + at.partial);
   gu.partial_stride = rows * 2 * F;
+  gu.zero = reinterpret_cast<int*>(ws + at.ticket);
+  gu.zero_n = at.tickets;
   gu.row_start = row_start;
   gu.tile_start = tile_start;
   gu.El = El;
@@ -631,8 +702,11 @@ hipError_t launch_expert_mlp_i8(const int8_t* send_q, const float* send_scale, c
   dn.split = p.dn_split;
   dn.split_stages = p.dn_stages;
   dn.partial = reinterpret_cast<int*>(ws + at.partial);
-  dn.partial_stride = rows * L.H;
-  const int64_t mtiles = ceil_div_host64(rows, kTiles[p.tile].bm) + std::min<int64_t>(El, rows);
+  dn.ticket = reinterpret_cast<int*>(ws + at.ticket);
+  dn.h = gu.h;
+  dn.h_top = gu.h_top;
+  dn.h_tiles = gu.h_tiles;
+  const int64_t mtiles = row_tiles_most(rows, El, kTiles[p.tile].bm);
   if (p.tile == 0) launch_gemms<0, OpI16, 1, 4, 3, 4>(gu, dn, rows, mtiles, num_cus, stream);
   else if (p.tile == 1) launch_gemms<1, OpI32, 2, 2, 3, 3>(gu, dn, rows, mtiles, num_cus, stream);
   else if (p.tile == 2) launch_gemms<2, OpI32, 2, 4, 3, 3>(gu, dn, rows, mtiles, num_cus, stream);

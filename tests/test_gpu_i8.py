@@ -150,6 +150,11 @@ CASES = [
     ("one_row", [1, 0, 0, 0], 1, 1, 1, 1, 16, 16, 32, False, False),
     ("empty", [0, 0, 0, 0], 4, 2, 1, 4, 64, 32, 32, False, False),
     ("ranks_ragged", [3, 0, 17, 1, 16, 2, 0, 15], 40, 2, 4, 17, 144, 80, 32, False, False),
+    # at most eight rows: the down pass makes h's codes itself, in parts of at most 32 stages
+    ("few_wide", [1, 0, 1, 0], 1, 2, 1, 1, 272, 8208, 32, False, True),
+    ("few_ranks", [1, 0, 2, 0, 0, 1, 1, 0, 1, 0, 0, 2], 4, 2, 3, 4, 1040, 1424, 32, False, False),
+    ("few_tall", [8, 0], 8, 1, 1, 8, 2064, 4112, 32, True, True),
+    ("nine", [9, 0], 9, 1, 1, 9, 2064, 4112, 32, True, True),
     ("rows_16_32", [16, 33, 32, 31], 64, 2, 1, 33, 544, 288, 32, False, False),
     ("wide", [9, 23], 32, 1, 1, 32, 1184, 736, 32, False, False),
     # few tiles and a wide K: a pass is split, its last part shorter; with two ranks
