@@ -687,11 +687,17 @@ def _opt(t: Optional[torch.Tensor], name: str, dtype, shape, dev: int) -> Option
     return None if t is None else _arg(t, name, dtype, shape, dev)
 
 
-def _layout_args(L: Layout, names, dev: int) -> None:
-    """Checks the layout arrays that a call's kernels read or write."""
-    shapes = {"expert_offset": (L.E + 1,), "row_token": (L.rows_max,), "row_slot": (L.rows_max,), "pair_row": (L.T, L.k)}
+def _layout(L: Layout, names, dev: int) -> _CLayout:
+    """The C descriptor, after checks of the arrays that a call's kernels read or write."""
     for name in names:
-        _arg(getattr(L, name), "layout." + name, torch.int32, shapes.get(name, (L.E,)), dev)
+        t = getattr(L, name)
+        shape = ((L.E + 1,) if name == "expert_offset" else (L.T, L.k) if name == "pair_row" else
+                 (L.E,) if name[0] == "e" else (L.rows_max,))
+        if t.dtype is not torch.int32 or t.shape != shape or t.get_device() != dev or not t.is_contiguous():
+            _arg(t, "layout." + name, torch.int32, shape, dev)  # says which
+    return _CLayout(L.T, L.k, L.E, L.R, L.C, L.H, L.expert_count.data_ptr() or None, L.expert_kept.data_ptr() or None,
+                    L.expert_overflow.data_ptr() or None, L.expert_offset.data_ptr() or None,
+                    L.row_token.data_ptr() or None, L.row_slot.data_ptr() or None, L.pair_row.data_ptr() or None)
 
 
 _LAYOUT_ALL = ("expert_count", "expert_kept", "expert_overflow", "expert_offset", "row_token", "row_slot", "pair_row")
@@ -723,9 +729,8 @@ def moe_dispatch_i8(x: torch.Tensor, topk_ids: torch.Tensor, layout: Layout, sen
     """moe_dispatch with int8 send rows: codes [rows_max, H] and one float32 scale per row. x must be bf16."""
     dev = _device(x, "x")
     L = layout
-    _layout_args(L, _LAYOUT_ALL, dev)
+    cl = _layout(L, _LAYOUT_ALL, dev)
     p_ws, n_ws, ws = _scratch(_size("moe_dispatch_workspace_bytes", L.T, L.k, L.E), workspace, dev, stream)
-    cl = L.c_struct()
     st = load_library().moe_dispatch_i8(
         _arg(x, "x", torch.bfloat16, (L.T, L.H), dev), MOE_BF16, _arg(topk_ids, "topk_ids", torch.int32, (L.T, L.k), dev),
         ctypes.byref(cl), _arg(send_q, "send_q", torch.int8, (L.rows_max, L.H), dev),
@@ -743,10 +748,9 @@ def moe_expert_mlp_i8(send_q: torch.Tensor, send_scale: torch.Tensor, layout: La
     L = layout
     El, F = L.E // L.R, gu_codes.shape[1] // 2
     i8, f32 = torch.int8, torch.float32
-    _layout_args(L, ("expert_kept", "expert_offset"), dev)
+    cl = _layout(L, ("expert_kept", "expert_offset"), dev)
     need = _size("moe_expert_mlp_i8_workspace_bytes", L.T, L.k, L.E, L.R, L.C, L.H, F)
     p_ws, n_ws, ws = _scratch(need, workspace, dev, stream)
-    cl = L.c_struct()
     st = load_library().moe_expert_mlp_i8(
         _arg(send_q, "send_q", i8, (L.rows_max, L.H), dev), _arg(send_scale, "send_scale", f32, (L.rows_max,), dev),
         ctypes.byref(cl), _arg(gu_codes, "gu_codes", i8, (El, 2 * F, L.H), dev),
@@ -788,8 +792,7 @@ def moe_combine_backward(dy: torch.Tensor, out_buf: torch.Tensor, layout: Layout
     """Gradients of moe_combine: d_topk_w [T, k], and d_out_buf [rows_max, H] unless it is left out."""
     dev = _device(dy, "dy")
     L, f32 = layout, torch.float32
-    _layout_args(L, ("pair_row",), dev)
-    cl = L.c_struct()
+    cl = _layout(L, ("pair_row",), dev)
     st = load_library().moe_combine_backward(
         _arg(dy, "dy", dy.dtype, (L.T, L.H), dev), _dtype_code(dy),
         _arg(out_buf, "out_buf", dy.dtype, (L.rows_max, L.H), dev), ctypes.byref(cl),

@@ -117,9 +117,12 @@ __device__ __forceinline__ int part_sum(const BalanceArgs& a, int64_t s, int64_t
 // A workgroup takes `tokens` consecutive tokens; where they belong to several sequences it goes through these in turn, with
 // the sequence's f in LDS. A group loads U tokens at once: a large batch is one such round, and its loads are what it waits for
 // (one token after another: 30 us for 16384 x 256, 14 with four at once).
-template <int G, int VW, int NV>
+// MANY: more than kFewSeqs sequences, whose tokens would be few at a time: a group finds its token's sequence and reads its f
+// itself (59 tokens in 60 sequences: 37 us one after another, 12 so).
+constexpr int kFewSeqs = 8;
+template <int G, int VW, int NV, bool MANY>
 __global__ __launch_bounds__(NTH) void balance_rows_kernel(BalanceArgs a, int tokens) {
-  constexpr int TPP = NTH / G, U = NV > 2 ? 2 : 4;  // tokens per pass, passes at once
+  constexpr int TPP = NTH / G, U = MANY ? 1 : NV > 2 ? 2 : 4;  // tokens per pass, passes at once
   __shared__ float s_f[MOE_MAX_EXPERTS];
   __shared__ double s_sum[NW];
   __shared__ int s_n, s_used, s_last;
@@ -133,109 +136,140 @@ __global__ __launch_bounds__(NTH) void balance_rows_kernel(BalanceArgs a, int to
     for (int s = tid; s < a.S; s += NTH) used += part_sum(a, s, a.E) > 0;
     if (used) atomicAdd(&s_used, used);
   }
-  // the sequence of the first token: the last one that begins at or before it
-  int s = 0;
-  for (int hi = a.S; hi - s > 1;) {
-    const int mid = (s + hi) >> 1;
-    if (a.seq_offset[mid] <= t_begin) s = mid;
-    else hi = mid;
-  }
+  // softmax, loss and gradient of token t, whose logits are x; f and factor are its sequence's
   double sum = 0.0;
-  int t0 = t_begin;
-  while (t0 < t_end) {
-    int begin = 0, end = 0;
-    if (s < a.S) seq_range(a, s, begin, end);
-    // tokens from t0 on that share a sequence, or share having none
-    int t1 = t_end;
-    bool in = false;
-    if (s < a.S) {
-      in = t0 >= begin && t0 < end;
-      t1 = in ? min(t_end, end) : t0 < begin ? min(t_end, begin) : t0;
-    }
-    if (t1 > t0) {
-      __syncthreads();  // s_f has been read
-      if (in) {
-        for (int e = tid; e <= a.E; e += NTH) {
-          const int c = part_sum(a, s, e);
-          if (e < a.E) s_f[e] = (float)c;
-          else s_n = c;
+  auto token = [&](int t, bool write, bool live, float (&x)[NV][VW], const float (&f)[NV][VW], float factor) {
+    float m = -INFINITY;
+#pragma unroll
+    for (int j = 0; j < NV; ++j)
+#pragma unroll
+      for (int q = 0; q < VW; ++q) m = fmaxf(m, x[j][q]);
+    m = group_max<G>(m);
+    const float base = m == -INFINITY ? 0.f : m;  // every logit -inf: p is 0 and the token adds nothing
+    float z = 0.f, d = 0.f;
+#pragma unroll
+    for (int j = 0; j < NV; ++j)
+#pragma unroll
+      for (int q = 0; q < VW; ++q) {
+        x[j][q] = expf(x[j][q] - base);
+        z += x[j][q];
+        d = fmaf(x[j][q], f[j][q], d);
+      }
+    z = group_sum<G>(z);
+    d = group_sum<G>(d);
+    const float iz = z > 0.f ? 1.f / z : z == 0.f ? 0.f : z;  // NaN stays NaN
+    const float dot = d * iz;
+    if (gl == 0 && live) sum += (double)(factor * dot);
+    if (a.d_logits && write) {
+      float* out = a.d_logits + (int64_t)t * a.E;
+#pragma unroll
+      for (int j = 0; j < NV; ++j) {
+        const int e = (gl + j * G) * VW;
+        if (e < a.E) {
+          float o[VW];
+#pragma unroll
+          for (int q = 0; q < VW; ++q) o[q] = live ? factor * (x[j][q] * iz) * (f[j][q] - dot) : 0.f;
+          if constexpr (VW == 4) st16_nt(out + e, pack(o));
+          else out[e] = o[0];
         }
       }
-      __syncthreads();
-      const int n = in ? s_n : 0;
+    }
+  };
+  auto load = [&](int t, bool live, float (&x)[NV][VW]) {
+    const float* row = a.logits + (int64_t)t * a.E;
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      const int e = (gl + j * G) * VW;
+      if constexpr (VW == 4) {
+        u32x4 v{0xff800000u, 0xff800000u, 0xff800000u, 0xff800000u};
+        if (live && e < a.E) v = ld16_nt(row + e);
+        unpack(v, x[j]);
+      } else {
+        x[j][0] = live && e < a.E ? row[e] : -INFINITY;
+      }
+    }
+  };
+  if constexpr (MANY) {
+    __syncthreads();  // s_used
+    for (int t = t_begin + tid / G; t < t_end; t += TPP) {
+      int s = 0;  // the last sequence that begins at or before the token
+      for (int hi = a.S; hi - s > 1;) {
+        const int mid = (s + hi) >> 1;
+        if (a.seq_offset[mid] <= t) s = mid;
+        else hi = mid;
+      }
+      int begin, end;
+      seq_range(a, s, begin, end);
+      const int n = t >= begin && t < end ? a.part[(int64_t)s * (a.E + 1) + a.E] : 0;
+      const bool live = n > 0 && (!a.mask || a.mask[t] != 0);
       const float unit = n > 0 ? 1.f / ((float)a.k * (float)n) : 0.f;
-      const float factor = n > 0 ? a.weight * (float)a.E / ((float)n * (float)(a.S > 1 ? s_used : 1)) : 0.f;
-      float f[NV][VW];
+      float x[NV][VW], f[NV][VW];
+      load(t, live, x);
 #pragma unroll
       for (int j = 0; j < NV; ++j)
 #pragma unroll
         for (int q = 0; q < VW; ++q) {
           const int e = (gl + j * G) * VW + q;
-          f[j][q] = n > 0 && e < a.E ? s_f[e] * unit : 0.f;
+          f[j][q] = n > 0 && e < a.E ? (float)a.part[(int64_t)s * (a.E + 1) + e] * unit : 0.f;
         }
-      for (int tu = t0 + tid / G; tu < t1; tu += TPP * U) {
-        float x[U][NV][VW];
-        bool live[U];
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-          const int t = tu + u * TPP;
-          live[u] = n > 0 && t < t1 && (!a.mask || a.mask[t] != 0);
-          const float* row = a.logits + (int64_t)t * a.E;
-#pragma unroll
-          for (int j = 0; j < NV; ++j) {
-            const int e = (gl + j * G) * VW;
-            if constexpr (VW == 4) {
-              u32x4 v{0xff800000u, 0xff800000u, 0xff800000u, 0xff800000u};
-              if (live[u] && e < a.E) v = ld16_nt(row + e);
-              unpack(v, x[u][j]);
-            } else {
-              x[u][j][0] = live[u] && e < a.E ? row[e] : -INFINITY;
-            }
-          }
-        }
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-          const int t = tu + u * TPP;
-          float m = -INFINITY;
-#pragma unroll
-          for (int j = 0; j < NV; ++j)
-#pragma unroll
-            for (int q = 0; q < VW; ++q) m = fmaxf(m, x[u][j][q]);
-          m = group_max<G>(m);
-          const float base = m == -INFINITY ? 0.f : m;  // every logit -inf: p is 0 and the token adds nothing
-          float z = 0.f, d = 0.f;
-#pragma unroll
-          for (int j = 0; j < NV; ++j)
-#pragma unroll
-            for (int q = 0; q < VW; ++q) {
-              x[u][j][q] = expf(x[u][j][q] - base);
-              z += x[u][j][q];
-              d = fmaf(x[u][j][q], f[j][q], d);
-            }
-          z = group_sum<G>(z);
-          d = group_sum<G>(d);
-          const float iz = z > 0.f ? 1.f / z : z == 0.f ? 0.f : z;  // NaN stays NaN
-          const float dot = d * iz;
-          if (gl == 0 && live[u]) sum += (double)(factor * dot);
-          if (a.d_logits && t < t1) {
-            float* out = a.d_logits + (int64_t)t * a.E;
-#pragma unroll
-            for (int j = 0; j < NV; ++j) {
-              const int e = (gl + j * G) * VW;
-              if (e < a.E) {
-                float o[VW];
-#pragma unroll
-                for (int q = 0; q < VW; ++q) o[q] = live[u] ? factor * (x[u][j][q] * iz) * (f[j][q] - dot) : 0.f;
-                if constexpr (VW == 4) st16_nt(out + e, pack(o));
-                else out[e] = o[0];
-              }
-            }
-          }
-        }
-      }
-      t0 = t1;
+      token(t, true, live, x, f, n > 0 ? a.weight * (float)a.E / ((float)n * (float)s_used) : 0.f);
     }
-    if (s < a.S && t0 >= end) ++s;
+  } else {
+    // the sequence of the first token: the last one that begins at or before it
+    int s = 0;
+    for (int hi = a.S; hi - s > 1;) {
+      const int mid = (s + hi) >> 1;
+      if (a.seq_offset[mid] <= t_begin) s = mid;
+      else hi = mid;
+    }
+    int t0 = t_begin;
+    while (t0 < t_end) {
+      int begin = 0, end = 0;
+      if (s < a.S) seq_range(a, s, begin, end);
+      // tokens from t0 on that share a sequence, or share having none
+      int t1 = t_end;
+      bool in = false;
+      if (s < a.S) {
+        in = t0 >= begin && t0 < end;
+        t1 = in ? min(t_end, end) : t0 < begin ? min(t_end, begin) : t0;
+      }
+      if (t1 > t0) {
+        __syncthreads();  // s_f has been read
+        if (in) {
+          for (int e = tid; e <= a.E; e += NTH) {
+            const int c = part_sum(a, s, e);
+            if (e < a.E) s_f[e] = (float)c;
+            else s_n = c;
+          }
+        }
+        __syncthreads();
+        const int n = in ? s_n : 0;
+        const float unit = n > 0 ? 1.f / ((float)a.k * (float)n) : 0.f;
+        const float factor = n > 0 ? a.weight * (float)a.E / ((float)n * (float)(a.S > 1 ? s_used : 1)) : 0.f;
+        float f[NV][VW];
+#pragma unroll
+        for (int j = 0; j < NV; ++j)
+#pragma unroll
+          for (int q = 0; q < VW; ++q) {
+            const int e = (gl + j * G) * VW + q;
+            f[j][q] = n > 0 && e < a.E ? s_f[e] * unit : 0.f;
+          }
+        for (int tu = t0 + tid / G; tu < t1; tu += TPP * U) {
+          float x[U][NV][VW];
+          bool live[U];
+#pragma unroll
+          for (int u = 0; u < U; ++u) {
+            const int t = tu + u * TPP;
+            live[u] = n > 0 && t < t1 && (!a.mask || a.mask[t] != 0);
+            load(t, live[u], x[u]);
+          }
+#pragma unroll
+          for (int u = 0; u < U; ++u) token(tu + u * TPP, tu + u * TPP < t1, live[u], x[u], f, factor);
+        }
+        t0 = t1;
+      }
+      if (s < a.S && t0 >= end) ++s;
+    }
   }
   // counts of the whole batch, a slice per workgroup
   for (int64_t i = (int64_t)blockIdx.x * NTH + tid; i < (int64_t)a.S * a.E; i += (int64_t)gridDim.x * NTH) {
@@ -275,6 +309,7 @@ __global__ __launch_bounds__(NTH) void balance_rows_kernel(BalanceArgs a, int to
 // Tokens per workgroup of balance_rows: a workgroup for every CU. More of them would queue for the one ticket.
 constexpr int kMaxGroups = 256;
 int rows_per_group(int T) { return std::max(16, ceil_div_host(T, kMaxGroups)); }
+static_assert(kMaxSplits / (kFewSeqs + 1) <= 1, "many sequences are not counted in parts");
 int count_splits(int T, int S) { return std::max(1, std::min(kMaxSplits / S, T / 256)); }
 
 }  // namespace
@@ -309,7 +344,11 @@ hipError_t launch_balance(const float* logits, const int* ids, const int* seq_of
   balance_count_kernel<<<dim3(a.splits, std::min(S, 65535)), NTH, 0, stream>>>(a);
   const hipError_t st = hipGetLastError();
   if (st != hipSuccess) return st;
-#define MOE_BALANCE(G, VW, NV) balance_rows_kernel<G, VW, NV><<<groups, NTH, 0, stream>>>(a, tokens)
+#define MOE_BALANCE(G, VW, NV)                                                             \
+  do {                                                                                    \
+    if (S > kFewSeqs) balance_rows_kernel<G, VW, NV, true><<<groups, NTH, 0, stream>>>(a, tokens); \
+    else balance_rows_kernel<G, VW, NV, false><<<groups, NTH, 0, stream>>>(a, tokens);     \
+  } while (0)
   if (E % 4 == 0 && (reinterpret_cast<uintptr_t>(logits) & 15) == 0 && (reinterpret_cast<uintptr_t>(d_logits) & 15) == 0) {
     if (E <= 16) MOE_BALANCE(4, 4, 1);
     else if (E <= 64) MOE_BALANCE(16, 4, 1);

@@ -1,8 +1,9 @@
 // int8 rows of a matrix: codes and a scale per row from f32 or bf16 values, and back (moe.h, "int8 experts").
 //
 // Both are one pass over the data, bound by HBM. To quantise, a row's values stay in registers between its maximum and its
-// codes, so it is read once: 16 or 64 lanes or a whole workgroup take a row, as many as give each lane a few loads of
-// 16 bytes.
+// codes, so it is read once: 16 or 64 lanes or a whole workgroup of 256 or 1024 take a row, as many as give each lane a few
+// loads of 16 bytes. To expand, every load and store of a wave is one contiguous piece (with 16 codes per lane, whose values
+// went out in stores 32 or 64 bytes apart, 8 x 4096 x 7168 to bf16 took 198 us).
 #include <algorithm>
 
 #include "common.h"
@@ -13,7 +14,7 @@ namespace moe {
 
 namespace {
 
-constexpr int NTH = 256;
+constexpr int kThreads = 256;
 
 template <int N>
 __device__ __forceinline__ void store_codes(int8_t* p, const uint32_t (&w)[N]) {
@@ -24,9 +25,10 @@ __device__ __forceinline__ void store_codes(int8_t* p, const uint32_t (&w)[N]) {
 
 // TPR threads per row, up to VPT 16-byte loads of each in registers; what a row has beyond them is read twice.
 template <typename T, int TPR, int VPT>
-__global__ __launch_bounds__(NTH) void quantize_i8_kernel(const T* __restrict__ w, int64_t rows, int K,
-                                                         int8_t* __restrict__ codes, float* __restrict__ scales) {
-  constexpr int VN = Vec<T>::N, RPB = NTH / TPR;
+__global__ __launch_bounds__(TPR < kThreads ? kThreads : TPR) void quantize_i8_kernel(const T* __restrict__ w, int64_t rows,
+                                                                                     int K, int8_t* __restrict__ codes,
+                                                                                     float* __restrict__ scales) {
+  constexpr int NTH = TPR < kThreads ? kThreads : TPR, VN = Vec<T>::N, RPB = NTH / TPR;
   __shared__ uint32_t s_top[NTH / 64];
   const int tid = threadIdx.x, lane = tid % TPR;
   const int nvec = K / VN;
@@ -89,6 +91,7 @@ __global__ __launch_bounds__(NTH) void quantize_i8_kernel(const T* __restrict__ 
 
 template <typename T, int TPR, int VPT>
 void launch_quantize_t(const T* w, int64_t rows, int K, int8_t* codes, float* scales, hipStream_t stream) {
+  constexpr int NTH = TPR < kThreads ? kThreads : TPR;
   const int64_t blocks = ceil_div_host64(rows, NTH / TPR);
   quantize_i8_kernel<T, TPR, VPT><<<(int)std::min<int64_t>(blocks, 1 << 20), NTH, 0, stream>>>(w, rows, K, codes, scales);
 }
@@ -100,33 +103,35 @@ void launch_quantize(const void* w, int64_t rows, int K, int8_t* codes, float* s
   if (nvec <= 32) launch_quantize_t<T, 16, 2>(p, rows, K, codes, scales, stream);
   else if (nvec <= 256) launch_quantize_t<T, 64, 4>(p, rows, K, codes, scales, stream);
   else if (nvec <= 1024) launch_quantize_t<T, 256, 4>(p, rows, K, codes, scales, stream);
-  else launch_quantize_t<T, 256, 16>(p, rows, K, codes, scales, stream);
+  else launch_quantize_t<T, 1024, 4>(p, rows, K, codes, scales, stream);
 }
 
-// 16 codes per thread: one 16-byte load, two or four 16-byte stores.
+// A thread's VN codes make one 16-byte store; U of them, a workgroup's width apart.
 template <typename T>
-__global__ __launch_bounds__(NTH) void dequantize_i8_kernel(const int8_t* __restrict__ codes,
-                                                           const float* __restrict__ scales, int64_t chunks,
-                                                           int per_row, T* __restrict__ w) {
-  for (int64_t base = (int64_t)blockIdx.x * NTH; base < chunks; base += (int64_t)gridDim.x * NTH) {
-    const int64_t at = base + threadIdx.x;
-    if (at >= chunks) return;
+__global__ __launch_bounds__(kThreads) void dequantize_i8_kernel(const int8_t* __restrict__ codes,
+                                                                const float* __restrict__ scales, int64_t vecs,
+                                                                int per_row, T* __restrict__ w) {
+  constexpr int VN = Vec<T>::N, U = 4, STEP = kThreads * U;
+  for (int64_t base = (int64_t)blockIdx.x * STEP; base < vecs; base += (int64_t)gridDim.x * STEP) {
     const int64_t row0 = base / per_row;  // uniform: the row of a thread is a 32-bit division from there
-    const int64_t row = row0 + ((unsigned)(base - row0 * per_row) + threadIdx.x) / (unsigned)per_row;
-    const float sc = scales[row];
-    const u32x4 c = ld16_nt(codes + at * 16);
-    float f[16];
+    const unsigned rest = (unsigned)(base - row0 * per_row);
+    u32x2 c[U];
+    float sc[U];
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+    for (int u = 0; u < U; ++u) {
+      const int64_t at = base + u * kThreads + threadIdx.x;
+      const bool in = at < vecs;
+      if constexpr (VN == 8) c[u] = in ? *reinterpret_cast<const u32x2*>(codes + at * VN) : u32x2{0u, 0u};
+      else c[u] = u32x2{in ? *reinterpret_cast<const uint32_t*>(codes + at * VN) : 0u, 0u};
+      sc[u] = in ? scales[row0 + (rest + u * kThreads + threadIdx.x) / (unsigned)per_row] : 0.f;
+    }
 #pragma unroll
-      for (int q = 0; q < 4; ++q) f[4 * i + q] = (float)(int8_t)(c[i] >> (8 * q)) * sc;
-    constexpr int VN = Vec<T>::N;
+    for (int u = 0; u < U; ++u) {
+      const int64_t at = base + u * kThreads + threadIdx.x;
+      float f[VN];
 #pragma unroll
-    for (int i = 0; i < 16 / VN; ++i) {
-      float o[VN];
-#pragma unroll
-      for (int q = 0; q < VN; ++q) o[q] = f[i * VN + q];
-      st16_nt(w + at * 16 + i * VN, pack(o));
+      for (int q = 0; q < VN; ++q) f[q] = (float)(int8_t)(c[u][q / 4] >> (8 * (q % 4))) * sc[u];
+      if (at < vecs) st16_nt(w + at * VN, pack(f));
     }
   }
 }
@@ -142,11 +147,12 @@ hipError_t launch_quantize_i8(const void* w, int bf16, int64_t rows, int K, int8
 
 hipError_t launch_dequantize_i8(const int8_t* codes, const float* scales, int64_t rows, int K, void* w, int bf16,
                                 hipStream_t stream) {
-  const int64_t chunks = rows * (K / 16);
-  const int grid = (int)std::min<int64_t>(ceil_div_host64(chunks, NTH), 1 << 22);
+  const int vn = bf16 ? 8 : 4;
+  const int64_t vecs = rows * (K / vn);
+  const int grid = (int)std::min<int64_t>(ceil_div_host64(vecs, kThreads * 4), 1 << 22);
   if (bf16)
-    dequantize_i8_kernel<bf16_t><<<grid, NTH, 0, stream>>>(codes, scales, chunks, K / 16, static_cast<bf16_t*>(w));
-  else dequantize_i8_kernel<float><<<grid, NTH, 0, stream>>>(codes, scales, chunks, K / 16, static_cast<float*>(w));
+    dequantize_i8_kernel<bf16_t><<<grid, kThreads, 0, stream>>>(codes, scales, vecs, K / vn, static_cast<bf16_t*>(w));
+  else dequantize_i8_kernel<float><<<grid, kThreads, 0, stream>>>(codes, scales, vecs, K / vn, static_cast<float*>(w));
   return hipGetLastError();
 }
 

@@ -18,6 +18,7 @@
 #include "kernels.h"
 #include "mfma.h"
 #include "tiles.h"
+#include "topk.h"
 
 namespace moe {
 
@@ -53,7 +54,18 @@ struct I8Args {
   int zero_n;
 };
 
-__device__ __forceinline__ float silu(float g) { return g / (1.0f + expf(-g)); }
+// g / (1 + e^-g). e^-g = 2^t with t = -g / ln 2 in two floats, the second as a first-order factor, so that it is off by two or
+// three steps for every g; the reciprocal is the hardware's, off by one. The library's expf and division cost a tile of the
+// gate/up pass as much as three of its stages.
+__device__ __forceinline__ float silu(float g) {
+  constexpr float kLog2e = 1.44269502162933349609375f, kLog2eLow = 1.92596299e-8f;  // 1 / ln 2 and what float leaves of it
+  const float t = g * -kLog2e;
+  const float low = fmaf(g, -kLog2eLow, fmaf(g, -kLog2e, -t));
+  const float e = __builtin_amdgcn_exp2f(t);
+  // (an infinite e takes no correction: inf - inf)
+  const float d = 1.0f + (e < INFINITY ? fmaf(e, low * 0.693147181f, e) : e);
+  return g * __builtin_amdgcn_rcpf(d);
+}
 
 // A stage's rows: 128 bytes each, 16-byte chunk c of row r at c ^ ((r >> 1) & 7), so that a fragment read touches every
 // bank once.
@@ -87,7 +99,7 @@ __global__ __launch_bounds__(WM * WN * 64, PER_CU * WM * WN / 4 > 1 ? PER_CU * W
   // the only LDS object (a second one makes the compiler wait for every load in flight before LDS reads): the stages, which
   // the output tile reuses; the tile's row scales and destination rows; the waves' row maxima; the plan's starts
   constexpr int SCALE_OFF = BODY, ROW_OFF = SCALE_OFF + BM * 4, TOP_OFF = ROW_OFF + BM * 4;
-  constexpr int PLAN_OFF = TOP_OFF + (GATED ? WN * BM * 4 : 16);
+  constexpr int PLAN_OFF = TOP_OFF + (GATED ? WN * (S / 16) * BM * 4 : 16);
   __shared__ __attribute__((aligned(1024))) unsigned char smem[PLAN_OFF + 2 * (MOE_MAX_EXPERTS + 1) * 4];
   float* s_scale = reinterpret_cast<float*>(smem + SCALE_OFF);
   int* s_row = reinterpret_cast<int*>(smem + ROW_OFF);
@@ -258,12 +270,14 @@ __global__ __launch_bounds__(WM * WN * 64, PER_CU * WM * WN / 4 > 1 ? PER_CU * W
         // stage st + 1 has to have landed when the group that runs first starts on it
         phase_end(j == PHASES - 1 && grp == 1);
         __builtin_amdgcn_s_setprio(1);
+        if (mb > 0) {  // waves without rows save the power
 #pragma unroll
-        for (int k = 0; k < KPH; ++k)
+          for (int k = 0; k < KPH; ++k)
 #pragma unroll
-          for (int i = 0; i < TM; ++i)
+            for (int i = 0; i < TM; ++i)
 #pragma unroll
-            for (int n = 0; n < NACC; ++n) Op::step(acc[i][n], frag[k][i], frag[k][TM + n]);
+              for (int n = 0; n < NACC; ++n) Op::step(acc[i][n], frag[k][i], frag[k][TM + n]);
+        }
         __builtin_amdgcn_s_setprio(0);
         phase_end(j == PHASES - 1 && grp == 0);
       };
@@ -367,30 +381,35 @@ __global__ __launch_bounds__(WM * WN * 64, PER_CU * WM * WN / 4 > 1 ? PER_CU * W
         sg[j] = w_scale[c];
         su[j] = w_scale[a.up + c];
       }
+      float* h = a.h + (int64_t)p0 * a.N;  // of the tile: 32-bit offsets from there
 #pragma unroll
-      for (int i = 0; i < TM; ++i)
+      for (int i = 0; i < TM; ++i) {
+        if (i >= mb) break;  // no rows
 #pragma unroll
         for (int q = 0; q < Op::NR; ++q) {
           const int r = wm * WTM + i * S + Op::out_row(lane, q);
           const float sr = s_scale[r];
-          uint32_t top = 0;
+          int top = 0;  // bits of |h|: positive, so they compare like integers
 #pragma unroll
           for (int j = 0; j < TN; ++j) {
-            const float g = (float)acc[i][j][q] * sr * sg[j], u = (float)acc[i][j + TN][q] * sr * su[j];
-            const float v = silu(g) * u;
+            const float v = silu((float)acc[i][j][q] * sr * sg[j]) * ((float)acc[i][j + TN][q] * sr * su[j]);
             const bool in = c_lane + j * S < a.N;
-            if (in) top = max(top, abs_bits(v));
-            if (in && r < m_rows) a.h[(int64_t)(p0 + r) * a.N + c_lane + j * S] = v;
+            if (in) top = max(top, (int)abs_bits(v));
+            if (in && r < m_rows) h[r * a.N + c_lane + j * S] = v;
           }
-#pragma unroll
-          for (int off = S / 2; off > 0; off >>= 1) top = max(top, (uint32_t)__shfl_xor((int)top, off, 64));
-          if (fr == 0) s_top[wn * BM + r] = top;
+          // over the 16 lanes of a DPP row, where they share r; the rest in LDS
+          top = max(top, dpp_i32<0xB1>(top));
+          top = max(top, dpp_i32<0x4E>(top));
+          top = max(top, dpp_i32<0x141>(top));
+          top = max(top, dpp_i32<0x140>(top));
+          if ((lane & 15) == 0) s_top[(wn * (S / 16) + fr / 16) * BM + r] = top;
         }
+      }
       lds_barrier();
       for (int r = tid; r < m_rows; r += NTH) {
         uint32_t top = 0;
 #pragma unroll
-        for (int w = 0; w < WN; ++w) top = max(top, s_top[w * BM + r]);
+        for (int w = 0; w < WN * (S / 16); ++w) top = max(top, s_top[w * BM + r]);
         a.h_top[(int64_t)(p0 + r) * a.h_tiles + nt] = top;
       }
     } else {
