@@ -361,34 +361,44 @@ __global__ __launch_bounds__(WT * 64, TI == 1 ? 4 : 2) void route_dx_kernel(Grad
   }
 }
 
-// Column sums of d_logits from those of 32 tokens: 64 columns per workgroup of eight waves, their sums added in order.
+// Column sums of d_logits from those of 32 tokens: 64 columns per workgroup of NW waves, their sums added in order.
+template <int NW>
 __device__ __forceinline__ void bias_sums(const GradArgs& a, int block, double* s) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, e = block * 64 + lane;
   double v = 0.0;
   if (e < a.r.E)
-    for (int i = wave; i < a.tb; i += 8) v += (double)a.bias_part[(int64_t)i * a.r.E + e];
+    for (int i0 = wave; i0 < a.tb; i0 += 8 * NW) {  // eight loads in flight
+      float p[8];
+#pragma unroll
+      for (int q = 0; q < 8; ++q) p[q] = i0 + q * NW < a.tb ? a.bias_part[(int64_t)(i0 + q * NW) * a.r.E + e] : 0.f;
+#pragma unroll
+      for (int q = 0; q < 8; ++q) v += (double)p[q];
+    }
   s[wave * 64 + lane] = v;
   __syncthreads();
   if (wave == 0 && e < a.r.E) {
     v = 0.0;
-    for (int i = 0; i < 8; ++i) v += s[i * 64 + lane];
+    for (int i = 0; i < NW; ++i) v += s[i * 64 + lane];
     a.r.d_bias[e] = (float)v;
   }
 }
 __global__ __launch_bounds__(512) void route_dbias_kernel(GradArgs a) {
   __shared__ double s[512];
-  bias_sums(a, blockIdx.x, s);
+  bias_sums<8>(a, blockIdx.x, s);
 }
 
 // d_w_router: eight waves, WE along the experts (32 each) and 8 / WE along the tokens, whose sums are added in the end; 128
 // columns of x. Tokens go in chunks of 16 steps: a thread loads 8 tokens x 16 bytes of the next chunk while this one is
-// multiplied. In LDS the chunk is fragments [16 steps][4 column blocks]; in a fragment the 16 bytes of column c are at place
+// multiplied. In LDS the chunk is fragments [step][4 column blocks]; in a fragment the 16 bytes of column c are at place
 // c ^ (its group of 8 in the 128 columns), so that the writes of a wave, at a stride of 4 or 8 columns, touch all banks.
-// Workgroups past the column tiles add up the bias.
-constexpr int kDwCols = 128, kDwSteps = 16, kDwChunkBytes = kDwSteps * 4 * kFrag;
+// Workgroups past the column tiles add up the bias. A second chunk of x on its way changed nothing (16000 tokens, H 4096, 8
+// experts: 43 us, 3.1 TB/s); two workgroups of four waves per CU were slower (52).
+constexpr int kDwCols = 128;
+constexpr int kDwSteps = 16, kDwChunkBytes = kDwSteps * 4 * kFrag;
 template <typename G, int WE>
 __global__ __launch_bounds__(512) void route_dw_kernel(GradArgs a, int col_tiles) {
-  constexpr int KW = 8 / WE, P = G::PARTS, VN = Vec<typename G::X>::N, CT = kDwSteps * G::STEP;
+  constexpr int NW = 8, KW = NW / WE, P = G::PARTS, VN = Vec<typename G::X>::N, CT = kDwSteps * G::STEP;
+  static_assert(CT / 8 * (kDwCols / VN) == NW * 64, "a thread loads 8 tokens x 16 bytes of a chunk");
   extern __shared__ __attribute__((aligned(1024))) unsigned char s_x[];  // two chunks
   const RouteBackward& r = a.r;
   const int tid = threadIdx.x, lane = tid & 63;
@@ -397,7 +407,7 @@ __global__ __launch_bounds__(512) void route_dw_kernel(GradArgs a, int col_tiles
   const int e_tiles = (a.eb + 7) / 8, units = col_tiles * e_tiles * a.splits, per = (units + 7) >> 3;
   const int unit = (blockIdx.x & 7) * per + (blockIdx.x >> 3);
   if ((int)blockIdx.x >= per * 8) {
-    bias_sums(a, blockIdx.x - per * 8, reinterpret_cast<double*>(s_x));
+    bias_sums<NW>(a, blockIdx.x - per * 8, reinterpret_cast<double*>(s_x));
     return;
   }
   if (unit >= units) return;
@@ -532,11 +542,17 @@ __global__ __launch_bounds__(NTH) void route_dw_sum_kernel(const float* __restri
   const int64_t at = ((int64_t)blockIdx.x * NTH + threadIdx.x) * 4;
   if (at >= n) return;
   float v[4] = {0.f, 0.f, 0.f, 0.f};
-  for (int s = 0; s < splits; ++s) {
-    float p[4];
-    unpack(ld16_nt(partial + s * n + at), p);
+  for (int s0 = 0; s0 < splits; s0 += 8) {  // eight loads in flight
+    u32x4 raw[8];
 #pragma unroll
-    for (int q = 0; q < 4; ++q) v[q] += p[q];
+    for (int i = 0; i < 8; ++i) raw[i] = s0 + i < splits ? ld16_nt(partial + (s0 + i) * n + at) : u32x4{0u, 0u, 0u, 0u};
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      float p[4];
+      unpack(raw[i], p);
+#pragma unroll
+      for (int q = 0; q < 4; ++q) v[q] += p[q];
+    }
   }
   st16(out + at, pack(v));
 }
