@@ -473,8 +473,8 @@ __global__ __launch_bounds__(SCATTER_WAVES * 64) void dispatch_scatter_fp8_kerne
 // ---- int8 rows ----
 // One workgroup quantises token row t of x (i8.h) and stores codes and scale to its kept rows (lane j < k of every wave holds
 // the row of pair (t, j), -1 if dropped). Up to VPT 16-byte slices per thread stay in registers between the row's maximum and
-// its codes; what a longer row has beyond them is read twice. A wave per token took 22 us where this takes 10 (128 tokens,
-// H 7168), and 61 against 58 for 4096 tokens.
+// its codes; what a longer row has beyond them is read twice. A wave per token took 22 us where this takes 15 (128 tokens,
+// H 7168), and 61 against 53 for 4096 tokens.
 template <int VPT>
 __device__ __forceinline__ void quantize_token_row(const bf16_t* __restrict__ x, int t, int H, int row,
                                                    int8_t* __restrict__ send_q, float* __restrict__ send_scale) {

@@ -218,6 +218,53 @@ def test_route_backward_wide_ranges(dtype):
         assert within(got[name].cpu(), ref, bound, got[name].dtype) <= 1.0, name
 
 
+def test_route_backward_of_tiny_and_huge_tokens():
+    """Tokens and columns whose size is far from one (subnormal gradients among them): fp16's powers of two are each's own."""
+    g = torch.Generator().manual_seed(31)
+    T, H, E = 70, 264, 24
+    rows = torch.tensor([-140.0, -126.0, -100.0, -60.0, 0.0, 60.0, 90.0])[torch.arange(T) % 7].unsqueeze(1)
+    cols = torch.tensor([-30.0, -20.0, 0.0, 20.0, 30.0, -126.0])[torch.arange(H) % 6]
+    d_in = (torch.randn(T, E, generator=g).double() * torch.exp2(rows.double())).float()
+    d_in[5] = 0.0
+    wr = (torch.randn(E, H, generator=g).double() * torch.exp2(cols.double())).float()
+    wr[:, 7] = 0.0
+    x = torch.randn(T, H, generator=g).to(BF16)
+    d_x = torch.empty(T, H, dtype=BF16, device=DEV)
+    ids, w = torch.zeros(T, 1, dtype=torch.int32), torch.ones(T, 1)
+    moe.moe_route_backward(x.to(DEV), wr.to(DEV), ids.to(DEV), w.to(DEV), None, d_in.to(DEV), torch.empty(T, E, device=DEV),
+                           d_x=d_x)
+    ref, bound = route_backward(x.double(), wr.double(), ids.long(), w.double(), None, d_in.double(), True)["d_x"]
+    # float32 sums of the scaled products are exact to U; a result that is subnormal in bf16 is off by half its step there
+    assert within(d_x.cpu(), ref, bound + 2.0 ** -134, BF16) <= 1.0
+
+
+def test_route_backward_non_finite_stays_apart():
+    g = torch.Generator().manual_seed(32)
+    T, H, E = 40, 136, 12
+    for dt in (F32, BF16):
+        d_in, wr = torch.randn(T, E, generator=g), torch.randn(E, H, generator=g)
+        x = torch.randn(T, H, generator=g).to(dt)
+        d_in[3, 5], d_in[17, 2] = float("inf"), float("nan")
+        wr[4, 9] = float("inf")
+        x[20, 30] = float("nan")
+        ids, w = torch.zeros(T, 1, dtype=torch.int32), torch.ones(T, 1)
+        d_x = torch.empty(T, H, dtype=dt, device=DEV)
+        d_wr, d_b = torch.empty(E, H, device=DEV), torch.empty(E, device=DEV)
+        moe.moe_route_backward(x.to(DEV), wr.to(DEV), ids.to(DEV), w.to(DEV), None, d_in.to(DEV),
+                               torch.empty(T, E, device=DEV), d_x=d_x, d_w_router=d_wr, d_bias=d_b)
+        bad = ~torch.isfinite(d_x.float()).cpu()
+        assert bad[3].all() and bad[17].all() and bad[:, 9].all()
+        keep = torch.ones(T, H, dtype=torch.bool)
+        keep[3], keep[17], keep[:, 9] = False, False, False
+        assert not bad[keep].any()
+        bad = ~torch.isfinite(d_wr).cpu()
+        assert bad[5].all() and bad[2].all() and bad[:, 30].all()
+        keep = torch.ones(E, H, dtype=torch.bool)
+        keep[5], keep[2], keep[:, 30] = False, False, False
+        assert not bad[keep].any()
+        assert torch.isfinite(d_b).cpu().nonzero().numel() == E - 2
+
+
 def test_route_backward_repeated_and_outside_ids():
     g = torch.Generator().manual_seed(6)
     T, H, E, k = 20, 64, 8, 3

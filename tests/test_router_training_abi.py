@@ -34,6 +34,7 @@ def test_balance_refusals(lib):
     assert call(S=0, off=P) == INVALID
     assert call(S=2) == INVALID                      # several sequences need their offsets
     assert call(T=1 << 30, k=2) == UNSUPPORTED
+    assert call(T=(1 << 30) + 1, k=1) == UNSUPPORTED
     assert call(S=1 << 30, off=P) == UNSUPPORTED
     assert call(wsb=16) == INVALID
     for a in ("lg", "ids", "loss", "count", "ws"):
@@ -43,7 +44,7 @@ def test_balance_refusals(lib):
 
 
 def test_combine_backward_refusals(lib):
-    def call(dy=P, dt=moe.MOE_BF16, out=P, w=P, dw=P, do=P, **kw):
+    def call(dy=P, dt=moe.MOE_BF16, out=P, w=P, dw=P, do=ctypes.c_void_p(0x2000), **kw):
         cl = _layout(**kw)
         return lib.moe_combine_backward(dy, dt, out, ctypes.byref(cl), w, dw, do, None)
     assert call(dt=4) == UNSUPPORTED
@@ -53,6 +54,7 @@ def test_combine_backward_refusals(lib):
         assert call(**{a: None}) == INVALID
     for a in ("dy", "out", "w", "dw", "do"):
         assert call(**{a: ODD}) == INVALID
+    assert call(do=P) == INVALID                     # not in place
     assert call(T=0, dy=None, out=None, w=None, dw=None, do=None) == 0
     assert lib.moe_combine_backward(P, moe.MOE_BF16, P, None, P, P, P, None) == INVALID
 
