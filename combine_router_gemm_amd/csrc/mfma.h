@@ -5,6 +5,10 @@
 
 namespace moe {
 
+typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
+typedef int i32x4 __attribute__((ext_vector_type(4)));
+typedef int i32x16 __attribute__((ext_vector_type(16)));
+
 // MFMA instruction choices. Each op multiplies S x KS by KS x S fragments into an S x S fp32 tile.
 // Lane l supplies 8 consecutive K of fragment row (l % S), starting at K = (l / S) * 8; A and B use
 // the same K assignment, so any K order inside a step gives the same sum.
