@@ -23,12 +23,13 @@ constexpr int NTH = 256;
 template <typename T, int VPT>
 __global__ __launch_bounds__(NTH) void combine_backward_kernel(const T* __restrict__ dy, const T* __restrict__ out_buf,
                                                               const int* __restrict__ pair_row,
-                                                              const float* __restrict__ topk_w, int H, int k,
+                                                              const float* __restrict__ topk_w, int T_, int H, int k,
                                                               float* __restrict__ d_w, T* __restrict__ d_out) {
   constexpr int VN = Vec<T>::N;
   __shared__ float s_sum[MOE_MAX_TOPK][NTH / 64];
   const int tid = threadIdx.x;
-  const int64_t t = blockIdx.x;
+  const int64_t t = (int64_t)blockIdx.y * gridDim.x + blockIdx.x;
+  if (t >= T_) return;
   const int nvec = H / VN;
   const T* g = dy + t * H;
   u32x4 raw[VPT];
@@ -583,8 +584,9 @@ hipError_t launch_combine_backward(const void* dy, int bf16, const void* out_buf
                                    const float* topk_w, float* d_w, void* d_out, hipStream_t stream) {
   const int nvec = L.H / (bf16 ? 8 : 4);
 #define MOE_GO(TY, VPT)                                                                                            \
-  combine_backward_kernel<TY, VPT><<<L.T, NTH, 0, stream>>>(static_cast<const TY*>(dy), static_cast<const TY*>(out_buf), \
-                                                            L.pair_row, topk_w, L.H, L.k, d_w, static_cast<TY*>(d_out))
+  combine_backward_kernel<TY, VPT>                                                                                 \
+      <<<token_grid(L.T), NTH, 0, stream>>>(static_cast<const TY*>(dy), static_cast<const TY*>(out_buf), L.pair_row, topk_w, \
+                                            L.T, L.H, L.k, d_w, static_cast<TY*>(d_out))
   if (bf16) {
     if (nvec <= NTH) MOE_GO(bf16_t, 1);
     else if (nvec <= 2 * NTH) MOE_GO(bf16_t, 2);

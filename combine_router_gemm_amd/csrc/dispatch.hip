@@ -532,7 +532,9 @@ __global__ __launch_bounds__(DR_THREADS) void dispatch_scatter_i8_kernel(
     const int* __restrict__ blk_base, const int* __restrict__ pair_local, const int* __restrict__ offset,
     int* __restrict__ row_token, int* __restrict__ row_slot, int* __restrict__ pair_row, int8_t* __restrict__ send_q,
     float* __restrict__ send_scale) {
-  const int t = blockIdx.x;
+  const int64_t at = (int64_t)blockIdx.y * gridDim.x + blockIdx.x;
+  if (at >= T_) return;
+  const int t = (int)at;
   const int row = resolve_pair_row(t, lane_id(), ids, k, E, C, blk_base, pair_local, offset, row_token, row_slot, pair_row,
                                    threadIdx.x < 64);
   quantize_token_row<VPT>(x, t, H, row, send_q, send_scale);
@@ -651,9 +653,10 @@ hipError_t launch_dispatch_i8(const void* x, const int* ids, const moe_layout_t&
   const hipError_t st = launch_counts(ids, L, blk_count, pair_local, stream);
   if (st != hipSuccess || L.T == 0) return st;
 #define MOE_SCATTER_I8(VPT)                                                                                      \
-  dispatch_scatter_i8_kernel<VPT><<<L.T, DR_THREADS, 0, stream>>>(xp, ids, L.T, L.H, L.k, L.E, L.C, blk_count, \
-                                                                             pair_local, L.expert_offset, L.row_token, \
-                                                                             L.row_slot, L.pair_row, send_q, send_scale)
+  dispatch_scatter_i8_kernel<VPT><<<token_grid(L.T), DR_THREADS, 0, stream>>>(xp, ids, L.T, L.H, L.k, L.E, L.C,  \
+                                                                              blk_count, pair_local, L.expert_offset, \
+                                                                              L.row_token, L.row_slot, L.pair_row, \
+                                                                              send_q, send_scale)
   MOE_PER_WIDTH(MOE_SCATTER_I8);
 #undef MOE_SCATTER_I8
 #undef MOE_PER_WIDTH

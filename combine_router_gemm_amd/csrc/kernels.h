@@ -10,6 +10,9 @@ namespace moe {
 
 inline int ceil_div_host(int a, int b) { return (a + b - 1) / b; }
 inline int64_t ceil_div_host64(int64_t a, int64_t b) { return (a + b - 1) / b; }
+// A workgroup for each of T tokens: token blockIdx.y * gridDim.x + blockIdx.x, where that is below T. A launch holds fewer than
+// 2^32 threads in each direction.
+inline dim3 token_grid(int T) { return dim3(T < 1 << 20 ? T : 1 << 20, ceil_div_host64(T, 1 << 20)); }
 inline size_t align256(size_t n) { return (n + 255) & ~(size_t)255; }
 
 // ---- route ----

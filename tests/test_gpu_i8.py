@@ -301,6 +301,31 @@ def test_rows_past_4_gib_of_h():
         assert within(out[sel].cpu(), ref, b, torch.bfloat16) <= 1.0
 
 
+def test_more_tokens_than_a_launch_holds_in_one_direction():
+    """2^24 workgroups of 256 threads are 2^32 threads. Rows and layout against the row kernel and moe_dispatch."""
+    T, H, E, k, C = (1 << 24) + 5, 16, 3, 1, 1 << 24
+    print(f"\n[gpu] dispatch i8 and combine backward {T} {H}", flush=True)
+    g = torch.Generator(device=DEV).manual_seed(9)
+    x = torch.randn(T, H, device=DEV, generator=g).bfloat16()
+    ids = torch.randint(0, E, (T, k), device=DEV, generator=g, dtype=torch.int32)
+    L, ref = moe.Layout(T, k, E, 1, C, H, device=DEV), moe.Layout(T, k, E, 1, C, H, device=DEV)
+    q, s = torch.empty(L.rows_max, H, dtype=torch.int8, device=DEV), torch.empty(L.rows_max, device=DEV)
+    moe.moe_dispatch_i8(x, ids, L, q, s)
+    send = torch.empty(L.rows_max, H, dtype=torch.bfloat16, device=DEV)
+    moe.moe_dispatch(x, ids, ref, send)
+    assert torch.equal(L.pair_row, ref.pair_row) and torch.equal(L.row_token, ref.row_token)
+    want_q, want_s = torch.empty_like(q), torch.empty_like(s)
+    moe.moe_quantize_i8(send, want_q, want_s)
+    assert torch.equal(q, want_q) and torch.equal(s, want_s)
+    w, d_w = torch.rand(T, k, device=DEV, generator=g), torch.full((T, k), -9.0, device=DEV)
+    d_out = torch.empty_like(send)
+    moe.moe_combine_backward(x, send, L, w, d_w, d_out_buf=d_out)
+    # every product is of equal values: sums of H squares, each addition off by half a step of the sum at most
+    exact = (x.double() ** 2).sum(1)
+    assert bool(((d_w[:, 0].double() - exact).abs() <= H * 2.0 ** -24 * exact).all())
+    assert torch.equal(d_out[L.pair_row[:, 0].long()], (w * x.float()).bfloat16())
+
+
 def test_binding_refusals():
     L, q, s, weights = case([3, 2], 5, 1, 1, 5, 64, 32, 2)
     args = [q.to(DEV), s.to(DEV)] + [w.to(DEV) for w in weights]
