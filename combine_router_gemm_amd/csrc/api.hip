@@ -622,13 +622,14 @@ int moe_route_backward(const void* x, moe_dtype_t xdt, const float* w_router, co
                        size_t workspace_bytes, hipStream_t stream) {
   if (!valid_dtype(xdt)) return MOE_ERR_UNSUPPORTED;
   if (T < 0 || H < 1 || E < 1 || E > MOE_MAX_EXPERTS || k < 1 || k > MOE_MAX_TOPK || k > E) return MOE_ERR_INVALID;
-  if (H % 8 != 0 || H > 1 << 21 || (int64_t)T * E > (int64_t)INT32_MAX) return MOE_ERR_UNSUPPORTED;
+  if (H % 8 != 0 || H > 1 << 21 || T > 1 << 26 || (int64_t)T * E > (int64_t)INT32_MAX) return MOE_ERR_UNSUPPORTED;
   if (T > 0 && (!d_logits || (!d_topk_w && !d_logits_in) || (d_topk_w && (!topk_ids || !topk_w)) ||
                 (d_x && !w_router) || (d_w_router && !x)))
     return MOE_ERR_INVALID;
   if (!al16(x) || !al16(w_router) || !al4(topk_ids) || !al4(topk_w) || !al4(d_topk_w) || !al4(d_logits_in) ||
       !al4(d_logits) || !al16(d_x) || !al16(d_w_router) || !al4(d_bias) || !al16(workspace))
     return MOE_ERR_INVALID;
+  if (d_x && (d_x == x || (void*)d_w_router == d_x)) return MOE_ERR_INVALID;
   const size_t need = moe_route_backward_workspace_bytes(T, H, E, xdt);
   if (need > 0 && (!workspace || workspace_bytes < need)) return MOE_ERR_INVALID;
   moe::RouteBackward r{x, xdt == MOE_BF16, w_router, topk_ids, topk_w, d_topk_w, d_logits_in, T, H, E, k, d_logits, d_x,

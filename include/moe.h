@@ -540,8 +540,8 @@ int moe_balance_loss(const float* logits, const int32_t* topk_ids, const int32_t
  *   dy         [T, H] (xdt) gradient of y
  *   out_buf    [rows_max, H] (xdt), layout and topk_w as moe_combine took them
  *   d_topk_w   [T, k] fp32 (output)
- *   d_out_buf  [rows_max, H] (xdt, output; neither out_buf nor dy itself), or NULL: frozen experts need none. Rows >= total are left as
- *              they were.
+ *   d_out_buf  [rows_max, H] (xdt, output; neither out_buf nor dy itself), or NULL: frozen experts need none. Rows >= total
+ *              are left as they were.
  * (The gradient of moe_dispatch, d_x[t] = the sum of its kept rows' gradients, is moe_combine of them with weights of 1.)
  */
 int moe_combine_backward(const void* dy, moe_dtype_t xdt, const void* out_buf, const moe_layout_t* layout,
@@ -560,9 +560,9 @@ size_t moe_route_backward_workspace_bytes(int T, int H, int E, moe_dtype_t xdt);
  *   d_topk_w     [T, k] fp32 (moe_combine_backward), or NULL: none
  *   d_logits_in  [T, E] fp32, what other losses add (moe_balance_loss), or NULL: none; not both may be NULL
  *   d_logits     [T, E] fp32 (output); may be d_logits_in itself
- *   d_x          [T, H] (xdt), d_w_router [E, H] fp32, d_bias [E] fp32: outputs, each may be NULL
+ *   d_x          [T, H] (xdt; not x itself), d_w_router [E, H] fp32, d_bias [E] fp32: outputs, each may be NULL
  *   workspace    device scratch of at least moe_route_backward_workspace_bytes(T, H, E, xdt) bytes
- * Requires H % 8 == 0, H <= 2^21 and T * E < 2^31 (else MOE_ERR_UNSUPPORTED). T == 0 writes zeros to d_w_router and
+ * Requires H % 8 == 0, H <= 2^21, T <= 2^26 and T * E < 2^31 (else MOE_ERR_UNSUPPORTED). T == 0 writes zeros to d_w_router and
  * d_bias.
  */
 int moe_route_backward(const void* x, moe_dtype_t xdt, const float* w_router, const int32_t* topk_ids,

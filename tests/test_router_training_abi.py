@@ -143,3 +143,17 @@ def test_binding_refuses_host_tensors(lib):
         moe.moe_combine_backward(torch.zeros(4, 64), torch.zeros(8, 64), L, torch.zeros(4, 2), torch.zeros(4, 2))
     with pytest.raises(moe.MoeError):
         moe.moe_route_backward(torch.zeros(4, 64), torch.zeros(8, 64), ids, torch.zeros(4, 2), torch.zeros(4, 2), None, lg)
+
+
+def test_route_backward_more_refusals(lib):
+    at = lambda a: ctypes.c_void_p(a)
+
+    def call(x=P, dx=at(0x2000), dwr=at(0x4000), T=4, H=64, E=8):
+        return lib.moe_route_backward(x, moe.MOE_BF16, P, P, P, P, P, T, H, E, 1, P, dx, dwr, None, P, 0, None)
+    assert call() == INVALID                          # the workspace is too small, and nothing else
+    assert call(T=(1 << 26) + 1, H=8, E=1) == UNSUPPORTED
+    # a workspace that suffices: only the aliases are left to refuse
+    def full(x, dx, dwr):
+        return lib.moe_route_backward(x, moe.MOE_BF16, P, P, P, P, P, 4, 64, 8, 1, P, dx, dwr, None, P, 1 << 40, None)
+    assert full(P, P, at(0x4000)) == INVALID          # d_x in place of x, which d_w_router reads
+    assert full(P, at(0x2000), at(0x2000)) == INVALID
