@@ -55,7 +55,7 @@ struct I8Args {
 };
 
 // g / (1 + e^-g). e^-g = 2^t with t = -g / ln 2 in two floats, the second as a first-order factor, so that it is off by two or
-// three steps for every g; the reciprocal is the hardware's, off by one. The library's expf and division cost a tile of the
+// three steps; the reciprocal is the hardware's, off by one (0 for g below -87, where it is subnormal). The library's expf and division cost a tile of the
 // gate/up pass as much as three of its stages.
 __device__ __forceinline__ float silu(float g) {
   constexpr float kLog2e = 1.44269502162933349609375f, kLog2eLow = 1.92596299e-8f;  // 1 / ln 2 and what float leaves of it
