@@ -3,7 +3,9 @@
 // A sequence s has n counted tokens; expert e has count[s, e] of their choices, f = count / (k n). With p = softmax of a
 // token's logits the sequence's loss is E / n sum_t sum_e f p, and, as f does not depend on the logits, a token's gradient is
 // E / n p (f - sum f p). The loss is linear in the tokens' dot products sum f p, which the gradient needs too: nothing but
-// the counts has to be known before the one pass over the logits.
+// the counts has to be known before the one pass over the logits. f enters less its smallest value over the experts, which the
+// gradient does not depend on: where the choices are nearly even the difference then keeps its digits, and it is 0 where they are
+// even (k = E); no term is larger than without.
 //
 //   balance_count   counts of each sequence's ids, in `splits` parts that need no clearing and no float atomics
 //   balance_rows    one pass over the logits: a group of lanes per token (softmax, dot product, gradient), a double partial of
@@ -136,9 +138,28 @@ __global__ __launch_bounds__(NTH) void balance_rows_kernel(BalanceArgs a, int to
     for (int s = tid; s < a.S; s += NTH) used += part_sum(a, s, a.E) > 0;
     if (used) atomicAdd(&s_used, used);
   }
-  // softmax, loss and gradient of token t, whose logits are x; f and factor are its sequence's
+  // This lane's f less the smallest f, which it returns, of a sequence of n tokens (0 if there are none) from its counts
+  auto shares = [&](auto&& count, int n, float (&f)[NV][VW]) {
+    const float unit = n > 0 ? 1.f / ((float)a.k * (float)n) : 0.f;
+    float least = INFINITY;
+#pragma unroll
+    for (int j = 0; j < NV; ++j)
+#pragma unroll
+      for (int q = 0; q < VW; ++q) {
+        const int e = (gl + j * G) * VW + q;
+        f[j][q] = n > 0 && e < a.E ? count(e) : 0.f;
+        least = e < a.E ? fminf(least, f[j][q]) : least;
+      }
+    least = -group_max<G>(-least);
+#pragma unroll
+    for (int j = 0; j < NV; ++j)
+#pragma unroll
+      for (int q = 0; q < VW; ++q) f[j][q] = (gl + j * G) * VW + q < a.E ? (f[j][q] - least) * unit : 0.f;
+    return least * unit;
+  };
+  // softmax, loss and gradient of token t, whose logits are x; f, least and factor are its sequence's
   double sum = 0.0;
-  auto token = [&](int t, bool write, bool live, float (&x)[NV][VW], const float (&f)[NV][VW], float factor) {
+  auto token = [&](int t, bool write, bool live, float (&x)[NV][VW], const float (&f)[NV][VW], float least, float factor) {
     float m = -INFINITY;
 #pragma unroll
     for (int j = 0; j < NV; ++j)
@@ -159,7 +180,7 @@ __global__ __launch_bounds__(NTH) void balance_rows_kernel(BalanceArgs a, int to
     d = group_sum<G>(d);
     const float iz = z > 0.f ? 1.f / z : z == 0.f ? 0.f : z;  // NaN stays NaN
     const float dot = d * iz;
-    if (gl == 0 && live) sum += (double)(factor * dot);
+    if (gl == 0 && live) sum += (double)(factor * (dot + (z > 0.f ? least : z)));
     if (a.d_logits && write) {
       float* out = a.d_logits + (int64_t)t * a.E;
 #pragma unroll
@@ -202,17 +223,10 @@ __global__ __launch_bounds__(NTH) void balance_rows_kernel(BalanceArgs a, int to
       seq_range(a, s, begin, end);
       const int n = t >= begin && t < end ? a.part[(int64_t)s * (a.E + 1) + a.E] : 0;
       const bool live = n > 0 && (!a.mask || a.mask[t] != 0);
-      const float unit = n > 0 ? 1.f / ((float)a.k * (float)n) : 0.f;
       float x[NV][VW], f[NV][VW];
       load(t, live, x);
-#pragma unroll
-      for (int j = 0; j < NV; ++j)
-#pragma unroll
-        for (int q = 0; q < VW; ++q) {
-          const int e = (gl + j * G) * VW + q;
-          f[j][q] = n > 0 && e < a.E ? (float)a.part[(int64_t)s * (a.E + 1) + e] * unit : 0.f;
-        }
-      token(t, true, live, x, f, n > 0 ? a.weight * (float)a.E / ((float)n * (float)s_used) : 0.f);
+      const float least = shares([&](int e) { return (float)a.part[(int64_t)s * (a.E + 1) + e]; }, n, f);
+      token(t, true, live, x, f, least, n > 0 ? a.weight * (float)a.E / ((float)n * (float)s_used) : 0.f);
     }
   } else {
     // the sequence of the first token: the last one that begins at or before it
@@ -244,16 +258,9 @@ __global__ __launch_bounds__(NTH) void balance_rows_kernel(BalanceArgs a, int to
         }
         __syncthreads();
         const int n = in ? s_n : 0;
-        const float unit = n > 0 ? 1.f / ((float)a.k * (float)n) : 0.f;
         const float factor = n > 0 ? a.weight * (float)a.E / ((float)n * (float)(a.S > 1 ? s_used : 1)) : 0.f;
         float f[NV][VW];
-#pragma unroll
-        for (int j = 0; j < NV; ++j)
-#pragma unroll
-          for (int q = 0; q < VW; ++q) {
-            const int e = (gl + j * G) * VW + q;
-            f[j][q] = n > 0 && e < a.E ? s_f[e] * unit : 0.f;
-          }
+        const float least = shares([&](int e) { return s_f[e]; }, n, f);
         for (int tu = t0 + tid / G; tu < t1; tu += TPP * U) {
           float x[U][NV][VW];
           bool live[U];
@@ -264,7 +271,7 @@ __global__ __launch_bounds__(NTH) void balance_rows_kernel(BalanceArgs a, int to
             load(t, live[u], x[u]);
           }
 #pragma unroll
-          for (int u = 0; u < U; ++u) token(tu + u * TPP, tu + u * TPP < t1, live[u], x[u], f, factor);
+          for (int u = 0; u < U; ++u) token(tu + u * TPP, tu + u * TPP < t1, live[u], x[u], f, least, factor);
         }
         t0 = t1;
       }

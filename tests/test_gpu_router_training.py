@@ -77,6 +77,24 @@ def test_balance_of_an_even_router_is_its_weight():
     assert float(loss) == 0.25 and torch.all(count == 16) and not d.any()
 
 
+@pytest.mark.parametrize("T,E,offset", [(100, 6, None), (70, 8, None), (33, 1, None), (90, 8, [0, 11, 40, 40, 85]),
+                                        (60, 5, list(range(0, 61, 5)))])
+def test_balance_gradient_of_even_choices_is_zero(T, E, offset):
+    """Every expert chosen by every token (k = E): the gradient is 0, not what is left of a difference of roundings."""
+    print(f"\n[gpu] balance even {T} {E} {offset}", flush=True)
+    g = torch.Generator().manual_seed(T)
+    logits = torch.randn(T, E, generator=g) * 3
+    ids = torch.stack([torch.randperm(E, generator=g) for _ in range(T)]).int()
+    S = 1 if offset is None else len(offset) - 1
+    loss, count = torch.empty(1, device=DEV), torch.empty(S, E, dtype=torch.int32, device=DEV)
+    d = torch.full((T, E), -9.0, device=DEV)
+    off = None if offset is None else torch.tensor(offset, dtype=torch.int32, device=DEV)
+    moe.moe_balance_loss(logits.to(DEV), ids.to(DEV), 0.25, loss, count, d_logits=d, seq_offset=off)
+    assert not d.any()
+    # f = 1 / E and the sum of p is 1, both rounded a few times: the factors and the softmax take some ten roundings
+    assert abs(float(loss) - 0.25) < 0.25 * 16 * 2.0 ** -24
+
+
 def test_balance_padding_and_masked_experts():
     """What a masked token holds does not matter; -inf logits have p = 0; a row of them adds nothing; ids out of range are not
     counted; a NaN of a counted token shows."""
