@@ -1,7 +1,8 @@
 // Gradients of the combine (moe_combine_backward) and of the router (moe_route_backward).
 //
 // combine: y[t] = sum_j w[t, j] out[row(t, j)] over kept slots, so d_w[t, j] = dy[t] . out[row] and d_out[row] = w[t, j] dy[t].
-//   One workgroup per token reads dy[t] once and its rows once. Bound: HBM.
+//   One workgroup per token reads dy[t] once and its rows once. Bound: HBM (16384 tokens, H 7168, 256 experts of at most 640
+//   rows: 344 us, 5.6 TB/s of reads and writes).
 //
 // router: w = softmax over the selected logits, logits = x Wr^T + b. With c_j = w_j (d_w_j - sum_i w_i d_w_i), the gradient of
 //   the logits is d_in plus c_j at the selected experts; then d_x = d_logits Wr, d_Wr = d_logits^T x, d_b = the column sums.
@@ -86,8 +87,8 @@ __global__ __launch_bounds__(NTH) void combine_backward_kernel(const T* __restri
 //   bf16 layers: d_w_router (fp32) is x, exact, times d_logits in three bf16 parts, which hold all of its 24 bits, on bf16 MFMA:
 //     every product is exact and the sums are fp32. d_x is rounded to bf16, so its operands are fp16 with a power of two for
 //     each token and each column of x that puts the largest value at 2^14: off by 2^-11 of itself each at most (2^-39 of the
-//     largest for what becomes subnormal), against 2^-8 of the result in its own rounding. One product instead of the three that two
-//     bf16 parts of each take: 57 -> 37 us for 4096 x 256 x 7168 (28 now).
+//     largest for what becomes subnormal), against 2^-8 of the result in its own rounding. One product instead of the three
+//     that two bf16 parts of each take: 57 -> 37 us for 4096 x 256 x 7168 (26 now).
 //   fp32 layers: fp32 MFMA.
 // Fragments: 32 rows x STEP k are the 1 KB that a wave loads at once, lane l row l % 32 and the 16 bytes of k from (l / 32) *
 // STEP / 2 on. All operands but x are laid out in fragments by route_grad_prep, their transposes made on the way:
@@ -264,11 +265,12 @@ __global__ __launch_bounds__(kPrepThreads) void route_grad_prep_kernel(GradArgs 
   }
 }
 
-// d_x: a wave computes 32 TI tokens x 32 NJ columns, WT waves. The columns' fragments are in LDS for good; the tokens' come from
+// d_x: a wave computes 32 TI tokens x 32 NJ columns, eight waves. The columns' fragments are in LDS for good; the tokens' come from
 // memory D - 1 steps ahead, across the ends of the token tiles. A lane has NJ neighbouring columns of a row.
-template <typename G, int NJ, int TI, int WT>
+constexpr int kDxWaves = 8;
+template <typename G, int NJ, int TI>
 __device__ __forceinline__ void route_dx(const GradArgs& a, unsigned char* s_w, int block_x, int block_y, int grid_y) {
-  constexpr int NT = WT * 64, D = 4;
+  constexpr int WT = kDxWaves, NT = WT * 64, D = 4;
   using X = typename G::X;
   const RouteBackward& r = a.r;
   const int tid = threadIdx.x, lane = tid & 63;
@@ -283,7 +285,7 @@ __device__ __forceinline__ void route_dx(const GradArgs& a, unsigned char* s_w, 
     for (int q = 0; q < 8; ++q)
       if (i + q * NT * 16 < block) st16(s_w + i + q * NT * 16, v[q]);
   }
-  const int tiles = (a.tb + TI * WT - 1) / (TI * WT);  // of 32 TI WT tokens
+  const int tiles = (a.tb - wt * TI + TI * WT - 1) / (TI * WT);  // of 32 TI WT tokens, those where this wave has any
   u32x4 fa[D][TI];  // 32-token blocks
   int tile = block_y, step = 0, ltile = block_y, lstep = 0;
   // the next step that is not on its way yet; past the last one a valid address, as a branch around loads makes the compiler
@@ -363,10 +365,10 @@ __device__ __forceinline__ void route_dx(const GradArgs& a, unsigned char* s_w, 
     if (tile < tiles) one(std::integral_constant<int, 3>{});
   }
 }
-template <typename G, int NJ, int TI, int WT>
-__global__ __launch_bounds__(WT * 64, TI == 1 ? 4 : 2) void route_dx_kernel(GradArgs a) {
+template <typename G, int NJ, int TI>
+__global__ __launch_bounds__(kDxWaves * 64, TI == 1 ? 4 : 2) void route_dx_kernel(GradArgs a) {
   extern __shared__ __attribute__((aligned(1024))) unsigned char smem[];
-  route_dx<G, NJ, TI, WT>(a, smem, blockIdx.x, blockIdx.y, gridDim.y);
+  route_dx<G, NJ, TI>(a, smem, blockIdx.x, blockIdx.y, gridDim.y);
 }
 
 // Column sums of d_logits from those of 32 tokens: 64 columns per workgroup of NW waves, their sums added in order.
@@ -400,7 +402,8 @@ __global__ __launch_bounds__(512) void route_dbias_kernel(GradArgs a) {
 // multiplied. In LDS the chunk is fragments [step][4 column blocks]; in a fragment the 16 bytes of column c are at place
 // c ^ (its group of 8 in the 128 columns), so that the writes of a wave, at a stride of 4 or 8 columns, touch all banks.
 // Workgroups past the column tiles add up the bias. A second chunk of x on its way changed nothing (16000 tokens, H 4096, 8
-// experts: 43 us, 3.1 TB/s); two workgroups of four waves per CU were slower (52).
+// experts: 43 us, 3.1 TB/s); two workgroups of four waves per CU were slower (52). 4096 tokens, H 7168, 256 experts: 50 us, the
+// matrix units busy 55 % of it.
 constexpr int kDwCols = 128;
 constexpr int kDwSteps = 16, kDwChunkBytes = kDwSteps * 4 * kFrag;
 template <typename G, int WE>
@@ -553,7 +556,7 @@ template <typename G, int NJ, int WE>
 __global__ __launch_bounds__(512) void route_dx_dw_kernel(GradArgs a, int dx_y, int col_tiles) {
   extern __shared__ __attribute__((aligned(1024))) unsigned char smem[];
   const int b = blockIdx.x, n = a.hb * dx_y;
-  if (b < n) route_dx<G, NJ, 1, 8>(a, smem, b % a.hb, b / a.hb, dx_y);
+  if (b < n) route_dx<G, NJ, 1>(a, smem, b % a.hb, b / a.hb, dx_y);
   else route_dw<G, WE>(a, smem, b - n, col_tiles);
 }
 
@@ -659,12 +662,12 @@ bool launch_dx_dw(const GradArgs& a, hipStream_t stream) {
   return true;
 }
 
-template <typename G, int NJ, int TI, int WT>
+template <typename G, int NJ, int TI>
 hipError_t launch_dx(const GradArgs& a, hipStream_t stream) {
-  const int tiles = ceil_div_host(a.tb, TI * WT);
+  const int tiles = ceil_div_host(a.tb, TI * kDxWaves);
   // two workgroups per CU, whose stores and products overlap, where the LDS takes them
   const dim3 grid(a.hb, std::max(1, std::min(tiles, 512 / a.hb)));
-  route_dx_kernel<G, NJ, TI, WT><<<grid, WT * 64, a.ek * NJ * kFrag, stream>>>(a);
+  route_dx_kernel<G, NJ, TI><<<grid, kDxWaves * 64, a.ek * NJ * kFrag, stream>>>(a);
   return hipGetLastError();
 }
 
@@ -700,10 +703,16 @@ hipError_t launch_route_backward_t(const RouteBackward& r, hipStream_t stream) {
       else if constexpr (!G::SCALED) joint = launch_dx_dw<G, 2, 8>(a, stream);
     }
     if (st == hipSuccess && r.d_x && !joint) {
-      const bool few = a.tb <= 4;  // tokens for two waves at most
-      if (a.nj == 4)
-        st = few ? launch_dx<G, 4, 1, 4>(a, stream) : a.ek <= 16 ? launch_dx<G, 4, 1, 8>(a, stream) : launch_dx<G, 4, 2, 8>(a, stream);
-      else if constexpr (!G::SCALED) st = few ? launch_dx<G, 2, 1, 4>(a, stream) : launch_dx<G, 2, 2, 8>(a, stream);
+      // 64 tokens per wave take every fragment of the weight out of LDS half as often, which pays for more than 256 experts
+      // (4096 tokens, H 7168, 384 and 512 experts: 42.5 and 49.5 us against 46.1 and 54.3; 256: 35.5 against 29.3), given
+      // tokens for all waves. fp32 products hide it (256 experts: 151 us either way).
+      if (a.nj == 2) {
+        if constexpr (!G::SCALED) st = launch_dx<G, 2, 1>(a, stream);
+      } else if (G::SCALED && a.ek > 16 && a.tb > kDxWaves) {
+        if constexpr (G::SCALED) st = launch_dx<G, 4, 2>(a, stream);
+      } else {
+        st = launch_dx<G, 4, 1>(a, stream);
+      }
     }
     if (st != hipSuccess) return st;
   }
