@@ -118,7 +118,7 @@ __device__ __forceinline__ int part_sum(const BalanceArgs& a, int64_t s, int64_t
 // G lanes per token, NV vectors of VW logits per lane: lane i of the group holds logits (i + j G) VW .. of j < NV.
 // A workgroup takes `tokens` consecutive tokens; where they belong to several sequences it goes through these in turn, with
 // the sequence's f in LDS. A group loads U tokens at once: a large batch is one such round, and its loads are what it waits for
-// (one token after another: 30 us for 16384 x 256, 14 with four at once).
+// (one token after another: 30 us for 16384 x 256, 16 with four at once).
 // MANY: more than kFewSeqs sequences, whose tokens would be few at a time: a group finds its token's sequence and reads its f
 // itself (59 tokens in 60 sequences: 37 us one after another, 12 so).
 constexpr int kFewSeqs = 8;

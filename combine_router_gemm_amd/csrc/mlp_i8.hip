@@ -9,7 +9,9 @@
 //
 //   i8_gemm_kernel  rows and weight rows go to LDS directly, in stages of 128 k (128 bytes of a row: whole cache lines), NS
 //                   stages in flight; 32- and 64-row tiles stream the weights of experts with few rows and are bound by their
-//                   bytes, 128- and 256-row ones by the matrix units and the power that they draw.
+//                   bytes (48 experts of 7168 x 2048, 128 tokens: gate/up 213 us, 6.6 TB/s, down 113, 6.2 TB/s), 128- and
+//                   256-row ones by the matrix units and the power that they draw (32 experts of 7168 x 2048, 1024 rows each:
+//                   gate/up 945-980 us, down 530-560, 1.9 PFLOP/s at 1.8 GHz).
 #include <algorithm>
 #include <type_traits>
 
@@ -55,8 +57,8 @@ struct I8Args {
 };
 
 // g / (1 + e^-g). e^-g = 2^t with t = -g / ln 2 in two floats, the second as a first-order factor, so that it is off by two or
-// three steps; the reciprocal is the hardware's, off by one (0 for g below -87, where it is subnormal). The library's expf and division cost a tile of the
-// gate/up pass as much as three of its stages.
+// three steps; the reciprocal is the hardware's, off by one (0 for g below -87, where it is subnormal). The library's expf and
+// division cost a tile of the gate/up pass as much as three of its stages.
 __device__ __forceinline__ float silu(float g) {
   constexpr float kLog2e = 1.44269502162933349609375f, kLog2eLow = 1.92596299e-8f;  // 1 / ln 2 and what float leaves of it
   const float t = g * -kLog2e;
@@ -74,9 +76,12 @@ __device__ __forceinline__ int swizzle(int r) { return (r >> 1) & 7; }
 // BM rows x BN weight rows per tile (gate/up: the gate and the up rows of BN / 2 columns), WM x WN waves.
 // PP: eight waves in two groups, one of each on every SIMD, that run the same sequence (read half a stage of fragments,
 // barrier, multiply them, barrier) one barrier apart: while one group reads and loads the other keeps the matrix units busy.
+// Four waves of 128 x 128, reads and loads spread between the products, read a third less LDS and were no faster: gate/up 1025 us
+// against 972, down 643 against 557, of which the longer epilogue is most. Nor did it change anything to look up rows and
+// scales behind the first loads instead of before them, or to store a lane's neighbouring columns directly.
 // SPLIT: K cut over workgroups, where the tiles are few (see i8_plan).
 // FEW: a down pass of at most kFewRows rows in all, which takes h itself and makes the codes of its part of K while the first
-// weights are on their way, in place of a launch for them (one Mixtral-shaped token 85 -> 73 us with the join in the kernel).
+// weights are on their way, in place of a launch for them (one Mixtral-shaped token 85 -> 75 us with the join in the kernel).
 constexpr int kFewRows = 8, kFewStages = 32;
 template <typename Op, int BM, int BN, int WM, int WN, int NS, int PER_CU, bool PP, bool GATED, bool SPLIT = false,
           bool FEW = false>
@@ -572,17 +577,17 @@ int64_t row_tiles(int64_t rows_max, int El, int bm) {
 // workgroups per CU 1.32 (64 rows) and 0.89 (32 rows); a last round of one workgroup per CU takes 1.15 and 0.85. Whole MLPs (us)
 // by rows of a tile, which this rule orders right but for ties:
 //   experts, H, F, rows each      32      64     128     256
-//   32, 7168, 2048, 32           246     247     286     346
-//   32, 7168, 2048, 64           412     277     308     366
-//   32, 7168, 2048, 128          745     460     352     395
-//   32, 7168, 2048, 256         1462     821     535     471
-//   8, 4096, 14336, 32           244     248     323     422
-//   8, 4096, 14336, 96           591     510     370     448
-//   12, 1184, 736, 64           29.9    30.3    38.6    46.3
-//   12, 1184, 736, 128          43.4    37.6    44.8    49.3
-//   12, 1184, 736, 384          87.4    67.8    50.2    62.7
-//   16, 2048, 768, 128          56.6    43.8    50.5    55.3
-//   48, 1024, 512, 96           60.8    54.2    46.6    50.9
+//   32, 7168, 2048, 32           242     244     272     339
+//   32, 7168, 2048, 64           410     272     297     359
+//   32, 7168, 2048, 128          752     461     340     382
+//   32, 7168, 2048, 256         1476     822     521     450
+//   8, 4096, 14336, 32           242     241     296     391
+//   8, 4096, 14336, 96           611     506     348     428
+//   12, 1184, 736, 64           27.9    27.1    32.5    43.2
+//   12, 1184, 736, 128          40.3    34.8    38.5    45.6
+//   12, 1184, 736, 384          79.7    62.2    46.3    55.3
+//   16, 2048, 768, 128          51.1    40.6    44.1    51.8
+//   48, 1024, 512, 96           53.7    47.9    40.3    47.6
 double tile_cost(int i, int64_t rows_max, int El, int H, int F) {
   constexpr double full[] = {0.89, 1.32, 1.5, 2.3}, rest[] = {0.85, 1.15, 1.5, 2.3};
   const int64_t m = row_tiles(rows_max, El, kTiles[i].bm), slots = kTiles[i].per_cu * kPlanCus;
