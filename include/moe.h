@@ -501,7 +501,7 @@ int moe_expert_mlp_i8(const int8_t* send_q, const float* send_scale, const moe_l
  * moe_expert_mlp_i8_tiling -- what moe_expert_mlp_i8 cuts a call of these sizes into, from the sizes alone (the result does
  * not depend on it: the sums are exact).
  *   tile_rows       rows per tile: 32, 64, 128 or 256
- *   gate_up_parts, down_parts  parts of the pass's K whose int32 sums a further launch adds, 1 where it is not split
+ *   gate_up_parts, down_parts  parts that a pass's K is cut into, whose int32 sums are added: 1 where it is not
  * Returns what moe_expert_mlp_i8 would return for the sizes, and writes nothing unless that is MOE_OK.
  */
 int moe_expert_mlp_i8_tiling(int T, int k, int E, int R, int C, int H, int F, int* tile_rows, int* gate_up_parts,
