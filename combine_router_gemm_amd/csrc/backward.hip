@@ -85,10 +85,13 @@ __global__ __launch_bounds__(NTH) void combine_backward_kernel(const T* __restri
 // ---- router ----
 // The gradient of the logits, T x E values, is small, but a factor of both products (2 T E H operations each).
 //   bf16 layers: d_w_router (fp32) is x, exact, times d_logits in three bf16 parts, which hold all of its 24 bits, on bf16 MFMA:
-//     every product is exact and the sums are fp32. d_x is rounded to bf16, so its operands are fp16 with a power of two for
-//     each token and each column of x that puts the largest value at 2^14: off by 2^-11 of itself each at most (2^-39 of the
-//     largest for what becomes subnormal), against 2^-8 of the result in its own rounding. One product instead of the three
-//     that two bf16 parts of each take: 57 -> 37 us for 4096 x 256 x 7168 (26 now).
+//     every product is exact and the sums are fp32. d_x has two fp32 operands. Each is two fp16 parts, after a power of two for
+//     each token and each column of x that puts the largest value at 2^14: off by 2^-22 of itself at most (2^-39 of the largest
+//     for what becomes subnormal). Three products, without the one of the two second parts (2^-22 again), so that d_x is what
+//     fp32 gives. One fp16 part is not enough, though d_x is rounded to bf16: gradients of a softmax sum to 0 over the
+//     experts, what the router's rows share cancels, and 2^-11 of it would stay (rows that are a common one and a hundredth of
+//     it their own: d_x off by 0.03 of its norm, with two parts by 0.0017, its rounding). A token or column that holds an
+//     infinity or NaN is left out of the product and computed apart in fp32.
 //   fp32 layers: fp32 MFMA.
 // Fragments: 32 rows x STEP k are the 1 KB that a wave loads at once, lane l row l % 32 and the 16 bytes of k from (l / 32) *
 // STEP / 2 on. All operands but x are laid out in fragments by route_grad_prep, their transposes made on the way:
@@ -96,10 +99,11 @@ __global__ __launch_bounds__(NTH) void combine_backward_kernel(const T* __restri
 //   route_dx          the weight's fragments of 32 NJ columns stay in LDS while the tokens stream past
 //   route_dw          x is transposed on its way to LDS; the tokens are split over workgroups where the tiles are few
 constexpr int kRows = 32, kFrag = 1024;  // rows of a fragment, its bytes
+constexpr int kNonFinite = 1 << 16;      // in place of a power of two: not all of the values are finite
 
 struct GradBf16 {
   using X = bf16_t;
-  static constexpr int STEP = 16, PARTS = 3;  // k of a fragment; parts of d_logits in d_w_router
+  static constexpr int STEP = 16, PARTS = 3, DXP = 2;  // k of a fragment; parts of d_logits in d_w_router, of d_x's operands
   static constexpr bool SCALED = true;
   static __device__ __forceinline__ void dx(f32x16& acc, u32x4 a, u32x4 b) {
     acc = __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b), acc, 0, 0, 0);
@@ -107,12 +111,17 @@ struct GradBf16 {
   static __device__ __forceinline__ void dw(f32x16& acc, u32x4 a, u32x4 b) {
     acc = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), acc, 0, 0, 0);
   }
-  // eight values times 2^e in fp16
-  static __device__ __forceinline__ u32x4 dx_operand(const float (&v)[8], int e) {
-    f16x8 o;
+  // eight values times 2^e in two fp16 parts; zeros for values that are computed apart
+  static __device__ __forceinline__ void dx_operand(const float (&v)[8], int e, u32x4 (&o)[2]) {
+    f16x8 hi, lo;
 #pragma unroll
-    for (int q = 0; q < 8; ++q) o[q] = (_Float16)ldexpf(v[q], e);
-    return __builtin_bit_cast(u32x4, o);
+    for (int q = 0; q < 8; ++q) {
+      const float s = e == kNonFinite ? 0.f : ldexpf(v[q], e);
+      hi[q] = (_Float16)s;
+      lo[q] = (_Float16)(s - (float)hi[q]);
+    }
+    o[0] = __builtin_bit_cast(u32x4, hi);
+    o[1] = __builtin_bit_cast(u32x4, lo);
   }
   static __device__ __forceinline__ u32x4 dw_part(float (&v)[8]) {  // and what it leaves
     const u32x4 o = pack(v);
@@ -123,7 +132,7 @@ struct GradBf16 {
 };
 struct GradF32 {
   using X = float;
-  static constexpr int STEP = 8, PARTS = 1;
+  static constexpr int STEP = 8, PARTS = 1, DXP = 1;
   static constexpr bool SCALED = false;
   static __device__ __forceinline__ void dx(f32x16& acc, u32x4 a, u32x4 b) {
 #pragma unroll
@@ -131,16 +140,16 @@ struct GradF32 {
       acc = __builtin_amdgcn_mfma_f32_32x32x2f32(__uint_as_float(a[q]), __uint_as_float(b[q]), acc, 0, 0, 0);
   }
   static __device__ __forceinline__ void dw(f32x16& acc, u32x4 a, u32x4 b) { dx(acc, a, b); }
-  static __device__ __forceinline__ u32x4 dx_operand(const float (&v)[4], int) { return pack(v); }
+  static __device__ __forceinline__ void dx_operand(const float (&v)[4], int, u32x4 (&o)[1]) { o[0] = pack(v); }
   static __device__ __forceinline__ u32x4 dw_part(float (&v)[4]) { return pack(v); }
 };
 
 struct GradArgs {
   RouteBackward r;
   int tb, ek, eb, hb, nj;  // blocks of 32 tokens, k steps and blocks of 32 experts, blocks of 32 nj columns
-  unsigned char* px;       // [tb][ek] fragments: rows tokens, k experts
+  unsigned char* px;       // [tb][ek][DXP] fragments: rows tokens, k experts
   unsigned char* pw;       // [eb][tb 32 / STEP][PARTS] fragments: rows experts, k tokens
-  unsigned char* wt;       // [hb][ek][nj] fragments: rows columns of x, k experts; row c of fragment j is column nj c + j
+  unsigned char* wt;       // [hb][ek][DXP][nj] fragments: rows columns of x, k experts; row c of fragment j is column nj c + j
   int* t_exp;              // [32 tb], h_exp [32 nj hb]: the powers of two of the fp16 operands
   int* h_exp;
   float* bias_part;        // [tb][E]
@@ -148,9 +157,11 @@ struct GradArgs {
   int splits, chunks_per_split;
 };
 
-// The power of two that puts a largest value, given by its bits, into [2^14, 2^15); 0 for zero, infinities and NaN.
+// The power of two that puts a largest value, given by its bits, into [2^14, 2^15); 0 for zero, kNonFinite for infinities and
+// NaN.
 __device__ __forceinline__ int fp16_exp(uint32_t top) {
-  if (top == 0 || top >= 0x7f800000u) return 0;
+  if (top >= 0x7f800000u) return kNonFinite;
+  if (top == 0) return 0;
   return 15 - (int)(__builtin_amdgcn_frexp_expf(__uint_as_float(top)));
 }
 
@@ -231,7 +242,11 @@ __global__ __launch_bounds__(kPrepThreads) void route_grad_prep_kernel(GradArgs 
         float v[N];
 #pragma unroll
         for (int q = 0; q < N; ++q) v[q] = s[(l & 31) * PITCH + step * G::STEP + (l >> 5) * N + q];
-        st16(a.px + ((int64_t)blockIdx.x * a.ek + step) * kFrag + l * 16, G::dx_operand(v, G::SCALED ? s_exp[l & 31] : 0));
+        u32x4 o[G::DXP];
+        G::dx_operand(v, G::SCALED ? s_exp[l & 31] : 0, o);
+#pragma unroll
+        for (int p = 0; p < G::DXP; ++p)
+          st16(a.px + (((int64_t)blockIdx.x * a.ek + step) * G::DXP + p) * kFrag + l * 16, o[p]);
       }
     return;
   }
@@ -260,22 +275,45 @@ __global__ __launch_bounds__(kPrepThreads) void route_grad_prep_kernel(GradArgs 
     float v[N];
 #pragma unroll
     for (int q = 0; q < N; ++q) v[q] = s[(step * G::STEP + half * N + q) * WP + col];
-    st16(a.wt + (((int64_t)b * a.ek + step) * a.nj + j) * kFrag + (half * 32 + row0 + row) * 16,
-         G::dx_operand(v, G::SCALED ? s_exp[col] : 0));
+    u32x4 o[G::DXP];
+    G::dx_operand(v, G::SCALED ? s_exp[col] : 0, o);
+#pragma unroll
+    for (int p = 0; p < G::DXP; ++p)
+      st16(a.wt + ((((int64_t)b * a.ek + step) * G::DXP + p) * a.nj + j) * kFrag + (half * 32 + row0 + row) * 16, o[p]);
+  }
+}
+
+// d_x of a block's tokens and a lane's NJ columns where either holds an infinity or NaN: fp32 products, one after another
+template <int NJ>
+__device__ __forceinline__ void route_dx_apart(const GradArgs& a, int64_t t0, int h, int lane) {
+  const RouteBackward& r = a.r;
+#pragma unroll 1
+  for (int i = 0; i < 16 * NJ; ++i) {
+    const int64_t t = t0 + Op32::out_row(lane, i / NJ);
+    const int c = h + i % NJ;
+    if (t >= r.T || c >= r.H || max(a.t_exp[t], a.h_exp[c]) != kNonFinite) continue;
+    float v = 0.f;
+#pragma unroll 1
+    for (int e = 0; e < r.E; ++e) v = fmaf(r.d_logits[t * r.E + e], r.w_router[(int64_t)e * r.H + c], v);
+    static_cast<bf16_t*>(r.d_x)[t * r.H + c] = (bf16_t)v;
   }
 }
 
 // d_x: a wave computes 32 TI tokens x 32 NJ columns, eight waves. The columns' fragments are in LDS for good; the tokens' come from
 // memory D - 1 steps ahead, across the ends of the token tiles. A lane has NJ neighbouring columns of a row.
 constexpr int kDxWaves = 8;
-template <typename G, int NJ, int TI>
+template <typename G>
+int dx_lds(int ek, int nj) {  // the fragments and, behind them, the columns' powers of two
+  return ek * G::DXP * nj * kFrag + (G::SCALED ? 32 * nj * (int)sizeof(int) : 0);
+}
+template <typename G, int NJ, int TI, int D>
 __device__ __forceinline__ void route_dx(const GradArgs& a, unsigned char* s_w, int block_x, int block_y, int grid_y) {
-  constexpr int WT = kDxWaves, NT = WT * 64, D = 4;
+  constexpr int WT = kDxWaves, NT = WT * 64, P = G::DXP;
   using X = typename G::X;
   const RouteBackward& r = a.r;
   const int tid = threadIdx.x, lane = tid & 63;
   const int wt = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int block = a.ek * NJ * kFrag;
+  const int block = a.ek * P * NJ * kFrag;
   for (int i = tid * 16; i < block; i += NT * 16 * 8) {
     u32x4 v[8];
 #pragma unroll
@@ -286,15 +324,16 @@ __device__ __forceinline__ void route_dx(const GradArgs& a, unsigned char* s_w, 
       if (i + q * NT * 16 < block) st16(s_w + i + q * NT * 16, v[q]);
   }
   const int tiles = (a.tb - wt * TI + TI * WT - 1) / (TI * WT);  // of 32 TI WT tokens, those where this wave has any
-  u32x4 fa[D][TI];  // 32-token blocks
+  u32x4 fa[D][TI][P];  // 32-token blocks
   int tile = block_y, step = 0, ltile = block_y, lstep = 0;
   // the next step that is not on its way yet; past the last one a valid address, as a branch around loads makes the compiler
   // wait for all of them
-  auto load = [&](u32x4 (&f)[TI]) {
+  auto load = [&](u32x4 (&f)[TI][P]) {
 #pragma unroll
     for (int i = 0; i < TI; ++i) {
       const int tb = min((ltile * WT + wt) * TI + i, a.tb - 1);
-      f[i] = ld16(a.px + ((int64_t)tb * a.ek + lstep) * kFrag + lane * 16);
+#pragma unroll
+      for (int p = 0; p < P; ++p) f[i][p] = ld16(a.px + (((int64_t)tb * a.ek + lstep) * P + p) * kFrag + lane * 16);
     }
     if (++lstep == a.ek) {
       lstep = 0;
@@ -313,33 +352,44 @@ __device__ __forceinline__ void route_dx(const GradArgs& a, unsigned char* s_w, 
   clear();
 #pragma unroll
   for (int i = 0; i < D - 1; ++i) load(fa[i]);
-  const int h = block_x * 32 * NJ + NJ * (lane & 31);
-  int he[NJ];
-#pragma unroll
-  for (int j = 0; j < NJ; ++j) he[j] = G::SCALED ? a.h_exp[h + j] : 0;
+  if (G::SCALED && tid < 32 * NJ) reinterpret_cast<int*>(s_w + block)[tid] = a.h_exp[block_x * 32 * NJ + tid];
   __syncthreads();
   auto one = [&](auto U) {
     constexpr int u = decltype(U)::value;
     load(fa[(u + D - 1) % D]);
-    u32x4 fb[NJ];
+    u32x4 fb[P][NJ];
 #pragma unroll
-    for (int j = 0; j < NJ; ++j) fb[j] = ld16(s_w + (step * NJ + j) * kFrag + lane * 16);
+    for (int p = 0; p < P; ++p)
 #pragma unroll
-    for (int i = 0; i < TI; ++i)
+      for (int j = 0; j < NJ; ++j) fb[p][j] = ld16(s_w + ((step * P + p) * NJ + j) * kFrag + lane * 16);
 #pragma unroll
-      for (int j = 0; j < NJ; ++j) G::dx(acc[i][j], fa[u][i], fb[j]);
+    for (int p = 2 * P - 2; p >= 0; --p)  // the parts' products, the smaller ones first: (0, 1), (1, 0), (0, 0)
+#pragma unroll
+      for (int i = 0; i < TI; ++i)
+#pragma unroll
+        for (int j = 0; j < NJ; ++j) G::dx(acc[i][j], fa[u][i][p & 1], fb[p >> 1][j]);
     if (++step == a.ek) {
+      const int h = block_x * 32 * NJ + NJ * (lane & 31);
+      const int* s_he = reinterpret_cast<const int*>(s_w + block) + NJ * (lane & 31);
 #pragma unroll
       for (int i = 0; i < TI; ++i) {
         const int tb = (tile * WT + wt) * TI + i;
         const int64_t t0 = (int64_t)tb * kRows;
         // the powers of two of the block's tokens, by scalar loads: vector loads would wait for the fragments on their way
         const auto* te = (const __attribute__((address_space(4))) int*)(a.t_exp + (int64_t)min(tb, a.tb - 1) * kRows);
-        if (t0 < r.T)
+        int he[NJ];
+        int most = 0;  // the largest of the powers, or 0: kNonFinite where something has to be computed apart
+#pragma unroll
+        for (int j = 0; j < NJ; ++j) {
+          he[j] = G::SCALED ? s_he[j] : 0;
+          most = max(most, he[j]);
+        }
+        if (t0 < r.T) {
 #pragma unroll
           for (int q = 0; q < 16; ++q) {
             const int64_t t = t0 + Op32::out_row(lane, q);
             const int ti = !G::SCALED ? 0 : lane < 32 ? te[Op32::out_row(0, q)] : te[Op32::out_row(32, q)];
+            most = max(most, ti);
             if (t < r.T && h < r.H) {
               X* o = static_cast<X*>(r.d_x) + t * r.H + h;
               float v[NJ];
@@ -347,11 +397,15 @@ __device__ __forceinline__ void route_dx(const GradArgs& a, unsigned char* s_w, 
               for (int j = 0; j < NJ; ++j) v[j] = G::SCALED ? ldexpf(acc[i][j][q], -ti - he[j]) : acc[i][j][q];
               if constexpr (sizeof(X) == 4 && NJ == 4) *reinterpret_cast<u32x4*>(o) = pack(v);
               else if constexpr (sizeof(X) == 4) *reinterpret_cast<f32x2*>(o) = f32x2{v[0], v[1]};
+              else if constexpr (NJ == 2) __builtin_nontemporal_store(pack2_bf16(v[0], v[1]), reinterpret_cast<uint32_t*>(o));
               else  // (non-temporal: 29.4 -> 27.7 us)
                 __builtin_nontemporal_store(u32x2{pack2_bf16(v[0], v[1]), pack2_bf16(v[2], v[3])},
                                             reinterpret_cast<u32x2*>(o));
             }
           }
+          if constexpr (G::SCALED)
+            if (most == kNonFinite) route_dx_apart<NJ>(a, t0, h, lane);
+        }
       }
       clear();
       step = 0;
@@ -361,14 +415,18 @@ __device__ __forceinline__ void route_dx(const GradArgs& a, unsigned char* s_w, 
   while (tile < tiles) {
     one(std::integral_constant<int, 0>{});
     if (tile < tiles) one(std::integral_constant<int, 1>{});
-    if (tile < tiles) one(std::integral_constant<int, 2>{});
-    if (tile < tiles) one(std::integral_constant<int, 3>{});
+    if constexpr (D == 4) {
+      if (tile < tiles) one(std::integral_constant<int, 2>{});
+      if (tile < tiles) one(std::integral_constant<int, 3>{});
+    }
   }
 }
-template <typename G, int NJ, int TI>
-__global__ __launch_bounds__(kDxWaves * 64, TI == 1 ? 4 : 2) void route_dx_kernel(GradArgs a) {
+// PER_CU workgroups share a CU
+template <typename G, int NJ, int TI, int D, int PER_CU>
+__global__ __launch_bounds__(kDxWaves * 64, 2 * PER_CU) void route_dx_kernel(GradArgs a) {
+  static_assert(D == 2 || D == 4, "the loop over the steps");
   extern __shared__ __attribute__((aligned(1024))) unsigned char smem[];
-  route_dx<G, NJ, TI>(a, smem, blockIdx.x, blockIdx.y, gridDim.y);
+  route_dx<G, NJ, TI, D>(a, smem, blockIdx.x, blockIdx.y, gridDim.y);
 }
 
 // Column sums of d_logits from those of 32 tokens: 64 columns per workgroup of NW waves, their sums added in order.
@@ -556,7 +614,7 @@ template <typename G, int NJ, int WE>
 __global__ __launch_bounds__(512) void route_dx_dw_kernel(GradArgs a, int dx_y, int col_tiles) {
   extern __shared__ __attribute__((aligned(1024))) unsigned char smem[];
   const int b = blockIdx.x, n = a.hb * dx_y;
-  if (b < n) route_dx<G, NJ, 1>(a, smem, b % a.hb, b / a.hb, dx_y);
+  if (b < n) route_dx<G, NJ, 1, 4>(a, smem, b % a.hb, b / a.hb, dx_y);
   else route_dw<G, WE>(a, smem, b - n, col_tiles);
 }
 
@@ -615,7 +673,8 @@ GradSizes grad_sizes(int T, int H, int E) {
   g.tb = ceil_div_host(T, kRows);
   g.ek = ceil_div_host(E, G::STEP);
   g.eb = ceil_div_host(E, kRows);
-  g.nj = g.ek <= 32 ? 4 : 2;  // the weight's fragments of 32 nj columns take 1 KB ek nj of LDS, 128 KB at most
+  // the weight's fragments of 32 nj columns take DXP KB ek nj of LDS, 128 KB at most
+  g.nj = g.ek * G::DXP <= 32 ? 4 : 2;
   g.hb = ceil_div_host(H, 32 * g.nj);
   // d_w_router: parts of the tokens, as many as give every CU a workgroup
   const int chunks = std::max(1, ceil_div_host(T, kDwSteps * G::STEP));
@@ -630,9 +689,9 @@ GradSizes grad_sizes(int T, int H, int E) {
     return here;
   };
   g.bias = take((size_t)g.tb * E * sizeof(float));
-  g.px = take((size_t)g.tb * g.ek * kFrag);
+  g.px = take((size_t)g.tb * g.ek * G::DXP * kFrag);
   g.pw = take((size_t)g.eb * g.tb * (kRows / G::STEP) * G::PARTS * kFrag);
-  g.wt = take((size_t)g.hb * g.ek * g.nj * kFrag);
+  g.wt = take((size_t)g.hb * g.ek * G::DXP * g.nj * kFrag);
   g.t_exp = take((size_t)g.tb * kRows * sizeof(int));
   g.h_exp = take((size_t)g.hb * 32 * g.nj * sizeof(int));
   g.partial = take(g.splits > 1 ? (size_t)g.splits * E * H * sizeof(float) : 0);
@@ -656,18 +715,17 @@ bool launch_dx_dw(const GradArgs& a, hipStream_t stream) {
   const int tiles = ceil_div_host(a.r.H, kDwCols), units = tiles * a.splits * ceil_div_host(a.eb, 8);
   const int dx_y = ceil_div_host(a.tb, 8), bias = a.r.d_bias ? ceil_div_host(a.r.E, 64) : 0;
   if ((int64_t)a.hb * dx_y + units > 256) return false;
-  const int lds = std::max(2 * kDwChunkBytes, a.ek * NJ * kFrag);
+  const int lds = std::max(2 * kDwChunkBytes, dx_lds<G>(a.ek, NJ));
   route_dx_dw_kernel<G, NJ, WE>
       <<<a.hb * dx_y + ceil_div_host(units, 8) * 8 + bias, 512, lds, stream>>>(a, dx_y, tiles);
   return true;
 }
 
-template <typename G, int NJ, int TI>
+template <typename G, int NJ, int TI, int D, int PER_CU>
 hipError_t launch_dx(const GradArgs& a, hipStream_t stream) {
   const int tiles = ceil_div_host(a.tb, TI * kDxWaves);
-  // two workgroups per CU, whose stores and products overlap, where the LDS takes them
-  const dim3 grid(a.hb, std::max(1, std::min(tiles, 512 / a.hb)));
-  route_dx_kernel<G, NJ, TI><<<grid, kDxWaves * 64, a.ek * NJ * kFrag, stream>>>(a);
+  const dim3 grid(a.hb, std::max(1, std::min(tiles, PER_CU * 256 / a.hb)));
+  route_dx_kernel<G, NJ, TI, D, PER_CU><<<grid, kDxWaves * 64, dx_lds<G>(a.ek, NJ), stream>>>(a);
   return hipGetLastError();
 }
 
@@ -700,18 +758,19 @@ hipError_t launch_route_backward_t(const RouteBackward& r, hipStream_t stream) {
       if (a.nj == 4)
         joint = a.eb <= 1 ? launch_dx_dw<G, 4, 1>(a, stream) : a.eb <= 2 ? launch_dx_dw<G, 4, 2>(a, stream)
                 : a.eb <= 4 ? launch_dx_dw<G, 4, 4>(a, stream) : launch_dx_dw<G, 4, 8>(a, stream);
-      else if constexpr (!G::SCALED) joint = launch_dx_dw<G, 2, 8>(a, stream);
+      else joint = launch_dx_dw<G, 2, 8>(a, stream);
     }
     if (st == hipSuccess && r.d_x && !joint) {
-      // 64 tokens per wave take every fragment of the weight out of LDS half as often, which pays for more than 256 experts
-      // (4096 tokens, H 7168, 384 and 512 experts: 42.5 and 49.5 us against 46.1 and 54.3; 256: 35.5 against 29.3), given
-      // tokens for all waves. fp32 products hide it (256 experts: 151 us either way).
-      if (a.nj == 2) {
-        if constexpr (!G::SCALED) st = launch_dx<G, 2, 1>(a, stream);
-      } else if (G::SCALED && a.ek > 16 && a.tb > kDxWaves) {
-        if constexpr (G::SCALED) st = launch_dx<G, 4, 2>(a, stream);
+      if constexpr (G::SCALED) {
+        // Two workgroups per CU, whose stores and products overlap, where half the LDS and half the registers do (16 experts,
+        // 16384 tokens, H 4096: 30.7 us against 38.5 with one; 64 experts, 4096 tokens, H 7168: 23.9 against 26.9). With one,
+        // 64 tokens per wave take every fragment of the weight out of LDS half as often, which pays with two blocks of
+        // columns, given tokens for all waves (4096 tokens, H 7168, 384 and 512 experts: 83 and 103 us against 89 and 117;
+        // 240 tokens, H 20480, 512 experts: 40 against 33; four blocks, 256 experts: 53 either way).
+        if (a.nj == 2) st = a.tb > kDxWaves ? launch_dx<G, 2, 2, 4, 1>(a, stream) : launch_dx<G, 2, 1, 4, 1>(a, stream);
+        else st = a.ek <= 8 ? launch_dx<G, 4, 1, 2, 2>(a, stream) : launch_dx<G, 4, 1, 4, 1>(a, stream);
       } else {
-        st = launch_dx<G, 4, 1>(a, stream);
+        st = a.nj == 2 ? launch_dx<G, 2, 1, 4, 2>(a, stream) : launch_dx<G, 4, 1, 4, 2>(a, stream);
       }
     }
     if (st != hipSuccess) return st;

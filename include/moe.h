@@ -555,7 +555,8 @@ size_t moe_route_backward_workspace_bytes(int T, int H, int E, moe_dtype_t xdt);
  *   d_logits[t, e] = d_logits_in[t, e] + sum over j with topk_ids[t, j] = e of
  *                    topk_w[t, j] * (d_topk_w[t, j] - sum_i topk_w[t, i] * d_topk_w[t, i])
  *   d_x = d_logits w_router (rounded once to xdt), d_w_router = d_logits^T x, d_bias = sum_t d_logits[t], sums in fp32 or
- *   more (d_logits itself is the gradient of a [T, E] bias)
+ *   more (d_logits itself is the gradient of a [T, E] bias). The products are fp32's; in d_x of bf16 layers an operand enters
+ *   with 22 bits: off by 2^-22 of itself, and by 2^-39 of the largest of its token or column, at most
  *   x            [T, H] (xdt), w_router [E, H] fp32, topk_ids and topk_w [T, k] as moe_route took and wrote them
  *   d_topk_w     [T, k] fp32 (moe_combine_backward), or NULL: none
  *   d_logits_in  [T, E] fp32, what other losses add (moe_balance_loss), or NULL: none; not both may be NULL
