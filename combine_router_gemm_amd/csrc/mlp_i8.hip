@@ -56,17 +56,19 @@ struct I8Args {
   int zero_n;
 };
 
-// g / (1 + e^-g). e^-g = 2^t with t = -g / ln 2 in two floats, the second as a first-order factor, so that it is off by two or
-// three steps; the reciprocal is the hardware's, off by one (0 for g below -87, where it is subnormal). The library's expf and
-// division cost a tile of the gate/up pass as much as three of its stages.
+// g / (1 + e^-g), from 2^t = e^-|g|, which cannot overflow: g / (1 + 2^t) for g >= 0, g 2^t / (1 + 2^t) below. t is a whole number
+// n and a rest, taken with what a float leaves of |g| / ln 2, and n goes into exponents: g 2^t is rounded where it is subnormal
+// itself, 2^t alone would be lost before (g below -87: a row's codes and scale depend on its values' ratios, however small they
+// are). Off by two or three steps: exp2 and the reciprocal are the hardware's, off by one each. The library's expf and division
+// cost a tile of the gate/up pass as much as three of its stages.
 __device__ __forceinline__ float silu(float g) {
   constexpr float kLog2e = 1.44269502162933349609375f, kLog2eLow = 1.92596299e-8f;  // 1 / ln 2 and what float leaves of it
-  const float t = g * -kLog2e;
-  const float low = fmaf(g, -kLog2eLow, fmaf(g, -kLog2e, -t));
-  const float e = __builtin_amdgcn_exp2f(t);
-  // (an infinite e takes no correction: inf - inf)
-  const float d = 1.0f + (e < INFINITY ? fmaf(e, low * 0.693147181f, e) : e);
-  return g * __builtin_amdgcn_rcpf(d);
+  const float x = fminf(fabsf(g), 256.f);  // e^-256 is 0 beside and times any float32
+  const float t = x * -kLog2e, n = rintf(t);
+  const float rest = (t - n) + fmaf(x, -kLog2eLow, fmaf(x, -kLog2e, -t));
+  const float e = __builtin_amdgcn_exp2f(rest);
+  const float top = g < 0.f ? ldexpf(g * e, (int)n) : g;
+  return top * __builtin_amdgcn_rcpf(1.0f + ldexpf(e, (int)n));
 }
 
 // A stage's rows: 128 bytes each, 16-byte chunk c of row r at c ^ ((r >> 1) & 7), so that a fragment read touches every
