@@ -584,7 +584,7 @@ int moe_balance_loss(const float* logits, const int32_t* topk_ids, const int32_t
                      void* workspace, size_t workspace_bytes, hipStream_t stream) {
   if (T < 0 || E < 1 || E > MOE_MAX_EXPERTS || k < 1 || k > MOE_MAX_TOPK || k > E || S < 1) return MOE_ERR_INVALID;
   if (!seq_offset && S != 1) return MOE_ERR_INVALID;
-  if (T > 1 << 30 || (int64_t)T * k > (int64_t)INT32_MAX || (int64_t)S * E > (int64_t)INT32_MAX)
+  if (T > 1 << 30 || S > 1 << 30 || (int64_t)T * k > (int64_t)INT32_MAX || (int64_t)S * E > (int64_t)INT32_MAX)
     return MOE_ERR_UNSUPPORTED;
   if (!loss || !expert_count || (T > 0 && (!logits || !topk_ids))) return MOE_ERR_INVALID;
   if (!al4(logits) || !al4(topk_ids) || !al4(seq_offset) || !al4(loss) || !al4(expert_count) || !al4(d_logits) ||

@@ -527,7 +527,7 @@ size_t moe_balance_loss_workspace_bytes(int T, int E, int S);
  *               a gradient of 0, whatever their logits hold; so does a token whose logits are all -inf (its p is 0).
  *   workspace   device scratch of at least moe_balance_loss_workspace_bytes(T, E, S) bytes; no contents need clearing, and
  *               calls that overlap must use separate workspaces
- * Requires T <= 2^30, T * k and S * E below 2^31 (else MOE_ERR_UNSUPPORTED). T == 0 writes a loss and counts of 0.
+ * Requires T and S <= 2^30, T * k and S * E below 2^31 (else MOE_ERR_UNSUPPORTED). T == 0 writes a loss and counts of 0.
  */
 int moe_balance_loss(const float* logits, const int32_t* topk_ids, const int32_t* seq_offset, const uint8_t* token_mask,
                      int T, int E, int k, int S, float weight, float* loss, int32_t* expert_count, float* d_logits,
