@@ -4,8 +4,8 @@
 // token's logits the sequence's loss is E / n sum_t sum_e f p, and, as f does not depend on the logits, a token's gradient is
 // E / n p (f - sum f p). The loss is linear in the tokens' dot products sum f p, which the gradient needs too: nothing but
 // the counts has to be known before the one pass over the logits. f enters less its smallest value over the experts, which the
-// gradient does not depend on: where the choices are nearly even the difference then keeps its digits, and it is 0 where they are
-// even (k = E); no term is larger than without.
+// gradient does not depend on: where the choices are nearly even the difference, taken of the counts, then keeps its digits, and
+// it is 0 where they are even (k = E); no term is larger than without.
 //
 //   balance_count   counts of each sequence's ids, in `splits` parts that need no clearing and no float atomics
 //   balance_rows    one pass over the logits: a group of lanes per token (softmax, dot product, gradient), a double partial of
@@ -104,6 +104,18 @@ __device__ __forceinline__ float group_max(float v) {
   return v;
 }
 
+template <int G>
+__device__ __forceinline__ int group_max_i32(int v) {
+  if constexpr (G == 64) return wave_max_i32(v);
+  v = max(v, dpp_i32<0xB1>(v));
+  v = max(v, dpp_i32<0x4E>(v));
+  if constexpr (G == 16) {
+    v = max(v, dpp_i32<0x141>(v));
+    v = max(v, dpp_i32<0x140>(v));
+  }
+  return v;
+}
+
 // Entry e of sequence s over its parts, whose loads go out together (one after another they are 16 round trips: 7 us)
 constexpr int kMaxSplits = 16;
 __device__ __forceinline__ int part_sum(const BalanceArgs& a, int64_t s, int64_t e) {
@@ -117,15 +129,15 @@ __device__ __forceinline__ int part_sum(const BalanceArgs& a, int64_t s, int64_t
 
 // G lanes per token, NV vectors of VW logits per lane: lane i of the group holds logits (i + j G) VW .. of j < NV.
 // A workgroup takes `tokens` consecutive tokens; where they belong to several sequences it goes through these in turn, with
-// the sequence's f in LDS. A group loads U tokens at once: a large batch is one such round, and its loads are what it waits for
-// (one token after another: 30 us for 16384 x 256, 16 with four at once).
-// MANY: more than kFewSeqs sequences, whose tokens would be few at a time: a group finds its token's sequence and reads its f
-// itself (59 tokens in 60 sequences: 37 us one after another, 12 so).
+// the sequence's counts in LDS. A group loads U tokens at once: a large batch is one such round, and its loads are what it waits
+// for (one token after another: 30 us for 16384 x 256, 16 with four at once).
+// MANY: more than kFewSeqs sequences, whose tokens would be few at a time: a group finds its token's sequence and reads its
+// counts itself (59 tokens in 60 sequences: 37 us one after another, 12 so).
 constexpr int kFewSeqs = 8;
 template <int G, int VW, int NV, bool MANY>
 __global__ __launch_bounds__(NTH) void balance_rows_kernel(BalanceArgs a, int tokens) {
   constexpr int TPP = NTH / G, U = MANY ? 1 : NV > 2 ? 2 : 4;  // tokens per pass, passes at once
-  __shared__ float s_f[MOE_MAX_EXPERTS];
+  __shared__ int s_count[MOE_MAX_EXPERTS];
   __shared__ double s_sum[NW];
   __shared__ int s_n, s_used, s_last;
   const int tid = threadIdx.x, gl = tid % G;
@@ -141,21 +153,21 @@ __global__ __launch_bounds__(NTH) void balance_rows_kernel(BalanceArgs a, int to
   // This lane's f less the smallest f, which it returns, of a sequence of n tokens (0 if there are none) from its counts
   auto shares = [&](auto&& count, int n, float (&f)[NV][VW]) {
     const float unit = n > 0 ? 1.f / ((float)a.k * (float)n) : 0.f;
-    float least = INFINITY;
+    int c[NV][VW], least = INT32_MAX;
 #pragma unroll
     for (int j = 0; j < NV; ++j)
 #pragma unroll
       for (int q = 0; q < VW; ++q) {
         const int e = (gl + j * G) * VW + q;
-        f[j][q] = n > 0 && e < a.E ? count(e) : 0.f;
-        least = e < a.E ? fminf(least, f[j][q]) : least;
+        c[j][q] = n > 0 && e < a.E ? count(e) : 0;
+        least = e < a.E ? min(least, c[j][q]) : least;
       }
-    least = -group_max<G>(-least);
+    least = -group_max_i32<G>(-least);
 #pragma unroll
     for (int j = 0; j < NV; ++j)
 #pragma unroll
-      for (int q = 0; q < VW; ++q) f[j][q] = (gl + j * G) * VW + q < a.E ? (f[j][q] - least) * unit : 0.f;
-    return least * unit;
+      for (int q = 0; q < VW; ++q) f[j][q] = (gl + j * G) * VW + q < a.E ? (float)(c[j][q] - least) * unit : 0.f;
+    return (float)least * unit;
   };
   // softmax, loss and gradient of token t, whose logits are x; f, least and factor are its sequence's
   double sum = 0.0;
@@ -225,7 +237,7 @@ __global__ __launch_bounds__(NTH) void balance_rows_kernel(BalanceArgs a, int to
       const bool live = n > 0 && (!a.mask || a.mask[t] != 0);
       float x[NV][VW], f[NV][VW];
       load(t, live, x);
-      const float least = shares([&](int e) { return (float)a.part[(int64_t)s * (a.E + 1) + e]; }, n, f);
+      const float least = shares([&](int e) { return a.part[(int64_t)s * (a.E + 1) + e]; }, n, f);
       token(t, true, live, x, f, least, n > 0 ? a.weight * (float)a.E / ((float)n * (float)s_used) : 0.f);
     }
   } else {
@@ -248,11 +260,11 @@ __global__ __launch_bounds__(NTH) void balance_rows_kernel(BalanceArgs a, int to
         t1 = in ? min(t_end, end) : t0 < begin ? min(t_end, begin) : t0;
       }
       if (t1 > t0) {
-        __syncthreads();  // s_f has been read
+        __syncthreads();  // s_count has been read
         if (in) {
           for (int e = tid; e <= a.E; e += NTH) {
             const int c = part_sum(a, s, e);
-            if (e < a.E) s_f[e] = (float)c;
+            if (e < a.E) s_count[e] = c;
             else s_n = c;
           }
         }
@@ -260,7 +272,7 @@ __global__ __launch_bounds__(NTH) void balance_rows_kernel(BalanceArgs a, int to
         const int n = in ? s_n : 0;
         const float factor = n > 0 ? a.weight * (float)a.E / ((float)n * (float)(a.S > 1 ? s_used : 1)) : 0.f;
         float f[NV][VW];
-        const float least = shares([&](int e) { return s_f[e]; }, n, f);
+        const float least = shares([&](int e) { return s_count[e]; }, n, f);
         for (int tu = t0 + tid / G; tu < t1; tu += TPP * U) {
           float x[U][NV][VW];
           bool live[U];
