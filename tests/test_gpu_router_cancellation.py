@@ -76,12 +76,15 @@ def test_values_of_one_token_and_column_far_apart():
     assert within(d_x.cpu(), dl @ wr.double(), tight(dl, torch.zeros_like(dl), wr.double()), BF16) <= 1.0
 
 
-@pytest.mark.parametrize("E", [12, 300])
-def test_an_infinity_gives_what_float32_gives(E):
+# two workgroups to a CU, one, two blocks of columns with 32 and with 64 tokens per wave; and the joint launch
+@pytest.mark.parametrize("T,E,joint", [(70, 12, False), (300, 200, False), (70, 300, False), (600, 300, False), (70, 12, True),
+                                       (300, 200, True), (70, 300, True)])
+def test_an_infinity_gives_what_float32_gives(T, E, joint):
     """An infinite gradient or weight: infinities of the products' signs, NaN where they cancel or meet a zero, whatever the
     size of the token's and the column's other values; and nothing else."""
+    print(f"\n[gpu] d_x with infinities {T} {E} {joint}", flush=True)
     g = torch.Generator().manual_seed(E)
-    T, H = 70, 136
+    H = 136
     d_in, wr = torch.randn(T, E, generator=g), torch.randn(E, H, generator=g)
     inf = float("inf")
     d_in[3, 5], d_in[3, 7], d_in[3, 8] = inf, -1e6, 1e30
@@ -94,12 +97,14 @@ def test_an_infinity_gives_what_float32_gives(E):
     d_x = torch.empty(T, H, dtype=BF16, device=DEV)
     ids, w = torch.zeros(T, 1, dtype=torch.int32), torch.ones(T, 1)
     moe.moe_route_backward(torch.zeros(T, H, dtype=BF16, device=DEV), wr.to(DEV), ids.to(DEV), w.to(DEV), None,
-                           d_in.to(DEV), torch.empty(T, E, device=DEV), d_x=d_x)
+                           d_in.to(DEV), torch.empty(T, E, device=DEV), d_x=d_x,
+                           d_w_router=torch.empty(E, H, device=DEV) if joint else None)
     ref = d_in.double() @ wr.double()
     got = d_x.cpu().double()
     bad = ~torch.isfinite(ref)
     assert bad[[3, 9, 17, 40]].all() and bad[:, [9, 33]].all()
-    assert torch.equal(torch.nan_to_num(got[bad], nan=5.0), torch.nan_to_num(ref[bad], nan=5.0))
+    same = torch.equal(torch.nan_to_num(got[bad], nan=5.0), torch.nan_to_num(ref[bad], nan=5.0))
+    assert same  # (a failure would spell out the tensors)
     fin = lambda t: torch.where(torch.isfinite(t), t, torch.zeros_like(t))
     dl, wf = fin(d_in.double()), fin(wr.double())
     got, ref = torch.where(bad, torch.zeros_like(got), got), torch.where(bad, torch.zeros_like(ref), ref)

@@ -14,7 +14,8 @@ pytestmark = pytest.mark.gpu
 # a workgroup takes 256 or 512 tokens of 128 or 64 columns, and at most 512 workgroups divided over the columns are launched;
 # the launches are joined where they need no more than 256 workgroups in all
 @pytest.mark.parametrize("T,H,E,k,dtype", [(4600, 7168, 256, 8, BF16), (4600, 7168, 256, 8, F32), (2200, 20480, 512, 8, BF16),
-                                           (2200, 20480, 512, 8, F32), (9001, 8192, 40, 4, BF16), (9001, 8192, 40, 4, F32)])
+                                           (2200, 20480, 512, 8, F32), (9001, 8192, 40, 4, BF16), (9001, 8192, 40, 4, F32),
+                                           (250, 20480, 400, 8, BF16), (250, 20480, 400, 8, F32)])
 def test_route_backward_of_many_tiles(T, H, E, k, dtype):
     print(f"\n[gpu] route backward {T} {H} {E} {k} {dtype}", flush=True)
     g = torch.Generator().manual_seed(T + H + E)
