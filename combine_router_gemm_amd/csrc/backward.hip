@@ -123,11 +123,18 @@ struct GradBf16 {
     o[0] = __builtin_bit_cast(u32x4, hi);
     o[1] = __builtin_bit_cast(u32x4, lo);
   }
-  static __device__ __forceinline__ u32x4 dw_part(float (&v)[8]) {  // and what it leaves
-    const u32x4 o = pack(v);
+  // the values' nearest bf16, and in v what it leaves. What would round to an infinity takes the largest bf16, so that the parts
+  // hold every finite value; an infinity or NaN is the part itself and leaves 0.
+  static __device__ __forceinline__ u32x4 dw_part(float (&v)[8]) {
+    constexpr float kMost = 0x1.fep127f;
+    float c[8];
 #pragma unroll
-    for (int q = 0; q < 8; ++q) v[q] = bf16_rest(v[q]);
-    return o;
+    for (int q = 0; q < 8; ++q) {
+      const bool finite = fabsf(v[q]) < INFINITY;
+      c[q] = finite ? fminf(fmaxf(v[q], -kMost), kMost) : v[q];
+      v[q] = finite ? v[q] - (float)(bf16_t)c[q] : 0.f;
+    }
+    return pack(c);
   }
 };
 struct GradF32 {

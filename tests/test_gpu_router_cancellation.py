@@ -109,3 +109,30 @@ def test_an_infinity_gives_what_float32_gives(T, E, joint):
     dl, wf = fin(d_in.double()), fin(wr.double())
     got, ref = torch.where(bad, torch.zeros_like(got), got), torch.where(bad, torch.zeros_like(ref), ref)
     assert within(got.to(BF16), ref, tight(dl, torch.zeros_like(dl), wf), BF16) <= 1.0
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("T,H,E", [(40, 136, 12), (300, 264, 130)])
+def test_d_w_router_at_the_ends_of_the_range(T, H, E, dtype):
+    """Gradients of the logits up to the largest float32 (beyond the largest bf16, 3.39e38, too), and infinite ones: infinities of
+    the products' signs and NaN where they cancel or meet a zero, as in float32; the rest to the bound of its sums."""
+    print(f"\n[gpu] d_w_router at the ends {T} {H} {E} {dtype}", flush=True)
+    g = torch.Generator().manual_seed(T + E)
+    d_in, x = torch.randn(T, E, generator=g), torch.randn(T, H, generator=g).to(dtype)
+    x[5:8] *= 2.0 ** -10
+    big = torch.finfo(F32).max
+    d_in[5, 1], d_in[6, 2], d_in[7, 3] = big, -big, 3.3960e38
+    inf = float("inf")
+    d_in[9, 4], d_in[10, 5], d_in[11, 5], d_in[12, 6] = -inf, inf, -inf, float("nan")
+    x[9, 3] = 0.0
+    ids, w = torch.zeros(T, 1, dtype=torch.int32), torch.ones(T, 1)
+    d_wr, d_b = torch.empty(E, H, device=DEV), torch.empty(E, device=DEV)
+    moe.moe_route_backward(x.to(DEV), torch.zeros(E, H, device=DEV), ids.to(DEV), w.to(DEV), None, d_in.to(DEV),
+                           torch.empty(T, E, device=DEV), d_w_router=d_wr, d_bias=d_b)
+    ref = d_in.double().T @ x.double()
+    got, bad = d_wr.cpu().double(), ~torch.isfinite(ref)
+    assert bad[4:7].all() and bad.sum() == 3 * H
+    same = torch.equal(torch.nan_to_num(got[bad], nan=5.0), torch.nan_to_num(ref[bad], nan=5.0))
+    assert same
+    bound = (T + 2) * U * (torch.nan_to_num(d_in.double(), posinf=0.0, neginf=0.0).abs().T @ x.double().abs())
+    assert within(torch.where(bad, torch.zeros_like(got), got), torch.where(bad, torch.zeros_like(ref), ref), bound, F32) <= 1.0
