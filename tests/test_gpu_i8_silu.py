@@ -19,7 +19,9 @@ GONE = [-200.0, -1.0e9, -3.0e38]  # silu below half of float32's smallest step
 
 
 # H, F, rows per tile, whether the gate/up pass is split
-@pytest.mark.parametrize("H,F,copies,tile,split", [(16, 32, 1, 32, False), (2064, 48, 1, 32, True), (32, 32, 40, None, False)])
+@pytest.mark.parametrize("H,F,copies,tile,split", [(16, 32, 1, 32, False), (2064, 48, 1, 32, True), (32, 32, 40, 32, False),
+                                                        (512, 512, 100, 64, False), (512, 512, 300, 128, False),
+                                                        (1184, 736, 300, 256, False)])
 def test_ends_of_silu(H, F, copies, tile, split):
     print(f"\n[gpu] silu of int8 experts {H} {F} {copies}", flush=True)
     g = torch.Generator().manual_seed(H)
@@ -27,7 +29,7 @@ def test_ends_of_silu(H, F, copies, tile, split):
     counts = [len(v) for v in goal]
     T = sum(counts)
     cut = moe.moe_expert_mlp_i8_tiling(T, 1, 3, 1, T, H, F)
-    assert (tile is None or cut[0] == tile) and (cut[1] > 1) == split
+    assert (cut[0], cut[1] > 1) == (tile, split)
     L = layout_of(counts, T, 1, 1, T, H)
     levels = torch.randint(-127, 128, (3, F), generator=g)
     levels[:, 0] = 127
