@@ -2,7 +2,9 @@
 //
 // combine: y[t] = sum_j w[t, j] out[row(t, j)] over kept slots, so d_w[t, j] = dy[t] . out[row] and d_out[row] = w[t, j] dy[t].
 //   One workgroup per token reads dy[t] once and its rows once. Bound: HBM (16384 tokens, H 7168, 256 experts of at most 640
-//   rows: 344 us, 5.6 TB/s of reads and writes).
+//   rows: 344 us, 5.6 TB/s of reads and writes; without d_out 153 us). A row of fewer than 256 slices leaves lanes idle: k 8
+//   and H 128 in f32 take 72 us, H 512 in bf16 80, where their bytes are 28 and 55 at a copy's rate; H 2048 in bf16 takes 206,
+//   5.5 TB/s.
 //
 // router: w = softmax over the selected logits, logits = x Wr^T + b. With c_j = w_j (d_w_j - sum_i w_i d_w_i), the gradient of
 //   the logits is d_in plus c_j at the selected experts; then d_x = d_logits Wr, d_Wr = d_logits^T x, d_b = the column sums.
@@ -405,7 +407,7 @@ __device__ __forceinline__ void route_dx(const GradArgs& a, unsigned char* s_w, 
               if constexpr (sizeof(X) == 4 && NJ == 4) *reinterpret_cast<u32x4*>(o) = pack(v);
               else if constexpr (sizeof(X) == 4) *reinterpret_cast<f32x2*>(o) = f32x2{v[0], v[1]};
               else if constexpr (NJ == 2) __builtin_nontemporal_store(pack2_bf16(v[0], v[1]), reinterpret_cast<uint32_t*>(o));
-              else  // (non-temporal: 29.4 -> 27.7 us)
+              else  // (non-temporal: 29.4 -> 27.7 us with operands of one part)
                 __builtin_nontemporal_store(u32x2{pack2_bf16(v[0], v[1]), pack2_bf16(v[2], v[3])},
                                             reinterpret_cast<u32x2*>(o));
             }
@@ -715,8 +717,8 @@ hipError_t launch_dw(const GradArgs& a, hipStream_t stream) {
   return hipGetLastError();
 }
 
-// Both products in one launch, if they fit the CUs together (17 tokens, H 1216, 215 experts: 23 -> 15 us with the preparation);
-// returns whether they did
+// Both products in one launch, if they fit the CUs together (17 tokens, H 1216, 215 experts: 23 -> 15 us with the preparation
+// when d_x's operands had one part; 17 with two); returns whether they did
 template <typename G, int NJ, int WE>
 bool launch_dx_dw(const GradArgs& a, hipStream_t stream) {
   const int tiles = ceil_div_host(a.r.H, kDwCols), units = tiles * a.splits * ceil_div_host(a.eb, 8);
@@ -770,13 +772,14 @@ hipError_t launch_route_backward_t(const RouteBackward& r, hipStream_t stream) {
     if (st == hipSuccess && r.d_x && !joint) {
       if constexpr (G::SCALED) {
         // Two workgroups per CU, whose stores and products overlap, where half the LDS and half the registers do (16 experts,
-        // 16384 tokens, H 4096: 30.7 us against 38.5 with one; 64 experts, 4096 tokens, H 7168: 23.9 against 26.9). With one,
+        // 16384 tokens, H 4096: 29.5 us against 38.5 with one; 64 experts, 4096 tokens, H 7168: 23.2 against 26.9). With one,
         // 64 tokens per wave take every fragment of the weight out of LDS half as often, which pays with two blocks of
-        // columns, given tokens for all waves (4096 tokens, H 7168, 384 and 512 experts: 83 and 103 us against 89 and 117;
+        // columns, given tokens for all waves (4096 tokens, H 7168, 384 and 512 experts: 82 and 105 us against 89 and 117;
         // 240 tokens, H 20480, 512 experts: 40 against 33; four blocks, 256 experts: 53 either way).
         if (a.nj == 2) st = a.tb > kDxWaves ? launch_dx<G, 2, 2, 4, 1>(a, stream) : launch_dx<G, 2, 1, 4, 1>(a, stream);
         else st = a.ek <= 8 ? launch_dx<G, 4, 1, 2, 2>(a, stream) : launch_dx<G, 4, 1, 4, 1>(a, stream);
       } else {
+        // (256 experts, 4096 tokens, H 7168: 149 us, 101 TFLOP/s; 64 tokens per wave took as long)
         st = a.nj == 2 ? launch_dx<G, 2, 1, 4, 2>(a, stream) : launch_dx<G, 4, 1, 4, 2>(a, stream);
       }
     }

@@ -132,7 +132,12 @@ __device__ __forceinline__ int part_sum(const BalanceArgs& a, int64_t s, int64_t
 // the sequence's counts in LDS. A group loads U tokens at once: a large batch is one such round, and its loads are what it waits
 // for (one token after another: 30 us for 16384 x 256, 16 with four at once).
 // MANY: more than kFewSeqs sequences, whose tokens would be few at a time: a group finds its token's sequence and reads its
-// counts itself (59 tokens in 60 sequences: 37 us one after another, 12 so).
+// counts itself, which have to be in one part. Kernel times (us) one sequence after another, and so:
+//   tokens x experts, sequences   301 x 24, 9   301 x 24, 16   4000 x 24, 9   4000 x 256, 9   4000 x 256, 16   16384 x 256, 16
+//                                    13.7  6.3     17.2   6.5     11.1   8.7      15.2  10.5       15.6  10.8        20.2   19.9
+// Fewer sequences are counted in parts where the batch is large (16 / S of them from 4096 / S tokens on), hence the border.
+// Batches of under 512 tokens have one part: below it, they would take 6.0 us so at two sequences of 24 experts instead of 10.4,
+// 6.2 instead of 10.8 at five, and 8.0 instead of 19.5 at eight of 256.
 constexpr int kFewSeqs = 8;
 template <int G, int VW, int NV, bool MANY>
 __global__ __launch_bounds__(NTH) void balance_rows_kernel(BalanceArgs a, int tokens) {
@@ -304,8 +309,9 @@ __global__ __launch_bounds__(NTH) void balance_rows_kernel(BalanceArgs a, int to
     double v = 0.0;
     for (int w = 0; w < NW; ++w) v += s_sum[w];
     __hip_atomic_store(&a.partial[blockIdx.x], v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    // an agent-scope store writes through to where every XCD reads it: its acknowledgement is all the order it needs, and
-    // a fence's write-back of the L2 would flush the gradients as well
+    // an agent-scope store writes through to where every XCD reads it: its acknowledgement is all the order it needs (the
+    // release and acquire that the memory model asks for beside it are for plain accesses, which the L2s may hold: with them
+    // 17.5 us instead of 15.4 for 16384 x 256, as the write-back flushes the gradients as well)
     wait_loads<0>();
     s_last = __hip_atomic_fetch_add(a.ticket, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) == (int)gridDim.x - 1;
   }

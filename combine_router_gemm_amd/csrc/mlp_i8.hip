@@ -11,7 +11,7 @@
 //                   stages in flight; 32- and 64-row tiles stream the weights of experts with few rows and are bound by their
 //                   bytes (48 experts of 7168 x 2048, 128 tokens: gate/up 213 us, 6.6 TB/s, down 113, 6.2 TB/s), 128- and
 //                   256-row ones by the matrix units and the power that they draw (32 experts of 7168 x 2048, 1024 rows each:
-//                   gate/up 945-980 us, down 530-560, 1.9 PFLOP/s at 1.8 GHz).
+//                   gate/up 975-990 us, down 535-560, 1.9 PFLOP/s at 1.8 GHz).
 #include <algorithm>
 #include <type_traits>
 
@@ -342,7 +342,9 @@ __global__ __launch_bounds__(WM * WN * 64, PER_CU * WM * WN / 4 > 1 ? PER_CU * W
                              __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
         }
         // agent-scope stores write through to where every XCD reads them, so their acknowledgement is all the order that
-        // the count needs. Nothing waits for another workgroup: the last to arrive finishes the tile.
+        // the count needs. Nothing waits for another workgroup: the last to arrive finishes the tile. (The memory model's release
+        // and acquire, which are for plain accesses that an L2 may hold, would write back and drop caches for every part: 38 us
+        // instead of 26 for one Mixtral-shaped token's down pass.)
         int* s_last = reinterpret_cast<int*>(s_top);
         wait_loads<0>();
         lds_barrier();
@@ -569,7 +571,8 @@ struct I8Plan {
   int tile, gu_split, gu_stages, dn_split, dn_stages;
 };
 
-// Tiles of a row block count when the rows are spread over the experts; fewer rows than experts reach as many at most
+// Tiles of a row block count when the rows are spread evenly over the experts (hot experts, which a call's sizes do not show,
+// have other counts); fewer rows than experts reach as many at most
 int64_t row_tiles(int64_t rows_max, int El, int bm) {
   const int64_t n = std::min<int64_t>(El, rows_max);
   return n * ceil_div_host64(ceil_div_host64(rows_max, n), bm);

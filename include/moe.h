@@ -541,7 +541,8 @@ int moe_balance_loss(const float* logits, const int32_t* topk_ids, const int32_t
  *   out_buf    [rows_max, H] (xdt), layout and topk_w as moe_combine took them
  *   d_topk_w   [T, k] fp32 (output)
  *   d_out_buf  [rows_max, H] (xdt, output; neither out_buf nor dy itself), or NULL: frozen experts need none. Rows >= total
- *              are left as they were.
+ *              are left as they were. It is for a caller's own backward of the experts: this library has none, so the d_x of
+ *              moe_route_backward is the router's part alone.
  * (The gradient of moe_dispatch, d_x[t] = the sum of its kept rows' gradients, is moe_combine of them with weights of 1.)
  */
 int moe_combine_backward(const void* dy, moe_dtype_t xdt, const void* out_buf, const moe_layout_t* layout,
@@ -556,7 +557,8 @@ size_t moe_route_backward_workspace_bytes(int T, int H, int E, moe_dtype_t xdt);
  *                    topk_w[t, j] * (d_topk_w[t, j] - sum_i topk_w[t, i] * d_topk_w[t, i])
  *   d_x = d_logits w_router (rounded once to xdt), d_w_router = d_logits^T x, d_bias = sum_t d_logits[t], sums in fp32 or
  *   more (d_logits itself is the gradient of a [T, E] bias). The products are fp32's; in d_x of bf16 layers an operand enters
- *   with 22 bits: off by 2^-22 of itself, and by 2^-39 of the largest of its token or column, at most
+ *   with 22 bits: off by 2^-22 of itself, and by 2^-39 of the largest of its token or column, at most. Infinities and NaN give
+ *   what they give in fp32, but that an infinite x may make its column of d_w_router NaN in bf16 layers
  *   x            [T, H] (xdt), w_router [E, H] fp32, topk_ids and topk_w [T, k] as moe_route took and wrote them
  *   d_topk_w     [T, k] fp32 (moe_combine_backward), or NULL: none
  *   d_logits_in  [T, E] fp32, what other losses add (moe_balance_loss), or NULL: none; not both may be NULL
