@@ -101,7 +101,8 @@ __global__ __launch_bounds__(NTH) void combine_backward_kernel(const T* __restri
 //   route_dx          the weight's fragments of 32 NJ columns stay in LDS while the tokens stream past
 //   route_dw          x is transposed on its way to LDS; the tokens are split over workgroups where the tiles are few
 constexpr int kRows = 32, kFrag = 1024;  // rows of a fragment, its bytes
-constexpr int kNonFinite = 1 << 16;      // in place of a power of two: not all of the values are finite
+// in place of a power of two: there are infinities among the values; there are NaN
+constexpr int kInfinite = 1 << 16, kNan = 1 << 17;
 
 struct GradBf16 {
   using X = bf16_t;
@@ -118,7 +119,7 @@ struct GradBf16 {
     f16x8 hi, lo;
 #pragma unroll
     for (int q = 0; q < 8; ++q) {
-      const float s = e == kNonFinite ? 0.f : ldexpf(v[q], e);
+      const float s = e >= kInfinite ? 0.f : ldexpf(v[q], e);
       hi[q] = (_Float16)s;
       lo[q] = (_Float16)(s - (float)hi[q]);
     }
@@ -166,10 +167,9 @@ struct GradArgs {
   int splits, chunks_per_split;
 };
 
-// The power of two that puts a largest value, given by its bits, into [2^14, 2^15); 0 for zero, kNonFinite for infinities and
-// NaN.
+// The power of two that puts a largest value, given by its bits, into [2^14, 2^15); 0 for zero, kInfinite, kNan.
 __device__ __forceinline__ int fp16_exp(uint32_t top) {
-  if (top >= 0x7f800000u) return kNonFinite;
+  if (top >= 0x7f800000u) return top == 0x7f800000u ? kInfinite : kNan;
   if (top == 0) return 0;
   return 15 - (int)(__builtin_amdgcn_frexp_expf(__uint_as_float(top)));
 }
@@ -292,7 +292,9 @@ __global__ __launch_bounds__(kPrepThreads) void route_grad_prep_kernel(GradArgs 
   }
 }
 
-// d_x of a block's tokens and a lane's NJ columns where either holds an infinity or NaN: fp32 products, one after another
+// d_x of a block's tokens and a lane's NJ columns where either holds a NaN, which all of its products are, or an infinity: fp32
+// products, eight at once on their way, until they are NaN. 4096 tokens, H 7168, 256 experts, the call: 123 us without, 192 where
+// every value is NaN, 178 with one infinity, 8.1 ms with one in every token.
 template <int NJ>
 __device__ __forceinline__ void route_dx_apart(const GradArgs& a, int64_t t0, int h, int lane) {
   const RouteBackward& r = a.r;
@@ -300,10 +302,22 @@ __device__ __forceinline__ void route_dx_apart(const GradArgs& a, int64_t t0, in
   for (int i = 0; i < 16 * NJ; ++i) {
     const int64_t t = t0 + Op32::out_row(lane, i / NJ);
     const int c = h + i % NJ;
-    if (t >= r.T || c >= r.H || max(a.t_exp[t], a.h_exp[c]) != kNonFinite) continue;
-    float v = 0.f;
+    if (t >= r.T || c >= r.H) continue;
+    const int most = max(a.t_exp[t], a.h_exp[c]);
+    if (most < kInfinite) continue;
+    float v = most == kNan ? __uint_as_float(0x7fc00000u) : 0.f;
 #pragma unroll 1
-    for (int e = 0; e < r.E; ++e) v = fmaf(r.d_logits[t * r.E + e], r.w_router[(int64_t)e * r.H + c], v);
+    for (int e0 = 0; e0 < r.E && v == v; e0 += 8) {
+      float d[8], w[8];
+#pragma unroll
+      for (int q = 0; q < 8; ++q) {
+        const bool in = e0 + q < r.E;
+        d[q] = in ? r.d_logits[t * r.E + e0 + q] : 0.f;
+        w[q] = in ? r.w_router[(int64_t)(e0 + q) * r.H + c] : 0.f;
+      }
+#pragma unroll
+      for (int q = 0; q < 8; ++q) v = fmaf(d[q], w[q], v);
+    }
     static_cast<bf16_t*>(r.d_x)[t * r.H + c] = (bf16_t)v;
   }
 }
@@ -387,7 +401,7 @@ __device__ __forceinline__ void route_dx(const GradArgs& a, unsigned char* s_w, 
         // the powers of two of the block's tokens, by scalar loads: vector loads would wait for the fragments on their way
         const auto* te = (const __attribute__((address_space(4))) int*)(a.t_exp + (int64_t)min(tb, a.tb - 1) * kRows);
         int he[NJ];
-        int most = 0;  // the largest of the powers, or 0: kNonFinite where something has to be computed apart
+        int most = 0;  // the largest of the powers, or 0: kInfinite or kNan where something has to be computed apart
 #pragma unroll
         for (int j = 0; j < NJ; ++j) {
           he[j] = G::SCALED ? s_he[j] : 0;
@@ -413,7 +427,7 @@ __device__ __forceinline__ void route_dx(const GradArgs& a, unsigned char* s_w, 
             }
           }
           if constexpr (G::SCALED)
-            if (most == kNonFinite) route_dx_apart<NJ>(a, t0, h, lane);
+            if (most >= kInfinite) route_dx_apart<NJ>(a, t0, h, lane);
         }
       }
       clear();
